@@ -36,6 +36,8 @@ DDP, STAGE1, STAGE2, STAGE3, FSDP, MEGATRON_DO = range(6)
 BF16, FP32 = 0, 1
 INDEX_FULL, INDEX_SHARD = 0, 1
 K_INNER, K_OUTER = 0, 1
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = range(5)
+SAVED_BF16, SAVED_E4M3 = 0, 1
 MIX_STEP_STREAMS, MIX_READS, MIX_WRITES = 0, 1, 2
 MAX_RANKS_PER_CALL = 64
 NOALLOC_MAX_PARTIALS = 524288
@@ -45,6 +47,9 @@ GRAD_CHUNK_DEFAULT = 16384                         # chunked gradients, likewise
 
 STRATEGY = {"ddp": DDP, "zero1": STAGE1, "zero1_allreduce": STAGE1, "zero2": STAGE2,
             "zero3": STAGE3, "fsdp": FSDP, "fsdp2": FSDP, "megatron_do": MEGATRON_DO}
+
+ACTIVATION = {"none": ACT_NONE, "relu": ACT_RELU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH,
+              "silu": ACT_SILU}
 
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
@@ -140,6 +145,50 @@ _lib.zero_fsdp_linear_forward.restype = _I32
 _lib.zero_fsdp_linear_backward.argtypes = [_P, _I32, ctypes.POINTER(ctypes.c_void_p), _I64, _P,
                                            _P, _P, _P, _I32, _P, _P]
 _lib.zero_fsdp_linear_backward.restype = _I32
+
+
+class _Saved(ctypes.Structure):
+    _fields_ = [("data", _P), ("ld", _I64), ("scales", _P), ("ld_scales", _I64), ("format", _I32)]
+
+
+class _Epilogue(ctypes.Structure):
+    _fields_ = [("bias", _P), ("residual", _P), ("ldr", _I64), ("preact", ctypes.POINTER(_Saved)),
+                ("output", ctypes.POINTER(_Saved)), ("bias_dtype", _I32), ("residual_dtype", _I32),
+                ("act", _I32)]
+
+
+_SP = ctypes.POINTER(_Saved)
+_EP = ctypes.POINTER(_Epilogue)
+_PP = ctypes.POINTER(ctypes.c_void_p)
+_lib.zero_saved_write.argtypes = [_I64, _I64, _P, _I64, _I32, _SP, _P]
+_lib.zero_saved_write.restype = _I32
+_lib.zero_saved_read.argtypes = [_I64, _I64, _SP, _P, _I64, _I32, _P]
+_lib.zero_saved_read.restype = _I32
+_lib.zero_gemm_bf16_epilogue.argtypes = [_I64, _I64, _I64, _P, _I64, _I32, _P, _I64, _I32, _P, _I64,
+                                         _I32, _EP, _P]
+_lib.zero_gemm_bf16_epilogue.restype = _I32
+_lib.zero_act_backward.argtypes = [_I64, _I64, _P, _I64, _I32, _I32, _SP, _P, _I64, _P, _P, _I64, _P]
+_lib.zero_act_backward.restype = _I32
+_lib.zero_act_backward_workspace.argtypes = [_I64, _I64]
+_lib.zero_act_backward_workspace.restype = _I64
+_lib.zero_gemm_saved_bf16.argtypes = [_I64, _I64, _I64, _SP, _P, _I64, _P, _I64, _I32, _P]
+_lib.zero_gemm_saved_bf16.restype = _I32
+_lib.zero_gemm_grouped_rows_bf16.argtypes = [_I32, _P, _I64, _I64, _I64, _P, _I64, _P, _I64, _I32,
+                                             _I64, _P, _I64, _I32, _EP, _P]
+_lib.zero_gemm_grouped_rows_bf16.restype = _I32
+_lib.zero_gemm_grouped_depth_bf16.argtypes = [_I32, _P, _I64, _I64, _I64, _P, _I64, _P, _I64, _P,
+                                              _I64, _I64, _I32, _P]
+_lib.zero_gemm_grouped_depth_bf16.restype = _I32
+_lib.zero_fsdp_linear_act_forward.argtypes = [_P, _I32, _PP, _I64, _P, _P, _EP, _P, _I32, _P]
+_lib.zero_fsdp_linear_act_forward.restype = _I32
+_lib.zero_fsdp_linear_act_backward.argtypes = [_P, _I32, _PP, _I64, _SP, _I32, _SP, _P, _P, _P, _P,
+                                               _I32, _P, _P, _P, _I64, _P]
+_lib.zero_fsdp_linear_act_backward.restype = _I32
+_lib.zero_fsdp_experts_forward.argtypes = [_P, _I32, _I32, _PP, _P, _I64, _P, _P, _EP, _P, _I32, _P]
+_lib.zero_fsdp_experts_forward.restype = _I32
+_lib.zero_fsdp_experts_backward.argtypes = [_P, _I32, _I32, _PP, _P, _I64, _P, _P, _P, _P, _I32, _P,
+                                            _P]
+_lib.zero_fsdp_experts_backward.restype = _I32
 _lib.zero_stream_mix.argtypes = [_I32, ctypes.POINTER(ctypes.c_void_p), _I32, _P, _P, _P, _P,
                                  _I64, _I64, _I64, _P]
 _lib.zero_stream_mix.restype = _I32
@@ -159,6 +208,11 @@ EXPORTS = ("zero_shard_init", "zero_shard_init_rows", "zero_layout_rows", "zero_
            "zero_grad_accumulate", "zero_stream_mix", "zero_fsdp_sweep", "zero_fsdp_sweep_table", "zero_gemm_bf16",
            "zero_gemm_bf16_nt",
            "zero_transpose_bf16", "zero_fsdp_linear_forward", "zero_fsdp_linear_backward",
+           "zero_saved_write", "zero_saved_read", "zero_gemm_bf16_epilogue", "zero_act_backward",
+           "zero_act_backward_workspace", "zero_gemm_saved_bf16", "zero_gemm_grouped_rows_bf16",
+           "zero_gemm_grouped_depth_bf16", "zero_fsdp_linear_act_forward",
+           "zero_fsdp_linear_act_backward", "zero_fsdp_experts_forward",
+           "zero_fsdp_experts_backward",
            "zero_status_str", "zero_last_error")
 
 
@@ -193,6 +247,7 @@ _DTYPES = {
     "fp64": (torch.float64,),
     "bf16": (torch.int16, torch.uint16, torch.bfloat16),   # bf16 bit patterns
     "int64": (torch.int64,),
+    "codes": (torch.uint8, torch.float8_e4m3fn),           # one byte each
 }
 
 
@@ -746,6 +801,330 @@ def fsdp_linear_backward(layout: Layout, unit: int, w_shards, batch: int, x, dy,
                                           _addr(dy), _addr(w_full), _addr(dx), dx_dtype,
                                           _addr(dw_full), _stream(stream)),
            "zero_fsdp_linear_backward")
+
+
+# ------------------------------------------------------- layer operators --
+
+def _one_device(stream, *tensors) -> None:
+    """The tensors of a call share a device, and it is the one that the
+    default stream (the current device's) belongs to."""
+    at = None
+    for x in tensors:
+        if x is None or x.__class__ is int or not hasattr(x, "get_device"):
+            continue
+        d = x.get_device()
+        if at is None:
+            at = d
+        elif d != at:
+            raise ValueError(f"tensors of one call on two devices ({at} and {d})")
+    if at is not None and at >= 0 and stream is None and at != torch.cuda.current_device():
+        raise ValueError(f"tensors on device {at}, but the current device is "
+                         f"{torch.cuda.current_device()}: switch to it, or give a stream of it")
+
+
+def _extent(rows: int, ld: int, cols: int) -> Optional[int]:
+    """Elements from a matrix's start to its last one (None: a size that the
+    library refuses)."""
+    if rows < 0 or cols < 0 or ld < cols:
+        return None
+    return 0 if rows == 0 or cols == 0 else (rows - 1) * ld + cols
+
+
+class Saved:
+    """A rows x cols activation matrix kept for the backward pass: bf16
+    (`scales` None), or 8-bit codes with one exponent byte per 32 rows of a
+    column.  Keeps its buffers alive."""
+
+    def __init__(self, data, ld: int, scales=None, ld_scales: int = 0):
+        self.data, self.scales = data, scales
+        self.format = SAVED_BF16 if scales is None else SAVED_E4M3
+        self.s = _Saved(_addr(data), ld, _addr(scales), ld_scales, self.format)
+        self._checked = None
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, device="cuda") -> "Saved":
+        """An 8-bit checkpoint of rows x cols with buffers of its own."""
+        ld, lds = -(-max(cols, 1) // 16) * 16, -(-max(cols, 1) // 4) * 4
+        return cls(torch.empty((max(rows, 1), ld), dtype=torch.uint8, device=device), ld,
+                   torch.empty((max(-(-rows // 32), 1), lds), dtype=torch.uint8, device=device), lds)
+
+    def ref(self):
+        return ctypes.byref(self.s)
+
+    def check(self, what: str, rows: int, cols: int) -> None:
+        if self._checked == (rows, cols):
+            return
+        n = _extent(rows, self.s.ld, cols)
+        if self.format == SAVED_BF16:
+            _need(self.data, what, n, "bf16")
+        else:
+            _need(self.data, f"{what} codes", n, "codes")
+            _need(self.scales, f"{what} scales", _extent(-(-rows // 32), self.s.ld_scales, cols),
+                  "codes")
+        if n is not None:
+            self._checked = (rows, cols)
+
+
+def _saved_ref(s: Optional[Saved]):
+    return None if s is None else s.ref()
+
+
+def _act(act) -> int:
+    if isinstance(act, str):
+        if act not in ACTIVATION:
+            raise ValueError(f"unknown activation {act!r} (one of {', '.join(ACTIVATION)})")
+        return ACTIVATION[act]
+    return int(act)
+
+
+class Epilogue:
+    """C = act(z) + residual with z = A B + bias; `preact` keeps z, `output`
+    keeps C in 8 bits.  `act` is a name of ACTIVATION or its number; the
+    types of bias and residual are taken from tensors, else bias_dtype and
+    residual_dtype (raw addresses).  Keeps its buffers alive."""
+
+    def __init__(self, bias=None, act=ACT_NONE, residual=None, ldr: int = 0, preact: Optional[Saved] = None,
+                 output: Optional[Saved] = None, bias_dtype: int = BF16, residual_dtype: int = BF16):
+        self.bias, self.residual, self.preact, self.output = bias, residual, preact, output
+        kind = lambda x, given: (FP32 if x.dtype == torch.float32 else BF16) \
+            if hasattr(x, "dtype") else given
+        self.s = _Epilogue(_addr(bias), _addr(residual), ldr,
+                           None if preact is None else ctypes.pointer(preact.s),
+                           None if output is None else ctypes.pointer(output.s),
+                           kind(bias, bias_dtype), kind(residual, residual_dtype), _act(act))
+
+    def ref(self):
+        return ctypes.byref(self.s)
+
+    def check(self, M: int, N: int) -> None:
+        _need(self.bias, "bias", N if N >= 0 else None, _kind(self.s.bias_dtype))
+        _need(self.residual, "residual", _extent(M, self.s.ldr, N), _kind(self.s.residual_dtype))
+        if self.preact is not None:
+            self.preact.check("preact", M, N)
+        if self.output is not None:
+            self.output.check("output", M, N)
+
+    def tensors(self):
+        kept = [x for s in (self.preact, self.output) if s is not None for x in (s.data, s.scales)]
+        return [self.bias, self.residual, *kept]
+
+
+def _check_epilogue(ep: Optional[Epilogue], M: int, N: int):
+    """(the C argument, the epilogue's tensors) of a call's M x N product."""
+    if ep is None:
+        return None, ()
+    ep.check(M, N)
+    return ep.ref(), ep.tensors()
+
+
+def saved_write(rows: int, cols: int, x, ldx: int, out: Saved, x_dtype: Optional[int] = None,
+                stream=None) -> None:
+    """x (rows x cols, bf16 or fp32: taken from the tensor, BF16 for a raw
+    address unless given) into the 8-bit checkpoint `out`."""
+    if x_dtype is None:
+        x_dtype = FP32 if getattr(x, "dtype", None) == torch.float32 else BF16
+    _need(x, "x", _extent(rows, ldx, cols), _kind(x_dtype))
+    out.check("out", rows, cols)
+    _one_device(stream, x, out.data, out.scales)
+    _check(_lib.zero_saved_write(rows, cols, _addr(x), ldx, x_dtype, out.ref(), _stream(stream)),
+           "zero_saved_write")
+
+
+def saved_read(rows: int, cols: int, saved: Saved, out, ldo: int, out_dtype: Optional[int] = None,
+               stream=None) -> None:
+    """The values of an 8-bit checkpoint, exact in bf16 and in fp32."""
+    if out_dtype is None:
+        out_dtype = FP32 if getattr(out, "dtype", None) == torch.float32 else BF16
+    saved.check("saved", rows, cols)
+    _need(out, "out", _extent(rows, ldo, cols), _kind(out_dtype))
+    _one_device(stream, out, saved.data, saved.scales)
+    _check(_lib.zero_saved_read(rows, cols, saved.ref(), _addr(out), ldo, out_dtype,
+                                _stream(stream)), "zero_saved_read")
+
+
+def gemm_bf16_epilogue(M: int, N: int, K: int, A, lda: int, a_order: int, B, ldb: int, b_order: int,
+                       C, ldc: int, c_dtype: int = FP32, epilogue: Optional[Epilogue] = None,
+                       stream=None) -> None:
+    """gemm_bf16 with bias, activation, residual and kept outputs."""
+    if M > 0 and N > 0 and K >= 0:
+        _need(A, "A", _operand_extent(M, K, lda, a_order), "bf16")
+        _need(B, "B", _operand_extent(N, K, ldb, b_order), "bf16")
+        _need(C, "C", (M - 1) * ldc + N, _kind(c_dtype))
+    ref, more = _check_epilogue(epilogue, M, N)
+    _one_device(stream, A, B, C, *more)
+    _check(_lib.zero_gemm_bf16_epilogue(M, N, K, _addr(A), lda, a_order, _addr(B), ldb, b_order,
+                                        _addr(C), ldc, c_dtype, ref, _stream(stream)),
+           "zero_gemm_bf16_epilogue")
+
+
+def act_backward_workspace(rows: int, cols: int) -> int:
+    """Floats of workspace that dbias of rows x cols needs."""
+    return _lib.zero_act_backward_workspace(rows, cols)
+
+
+def _check_act_backward(rows, cols, dy, ldy, dy_dtype, preact, dz, ldz, dbias, workspace):
+    _need(dy, "dy", _extent(rows, ldy, cols), _kind(dy_dtype))
+    if preact is not None:
+        preact.check("preact", rows, cols)
+    _need(dz, "dz", _extent(rows, ldz, cols), "bf16")
+    if dbias is not None:
+        _need(dbias, "dbias", max(cols, 0), "fp32")
+        _need(workspace, "workspace", act_backward_workspace(rows, cols), "fp32")
+
+
+def _numel(x) -> int:
+    """Elements of a workspace; a raw address is taken at its caller's word."""
+    return 0 if x is None else x.numel() if hasattr(x, "numel") else (1 << 62)
+
+
+def act_backward(rows: int, cols: int, dy, ldy: int, act, preact: Optional[Saved], dz, ldz: int,
+                 dbias=None, workspace=None, dy_dtype: Optional[int] = None, stream=None) -> None:
+    """dz = dy act'(preact) in bf16 and dbias = its column sums in fp32."""
+    if dy_dtype is None:
+        dy_dtype = FP32 if getattr(dy, "dtype", None) == torch.float32 else BF16
+    _check_act_backward(rows, cols, dy, ldy, dy_dtype, preact, dz, ldz, dbias, workspace)
+    more = () if preact is None else (preact.data, preact.scales)
+    _one_device(stream, dy, dz, dbias, workspace, *more)
+    _check(_lib.zero_act_backward(rows, cols, _addr(dy), ldy, dy_dtype, _act(act), _saved_ref(preact),
+                                  _addr(dz), ldz, _addr(dbias), _addr(workspace), _numel(workspace),
+                                  _stream(stream)), "zero_act_backward")
+
+
+def gemm_saved_bf16(M: int, N: int, K: int, A: Saved, B, ldb: int, C, ldc: int, c_dtype: int = FP32,
+                    stream=None) -> None:
+    """C = A^T B from a kept K x M operand and a K x N bf16 one."""
+    if M > 0 and N > 0 and K >= 0:
+        A.check("A", K, M)
+        _need(B, "B", _extent(K, ldb, N), "bf16")
+        _need(C, "C", (M - 1) * ldc + N, _kind(c_dtype))
+    _one_device(stream, A.data, A.scales, B, C)
+    _check(_lib.zero_gemm_saved_bf16(M, N, K, A.ref(), _addr(B), ldb, _addr(C), ldc, c_dtype,
+                                     _stream(stream)), "zero_gemm_saved_bf16")
+
+
+def _group_count(n: int) -> Optional[int]:
+    return n + 1 if n >= 1 else None
+
+
+def gemm_grouped_rows_bf16(n_groups: int, offsets, rows: int, N: int, K: int, A, lda: int, B,
+                           ldb: int, b_order: int, stride_b: int, C, ldc: int, c_dtype: int = BF16,
+                           epilogue: Optional[Epilogue] = None, stream=None) -> None:
+    """C[r] = epilogue(A[r] B_e) for the rows r of group e; `offsets` is a
+    device int64 tensor of n_groups + 1."""
+    _need(offsets, "offsets", _group_count(n_groups), "int64")
+    if n_groups >= 1 and rows > 0 and N > 0 and K >= 0:
+        _need(A, "A", _operand_extent(rows, K, lda, K_INNER), "bf16")
+        _need(B, "B", (n_groups - 1) * stride_b + _operand_extent(N, K, ldb, b_order), "bf16")
+        _need(C, "C", (rows - 1) * ldc + N, _kind(c_dtype))
+    ref, more = _check_epilogue(epilogue, rows, N)
+    _one_device(stream, offsets, A, B, C, *more)
+    _check(_lib.zero_gemm_grouped_rows_bf16(n_groups, _addr(offsets), rows, N, K, _addr(A), lda,
+                                            _addr(B), ldb, b_order, stride_b, _addr(C), ldc, c_dtype,
+                                            ref, _stream(stream)),
+           "zero_gemm_grouped_rows_bf16")
+
+
+def gemm_grouped_depth_bf16(n_groups: int, offsets, rows: int, M: int, N: int, A, lda: int, B,
+                            ldb: int, C, ldc: int, stride_c: int, c_dtype: int = FP32,
+                            stream=None) -> None:
+    """C_e = sum over the rows r of group e of A[r]^T B[r]."""
+    _need(offsets, "offsets", _group_count(n_groups), "int64")
+    if n_groups >= 1 and M > 0 and N > 0 and rows >= 0:
+        _need(A, "A", _extent(rows, lda, M), "bf16")
+        _need(B, "B", _extent(rows, ldb, N), "bf16")
+        _need(C, "C", (n_groups - 1) * stride_c + (M - 1) * ldc + N, _kind(c_dtype))
+    _one_device(stream, offsets, A, B, C)
+    _check(_lib.zero_gemm_grouped_depth_bf16(n_groups, _addr(offsets), rows, M, N, _addr(A), lda,
+                                             _addr(B), ldb, _addr(C), ldc, stride_c, c_dtype,
+                                             _stream(stream)), "zero_gemm_grouped_depth_bf16")
+
+
+def fsdp_linear_act_forward(layout: Layout, unit: int, w_shards, batch: int, x, w_full, y,
+                            epilogue: Optional[Epilogue] = None, y_dtype: int = BF16,
+                            stream=None) -> None:
+    """fsdp_linear_forward with an epilogue."""
+    _need_len("w_shards", w_shards, _parts(layout))
+    d = _check_layer(layout, unit, w_shards, w_full, batch)
+    ref, more = None, ()
+    if d is not None:
+        _need(x, "x", batch * d[0], "bf16")
+        _need(y, "y", batch * d[1], _kind(y_dtype))
+        ref, more = _check_epilogue(epilogue, batch, d[1])
+    elif epilogue is not None:
+        ref = epilogue.ref()
+    _one_device(stream, x, w_full, y, *w_shards, *more)
+    _check(_lib.zero_fsdp_linear_act_forward(layout.handle, unit, _ptrs(w_shards), batch, _addr(x),
+                                             _addr(w_full), ref, _addr(y), y_dtype,
+                                             _stream(stream)), "zero_fsdp_linear_act_forward")
+
+
+def fsdp_linear_act_backward(layout: Layout, unit: int, w_shards, batch: int, x: Saved, act,
+                             preact: Optional[Saved], dy, w_full, dz, dx, dw_full, dbias=None,
+                             workspace=None, dx_dtype: int = BF16, stream=None) -> None:
+    """fsdp_linear_backward through the epilogue, from the kept x and z."""
+    _need_len("w_shards", w_shards, _parts(layout))
+    d = _check_layer(layout, unit, w_shards, w_full, batch)
+    if d is not None:
+        x.check("x", batch, d[0])
+        _check_act_backward(batch, d[1], dy, d[1], BF16, preact, dz, d[1], dbias, workspace)
+        _need(dx, "dx", batch * d[0], _kind(dx_dtype))
+        _need(dw_full, "dw_full", d[3], "fp32")
+    more = () if preact is None else (preact.data, preact.scales)
+    _one_device(stream, x.data, x.scales, dy, w_full, dz, dx, dw_full, dbias, workspace, *w_shards,
+                *more)
+    _check(_lib.zero_fsdp_linear_act_backward(layout.handle, unit, _ptrs(w_shards), batch, x.ref(),
+                                              _act(act), _saved_ref(preact), _addr(dy),
+                                              _addr(w_full), _addr(dz), _addr(dx), dx_dtype,
+                                              _addr(dw_full), _addr(dbias), _addr(workspace),
+                                              _numel(workspace), _stream(stream)),
+           "zero_fsdp_linear_act_backward")
+
+
+def _check_experts(layout, unit, n_experts, w_shards, offsets, rows, w_full):
+    """(in, out, padded) of an expert layer's unit, or None if the library
+    will refuse it."""
+    _need_len("w_shards", w_shards, _parts(layout))
+    d = _check_layer(layout, unit, w_shards, w_full, rows)
+    _need(offsets, "offsets", _group_count(n_experts), "int64")
+    if d is None or n_experts < 1 or d[0] % n_experts:
+        return None
+    return d[0] // n_experts, d[1], d[3]
+
+
+def fsdp_experts_forward(layout: Layout, unit: int, n_experts: int, w_shards, offsets, rows: int, x,
+                         w_full, y, epilogue: Optional[Epilogue] = None, y_dtype: int = BF16,
+                         stream=None) -> None:
+    """The grouped forward of an expert layer whose weights (n_experts * in
+    rows x out) are one row-sharded unit."""
+    d = _check_experts(layout, unit, n_experts, w_shards, offsets, rows, w_full)
+    ref, more = None, ()
+    if d is not None:
+        _need(x, "x", rows * d[0], "bf16")
+        _need(y, "y", rows * d[1], _kind(y_dtype))
+        ref, more = _check_epilogue(epilogue, rows, d[1])
+    elif epilogue is not None:
+        ref = epilogue.ref()
+    _one_device(stream, offsets, x, w_full, y, *w_shards, *more)
+    _check(_lib.zero_fsdp_experts_forward(layout.handle, unit, n_experts, _ptrs(w_shards),
+                                          _addr(offsets), rows, _addr(x), _addr(w_full), ref,
+                                          _addr(y), y_dtype, _stream(stream)),
+           "zero_fsdp_experts_forward")
+
+
+def fsdp_experts_backward(layout: Layout, unit: int, n_experts: int, w_shards, offsets, rows: int,
+                          x, dy, w_full, dx, dw_full, dx_dtype: int = BF16, stream=None) -> None:
+    """The grouped dx and the experts' dW (dw_full: the padded unit, fp32)."""
+    d = _check_experts(layout, unit, n_experts, w_shards, offsets, rows, w_full)
+    if d is not None:
+        _need(x, "x", rows * d[0], "bf16")
+        _need(dy, "dy", rows * d[1], "bf16")
+        _need(dx, "dx", rows * d[0], _kind(dx_dtype))
+        _need(dw_full, "dw_full", d[2], "fp32")
+    _one_device(stream, offsets, x, dy, w_full, dx, dw_full, *w_shards)
+    _check(_lib.zero_fsdp_experts_backward(layout.handle, unit, n_experts, _ptrs(w_shards),
+                                           _addr(offsets), rows, _addr(x), _addr(dy),
+                                           _addr(w_full), _addr(dx), dx_dtype, _addr(dw_full),
+                                           _stream(stream)), "zero_fsdp_experts_backward")
 
 
 def stream_mix(kind: int, grads, master, m, v, param, n: int, stream=None,

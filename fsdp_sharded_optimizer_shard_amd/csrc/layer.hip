@@ -1,0 +1,1591 @@
+// What a linear layer does around its product: the product with bias,
+// activation and residual in its epilogue, the gradient of that epilogue,
+// activations kept in 8 bits for the backward pass, and products grouped by
+// expert.  The products run on the tiles of gemm_tile.h.
+#include <hip/hip_runtime.h>
+
+#include <climits>
+#include <cstdint>
+#include <type_traits>
+
+#include "act.h"
+#include "gemm_tile.h"
+#include "products.h"
+
+namespace zs {
+
+namespace {
+
+// ------------------------------------------------------ loads and stores --
+
+// x[0 .. n) of 8 neighbouring values of dtype DT at element i; `vec`: the
+// address is 16-byte aligned (and n is 8).
+__device__ __forceinline__ void load8(const void *p, bool bf16, int64_t i, bool vec, int n, float (&x)[8])
+{
+    if (bf16) {
+        const uint16_t *q = static_cast<const uint16_t *>(p) + i;
+        if (vec) {
+            const uint4 w = *reinterpret_cast<const uint4 *>(q);
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                x[2 * k] = __uint_as_float(ww[k] << 16);
+                x[2 * k + 1] = __uint_as_float(ww[k] & 0xffff0000u);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                x[k] = k < n ? __uint_as_float((uint32_t)q[k] << 16) : 0.0f;
+        }
+    } else {
+        const float *q = static_cast<const float *>(p) + i;
+        if (vec) {
+            const float4 a = *reinterpret_cast<const float4 *>(q);
+            const float4 b = *reinterpret_cast<const float4 *>(q + 4);
+            x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+            x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                x[k] = k < n ? q[k] : 0.0f;
+        }
+    }
+}
+
+__device__ __forceinline__ void store8(void *p, bool bf16, int64_t i, bool vec, int n, const float (&x)[8])
+{
+    if (bf16) {
+        uint16_t *q = static_cast<uint16_t *>(p) + i;
+        uint32_t h[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            h[k] = f32_to_bf16_rne(x[k]);
+        if (vec) {
+            *reinterpret_cast<uint4 *>(q) = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16,
+                                                       h[4] | h[5] << 16, h[6] | h[7] << 16);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k < n)
+                    q[k] = (uint16_t)h[k];
+        }
+    } else {
+        float *q = static_cast<float *>(p) + i;
+        if (vec) {
+            *reinterpret_cast<float4 *>(q) = make_float4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<float4 *>(q + 4) = make_float4(x[4], x[5], x[6], x[7]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k < n)
+                    q[k] = x[k];
+        }
+    }
+}
+
+__device__ __forceinline__ uint2 load_bytes8(const uint8_t *q, bool vec, int n)
+{
+    if (vec)
+        return *reinterpret_cast<const uint2 *>(q);
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (k < n)
+            w[k >> 2] |= (uint32_t)q[k] << (8 * (k & 3));
+    return make_uint2(w[0], w[1]);
+}
+
+__device__ __forceinline__ void store_bytes8(uint8_t *q, bool vec, int n, uint2 w)
+{
+    if (vec) {
+        *reinterpret_cast<uint2 *>(q) = w;
+        return;
+    }
+    const uint32_t ww[2] = {w.x, w.y};
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (k < n)
+            q[k] = (uint8_t)(ww[k >> 2] >> (8 * (k & 3)));
+}
+
+// A wave's LDS traffic is in order; this keeps the compiler to that order
+// where one lane reads what another wrote.
+__device__ __forceinline__ void wave_lds_order()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// -------------------------------------------------------- the epilogue --
+
+struct EpiArgs {
+    void *C;
+    const void *bias, *residual;
+    void *z;           // kept pre-activation: bf16, or codes when z_scales is set
+    uint8_t *z_scales;
+    uint8_t *o, *o_scales;  // C kept in 8 bits
+    int64_t ldc, ldr, ldz, ldzs, ldo, ldos;
+    int32_t act;
+    bool c_bf16, bias_bf16, r_bf16;
+    bool c_vec, r_vec, z_vec;  // 16-byte aligned rows
+};
+
+// y = act(z) + residual with z = sum + bias, on the way from a wave's
+// accumulators to memory.  32 rows of the wave's tile at a time go through
+// its own corner of LDS (the K loop is done with it): the accumulators are
+// column-striped over lanes, memory wants whole rows, and the 8-bit code
+// wants whole columns of 32 rows -- which these 32 rows are, as every tile
+// begins at a multiple of 32 rows of C.  Rows in LDS are CW + 4 floats long,
+// so that the row pass's 16-byte reads of neighbouring rows interleave over
+// the banks.
+struct LayerEpi {
+    const EpiArgs &p;
+    ZS_LDS float *lds;  // 32 * (CW + 4) floats of this wave
+
+    // Codes of 32 rows x CW columns held in LDS, blocks along rows.  Lane:
+    // 4 columns of 32 / RG rows.
+    template <int CW>
+    __device__ __forceinline__ void encode(uint8_t *codes, int64_t ld, uint8_t *scales, int64_t lds_,
+                                           int64_t row0, int64_t col0, int64_t M, int64_t N,
+                                           int lane) const
+    {
+        constexpr int Q = CW / 4, RG = 64 / Q, R = 32 / RG;
+        const int quad = lane % Q, rg = lane / Q;
+        const int64_t col = col0 + 4 * quad, row = row0 + rg * R;
+        float x[R][4];
+        uint32_t mx[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const f32x4 v = *reinterpret_cast<const ZS_LDS f32x4 *>(lds + (rg * R + i) * (CW + 4) + 4 * quad);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                x[i][k] = v[k];
+                const uint32_t m = row + i < M ? mag_bits(v[k]) : 0u;
+                mx[k] = m > mx[k] ? m : mx[k];
+            }
+        }
+#pragma unroll
+        for (int s = Q; s < 64; s *= 2)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t m = (uint32_t)__shfl_xor((int)mx[k], s, 64);
+                mx[k] = m > mx[k] ? m : mx[k];
+            }
+        const int n = (int)(N - col < 4 ? N - col : 4);
+        if (n <= 0)
+            return;
+        float inv[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t b = block_byte(mx[k]);
+            inv[k] = inv_scale(b);
+            if (rg == 0 && k < n && row0 < M)
+                scales[(row0 >> 5) * lds_ + col + k] = (uint8_t)b;
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            if (row + i >= M)
+                break;
+            const uint32_t w = code4(coder_in(x[i][0]) * inv[0], coder_in(x[i][1]) * inv[1],
+                                     coder_in(x[i][2]) * inv[2], coder_in(x[i][3]) * inv[3]);
+            uint8_t *q = codes + (row + i) * ld + col;
+            if (n == 4) {
+                *reinterpret_cast<uint32_t *>(q) = w;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                    if (k < n)
+                        q[k] = (uint8_t)(w >> (8 * k));
+            }
+        }
+    }
+
+    template <int CW>
+    __device__ __forceinline__ void rows32(int64_t row0, int64_t col0, int64_t M, int64_t N, int lane) const
+    {
+        constexpr int LPR = CW / 8, RPI = 64 / LPR;  // lanes per row, rows per pass
+        wave_lds_order();
+        const int c = 8 * (lane % LPR);
+        const int64_t col = col0 + c;
+        const int n = (int)(N - col < 8 ? N - col : 8);
+        if (row0 < M && n > 0) {
+#pragma unroll
+            for (int it = 0; it < 32 / RPI; ++it) {
+                const int r = it * RPI + lane / LPR;
+                const int64_t row = row0 + r;
+                if (row >= M)
+                    break;
+                ZS_LDS f32x4 *q = reinterpret_cast<ZS_LDS f32x4 *>(lds + r * (CW + 4) + c);
+                const f32x4 lo = q[0], hi = q[1];
+                float x[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                if (p.z && !p.z_scales)
+                    store8(p.z, true, row * p.ldz + col, p.z_vec && n == 8, n, x);
+                by_act(p.act, [&](auto a) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        x[k] = act<decltype(a)::value>(x[k]);
+                });
+                if (p.residual) {
+                    float y[8];
+                    load8(p.residual, p.r_bf16, row * p.ldr + col, p.r_vec && n == 8, n, y);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        x[k] += y[k];
+                }
+                store8(p.C, p.c_bf16, row * p.ldc + col, p.c_vec && n == 8, n, x);
+            }
+        }
+        if (p.z_scales)
+            encode<CW>(static_cast<uint8_t *>(p.z), p.ldz, p.z_scales, p.ldzs, row0, col0, M, N, lane);
+        if (p.o) {
+            // C in 8 bits is coded from C as stored, so it is what coding C
+            // afterwards would give.
+            wave_lds_order();
+            if (row0 < M && n > 0) {
+#pragma unroll
+                for (int it = 0; it < 32 / RPI; ++it) {
+                    const int r = it * RPI + lane / LPR;
+                    const int64_t row = row0 + r;
+                    if (row >= M)
+                        break;
+                    float x[8];
+                    load8(p.C, p.c_bf16, row * p.ldc + col, p.c_vec && n == 8, n, x);
+                    ZS_LDS f32x4 *q = reinterpret_cast<ZS_LDS f32x4 *>(lds + r * (CW + 4) + c);
+                    q[0] = f32x4{x[0], x[1], x[2], x[3]};
+                    q[1] = f32x4{x[4], x[5], x[6], x[7]};
+                }
+            }
+            wave_lds_order();
+            encode<CW>(p.o, p.ldo, p.o_scales, p.ldos, row0, col0, M, N, lane);
+        }
+        wave_lds_order();
+    }
+
+    __device__ __forceinline__ float bias_at(int64_t col, int64_t N) const
+    {
+        if (!p.bias || col >= N)
+            return 0.0f;
+        return p.bias_bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t *>(p.bias)[col] << 16)
+                           : static_cast<const float *>(p.bias)[col];
+    }
+
+    // Rows 32 I .. of the wave's tile; by recursion, so that every accumulator
+    // index is a constant whatever the unroller thinks of the body.
+    template <int I, int TM, int TN>
+    __device__ __forceinline__ void step32(const f32x16 (&acc)[TM][TN], const float (&b)[TN], int64_t row0,
+                                           int64_t col0, int64_t M, int64_t N, int lane) const
+    {
+        if constexpr (I < TM) {
+            constexpr int CW = 32 * TN;
+            const int fr = lane & 31, fh = lane >> 5;
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int v = 0; v < 16; ++v)
+                    lds[(8 * (v >> 2) + 4 * fh + (v & 3)) * (CW + 4) + 32 * j + fr] = acc[I][j][v] + b[j];
+            rows32<CW>(row0 + 32 * I, col0, M, N, lane);
+            step32<I + 1>(acc, b, row0, col0, M, N, lane);
+        }
+    }
+
+    template <int I, int TM, int TN>
+    __device__ __forceinline__ void step16(const f32x4 (&acc)[TM][TN], const float (&b)[TN], int64_t row0,
+                                           int64_t col0, int64_t M, int64_t N, int lane) const
+    {
+        if constexpr (I < TM) {
+            constexpr int CW = 16 * TN;
+            const int r16 = lane & 15, g = lane >> 4;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        lds[(16 * h + 4 * g + v) * (CW + 4) + 16 * j + r16] = acc[I + h][j][v] + b[j];
+            rows32<CW>(row0 + 16 * I, col0, M, N, lane);
+            step16<I + 2>(acc, b, row0, col0, M, N, lane);
+        }
+    }
+
+    template <int TM, int TN>
+    __device__ __forceinline__ void tile32(const f32x16 (&acc)[TM][TN], int64_t row0, int64_t col0,
+                                           int64_t M, int64_t N, int lane) const
+    {
+        __syncthreads();  // every wave is done with the K loop's LDS
+        float b[TN];
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            b[j] = bias_at(col0 + 32 * j + (lane & 31), N);
+        step32<0>(acc, b, row0, col0, M, N, lane);
+    }
+
+    template <int TM, int TN>
+    __device__ __forceinline__ void tile16(const f32x4 (&acc)[TM][TN], int64_t row0, int64_t col0,
+                                           int64_t M, int64_t N, int lane) const
+    {
+        __syncthreads();
+        float b[TN];
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            b[j] = bias_at(col0 + 16 * j + (lane & 15), N);
+        step16<0>(acc, b, row0, col0, M, N, lane);
+    }
+};
+
+// ------------------------------------------------------ product kernels --
+
+// The wave's corner of the K loop's LDS: array w of the eight stages.
+#define ZS_STAGES(BM_, BN_)                                                                        \
+    __shared__ __attribute__((aligned(1024))) char a0[BM_ * 64], a1[BM_ * 64], a2[BM_ * 64],       \
+        a3[BM_ * 64];                                                                              \
+    __shared__ __attribute__((aligned(1024))) char b0[BN_ * 64], b1[BN_ * 64], b2[BN_ * 64],       \
+        b3[BN_ * 64];                                                                              \
+    ZS_LDS char *const As[kStages] = {(ZS_LDS char *)a0, (ZS_LDS char *)a1, (ZS_LDS char *)a2,     \
+                                      (ZS_LDS char *)a3};                                          \
+    ZS_LDS char *const Bs[kStages] = {(ZS_LDS char *)b0, (ZS_LDS char *)b1, (ZS_LDS char *)b2,     \
+                                      (ZS_LDS char *)b3}
+
+// By value: an array of LDS addresses indexed by the wave would have to exist
+// in memory.
+__device__ __forceinline__ ZS_LDS float *corner(ZS_LDS char *a0, ZS_LDS char *a1, ZS_LDS char *a2, ZS_LDS char *a3,
+                                                ZS_LDS char *b0, ZS_LDS char *b1, ZS_LDS char *b2, ZS_LDS char *b3)
+{
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    uint32_t p = (uint32_t)(uintptr_t)a0;
+    p = w == 1 ? (uint32_t)(uintptr_t)a1 : p;
+    p = w == 2 ? (uint32_t)(uintptr_t)a2 : p;
+    p = w == 3 ? (uint32_t)(uintptr_t)a3 : p;
+    p = w == 4 ? (uint32_t)(uintptr_t)b0 : p;
+    p = w == 5 ? (uint32_t)(uintptr_t)b1 : p;
+    p = w == 6 ? (uint32_t)(uintptr_t)b2 : p;
+    p = w == 7 ? (uint32_t)(uintptr_t)b3 : p;
+    return (ZS_LDS float *)p;
+}
+#define ZS_CORNER                                                                                  \
+    corner((ZS_LDS char *)a0, (ZS_LDS char *)a1, (ZS_LDS char *)a2, (ZS_LDS char *)a3,             \
+           (ZS_LDS char *)b0, (ZS_LDS char *)b1, (ZS_LDS char *)b2, (ZS_LDS char *)b3)
+
+#define ZS_PAIRS(BM_, BN_)                                                                         \
+    __shared__ __attribute__((aligned(1024))) char pa0[BM_ * 128], pa1[BM_ * 128];                 \
+    __shared__ __attribute__((aligned(1024))) char pb0[BN_ * 128], pb1[BN_ * 128];
+
+// Two waves to an array, each its half.
+#define ZS_CORNER_KP(HALF)                                                                         \
+    corner((ZS_LDS char *)pa0, (ZS_LDS char *)pa0 + (HALF), (ZS_LDS char *)pa1,                    \
+           (ZS_LDS char *)pa1 + (HALF), (ZS_LDS char *)pb0, (ZS_LDS char *)pb0 + (HALF),           \
+           (ZS_LDS char *)pb1, (ZS_LDS char *)pb1 + (HALF))
+#define ZS_P (ZS_LDS char *)pa0, (ZS_LDS char *)pa1, (ZS_LDS char *)pb0, (ZS_LDS char *)pb1
+
+// Block b of n_big + 2 (T - n_big): a whole tile, or a half of BM / 2 rows
+// (as gemm.hip's kernels place them).
+template <int BM, int BN>
+__device__ __forceinline__ bool place(int tiles_m, int tiles_n, int n_big, int64_t &m0, int64_t &n0)
+{
+    const int b = blockIdx.x;
+    int tm, tn;
+    if (b < n_big) {
+        grouped(xcd_order(b, n_big), tiles_m, tiles_n, tm, tn);
+        m0 = (int64_t)tm * BM;
+        n0 = (int64_t)tn * BN;
+        return true;
+    }
+    const int h = xcd_order(b - n_big, (int)gridDim.x - n_big);
+    grouped(n_big + h / 2, tiles_m, tiles_n, tm, tn);
+    m0 = (int64_t)tm * BM + (h & 1) * (BM / 2);
+    n0 = (int64_t)tn * BN;
+    return false;
+}
+
+template <int BM, int BN, bool A_KOUTER, bool B_KOUTER>
+__global__ __launch_bounds__(kGT) void epi_kernel(int64_t M, int64_t N, int64_t K,
+                                                  const uint16_t *__restrict__ A, int64_t lda,
+                                                  const uint16_t *__restrict__ B, int64_t ldb,
+                                                  EpiArgs args, int tiles_m, int tiles_n, int n_big)
+{
+    ZS_STAGES(BM, BN);
+    const LayerEpi epi{args, ZS_CORNER};
+    int64_t m0, n0;
+    if (place<BM, BN>(tiles_m, tiles_n, n_big, m0, n0))
+        gemm_tile<BM, BN, A_KOUTER, B_KOUTER>(M, N, K, A, lda, B, ldb, epi, m0, n0, As, Bs);
+    else if constexpr (BM == kBM)
+        gemm_tile<BM / 2, BN, A_KOUTER, B_KOUTER>(M, N, K, A, lda, B, ldb, epi, m0, n0, As, Bs);
+}
+
+template <int BM, int BN>
+__global__ __launch_bounds__(kGT) void epi_kernel_kp(int64_t M, int64_t N, int64_t K,
+                                                     const uint16_t *__restrict__ A, int64_t lda,
+                                                     const uint16_t *__restrict__ B, int64_t ldb,
+                                                     EpiArgs args, int tiles_m, int tiles_n, int n_big)
+{
+    ZS_PAIRS(BM, BN);
+    const LayerEpi epi{args, ZS_CORNER_KP((BM < BN ? BM : BN) * 64)};
+    int64_t m0, n0;
+    if (place<BM, BN>(tiles_m, tiles_n, n_big, m0, n0))
+        gemm_tile_kp<BM, BN>(M, N, K, A, lda, B, ldb, epi, m0, n0, ZS_P);
+    else if constexpr (BM == kBM)
+        gemm_tile_kp<BM / 2, BN>(M, N, K, A, lda, B, ldb, epi, m0, n0, ZS_P);
+}
+
+// Group e's rows [lo, hi), kept inside [0, rows] whatever the array holds.
+__device__ __forceinline__ void group_range(const int64_t *off, int e, int64_t rows, int64_t &lo, int64_t &hi)
+{
+    lo = off[e];
+    hi = off[e + 1];
+    lo = lo < 0 ? 0 : lo > rows ? rows : lo;
+    hi = hi < lo ? lo : hi > rows ? rows : hi;
+}
+
+// A group's tiles of BM rows, lane `lane` taking group c + lane (0 past the
+// last), and their inclusive sum over the lanes.
+template <int BM>
+__device__ __forceinline__ int lane_tiles(const int64_t *off, int n_groups, int c, int64_t rows, int lane,
+                                          int &sum)
+{
+    int64_t lo = 0, hi = 0;
+    if (c + lane < n_groups)
+        group_range(off, c + lane, rows, lo, hi);
+    const int t = (int)((hi - lo + BM - 1) / BM);
+    sum = t;
+#pragma unroll
+    for (int s = 1; s < 64; s *= 2) {
+        const int x = __shfl_up(sum, s, 64);
+        sum += lane >= s ? x : 0;
+    }
+    return t;
+}
+
+// Row tile `want` of all groups' tiles in order: its group and its number in
+// the group.  Every wave looks it up by itself, 64 groups at a time.
+template <int BM>
+__device__ __forceinline__ bool find_tile(const int64_t *off, int n_groups, int64_t rows, int want, int &e,
+                                          int &tile)
+{
+    const int lane = threadIdx.x & 63;
+    int before = 0;
+    for (int c = 0; c < n_groups; c += 64) {
+        int sum;
+        const int t = lane_tiles<BM>(off, n_groups, c, rows, lane, sum);
+        const uint64_t past = __ballot(before + sum > want);
+        if (past) {
+            const int l = __builtin_ctzll(past);
+            e = c + l;
+            tile = want - before - (__builtin_amdgcn_readlane(sum, l) - __builtin_amdgcn_readlane(t, l));
+            return true;
+        }
+        before += __builtin_amdgcn_readlane(sum, 63);
+    }
+    return false;
+}
+
+template <int BM>
+__device__ __forceinline__ int total_tiles(const int64_t *off, int n_groups, int64_t rows)
+{
+    int n = 0;
+    for (int c = 0; c < n_groups; c += 64) {
+        int sum;
+        lane_tiles<BM>(off, n_groups, c, rows, threadIdx.x & 63, sum);
+        n += __builtin_amdgcn_readlane(sum, 63);
+    }
+    return n;
+}
+
+// C[r] = epilogue(A[r] B_e) for the rows r of every group e.  The grid is the
+// most tiles the row count allows; blocks past the groups' real tiles leave.
+template <int BM, int BN, bool B_KOUTER>
+__global__ __launch_bounds__(kGT) void grouped_rows_kernel(const int64_t *__restrict__ off, int n_groups,
+                                                           int64_t rows, int64_t N, int64_t K,
+                                                           const uint16_t *__restrict__ A, int64_t lda,
+                                                           const uint16_t *__restrict__ B, int64_t ldb,
+                                                           int64_t stride_b, EpiArgs args, int tiles_n)
+{
+    const int tiles_m = total_tiles<BM>(off, n_groups, rows);
+    const int T = tiles_m * tiles_n;
+    if ((int)blockIdx.x >= T)
+        return;
+    int tm, tn, e, t;
+    grouped(xcd_order(blockIdx.x, T), tiles_m, tiles_n, tm, tn);
+    if (!find_tile<BM>(off, n_groups, rows, tm, e, t))
+        return;
+    int64_t lo, hi;
+    group_range(off, e, rows, lo, hi);
+    const int64_t M = hi - lo, m0 = (int64_t)t * BM, n0 = (int64_t)tn * BN;
+    if (t < 0 || m0 >= M)  // only with offsets that decrease
+        return;
+    args.C = static_cast<char *>(args.C) + lo * args.ldc * (args.c_bf16 ? 2 : 4);
+    if (args.residual)
+        args.residual = static_cast<const char *>(args.residual) + lo * args.ldr * (args.r_bf16 ? 2 : 4);
+    if (args.z)
+        args.z = static_cast<char *>(args.z) + lo * args.ldz * 2;
+    A += lo * lda;
+    B += e * stride_b;
+    if constexpr (B_KOUTER) {
+        ZS_STAGES(BM, BN);
+        const LayerEpi epi{args, ZS_CORNER};
+        gemm_tile<BM, BN, false, true>(M, N, K, A, lda, B, ldb, epi, m0, n0, As, Bs);
+    } else {
+        ZS_PAIRS(BM, BN);
+        const LayerEpi epi{args, ZS_CORNER_KP((BM < BN ? BM : BN) * 64)};
+        gemm_tile_kp<BM, BN>(M, N, K, A, lda, B, ldb, epi, m0, n0, ZS_P);
+    }
+}
+
+// C_e = sum over the rows r of group e of A[r]^T B[r]; an empty group's C_e is
+// zeros.
+template <int BM, int BN, bool OUT_BF16>
+__global__ __launch_bounds__(kGT) void grouped_depth_kernel(const int64_t *__restrict__ off, int64_t rows,
+                                                            int64_t M, int64_t N,
+                                                            const uint16_t *__restrict__ A, int64_t lda,
+                                                            const uint16_t *__restrict__ B, int64_t ldb,
+                                                            void *__restrict__ C, int64_t ldc,
+                                                            int64_t stride_c, int tiles_m, int tiles_n)
+{
+    ZS_STAGES(BM, BN);
+    const int per = tiles_m * tiles_n;
+    const int i = xcd_order(blockIdx.x, gridDim.x);
+    const int e = i / per;
+    int tm, tn;
+    grouped(i - e * per, tiles_m, tiles_n, tm, tn);
+    int64_t lo, hi;
+    group_range(off, e, rows, lo, hi);
+    const PlainEpi<OUT_BF16> epi{static_cast<char *>(C) + e * stride_c * (OUT_BF16 ? 2 : 4), ldc};
+    gemm_tile<BM, BN, true, true>(M, N, hi - lo, A + lo * lda, lda, B + lo * ldb, ldb, epi,
+                                  (int64_t)tm * BM, (int64_t)tn * BN, As, Bs);
+}
+
+// ------------------------------------------- products from 8-bit operands --
+
+// C = A^T B with A a K x M checkpoint (codes and exponent bytes) and B bf16,
+// both K-outer.  As gemm_tile, except for A: a stage holds 32 k rows of BM
+// code bytes, and next to it the one row of BM exponent bytes that serves
+// them all -- the blocks run along k, so a lane, which holds one row of C,
+// needs one exponent a stage.  A fragment is one ds_read_b64_tr_b8 (an 8 x 16
+// byte block transposed over 16 lanes: eight k of one row) and four
+// v_cvt_scalef32_pk_bf16_fp8, exact, on the vector unit beside the other
+// wave's MFMAs.
+//
+// The 32-byte unit U of k row kr sits at U ^ (kr & 7) (BM = 256; for BM = 128,
+// whose rows are half as long, U ^ ((kr >> 1) & 3)), so that the eight k rows
+// a half wave reads at once fall into eight different bank ranges.
+//
+// The exponent row of tile kt is fetched by wave kt % 8 alone.  Each wave's
+// wait counts its own instructions back from the newest, and one more of them
+// only makes that wait stricter.
+template <int BM>
+__device__ __forceinline__ int a8_swz(int kr) { return BM == 256 ? kr & 7 : (kr >> 1) & 3; }
+
+template <int BM, int BN, class Epi>
+__device__ __forceinline__ void gemm_tile_a8(int64_t M, int64_t N, int64_t K,
+                                             const uint8_t *__restrict__ A, int64_t lda,
+                                             const uint8_t *__restrict__ E, int64_t lde,
+                                             const uint16_t *__restrict__ B, int64_t ldb, const Epi &epi,
+                                             int64_t m0, int64_t n0, ZS_LDS char *const (&As)[kStages],
+                                             ZS_LDS char *const (&Es)[kStages],
+                                             ZS_LDS char *const (&Bs)[kStages])
+{
+    static_assert(BM == 256 || BM == 128, "");
+    constexpr int TM = BM / 64, TN = BN / 128;
+    constexpr int NF = TM + TN, NMF = TM * TN;
+    constexpr int NRD = TM + 2 * TN;
+    constexpr int NIB = Op<BN, true>::NI;
+    constexpr int D = 1 + NIB;
+
+    const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int wm = (wave >> 2) * (BM / 2), wn = (wave & 3) * (BN / 4);
+    const int fr = lane & 31, fh = lane >> 5;
+
+    // A's 1 KB instruction I: k rows KPI I .. of BM bytes.  A stage of 128
+    // rows is four of them; waves 4-7 repeat what waves 0-3 fetch.
+    constexpr int KPI = 1024 / BM, LPR = BM / 16;
+    const int I = BM == 256 ? wave : wave & 3;
+    uint32_t va, vb[2];
+    {
+        const int kr = KPI * I + lane / LPR, slot = lane % LPR;
+        const int c16 = (((slot >> 1) ^ a8_swz<BM>(kr)) << 1) | (slot & 1);
+        va = (uint32_t)(kr * lda + 16 * c16);
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+        vb[n] = n < NIB ? dma_offset<BN, true>(ldb, wave, lane, n) : 0u;
+    int fa_off[TM][2], fb_off[TN][2], fe_off[TM];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const int j = lane & 15, kr = 16 * s + 8 * fh + (j >> 1);
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+            fa_off[i][s] = kr * BM + ((((wm + 32 * i) >> 5) ^ a8_swz<BM>(kr)) << 5) +
+                           16 * ((lane >> 4) & 1) + 8 * (j & 1);
+#pragma unroll
+        for (int j2 = 0; j2 < TN; ++j2)
+            fb_off[j2][s] = frag_offset<BN, true>(wn + 32 * j2, s, lane);
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+        fe_off[i] = wm + 32 * i + fr;
+
+    f32x16 acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int v = 0; v < 16; ++v)
+                acc[i][j][v] = 0.0f;
+
+    const int64_t kt_n = (K + kBK - 1) / kBK;
+    auto dma = [&](auto st, int64_t kt) {
+        constexpr int S = decltype(st)::value;
+        const int64_t k0 = kt * kBK;
+        const __amdgpu_buffer_rsrc_t ra = rsrc(A + k0 * lda + m0, (K - 1 - k0) * lda + M - m0);
+        const __amdgpu_buffer_rsrc_t rb = rsrc(B + k0 * ldb + n0, ((K - 1 - k0) * ldb + N - n0) * 2);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (ZS_LDS void *)(As[S] + I * 1024), 16, va, 0, 0, 0);
+#pragma unroll
+        for (int n = 0; n < NIB; ++n)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (ZS_LDS void *)(Bs[S] + (wave + kNW * n) * 1024),
+                                                     16, vb[n], 0, 0, 0);
+        if (wave == (int)(kt & 7)) {
+            const __amdgpu_buffer_rsrc_t re = rsrc(E + kt * lde + m0, M - m0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(re, (ZS_LDS void *)Es[S], 4, 4 * lane, 0, 0, 0);
+        }
+    };
+    typedef int i32x2 __attribute__((ext_vector_type(2)));
+    i32x2 ra0[TM], ra1[TM];
+    bf16x8 fb0[TN], fb1[TN];
+    uint32_t e0[TM];
+    float sc[TM];
+    auto frags = [&](auto st, int s, i32x2 (&fa)[TM], bf16x8 (&fb)[TN]) {
+        constexpr int S = decltype(st)::value;
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+            fa[i] = __builtin_amdgcn_ds_read_tr8_b64_v2i32((ZS_LDS i32x2 *)(As[S] + fa_off[i][s]));
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            fb[j] = frag_read<BN, true>(Bs[S], fb_off[j][s]);
+    };
+    auto exps = [&](auto st) {
+        constexpr int S = decltype(st)::value;
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+            e0[i] = *reinterpret_cast<const ZS_LDS uint8_t *>(Es[S] + fe_off[i]);
+    };
+    auto widen = [&](i32x2 w, float s) {
+        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+        const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)w[0], s, false);
+        const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)w[0], s, true);
+        const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)w[1], s, false);
+        const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)w[1], s, true);
+        return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+    };
+    auto mma = [&](const i32x2 (&fa)[TM], const bf16x8 (&fb)[TN], int lo, int hi) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            if (i < lo || i >= hi)
+                continue;
+            const bf16x8 a = widen(fa[i], sc[i]);
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, fb[j], acc[i][j], 0, 0, 0);
+        }
+    };
+    auto wait_for = [&](int64_t kt1) {
+        const int64_t after = kt_n - 1 - kt1;
+        if (after >= 2)
+            wait_vm_lgkm0<2 * D>();
+        else if (after == 1)
+            wait_vm_lgkm0<D>();
+        else
+            wait_vm_lgkm0<0>();
+    };
+    auto take_exps = [&]() {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+            sc[i] = __uint_as_float(e0[i] << 23);
+    };
+    auto tile = [&](auto st, int64_t kt) {
+        constexpr int S = decltype(st)::value;
+        constexpr int SN = (S + kStages - 1) % kStages, S1 = (S + 1) % kStages;
+        __builtin_amdgcn_sched_barrier(0);
+        take_exps();
+        if (kt + kStages - 1 < kt_n)
+            dma(IC<SN>{}, kt + kStages - 1);
+        frags(IC<S>{}, 1, ra1, fb1);
+        mma(ra0, fb0, 0, TM);
+        seq<NF, NMF, NRD, 0>();
+        mma(ra1, fb1, 0, TM / 2);
+        __builtin_amdgcn_sched_barrier(0);
+        wait_for(kt + 1);
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        if (kt + 1 < kt_n) {
+            frags(IC<S1>{}, 0, ra0, fb0);
+            exps(IC<S1>{});
+        }
+        mma(ra1, fb1, TM / 2, TM);
+        seq<NF, NMF / 2, NRD, 0>();
+    };
+    if (kt_n > 0) {
+        dma(IC<0>{}, 0);
+        if (kt_n > 1)
+            dma(IC<1>{}, 1);
+        if (kt_n > 2)
+            dma(IC<2>{}, 2);
+        wait_for(0);
+        __builtin_amdgcn_s_barrier();
+        frags(IC<0>{}, 0, ra0, fb0);
+        exps(IC<0>{});
+        for (int64_t kt = 0; kt < kt_n; kt += kStages) {
+            tile(IC<0>{}, kt);
+            if (kt + 1 < kt_n)
+                tile(IC<1>{}, kt + 1);
+            if (kt + 2 < kt_n)
+                tile(IC<2>{}, kt + 2);
+            if (kt + 3 < kt_n)
+                tile(IC<3>{}, kt + 3);
+        }
+    }
+    epi.template tile32<TM, TN>(acc, m0 + wm, n0 + wn, M, N, lane);
+}
+
+template <int BM, int BN, bool OUT_BF16>
+__global__ __launch_bounds__(kGT) void saved_kernel(int64_t M, int64_t N, int64_t K,
+                                                    const uint8_t *__restrict__ A, int64_t lda,
+                                                    const uint8_t *__restrict__ E, int64_t lde,
+                                                    const uint16_t *__restrict__ B, int64_t ldb,
+                                                    void *__restrict__ C, int64_t ldc, int tiles_m,
+                                                    int tiles_n, int n_big)
+{
+    __shared__ __attribute__((aligned(1024))) char a0[BM * 32], a1[BM * 32], a2[BM * 32], a3[BM * 32];
+    __shared__ __attribute__((aligned(1024))) char b0[BN * 64], b1[BN * 64], b2[BN * 64], b3[BN * 64];
+    __shared__ __attribute__((aligned(256))) char e0[256], e1[256], e2[256], e3[256];
+    ZS_LDS char *const As[kStages] = {(ZS_LDS char *)a0, (ZS_LDS char *)a1, (ZS_LDS char *)a2,
+                                      (ZS_LDS char *)a3};
+    ZS_LDS char *const Bs[kStages] = {(ZS_LDS char *)b0, (ZS_LDS char *)b1, (ZS_LDS char *)b2,
+                                      (ZS_LDS char *)b3};
+    ZS_LDS char *const Es[kStages] = {(ZS_LDS char *)e0, (ZS_LDS char *)e1, (ZS_LDS char *)e2,
+                                      (ZS_LDS char *)e3};
+    const PlainEpi<OUT_BF16> epi{C, ldc};
+    int64_t m0, n0;
+    if (place<BM, BN>(tiles_m, tiles_n, n_big, m0, n0))
+        gemm_tile_a8<BM, BN>(M, N, K, A, lda, E, lde, B, ldb, epi, m0, n0, As, Es, Bs);
+    else if constexpr (BM == kBM)
+        gemm_tile_a8<BM / 2, BN>(M, N, K, A, lda, E, lde, B, ldb, epi, m0, n0, As, Es, Bs);
+}
+
+// ------------------------------------------------- elementwise kernels --
+
+// One wave: 32 rows x 128 columns, lane = 8 columns of 8 rows, so that a
+// block's largest magnitude is 8 values in the lane and two exchanges, and
+// every load is 16 bytes.
+struct Spot {
+    int64_t block, row, col;
+    int n, rg;
+};
+
+__device__ __forceinline__ Spot spot(int64_t wave, int64_t col_waves)
+{
+    const int lane = threadIdx.x & 63;
+    Spot s;
+    s.block = wave / col_waves;
+    s.rg = lane >> 4;
+    s.row = s.block * 32 + s.rg * 8;
+    s.col = (wave % col_waves) * 128 + (lane & 15) * 8;
+    return s;
+}
+
+__global__ __launch_bounds__(256) void saved_write_kernel(int64_t rows, int64_t cols, const void *x,
+                                                          int64_t ldx, bool x_bf16, bool x_vec,
+                                                          uint8_t *codes, int64_t ld, uint8_t *scales,
+                                                          int64_t lds, bool s_vec, int64_t waves,
+                                                          int64_t col_waves)
+{
+    const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (w >= waves)
+        return;
+    Spot s = spot(w, col_waves);
+    s.n = (int)(cols - s.col < 8 ? cols - s.col : 8);
+    float v[8][8];
+    uint32_t mx[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (s.n > 0 && s.row + i < rows)
+            load8(x, x_bf16, (s.row + i) * ldx + s.col, x_vec && s.n == 8, s.n, v[i]);
+        else
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                v[i][k] = 0.0f;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t m = mag_bits(v[i][k]);
+            mx[k] = m > mx[k] ? m : mx[k];
+        }
+#pragma unroll
+        for (int d = 16; d < 64; d *= 2) {
+            const uint32_t m = (uint32_t)__shfl_xor((int)mx[k], d, 64);
+            mx[k] = m > mx[k] ? m : mx[k];
+        }
+    }
+    if (s.n <= 0)
+        return;
+    uint32_t byte[8];
+    float inv[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        byte[k] = block_byte(mx[k]);
+        inv[k] = inv_scale(byte[k]);
+    }
+    if (s.rg == 0)
+        store_bytes8(scales + s.block * lds + s.col, s_vec && s.n == 8, s.n,
+                     make_uint2(byte[0] | byte[1] << 8 | byte[2] << 16 | byte[3] << 24,
+                                byte[4] | byte[5] << 8 | byte[6] << 16 | byte[7] << 24));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (s.row + i >= rows)
+            break;
+        float q[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            q[k] = coder_in(v[i][k]) * inv[k];
+        store_bytes8(codes + (s.row + i) * ld + s.col, s.n == 8, s.n,
+                     make_uint2(code4(q[0], q[1], q[2], q[3]), code4(q[4], q[5], q[6], q[7])));
+    }
+}
+
+__global__ __launch_bounds__(256) void saved_read_kernel(int64_t rows, int64_t cols, const uint8_t *codes,
+                                                         int64_t ld, const uint8_t *scales, int64_t lds,
+                                                         bool s_vec, void *out, int64_t ldo, bool o_bf16,
+                                                         bool o_vec, int64_t waves, int64_t col_waves)
+{
+    const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (w >= waves)
+        return;
+    const Spot s = spot(w, col_waves);
+    const int n = (int)(cols - s.col < 8 ? cols - s.col : 8);
+    if (n <= 0)
+        return;
+    const uint2 b = load_bytes8(scales + s.block * lds + s.col, s_vec && n == 8, n);
+    uint2 c[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        c[i] = s.row + i < rows ? load_bytes8(codes + (s.row + i) * ld + s.col, n == 8, n) : make_uint2(0, 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (s.row + i >= rows)
+            break;
+        float v[8];
+        decode8(c[i], b, v);
+        store8(out, o_bf16, (s.row + i) * ldo + s.col, o_vec && n == 8, n, v);
+    }
+}
+
+struct ActBackArgs {
+    int64_t rows, cols, ldy, ldz, ldd, ldzs;
+    const void *dy;
+    const void *z;
+    const uint8_t *z_scales;
+    void *dz;
+    float *sums;  // dbias when one block spans the rows, else one row of partial sums per block
+    int32_t act, units;  // units of 128 rows a block walks
+    bool y_bf16, y_vec, z_vec, zs_vec, d_vec;
+};
+
+// dz = dy act'(z) and the column sums of dz.  A block covers 128 columns of
+// `units` x 128 rows: thread = 8 columns of 8 rows a unit (rows of one
+// 32-row block, so one exponent load serves them), every access 16 bytes, or
+// 8 for codes.  The sums stay in registers over the units, then go through
+// LDS in row order and leave as one row per block, summed by sum_kernel in
+// row order too: no atomics, the same bits every time.
+template <int ZF>  // 0: no activation, 1: z in bf16, 2: z in 8 bits
+__global__ __launch_bounds__(256) void act_backward_kernel(ActBackArgs p)
+{
+    __shared__ float part[16][128 + 4];
+    const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
+    const int64_t col = (int64_t)blockIdx.x * 128 + cg * 8;
+    const int n = (int)(p.cols - col < 8 ? p.cols - col : 8);
+    float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (n > 0) {
+        for (int u = 0; u < p.units; ++u) {
+            const int64_t row = ((int64_t)blockIdx.y * p.units + u) * 128 + rg * 8;
+            if (row >= p.rows)
+                break;
+            uint2 b = make_uint2(0, 0);
+            if (ZF == 2)
+                b = load_bytes8(p.z_scales + (row >> 5) * p.ldzs + col, p.zs_vec && n == 8, n);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (row + i >= p.rows)
+                    break;
+                float y[8], z[8];
+                load8(p.dy, p.y_bf16, (row + i) * p.ldy + col, p.y_vec && n == 8, n, y);
+                if (ZF == 1)
+                    load8(p.z, true, (row + i) * p.ldz + col, p.z_vec && n == 8, n, z);
+                if (ZF == 2)
+                    decode8(load_bytes8(static_cast<const uint8_t *>(p.z) + (row + i) * p.ldz + col, n == 8,
+                                        n),
+                            b, z);
+                if (ZF != 0)
+                    by_act(p.act, [&](auto a) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            y[k] *= act_slope<decltype(a)::value>(z[k]);
+                    });
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    sum[k] += y[k];
+                if (p.dz)
+                    store8(p.dz, true, (row + i) * p.ldd + col, p.d_vec && n == 8, n, y);
+            }
+        }
+    }
+    if (!p.sums)
+        return;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        part[rg][cg * 8 + k] = sum[k];
+    __syncthreads();
+    const int64_t c = (int64_t)blockIdx.x * 128 + threadIdx.x;
+    if (threadIdx.x < 128 && c < p.cols) {
+        float s = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            s += part[r][threadIdx.x];
+        p.sums[(int64_t)blockIdx.y * p.cols + c] = s;
+    }
+}
+
+// out[c] = sum of n rows of partial sums, in row order.
+__global__ __launch_bounds__(64) void sum_kernel(const float *__restrict__ part, int64_t n, int64_t cols,
+                                                 float *__restrict__ out)
+{
+    const int64_t c = (int64_t)blockIdx.x * 64 + threadIdx.x;
+    if (c >= cols)
+        return;
+    float s = 0.0f;
+#pragma unroll 8
+    for (int64_t r = 0; r < n; ++r)
+        s += part[r * cols + c];
+    out[c] = s;
+}
+
+// --------------------------------------------------------- host checks --
+
+bool aligned(const void *p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+bool vec16(const void *p, int64_t ld, int es) { return aligned(p, 16) && ld * es % 16 == 0; }
+
+bool known_dtype(int32_t d) { return d == ZERO_BF16 || d == ZERO_FP32; }
+int bytes_of(int32_t d) { return d == ZERO_BF16 ? 2 : 4; }
+
+zero_status launched(const char *what)
+{
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess)
+        return fail(ZERO_ERR_HIP, "%s launch failed: %s", what, hipGetErrorString(e));
+    return ZERO_OK;
+}
+
+// A matrix argument: pointer, leading dimension and alignment.
+zero_status check_matrix(const char *what, const void *p, int64_t ld, int64_t cols, int32_t dtype)
+{
+    if (!known_dtype(dtype))
+        return fail(ZERO_ERR_INVALID_ARG, "%s: unknown dtype %d", what, dtype);
+    if (!p)
+        return fail(ZERO_ERR_INVALID_ARG, "%s is required", what);
+    if (ld < cols)
+        return fail(ZERO_ERR_INVALID_ARG, "%s: leading dimension %lld below %lld columns", what, (long long)ld,
+                    (long long)cols);
+    if (!aligned(p, bytes_of(dtype)))
+        return fail(ZERO_ERR_ALIGNMENT, "%s is misaligned", what);
+    return ZERO_OK;
+}
+
+// The most rows, columns and leading dimension of the elementwise calls: all
+// products of two of them, and byte offsets, then fit 63 bits.
+constexpr int64_t kMaxDim = int64_t(1) << 40, kMaxElems = int64_t(1) << 60;
+
+zero_status check_extent(int64_t rows, int64_t cols, int64_t ld)
+{
+    if (rows < 0 || cols < 0)
+        return fail(ZERO_ERR_INVALID_ARG, "negative size");
+    if (rows > kMaxDim || cols > kMaxDim || ld > kMaxDim || (ld > 0 && rows > kMaxElems / ld))
+        return fail(ZERO_ERR_UNSUPPORTED, "matrix too large (%lld x %lld, leading dimension %lld)",
+                    (long long)rows, (long long)cols, (long long)ld);
+    return ZERO_OK;
+}
+
+}  // namespace
+
+zero_status saved_check(const char *what, const zero_saved *s, int64_t rows, int64_t cols)
+{
+    if (!s)
+        return fail(ZERO_ERR_INVALID_ARG, "%s is required", what);
+    if (s->format != ZERO_SAVED_BF16 && s->format != ZERO_SAVED_E4M3)
+        return fail(ZERO_ERR_INVALID_ARG, "%s: unknown format %d", what, s->format);
+    zero_status st;
+    if ((st = check_extent(rows, cols, s->ld)) != ZERO_OK)
+        return st;
+    if (s->format == ZERO_SAVED_BF16)
+        return check_matrix(what, s->data, s->ld, cols, ZERO_BF16);
+    if (!s->data || !s->scales)
+        return fail(ZERO_ERR_INVALID_ARG, "%s: codes and scales are required", what);
+    if (s->ld < cols || s->ld_scales < cols)
+        return fail(ZERO_ERR_INVALID_ARG, "%s: leading dimension below %lld columns", what, (long long)cols);
+    if (s->ld % 16)
+        return fail(ZERO_ERR_UNSUPPORTED, "%s: the codes' leading dimension must be a multiple of 16", what);
+    if (s->ld_scales > kMaxDim)
+        return fail(ZERO_ERR_UNSUPPORTED, "%s: the scales' leading dimension is too large", what);
+    if (!aligned(s->data, 16))
+        return fail(ZERO_ERR_ALIGNMENT, "%s: codes must be 16-byte aligned", what);
+    return ZERO_OK;
+}
+
+// The epilogue of an M x N product, checked and translated; `grouped` refuses
+// what needs rows counted from a multiple of 32.
+zero_status epilogue_check(int64_t M, int64_t N, const zero_epilogue *ep, bool grouped)
+{
+    if (!ep)
+        return ZERO_OK;
+    if (ep->act < ZERO_ACT_NONE || ep->act > ZERO_ACT_SILU)
+        return fail(ZERO_ERR_INVALID_ARG, "unknown activation %d", ep->act);
+    zero_status st;
+    if (ep->bias) {
+        if (grouped)
+            return fail(ZERO_ERR_UNSUPPORTED, "a grouped product takes no bias");
+        if ((st = check_matrix("bias", ep->bias, N, N, ep->bias_dtype)) != ZERO_OK)
+            return st;
+    }
+    if (ep->residual) {
+        if ((st = check_matrix("residual", ep->residual, ep->ldr, N, ep->residual_dtype)) != ZERO_OK ||
+            (st = check_extent(M, N, ep->ldr)) != ZERO_OK)
+            return st;
+    }
+    if (ep->preact) {
+        if ((st = saved_check("preact", ep->preact, M, N)) != ZERO_OK)
+            return st;
+        if (grouped && ep->preact->format != ZERO_SAVED_BF16)
+            return fail(ZERO_ERR_UNSUPPORTED, "a grouped product keeps its pre-activation in bf16 only");
+    }
+    if (ep->output) {
+        if (grouped)
+            return fail(ZERO_ERR_UNSUPPORTED, "a grouped product keeps no 8-bit output");
+        if ((st = saved_check("output", ep->output, M, N)) != ZERO_OK)
+            return st;
+        if (ep->output->format != ZERO_SAVED_E4M3)
+            return fail(ZERO_ERR_UNSUPPORTED, "output is kept in 8 bits only");
+    }
+    return ZERO_OK;
+}
+
+namespace {
+
+EpiArgs epi_args(const zero_epilogue *ep, void *C, int64_t ldc, int32_t c_dtype)
+{
+    EpiArgs a = {};
+    a.C = C;
+    a.ldc = ldc;
+    a.c_bf16 = c_dtype == ZERO_BF16;
+    a.c_vec = vec16(C, ldc, bytes_of(c_dtype));
+    if (!ep)
+        return a;
+    a.act = ep->act;
+    a.bias = ep->bias;
+    a.bias_bf16 = ep->bias_dtype == ZERO_BF16;
+    a.residual = ep->residual;
+    a.ldr = ep->ldr;
+    a.r_bf16 = ep->residual_dtype == ZERO_BF16;
+    a.r_vec = ep->residual && vec16(ep->residual, ep->ldr, bytes_of(ep->residual_dtype));
+    if (ep->preact) {
+        a.z = ep->preact->data;
+        a.ldz = ep->preact->ld;
+        if (ep->preact->format == ZERO_SAVED_E4M3) {
+            a.z_scales = ep->preact->scales;
+            a.ldzs = ep->preact->ld_scales;
+        }
+        a.z_vec = vec16(a.z, a.ldz, 2);
+    }
+    if (ep->output) {
+        a.o = static_cast<uint8_t *>(ep->output->data);
+        a.ldo = ep->output->ld;
+        a.o_scales = ep->output->scales;
+        a.ldos = ep->output->ld_scales;
+    }
+    return a;
+}
+
+struct Grid {
+    int tm, tn, n_big;
+    dim3 grid;
+};
+
+// Tiles of bm x bn; with `halves`, a last wave of at most half the CUs runs
+// as twice as many half tiles.
+Grid tiles(int64_t M, int64_t N, int bm, int bn, bool halves)
+{
+    Grid g;
+    const int64_t tm = (M + bm - 1) / bm, tn = (N + bn - 1) / bn, T = tm * tn, P = cu_count();
+    const int64_t rem = T % P;
+    const int64_t big = halves && rem > 0 && rem <= P / 2 ? T - rem : T;
+    g.tm = (int)tm;
+    g.tn = (int)tn;
+    g.n_big = (int)big;
+    g.grid = dim3((unsigned)(big + 2 * (T - big)));
+    return g;
+}
+
+// 128 x 128 tiles where 256 x 256 ones would not fill half the CUs.
+bool small_tiles(int64_t M, int64_t N)
+{
+    const int64_t T = ((M + kBM - 1) / kBM) * ((N + kBN - 1) / kBN);
+    return 2 * T <= cu_count();
+}
+
+constexpr int64_t kMaxBlocks = int64_t(0xffffffffu) / (2 * kGT);
+
+}  // namespace
+
+// zero_gemm_saved_bf16's checks, with nothing launched.
+zero_status gemm_saved_check(int64_t M, int64_t N, int64_t K, const zero_saved *A, const uint16_t *B,
+                             int64_t ldb, const void *C, int64_t ldc, int32_t c_dtype)
+{
+    if (M < 0 || N < 0 || K < 0)
+        return fail(ZERO_ERR_INVALID_ARG, "negative GEMM size");
+    if (!known_dtype(c_dtype))
+        return fail(ZERO_ERR_INVALID_ARG, "unknown C dtype %d", c_dtype);
+    if (M == 0 || N == 0)
+        return ZERO_OK;
+    zero_status st;
+    if ((st = saved_check("A", A, K, M)) != ZERO_OK ||
+        (st = check_matrix("B", B, ldb, N, ZERO_BF16)) != ZERO_OK ||
+        (st = check_matrix("C", C, ldc, N, c_dtype)) != ZERO_OK)
+        return st;
+    if (M % 8 || N % 8 || ldb % 8 || A->ld % 8)
+        return fail(ZERO_ERR_UNSUPPORTED, "a product from a kept operand needs M, N and the leading "
+                    "dimensions multiples of 8");
+    if (A->format == ZERO_SAVED_E4M3 && (A->ld_scales % 4 || !aligned(A->scales, 4)))
+        return fail(ZERO_ERR_UNSUPPORTED, "the scales of a product's operand must be 4-byte aligned rows");
+    if (A->ld > (int64_t(1) << 25) || ldb > (int64_t(1) << 25))
+        return fail(ZERO_ERR_UNSUPPORTED, "leading dimension too large for 32-bit operand offsets (at most "
+                    "%lld)", 1ll << 25);
+    if (!aligned(A->data, 16) || !aligned(B, 16))
+        return fail(ZERO_ERR_ALIGNMENT, "A and B must be 16-byte aligned");
+    const int64_t tm = (M + kBM - 1) / kBM, tn = (N + kBN - 1) / kBN;
+    if (tm > kMaxBlocks / tn)
+        return fail(ZERO_ERR_UNSUPPORTED, "too many GEMM tiles for one launch");
+    return ZERO_OK;
+}
+
+zero_status gemm_saved_run(int64_t M, int64_t N, int64_t K, const zero_saved *A, const uint16_t *B,
+                           int64_t ldb, void *C, int64_t ldc, int32_t c_dtype, hipStream_t s)
+{
+    if (M == 0 || N == 0)
+        return ZERO_OK;
+    if (A->format == ZERO_SAVED_BF16)
+        return gemm_run(M, N, K, static_cast<const uint16_t *>(A->data), A->ld, ZERO_K_OUTER, B, ldb,
+                        ZERO_K_OUTER, C, ldc, c_dtype, s);
+    const uint8_t *codes = static_cast<const uint8_t *>(A->data);
+    (void)hipGetLastError();
+#define ZS_SAVED(BM_, BN_, BF)                                                                     \
+    hipLaunchKernelGGL((saved_kernel<BM_, BN_, BF>), g.grid, dim3(kGT), 0, s, M, N, K, codes, A->ld, \
+                       A->scales, A->ld_scales, B, ldb, C, ldc, g.tm, g.tn, g.n_big)
+    if (small_tiles(M, N)) {
+        const Grid g = tiles(M, N, 128, 128, false);
+        if (c_dtype == ZERO_BF16)
+            ZS_SAVED(128, 128, true);
+        else
+            ZS_SAVED(128, 128, false);
+    } else {
+        const Grid g = tiles(M, N, kBM, kBN, true);
+        if (c_dtype == ZERO_BF16)
+            ZS_SAVED(kBM, kBN, true);
+        else
+            ZS_SAVED(kBM, kBN, false);
+    }
+#undef ZS_SAVED
+    return launched("gemm_saved");
+}
+
+zero_status epilogue_gemm_run(int64_t M, int64_t N, int64_t K, const uint16_t *A, int64_t lda,
+                              int32_t a_order, const uint16_t *B, int64_t ldb, int32_t b_order, void *C,
+                              int64_t ldc, int32_t c_dtype, const zero_epilogue *ep, hipStream_t s)
+{
+    if (M == 0 || N == 0)
+        return ZERO_OK;
+    const EpiArgs a = epi_args(ep, C, ldc, c_dtype);
+    const bool ao = a_order == ZERO_K_OUTER, bo = b_order == ZERO_K_OUTER;
+    const bool small = small_tiles(M, N);
+    const Grid g = small ? tiles(M, N, 128, 128, false) : tiles(M, N, kBM, kBN, true);
+    (void)hipGetLastError();
+#define ZS_EPI(AO, BO)                                                                             \
+    do {                                                                                           \
+        if (small)                                                                                 \
+            hipLaunchKernelGGL((epi_kernel<128, 128, AO, BO>), g.grid, dim3(kGT), 0, s, M, N, K, A, \
+                               lda, B, ldb, a, g.tm, g.tn, g.n_big);                               \
+        else                                                                                       \
+            hipLaunchKernelGGL((epi_kernel<kBM, kBN, AO, BO>), g.grid, dim3(kGT), 0, s, M, N, K, A, \
+                               lda, B, ldb, a, g.tm, g.tn, g.n_big);                               \
+    } while (0)
+    if (ao && bo) {
+        ZS_EPI(true, true);
+    } else if (ao) {
+        ZS_EPI(true, false);
+    } else if (bo) {
+        ZS_EPI(false, true);
+    } else if (small) {
+        hipLaunchKernelGGL((epi_kernel_kp<128, 128>), g.grid, dim3(kGT), 0, s, M, N, K, A, lda, B, ldb, a,
+                           g.tm, g.tn, g.n_big);
+    } else {
+        hipLaunchKernelGGL((epi_kernel_kp<kBM, kBN>), g.grid, dim3(kGT), 0, s, M, N, K, A, lda, B, ldb, a,
+                           g.tm, g.tn, g.n_big);
+    }
+#undef ZS_EPI
+    return launched("gemm_epilogue");
+}
+
+// Rows a block of act_backward_kernel sums: enough that at most 64 rows of
+// partial sums are left.
+static int64_t act_units(int64_t rows)
+{
+    const int64_t u = (rows + 127) / 128;
+    return u <= 64 ? 1 : (u + 63) / 64;
+}
+
+static int64_t act_blocks(int64_t rows)
+{
+    const int64_t per = 128 * act_units(rows);
+    return (rows + per - 1) / per;
+}
+
+zero_status act_backward_check(int64_t rows, int64_t cols, const void *dy, int64_t ldy, int32_t dy_dtype,
+                               int32_t act, const zero_saved *preact, const uint16_t *dz, int64_t ldz,
+                               const float *dbias, const float *workspace, int64_t n_workspace)
+{
+    zero_status st;
+    if ((st = check_extent(rows, cols, ldy)) != ZERO_OK || (st = check_extent(rows, cols, ldz)) != ZERO_OK)
+        return st;
+    if (act < ZERO_ACT_NONE || act > ZERO_ACT_SILU)
+        return fail(ZERO_ERR_INVALID_ARG, "unknown activation %d", act);
+    if (!known_dtype(dy_dtype))
+        return fail(ZERO_ERR_INVALID_ARG, "dy: unknown dtype %d", dy_dtype);
+    if (cols == 0)
+        return ZERO_OK;
+    if (rows > 0) {
+        if ((st = check_matrix("dy", dy, ldy, cols, dy_dtype)) != ZERO_OK)
+            return st;
+        if (act != ZERO_ACT_NONE && (st = saved_check("preact", preact, rows, cols)) != ZERO_OK)
+            return st;
+        if (!dz && (act != ZERO_ACT_NONE || !dbias))
+            return fail(ZERO_ERR_INVALID_ARG, "dz is required");
+        if (dz && (st = check_matrix("dz", dz, ldz, cols, ZERO_BF16)) != ZERO_OK)
+            return st;
+    }
+    if (!aligned(dbias, 4) || !aligned(workspace, 4))
+        return fail(ZERO_ERR_ALIGNMENT, "dbias and workspace must be 4-byte aligned");
+    const int64_t need = dbias ? zero_act_backward_workspace(rows, cols) : 0;
+    if (need > 0 && (!workspace || n_workspace < need))
+        return fail(ZERO_ERR_INVALID_ARG, "dbias of %lld x %lld needs a workspace of %lld floats",
+                    (long long)rows, (long long)cols, (long long)need);
+    if ((cols + 127) / 128 > int64_t(0x7fffffff) / 256)
+        return fail(ZERO_ERR_UNSUPPORTED, "too many columns for one launch");
+    return ZERO_OK;
+}
+
+zero_status act_backward_run(int64_t rows, int64_t cols, const void *dy, int64_t ldy, int32_t dy_dtype,
+                             int32_t act, const zero_saved *preact, uint16_t *dz, int64_t ldz, float *dbias,
+                             float *workspace, hipStream_t s)
+{
+    if (cols == 0 || (rows == 0 && !dbias))
+        return ZERO_OK;
+    ActBackArgs p = {};
+    p.rows = rows;
+    p.cols = cols;
+    p.dy = dy;
+    p.ldy = ldy;
+    p.y_bf16 = dy_dtype == ZERO_BF16;
+    p.y_vec = vec16(dy, ldy, bytes_of(dy_dtype));
+    p.act = act;
+    p.dz = dz;
+    p.ldd = ldz;
+    p.d_vec = vec16(dz, ldz, 2);
+    if (act != ZERO_ACT_NONE && rows > 0) {
+        p.z = preact->data;
+        p.ldz = preact->ld;
+        p.z_vec = vec16(preact->data, preact->ld, 2);
+        if (preact->format == ZERO_SAVED_E4M3) {
+            p.z_scales = preact->scales;
+            p.ldzs = preact->ld_scales;
+            p.zs_vec = aligned(p.z_scales, 8) && p.ldzs % 8 == 0;
+        }
+    }
+    const int64_t blocks = rows > 0 ? act_blocks(rows) : 1;
+    p.units = (int32_t)act_units(rows);
+    p.sums = !dbias ? nullptr : blocks > 1 ? workspace : dbias;
+    const dim3 grid((unsigned)((cols + 127) / 128), (unsigned)blocks);
+    (void)hipGetLastError();
+    if (p.z_scales)
+        hipLaunchKernelGGL(act_backward_kernel<2>, grid, dim3(256), 0, s, p);
+    else if (p.z)
+        hipLaunchKernelGGL(act_backward_kernel<1>, grid, dim3(256), 0, s, p);
+    else
+        hipLaunchKernelGGL(act_backward_kernel<0>, grid, dim3(256), 0, s, p);
+    zero_status st = launched("act_backward");
+    if (st != ZERO_OK || !dbias || blocks == 1)
+        return st;
+    hipLaunchKernelGGL(sum_kernel, dim3((unsigned)((cols + 63) / 64)), dim3(64), 0, s, workspace, blocks, cols,
+                       dbias);
+    return launched("dbias");
+}
+
+// ------------------------------------------------------ grouped products --
+
+zero_status grouped_check(int32_t n_groups, const int64_t *offsets, int64_t rows)
+{
+    if (n_groups < 1 || rows < 0)
+        return fail(ZERO_ERR_INVALID_ARG, "a grouped product needs at least one group and rows >= 0");
+    if (!offsets)
+        return fail(ZERO_ERR_INVALID_ARG, "offsets is required");
+    if (!aligned(offsets, 8))
+        return fail(ZERO_ERR_ALIGNMENT, "offsets must be 8-byte aligned");
+    return ZERO_OK;
+}
+
+// The most tiles of bm rows that n_groups groups over `rows` rows can have.
+static int64_t most_tiles(int32_t n_groups, int64_t rows, int bm)
+{
+    const int64_t g = rows < n_groups ? rows : n_groups;
+    return (rows + g * (bm - 1)) / bm;
+}
+
+zero_status grouped_rows_check(int32_t n_groups, const int64_t *offsets, int64_t rows, int64_t N, int64_t K,
+                               const uint16_t *A, int64_t lda, const uint16_t *B, int64_t ldb,
+                               int32_t b_order, int64_t stride_b, const void *C, int64_t ldc,
+                               int32_t c_dtype, const zero_epilogue *ep)
+{
+    zero_status st;
+    if ((st = grouped_check(n_groups, offsets, rows)) != ZERO_OK ||
+        (st = gemm_check(rows, N, K, A, lda, ZERO_K_INNER, B, ldb, b_order, C, ldc, c_dtype)) != ZERO_OK ||
+        (st = epilogue_check(rows, N, ep, true)) != ZERO_OK)
+        return st;
+    if (rows == 0 || N == 0)
+        return ZERO_OK;
+    const int64_t extent = b_order == ZERO_K_OUTER ? (K > 0 ? (K - 1) * ldb + N : 0) : (N - 1) * ldb + K;
+    if (n_groups > 1 && (stride_b < extent || stride_b % 8))
+        return fail(ZERO_ERR_INVALID_ARG, "stride_b must be a multiple of 8 and at least %lld (got %lld)",
+                    (long long)extent, (long long)stride_b);
+    if (stride_b > kMaxElems / n_groups)
+        return fail(ZERO_ERR_UNSUPPORTED, "the groups' operands are too large");
+    if (most_tiles(n_groups, rows, 128) > kMaxBlocks / ((N + 127) / 128))
+        return fail(ZERO_ERR_UNSUPPORTED, "too many tiles for one launch");
+    return ZERO_OK;
+}
+
+zero_status grouped_rows_run(int32_t n_groups, const int64_t *offsets, int64_t rows, int64_t N, int64_t K,
+                             const uint16_t *A, int64_t lda, const uint16_t *B, int64_t ldb,
+                             int32_t b_order, int64_t stride_b, void *C, int64_t ldc, int32_t c_dtype,
+                             const zero_epilogue *ep, hipStream_t s)
+{
+    if (rows == 0 || N == 0)
+        return ZERO_OK;
+    const EpiArgs a = epi_args(ep, C, ldc, c_dtype);
+    const bool small = rows / n_groups <= 128 || 2 * most_tiles(n_groups, rows, kBM) * ((N + kBN - 1) / kBN) <=
+                                                     cu_count();
+    const int bm = small ? 128 : kBM, bn = small ? 128 : kBN;
+    const int tn = (int)((N + bn - 1) / bn);
+    const dim3 grid((unsigned)(most_tiles(n_groups, rows, bm) * tn));
+    (void)hipGetLastError();
+#define ZS_ROWS(BM_, BN_, BO)                                                                      \
+    hipLaunchKernelGGL((grouped_rows_kernel<BM_, BN_, BO>), grid, dim3(kGT), 0, s, offsets, n_groups, \
+                       rows, N, K, A, lda, B, ldb, stride_b, a, tn)
+    if (b_order == ZERO_K_OUTER) {
+        if (small)
+            ZS_ROWS(128, 128, true);
+        else
+            ZS_ROWS(kBM, kBN, true);
+    } else {
+        if (small)
+            ZS_ROWS(128, 128, false);
+        else
+            ZS_ROWS(kBM, kBN, false);
+    }
+#undef ZS_ROWS
+    return launched("gemm_grouped_rows");
+}
+
+zero_status grouped_depth_check(int32_t n_groups, const int64_t *offsets, int64_t rows, int64_t M, int64_t N,
+                                const uint16_t *A, int64_t lda, const uint16_t *B, int64_t ldb,
+                                const void *C, int64_t ldc, int64_t stride_c, int32_t c_dtype)
+{
+    zero_status st;
+    // K rounded down to gemm_check's multiple of 8: with both operands
+    // K-outer any number of rows will do.
+    if ((st = grouped_check(n_groups, offsets, rows)) != ZERO_OK ||
+        (st = gemm_check(M, N, rows / 8 * 8, A, lda, ZERO_K_OUTER, B, ldb, ZERO_K_OUTER, C, ldc,
+                         c_dtype)) != ZERO_OK)
+        return st;
+    if (M == 0 || N == 0)
+        return ZERO_OK;
+    if (n_groups > 1 && stride_c < (M - 1) * ldc + N)
+        return fail(ZERO_ERR_INVALID_ARG, "stride_c must be at least %lld (got %lld)",
+                    (long long)((M - 1) * ldc + N), (long long)stride_c);
+    if (stride_c > kMaxElems / n_groups)
+        return fail(ZERO_ERR_UNSUPPORTED, "the groups' results are too large");
+    const int64_t per = ((M + 127) / 128) * ((N + 127) / 128);
+    if (per > kMaxBlocks / n_groups)
+        return fail(ZERO_ERR_UNSUPPORTED, "too many tiles for one launch");
+    return ZERO_OK;
+}
+
+zero_status grouped_depth_run(int32_t n_groups, const int64_t *offsets, int64_t rows, int64_t M, int64_t N,
+                              const uint16_t *A, int64_t lda, const uint16_t *B, int64_t ldb, void *C,
+                              int64_t ldc, int64_t stride_c, int32_t c_dtype, hipStream_t s)
+{
+    if (M == 0 || N == 0)
+        return ZERO_OK;
+    const bool small = 2 * n_groups * ((M + kBM - 1) / kBM) * ((N + kBN - 1) / kBN) <= cu_count();
+    const int b = small ? 128 : kBM;
+    const int tm = (int)((M + b - 1) / b), tn = (int)((N + b - 1) / b);
+    const dim3 grid((unsigned)((int64_t)n_groups * tm * tn));
+    (void)hipGetLastError();
+#define ZS_DEPTH(B_, BF)                                                                           \
+    hipLaunchKernelGGL((grouped_depth_kernel<B_, B_, BF>), grid, dim3(kGT), 0, s, offsets, rows, M, N, A, \
+                       lda, B, ldb, C, ldc, stride_c, tm, tn)
+    if (c_dtype == ZERO_BF16) {
+        if (small)
+            ZS_DEPTH(128, true);
+        else
+            ZS_DEPTH(kBM, true);
+    } else {
+        if (small)
+            ZS_DEPTH(128, false);
+        else
+            ZS_DEPTH(kBM, false);
+    }
+#undef ZS_DEPTH
+    return launched("gemm_grouped_depth");
+}
+
+}  // namespace zs
+
+extern "C" {
+
+zero_status zero_saved_write(int64_t rows, int64_t cols, const void *x, int64_t ldx, int32_t x_dtype,
+                             const zero_saved *out, void *stream)
+{
+    using namespace zs;
+    zero_status st;
+    if ((st = check_extent(rows, cols, ldx)) != ZERO_OK)
+        return st;
+    if (rows == 0 || cols == 0)
+        return ZERO_OK;
+    if ((st = check_matrix("x", x, ldx, cols, x_dtype)) != ZERO_OK ||
+        (st = saved_check("out", out, rows, cols)) != ZERO_OK)
+        return st;
+    if (out->format != ZERO_SAVED_E4M3)
+        return fail(ZERO_ERR_UNSUPPORTED, "only the 8-bit format is written from a matrix");
+    const int64_t cw = (cols + 127) / 128, rb = (rows + 31) / 32;
+    if (rb > int64_t(0x7fffffff) / 64 / cw)
+        return fail(ZERO_ERR_UNSUPPORTED, "matrix too large for one launch");
+    (void)hipGetLastError();
+    hipLaunchKernelGGL(saved_write_kernel, dim3((unsigned)((rb * cw + 3) / 4)), dim3(256), 0,
+                       static_cast<hipStream_t>(stream), rows, cols, x, ldx, x_dtype == ZERO_BF16,
+                       vec16(x, ldx, bytes_of(x_dtype)), static_cast<uint8_t *>(out->data), out->ld,
+                       out->scales, out->ld_scales, aligned(out->scales, 8) && out->ld_scales % 8 == 0,
+                       rb * cw, cw);
+    return launched("saved_write");
+}
+
+zero_status zero_saved_read(int64_t rows, int64_t cols, const zero_saved *in, void *out, int64_t ldo,
+                            int32_t out_dtype, void *stream)
+{
+    using namespace zs;
+    zero_status st;
+    if ((st = check_extent(rows, cols, ldo)) != ZERO_OK)
+        return st;
+    if (rows == 0 || cols == 0)
+        return ZERO_OK;
+    if ((st = check_matrix("out", out, ldo, cols, out_dtype)) != ZERO_OK ||
+        (st = saved_check("in", in, rows, cols)) != ZERO_OK)
+        return st;
+    if (in->format != ZERO_SAVED_E4M3)
+        return fail(ZERO_ERR_UNSUPPORTED, "only the 8-bit format is read back");
+    const int64_t cw = (cols + 127) / 128, rb = (rows + 31) / 32;
+    if (rb > int64_t(0x7fffffff) / 64 / cw)
+        return fail(ZERO_ERR_UNSUPPORTED, "matrix too large for one launch");
+    (void)hipGetLastError();
+    hipLaunchKernelGGL(saved_read_kernel, dim3((unsigned)((rb * cw + 3) / 4)), dim3(256), 0,
+                       static_cast<hipStream_t>(stream), rows, cols,
+                       static_cast<const uint8_t *>(in->data), in->ld, in->scales, in->ld_scales,
+                       aligned(in->scales, 8) && in->ld_scales % 8 == 0, out, ldo, out_dtype == ZERO_BF16,
+                       vec16(out, ldo, bytes_of(out_dtype)), rb * cw, cw);
+    return launched("saved_read");
+}
+
+zero_status zero_gemm_bf16_epilogue(int64_t M, int64_t N, int64_t K, const uint16_t *A, int64_t lda,
+                                    int32_t a_order, const uint16_t *B, int64_t ldb, int32_t b_order,
+                                    void *C, int64_t ldc, int32_t c_dtype, const zero_epilogue *epilogue,
+                                    void *stream)
+{
+    zero_status st;
+    if ((st = zs::gemm_check(M, N, K, A, lda, a_order, B, ldb, b_order, C, ldc, c_dtype)) != ZERO_OK ||
+        (st = zs::epilogue_check(M, N, epilogue, false)) != ZERO_OK)
+        return st;
+    return zs::epilogue_gemm_run(M, N, K, A, lda, a_order, B, ldb, b_order, C, ldc, c_dtype, epilogue,
+                                 static_cast<hipStream_t>(stream));
+}
+
+int64_t zero_act_backward_workspace(int64_t rows, int64_t cols)
+{
+    if (rows <= 0 || cols <= 0)
+        return 0;
+    const int64_t b = zs::act_blocks(rows);
+    return b > 1 ? b * cols : 0;
+}
+
+zero_status zero_act_backward(int64_t rows, int64_t cols, const void *dy, int64_t ldy, int32_t dy_dtype,
+                              int32_t act, const zero_saved *preact, uint16_t *dz, int64_t ldz, float *dbias,
+                              float *workspace, int64_t n_workspace, void *stream)
+{
+    const zero_status st = zs::act_backward_check(rows, cols, dy, ldy, dy_dtype, act, preact, dz, ldz, dbias,
+                                                  workspace, n_workspace);
+    if (st != ZERO_OK)
+        return st;
+    return zs::act_backward_run(rows, cols, dy, ldy, dy_dtype, act, preact, dz, ldz, dbias, workspace,
+                                static_cast<hipStream_t>(stream));
+}
+
+zero_status zero_gemm_saved_bf16(int64_t M, int64_t N, int64_t K, const zero_saved *A, const uint16_t *B,
+                                 int64_t ldb, void *C, int64_t ldc, int32_t c_dtype, void *stream)
+{
+    const zero_status st = zs::gemm_saved_check(M, N, K, A, B, ldb, C, ldc, c_dtype);
+    if (st != ZERO_OK)
+        return st;
+    return zs::gemm_saved_run(M, N, K, A, B, ldb, C, ldc, c_dtype, static_cast<hipStream_t>(stream));
+}
+
+zero_status zero_gemm_grouped_rows_bf16(int32_t n_groups, const int64_t *offsets, int64_t rows, int64_t N,
+                                        int64_t K, const uint16_t *A, int64_t lda, const uint16_t *B,
+                                        int64_t ldb, int32_t b_order, int64_t stride_b, void *C,
+                                        int64_t ldc, int32_t c_dtype, const zero_epilogue *epilogue,
+                                        void *stream)
+{
+    const zero_status st = zs::grouped_rows_check(n_groups, offsets, rows, N, K, A, lda, B, ldb, b_order,
+                                                  stride_b, C, ldc, c_dtype, epilogue);
+    if (st != ZERO_OK)
+        return st;
+    return zs::grouped_rows_run(n_groups, offsets, rows, N, K, A, lda, B, ldb, b_order, stride_b, C, ldc,
+                                c_dtype, epilogue, static_cast<hipStream_t>(stream));
+}
+
+zero_status zero_gemm_grouped_depth_bf16(int32_t n_groups, const int64_t *offsets, int64_t rows, int64_t M,
+                                         int64_t N, const uint16_t *A, int64_t lda, const uint16_t *B,
+                                         int64_t ldb, void *C, int64_t ldc, int64_t stride_c,
+                                         int32_t c_dtype, void *stream)
+{
+    const zero_status st = zs::grouped_depth_check(n_groups, offsets, rows, M, N, A, lda, B, ldb, C, ldc,
+                                                   stride_c, c_dtype);
+    if (st != ZERO_OK)
+        return st;
+    return zs::grouped_depth_run(n_groups, offsets, rows, M, N, A, lda, B, ldb, C, ldc, stride_c, c_dtype,
+                                 static_cast<hipStream_t>(stream));
+}
+
+}  // extern "C"

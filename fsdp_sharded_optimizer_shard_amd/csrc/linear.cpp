@@ -13,15 +13,7 @@
 // multiple-of-8 rule on it.
 #include <hip/hip_runtime.h>
 
-#include "internal.h"
-
-namespace zs {
-zero_status zero_rows_fill(float *p, int64_t ld, int64_t r0, int64_t r1, int64_t cols,
-                           hipStream_t s);
-zero_status gemm_check(int64_t M, int64_t N, int64_t K, const uint16_t *A, int64_t lda,
-                       int32_t a_order, const uint16_t *B, int64_t ldb, int32_t b_order,
-                       const void *C, int64_t ldc, int32_t c_dtype);
-}
+#include "products.h"
 
 namespace {
 
@@ -51,6 +43,23 @@ zero_status check_shards(const zero_layout *L, const uint16_t *const *w_shards)
         if (reinterpret_cast<uintptr_t>(w_shards[q]) % 2)
             return zs::fail(ZERO_ERR_ALIGNMENT, "W shard of rank %d is misaligned", q);
     }
+    return ZERO_OK;
+}
+
+// An expert unit's dimensions: in is one expert's, in_pad the whole unit's
+// padded rows.
+zero_status expert_dims(const zero_layout *L, int32_t unit, int32_t n_experts, Dims *d)
+{
+    const zero_status st = layer_dims(L, unit, d);
+    if (st != ZERO_OK)
+        return st;
+    if (n_experts < 1 || d->in % n_experts)
+        return zs::fail(ZERO_ERR_INVALID_ARG, "unit %d has %lld rows, not a multiple of %d experts",
+                        unit, (long long)d->in, n_experts);
+    d->in /= n_experts;
+    if (d->in % 8 || d->out % 8)
+        return zs::fail(ZERO_ERR_UNSUPPORTED, "in_features and out_features must be "
+                        "multiples of 8");
     return ZERO_OK;
 }
 
@@ -122,6 +131,152 @@ zero_status zero_fsdp_linear_backward(const zero_layout *L, int32_t unit,
         return st;
     // padding rows of the row-sharded layout hold zero gradient
     return zs::zero_rows_fill(dw_full, d.out, d.in, d.in_pad, d.out, s);
+}
+
+// The layer with its epilogue: the checks of every step first, then the
+// all-gather and one product.
+zero_status zero_fsdp_linear_act_forward(const zero_layout *L, int32_t unit,
+                                         const uint16_t *const *w_shards, int64_t batch,
+                                         const uint16_t *x, uint16_t *w_full,
+                                         const zero_epilogue *epilogue, void *y, int32_t y_dtype,
+                                         void *stream)
+{
+    Dims d;
+    zero_status st = layer_dims(L, unit, &d);
+    if (st != ZERO_OK)
+        return st;
+    if (!w_shards || !x || !w_full || !y || batch < 0)
+        return zs::fail(ZERO_ERR_INVALID_ARG, "w_shards, x, w_full, y and batch >= 0 are "
+                        "required");
+    if ((st = check_shards(L, w_shards)) != ZERO_OK)
+        return st;
+    if (d.in % 8 || d.out % 8)
+        return zs::fail(ZERO_ERR_UNSUPPORTED, "in_features and out_features must be "
+                        "multiples of 8");
+    if ((st = zs::gemm_check(batch, d.out, d.in, x, d.in, ZERO_K_INNER, w_full, d.out,
+                             ZERO_K_OUTER, y, d.out, y_dtype)) != ZERO_OK ||
+        (st = zs::epilogue_check(batch, d.out, epilogue, false)) != ZERO_OK)
+        return st;
+    if ((st = zero_gather_params(L, unit, unit + 1, w_shards, L->parts, w_full, stream)) != ZERO_OK)
+        return st;
+    return zs::epilogue_gemm_run(batch, d.out, d.in, x, d.in, ZERO_K_INNER, w_full, d.out,
+                                 ZERO_K_OUTER, y, d.out, y_dtype, epilogue,
+                                 static_cast<hipStream_t>(stream));
+}
+
+zero_status zero_fsdp_linear_act_backward(const zero_layout *L, int32_t unit,
+                                          const uint16_t *const *w_shards, int64_t batch,
+                                          const zero_saved *x, int32_t act,
+                                          const zero_saved *preact, const uint16_t *dy,
+                                          uint16_t *w_full, uint16_t *dz, void *dx,
+                                          int32_t dx_dtype, float *dw_full, float *dbias,
+                                          float *workspace, int64_t n_workspace, void *stream)
+{
+    Dims d;
+    zero_status st = layer_dims(L, unit, &d);
+    if (st != ZERO_OK)
+        return st;
+    if (!w_shards || !x || !dy || !w_full || !dx || !dw_full || batch < 0)
+        return zs::fail(ZERO_ERR_INVALID_ARG, "w_shards, x, dy, w_full, dx, dw_full and batch >= 0 "
+                        "are required");
+    if ((st = check_shards(L, w_shards)) != ZERO_OK)
+        return st;
+    if (d.in % 8 || d.out % 8)
+        return zs::fail(ZERO_ERR_UNSUPPORTED, "in_features and out_features must be "
+                        "multiples of 8");
+    if (act != ZERO_ACT_NONE && !dz)
+        return zs::fail(ZERO_ERR_INVALID_ARG, "dz is required for an activation");
+    // Without an activation dz is dy itself.
+    const uint16_t *g = act == ZERO_ACT_NONE ? dy : dz;
+    const bool elementwise = act != ZERO_ACT_NONE || dbias;
+    if (elementwise &&
+        (st = zs::act_backward_check(batch, d.out, dy, d.out, ZERO_BF16, act, preact,
+                                     act == ZERO_ACT_NONE ? nullptr : dz, d.out, dbias, workspace,
+                                     n_workspace)) != ZERO_OK)
+        return st;
+    if ((st = zs::gemm_check(batch, d.in, d.out, g, d.out, ZERO_K_INNER, w_full, d.out,
+                             ZERO_K_INNER, dx, d.in, dx_dtype)) != ZERO_OK ||
+        (st = zs::gemm_saved_check(d.in, d.out, batch, x, g, d.out, dw_full, d.out,
+                                   ZERO_FP32)) != ZERO_OK)
+        return st;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    if ((st = zero_gather_params(L, unit, unit + 1, w_shards, L->parts, w_full, stream)) != ZERO_OK)
+        return st;
+    if (elementwise &&
+        (st = zs::act_backward_run(batch, d.out, dy, d.out, ZERO_BF16, act, preact,
+                                   act == ZERO_ACT_NONE ? nullptr : dz, d.out, dbias, workspace,
+                                   s)) != ZERO_OK)
+        return st;
+    // dX = dZ W^T and dW = X^T dZ from the kept X, as in
+    // zero_fsdp_linear_backward
+    if ((st = zs::gemm_run(batch, d.in, d.out, g, d.out, ZERO_K_INNER, w_full, d.out, ZERO_K_INNER,
+                           dx, d.in, dx_dtype, s)) != ZERO_OK)
+        return st;
+    if ((st = zs::gemm_saved_run(d.in, d.out, batch, x, g, d.out, dw_full, d.out, ZERO_FP32,
+                                 s)) != ZERO_OK)
+        return st;
+    return zs::zero_rows_fill(dw_full, d.out, d.in, d.in_pad, d.out, s);
+}
+
+// The expert layer: unit `unit` holds the experts' in x out weights one after
+// the other, so the unit has n_experts * in rows and its shards may cut
+// through an expert; the gathered unit is the operand of the grouped product.
+zero_status zero_fsdp_experts_forward(const zero_layout *L, int32_t unit, int32_t n_experts,
+                                      const uint16_t *const *w_shards, const int64_t *offsets,
+                                      int64_t rows, const uint16_t *x, uint16_t *w_full,
+                                      const zero_epilogue *epilogue, void *y, int32_t y_dtype,
+                                      void *stream)
+{
+    Dims d;
+    zero_status st = expert_dims(L, unit, n_experts, &d);
+    if (st != ZERO_OK)
+        return st;
+    if (!w_shards || !x || !w_full || !y || rows < 0)
+        return zs::fail(ZERO_ERR_INVALID_ARG, "w_shards, x, w_full, y and rows >= 0 are required");
+    if ((st = check_shards(L, w_shards)) != ZERO_OK)
+        return st;
+    const int64_t stride = d.in * d.out;
+    if ((st = zs::grouped_rows_check(n_experts, offsets, rows, d.out, d.in, x, d.in, w_full, d.out,
+                                     ZERO_K_OUTER, stride, y, d.out, y_dtype, epilogue)) != ZERO_OK)
+        return st;
+    if ((st = zero_gather_params(L, unit, unit + 1, w_shards, L->parts, w_full, stream)) != ZERO_OK)
+        return st;
+    return zs::grouped_rows_run(n_experts, offsets, rows, d.out, d.in, x, d.in, w_full, d.out, ZERO_K_OUTER,
+                                stride, y, d.out, y_dtype, epilogue,
+                                static_cast<hipStream_t>(stream));
+}
+
+zero_status zero_fsdp_experts_backward(const zero_layout *L, int32_t unit, int32_t n_experts,
+                                       const uint16_t *const *w_shards, const int64_t *offsets,
+                                       int64_t rows, const uint16_t *x, const uint16_t *dy,
+                                       uint16_t *w_full, void *dx, int32_t dx_dtype,
+                                       float *dw_full, void *stream)
+{
+    Dims d;
+    zero_status st = expert_dims(L, unit, n_experts, &d);
+    if (st != ZERO_OK)
+        return st;
+    if (!w_shards || !x || !dy || !w_full || !dx || !dw_full || rows < 0)
+        return zs::fail(ZERO_ERR_INVALID_ARG, "every buffer and rows >= 0 are required");
+    if ((st = check_shards(L, w_shards)) != ZERO_OK)
+        return st;
+    const int64_t stride = d.in * d.out;
+    if ((st = zs::grouped_rows_check(n_experts, offsets, rows, d.in, d.out, dy, d.out, w_full, d.out,
+                                     ZERO_K_INNER, stride, dx, d.in, dx_dtype, nullptr)) != ZERO_OK ||
+        (st = zs::grouped_depth_check(n_experts, offsets, rows, d.in, d.out, x, d.in, dy, d.out,
+                                      dw_full, d.out, stride, ZERO_FP32)) != ZERO_OK)
+        return st;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    if ((st = zero_gather_params(L, unit, unit + 1, w_shards, L->parts, w_full, stream)) != ZERO_OK)
+        return st;
+    if ((st = zs::grouped_rows_run(n_experts, offsets, rows, d.in, d.out, dy, d.out, w_full, d.out,
+                                   ZERO_K_INNER, stride, dx, d.in, dx_dtype, nullptr, s)) != ZERO_OK)
+        return st;
+    if ((st = zs::grouped_depth_run(n_experts, offsets, rows, d.in, d.out, x, d.in, dy, d.out, dw_full,
+                                    d.out, stride, ZERO_FP32, s)) != ZERO_OK)
+        return st;
+    const int64_t total = d.in * n_experts;
+    return zs::zero_rows_fill(dw_full, d.out, total, d.in_pad, d.out, s);
 }
 
 }  // extern "C"

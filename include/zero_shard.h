@@ -612,6 +612,185 @@ zero_status zero_fsdp_linear_backward(const zero_layout *layout, int32_t unit,
                                       void *dx, int32_t dx_dtype,
                                       float *dw_full, void *stream);
 
+/* ------------------------------------------------ layer operators -- */
+
+/* What a linear layer does around its product, and what it keeps for its
+   backward pass.  The pages leave the layer's inside to the model; they
+   count the bytes a rank holds ("DP, ZeRO-1/2/3, FSDP" notes, concepts
+   "Model states", which sets activations apart from the 16 bytes per
+   parameter), and these calls are about the other part: fewer passes over
+   the activations, and half the bytes of those kept.
+
+   An activation, z -> act(z), in fp32: RELU max(z, 0); GELU z Phi(z);
+   GELU_TANH z sigmoid(2 sqrt(2/pi) (z + 0.044715 z^3)); SILU z sigmoid(z).
+   Infinities take their limits (act(-inf) = 0 for all but NONE), NaN stays
+   NaN. */
+typedef enum zero_activation {
+    ZERO_ACT_NONE = 0,
+    ZERO_ACT_RELU = 1,
+    ZERO_ACT_GELU = 2,
+    ZERO_ACT_GELU_TANH = 3,
+    ZERO_ACT_SILU = 4
+} zero_activation;
+
+/* A rows x cols activation matrix kept for the backward pass.
+     ZERO_SAVED_BF16  data: rows x cols bf16, leading dimension ld.
+     ZERO_SAVED_E4M3  data: rows x cols e4m3 codes of one byte, leading
+                      dimension ld (a multiple of 16, data 16-byte aligned);
+                      scales: ceil(rows / 32) x cols bytes, leading dimension
+                      ld_scales.  One byte b serves the 32 rows (tokens)
+                      32 i .. 32 i + 31 of one column (feature): the values
+                      are code * 2^(b - 127), each exact in bf16.  b - 127 is
+                      the least e in [-117, 120] for which the block's
+                      largest finite magnitude is at most 448 * 2^e, and the
+                      code is x / 2^e rounded to nearest even, |x| first
+                      bounded by 240 * 2^120.  NaN and infinities become NaN
+                      and do not count for e.
+   Blocks run along tokens because dW = X^T dZ contracts over tokens, and so
+   that a feature with large values costs its neighbours no precision. */
+typedef enum zero_saved_format { ZERO_SAVED_BF16 = 0, ZERO_SAVED_E4M3 = 1 } zero_saved_format;
+
+typedef struct zero_saved {
+    void *data;
+    int64_t ld;
+    uint8_t *scales;   /* E4M3 only */
+    int64_t ld_scales; /* E4M3 only */
+    int32_t format;
+} zero_saved;
+
+/* *out = x (rows x cols, bf16 or fp32, leading dimension ldx) in 8 bits
+   (E4M3 only).  Bytes past column cols of a row are not written. */
+zero_status zero_saved_write(int64_t rows, int64_t cols, const void *x, int64_t ldx,
+                             int32_t x_dtype, const zero_saved *out, void *stream);
+
+/* out = the values *in stands for (E4M3 only; bf16 and fp32 both exact). */
+zero_status zero_saved_read(int64_t rows, int64_t cols, const zero_saved *in, void *out,
+                            int64_t ldo, int32_t out_dtype, void *stream);
+
+/* The epilogue of an M x N product: with z = A B + bias,
+       C = act(z) + residual,
+   in fp32, C rounded once to its type.  NULL members are left out.
+     bias      N values, bf16 or fp32;
+     residual  M x N, bf16 or fp32, leading dimension ldr; it may be C itself
+               (same type and leading dimension), else it must not overlap C;
+     preact    receives z, in either format (E4M3: coded from the fp32 z);
+     output    receives C in 8 bits (E4M3), coded from C as stored: the same
+               bytes that zero_saved_write of C would give. */
+typedef struct zero_epilogue {
+    const void *bias;
+    const void *residual;
+    int64_t ldr;
+    const zero_saved *preact;
+    const zero_saved *output;
+    int32_t bias_dtype;
+    int32_t residual_dtype;
+    int32_t act;
+} zero_epilogue;
+
+/* zero_gemm_bf16 with an epilogue (NULL: none).  Limits and errors as there,
+   and the epilogue's matrices checked like C.  K = 0 gives z = bias. */
+zero_status zero_gemm_bf16_epilogue(int64_t M, int64_t N, int64_t K, const uint16_t *A,
+                                    int64_t lda, int32_t a_order, const uint16_t *B,
+                                    int64_t ldb, int32_t b_order, void *C, int64_t ldc,
+                                    int32_t c_dtype, const zero_epilogue *epilogue,
+                                    void *stream);
+
+/* The gradient of that epilogue:
+       dz[i][j]  = dy[i][j] * act'(preact[i][j])     (bf16)
+       dbias[j]  = sum over i of dz[i][j]            (fp32, of the unrounded
+                                                      products; NULL: left out)
+   The residual's gradient is dy itself.  dy is bf16 or fp32; dz may be dy
+   (bf16, same leading dimension).  For ZERO_ACT_NONE preact is not read and
+   dz may be NULL (dbias alone).  relu'(0) = 0.  The sum runs in a fixed
+   order, so dbias has the same bits every time; it needs
+   `workspace` of zero_act_backward_workspace(rows, cols) floats (at most
+   64 cols; 0 up to 128 rows, and the workspace may then be NULL), used
+   until the call's work has run: calls that overlap in time, and captured
+   graphs that do, need one each.  rows = 0 writes zeros to dbias. */
+zero_status zero_act_backward(int64_t rows, int64_t cols, const void *dy, int64_t ldy,
+                              int32_t dy_dtype, int32_t act, const zero_saved *preact,
+                              uint16_t *dz, int64_t ldz, float *dbias, float *workspace,
+                              int64_t n_workspace, void *stream);
+int64_t zero_act_backward_workspace(int64_t rows, int64_t cols);
+
+/* C[i][j] = sum_{k < K} A[k][i] B[k][j] with A (K x M) kept in either format
+   and B K x N bf16: a layer's dW = X^T dZ from the kept X, read in place.
+   fp32 accumulation, C fp32 or bf16.  K is any number; M, N and the leading
+   dimensions of A and B multiples of 8 (codes: 16; the scales' rows 4-byte
+   aligned), at most 2^25; A and B 16-byte aligned.  K = 0 writes zeros. */
+zero_status zero_gemm_saved_bf16(int64_t M, int64_t N, int64_t K, const zero_saved *A,
+                                 const uint16_t *B, int64_t ldb, void *C, int64_t ldc,
+                                 int32_t c_dtype, void *stream);
+
+/* Products grouped by expert.  The rows of A are sorted by group: group e has
+   the rows offsets[e] .. offsets[e + 1] - 1, where `offsets` is a DEVICE array
+   of n_groups + 1 int64 (8-byte aligned) read when the kernels run -- a
+   router's counts never come to the host, and a captured call takes new
+   sizes at every replay.  Groups may be empty.  Offsets are clamped to
+   [0, rows] and a decreasing pair to an empty group, so nothing outside the
+   buffers is touched whatever the array holds; what such an array computes
+   is unspecified.
+
+   rows:   C[r] = epilogue(A[r] B_e), r in group e, with A rows x K bf16 and
+           B_e = B + e * stride_b (elements, a multiple of 8), N and K and the
+           orders as zero_gemm_bf16 has them (A K_INNER).  Rows in no group
+           are left as they were, in C and in the kept pre-activation.  The
+           epilogue has no bias and keeps nothing in 8 bits (a group does not
+           begin at a multiple of 32 rows): ZERO_ERR_UNSUPPORTED.
+   depth:  C_e[i][j] = sum over r in group e of A[r][i] B[r][j], C_e = C +
+           e * stride_c (elements); an empty group's C_e is zeros.  A is
+           rows x M, B rows x N, both bf16; any row count. */
+zero_status zero_gemm_grouped_rows_bf16(int32_t n_groups, const int64_t *offsets, int64_t rows,
+                                        int64_t N, int64_t K, const uint16_t *A, int64_t lda,
+                                        const uint16_t *B, int64_t ldb, int32_t b_order,
+                                        int64_t stride_b, void *C, int64_t ldc, int32_t c_dtype,
+                                        const zero_epilogue *epilogue, void *stream);
+zero_status zero_gemm_grouped_depth_bf16(int32_t n_groups, const int64_t *offsets, int64_t rows,
+                                         int64_t M, int64_t N, const uint16_t *A, int64_t lda,
+                                         const uint16_t *B, int64_t ldb, void *C, int64_t ldc,
+                                         int64_t stride_c, int32_t c_dtype, void *stream);
+
+/* zero_fsdp_linear_forward / _backward with the epilogue and its gradient:
+     forward:  w_full = all-gather(w_shards); y = act(x W + bias) + residual,
+               keeping what the epilogue names.
+     backward: w_full again; dz = dy act'(preact); dbias; dx = dz W^T;
+               dw_full = x^T dz from the kept x (bf16 or 8 bits), padding
+               rows zeroed.  dz is a batch x out bf16 buffer (it may be dy);
+               for ZERO_ACT_NONE it may be NULL and dy is used as it is.
+               dbias may be NULL; workspace as zero_act_backward.
+   batch is any number here; otherwise as zero_fsdp_linear_*. */
+zero_status zero_fsdp_linear_act_forward(const zero_layout *layout, int32_t unit,
+                                         const uint16_t *const *w_shards, int64_t batch,
+                                         const uint16_t *x, uint16_t *w_full,
+                                         const zero_epilogue *epilogue, void *y,
+                                         int32_t y_dtype, void *stream);
+zero_status zero_fsdp_linear_act_backward(const zero_layout *layout, int32_t unit,
+                                          const uint16_t *const *w_shards, int64_t batch,
+                                          const zero_saved *x, int32_t act,
+                                          const zero_saved *preact, const uint16_t *dy,
+                                          uint16_t *w_full, uint16_t *dz, void *dx,
+                                          int32_t dx_dtype, float *dw_full, float *dbias,
+                                          float *workspace, int64_t n_workspace, void *stream);
+
+/* An FSDP expert layer: unit `unit` of a row layout holds n_experts weights
+   of in x out one after the other (rows = n_experts * in, cols = out), sharded
+   by rows like any other unit.
+     forward:  w_full = all-gather; y = the grouped product of x by rows.
+     backward: w_full again; dx = grouped dy W_e^T; dw_full = the experts' dW
+               one after the other (fp32, the padded unit), ready for
+               zero_reduce_shard and zero_adam_step.
+   in and out multiples of 8.  Rows in no group keep their y and dx. */
+zero_status zero_fsdp_experts_forward(const zero_layout *layout, int32_t unit,
+                                      int32_t n_experts, const uint16_t *const *w_shards,
+                                      const int64_t *offsets, int64_t rows, const uint16_t *x,
+                                      uint16_t *w_full, const zero_epilogue *epilogue, void *y,
+                                      int32_t y_dtype, void *stream);
+zero_status zero_fsdp_experts_backward(const zero_layout *layout, int32_t unit,
+                                       int32_t n_experts, const uint16_t *const *w_shards,
+                                       const int64_t *offsets, int64_t rows, const uint16_t *x,
+                                       const uint16_t *dy, uint16_t *w_full, void *dx,
+                                       int32_t dx_dtype, float *dw_full, void *stream);
+
 /* ---------------------------------------------------------- errors -- */
 
 const char *zero_status_str(zero_status status);

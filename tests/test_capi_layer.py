@@ -1,0 +1,304 @@
+"""Host-side checks of the layer operators (no GPU): what each call refuses,
+with which status, before anything is launched.  Addresses are fake, so a
+check that misses would show as a HIP error."""
+import os
+import re
+
+import pytest
+import torch
+
+from fsdp_sharded_optimizer_shard_amd import zs
+
+FAKE = 0x7f0000000000
+HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                      "include", "zero_shard.h")
+INV, ALIGN, UNSUP = zs.ERR_INVALID_ARG, zs.ERR_ALIGNMENT, zs.ERR_UNSUPPORTED
+
+
+def refused(status, fn, *a, text="", **kw):
+    with pytest.raises(zs.ZeroShardError) as e:
+        fn(*a, stream=0, **kw)
+    assert e.value.status == status, str(e.value)
+    assert text in str(e.value)
+
+
+def s8(ld=64, lds=64, data=FAKE, scales=FAKE):
+    return zs.Saved(data, ld, scales, lds)
+
+
+def test_enums_equal_the_headers():
+    txt = open(HEADER).read()
+    defs = dict(re.findall(r"(ZERO_(?:ACT|SAVED)_[A-Z0-9_]+) = (\d+)", txt))
+    assert len(defs) == 7
+    for name, value in defs.items():
+        assert getattr(zs, name[len("ZERO_"):]) == int(value), name
+    assert zs.ACTIVATION == {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+
+@pytest.mark.parametrize("call", ["write", "read"])
+def test_checkpoint_refusals(call):
+    def go(rows=40, cols=64, x=FAKE, ldx=64, saved=None, dtype=zs.BF16):
+        saved = saved or s8()
+        if call == "write":
+            zs.saved_write(rows, cols, x, ldx, saved, dtype, stream=0)
+        else:
+            zs.saved_read(rows, cols, saved, x, ldx, dtype, stream=0)
+
+    def bad(status, **kw):
+        with pytest.raises(zs.ZeroShardError) as e:
+            go(**kw)
+        assert e.value.status == status, str(e.value)
+
+    bad(INV, rows=-1)
+    bad(INV, cols=-1)
+    bad(INV, x=None)
+    bad(INV, ldx=63)
+    bad(INV, dtype=2)
+    bad(INV, saved=s8(data=None))
+    bad(INV, saved=s8(ld=48))
+    bad(INV, saved=s8(lds=63))
+    bad(UNSUP, saved=s8(ld=72))                     # not a multiple of 16
+    bad(UNSUP, saved=zs.Saved(FAKE, 64))            # bf16: nothing to code
+    bad(ALIGN, x=FAKE + 1)
+    bad(ALIGN, x=FAKE + 2, dtype=zs.FP32)
+    bad(ALIGN, saved=s8(data=FAKE + 8))
+    bad(UNSUP, rows=1 << 50)
+    bad(UNSUP, rows=1 << 36, cols=64)               # one launch cannot hold it
+    go(rows=0)                                      # nothing to do
+    go(cols=0)
+
+
+def epi(**kw):
+    return zs.Epilogue(**kw)
+
+
+def test_epilogue_refusals():
+    def bad(status, ep, M=64, N=64, K=64, C=FAKE, ldc=64, text="", **kw):
+        refused(status, zs.gemm_bf16_epilogue, M, N, K, FAKE, max(K, 64), zs.K_INNER, FAKE, 64,
+                zs.K_OUTER, C, ldc, zs.BF16, ep, text=text, **kw)
+
+    bad(INV, epi(act=5), text="activation")
+    bad(INV, epi(act=-1))
+    bad(ALIGN, epi(bias=FAKE + 1))
+    bad(ALIGN, epi(bias=FAKE + 2, bias_dtype=zs.FP32))
+    bad(INV, epi(bias=FAKE, bias_dtype=7))
+    bad(INV, epi(residual=FAKE, ldr=63), text="residual")
+    bad(ALIGN, epi(residual=FAKE + 1, ldr=64))
+    bad(INV, epi(preact=zs.Saved(FAKE, 63)), text="preact")
+    bad(INV, epi(preact=zs.Saved(None, 64)))
+    bad(ALIGN, epi(preact=zs.Saved(FAKE + 1, 64)))
+    bad(UNSUP, epi(preact=s8(ld=72)))
+    bad(INV, epi(preact=s8(lds=8)))
+    bad(UNSUP, epi(output=zs.Saved(FAKE, 64)), text="8 bits")
+    bad(ALIGN, epi(output=s8(data=FAKE + 4)))
+    # the product's own limits still hold
+    bad(UNSUP, epi(), K=60)
+    bad(INV, epi(), C=None)
+    bad(INV, epi(), ldc=8)
+    bad(INV, epi(), M=-1)
+    with pytest.raises(ValueError):
+        zs.Epilogue(act="swish")
+    zs.gemm_bf16_epilogue(0, 64, 64, FAKE, 64, zs.K_INNER, FAKE, 64, zs.K_OUTER, FAKE, 64, zs.BF16,
+                          epi(act="silu"), stream=0)
+
+
+def test_act_backward_refusals():
+    def bad(status, rows=200, cols=64, dy=FAKE, ldy=64, act="gelu", z="bf16", dz=FAKE, ldz=64,
+            dbias=None, work=None, text="", **kw):
+        z = zs.Saved(FAKE, 64) if z == "bf16" else z
+        refused(status, zs.act_backward, rows, cols, dy, ldy, act, z, dz, ldz, dbias, work,
+                text=text, **kw)
+
+    bad(INV, rows=-1)
+    bad(INV, act=9)
+    bad(INV, dy_dtype=3)
+    bad(INV, dy=None)
+    bad(INV, ldy=8)
+    bad(INV, z=None, text="preact")
+    bad(INV, z=zs.Saved(FAKE, 8))
+    bad(UNSUP, z=s8(ld=72))
+    bad(INV, dz=None)
+    bad(INV, dz=None, act="none", z=None)           # neither dz nor dbias
+    bad(INV, ldz=8)
+    bad(ALIGN, dz=FAKE + 1)
+    bad(ALIGN, dbias=FAKE + 2, work=FAKE)
+    bad(ALIGN, dbias=FAKE, work=FAKE + 2)
+    bad(INV, dbias=FAKE, text="workspace")
+    bad(UNSUP, rows=1 << 41)
+    with pytest.raises(zs.ZeroShardError):          # a workspace one float short
+        zs._check(zs.raw().zero_act_backward(200, 64, FAKE, 64, 0, 2, zs.Saved(FAKE, 64).ref(), FAKE,
+                                             64, FAKE, FAKE, zs.act_backward_workspace(200, 64) - 1,
+                                             0), "zero_act_backward")
+    zs.act_backward(0, 64, None, 64, "gelu", None, None, 64, stream=0)
+    zs.act_backward(5, 0, None, 0, "gelu", None, None, 0, FAKE, stream=0)
+
+
+def test_workspace_size():
+    w = zs.act_backward_workspace
+    assert w(0, 10) == w(-1, 10) == w(10, 0) == 0
+    assert w(1, 10) == w(128, 10) == 0
+    assert w(129, 10) == 20
+    for rows in (200, 4096, 8192, 8193, 100_000, 1 << 30):
+        assert 0 < w(rows, 7) <= 64 * 7
+        assert w(rows, 7) <= -(-rows // 128) * 7
+
+
+def test_saved_product_refusals():
+    def bad(status, M=64, N=64, K=100, A=None, B=FAKE, ldb=64, C=FAKE, ldc=64, dt=zs.FP32):
+        refused(status, zs.gemm_saved_bf16, M, N, K, A or s8(), B, ldb, C, ldc, dt)
+
+    bad(INV, M=-8)
+    bad(INV, dt=4)
+    bad(INV, A=s8(data=None))
+    bad(INV, A=s8(ld=48))
+    bad(INV, B=None)
+    bad(INV, ldb=8)
+    bad(INV, ldc=8)
+    bad(UNSUP, M=60)
+    bad(UNSUP, N=60)
+    bad(UNSUP, ldb=68)
+    bad(UNSUP, A=s8(lds=66))                        # scale rows not 4-byte aligned
+    bad(UNSUP, A=s8(scales=FAKE + 2))
+    bad(UNSUP, ldb=1 << 26)
+    bad(UNSUP, A=s8(ld=1 << 26))
+    bad(ALIGN, B=FAKE + 8)
+    bad(ALIGN, C=FAKE + 2)
+    bad(ALIGN, A=s8(data=FAKE + 8))
+    bad(ALIGN, A=zs.Saved(FAKE + 2, 64))
+    bad(UNSUP, A=zs.Saved(FAKE, 68))
+    zs.gemm_saved_bf16(0, 64, 100, s8(), FAKE, 64, FAKE, 64, stream=0)
+
+
+def test_grouped_refusals():
+    def rows(status, n=4, off=FAKE, rows=100, N=64, K=64, sb=4096, ldb=64, order=zs.K_OUTER, ep=None,
+             lda=64):
+        refused(status, zs.gemm_grouped_rows_bf16, n, off, rows, N, K, FAKE, lda, FAKE, ldb, order,
+                sb, FAKE, 64, zs.BF16, ep)
+
+    rows(INV, n=0)
+    rows(INV, rows=-1)
+    rows(INV, off=None)
+    rows(ALIGN, off=FAKE + 4)
+    rows(INV, sb=4088)                              # operands would overlap
+    rows(INV, sb=4100)                              # not a multiple of 8
+    rows(UNSUP, sb=1 << 59)
+    rows(UNSUP, K=60)
+    rows(INV, lda=8)
+    rows(UNSUP, rows=1 << 40)
+    rows(UNSUP, ep=epi(bias=FAKE))
+    rows(UNSUP, ep=epi(preact=s8()))
+    rows(UNSUP, ep=epi(output=s8()))
+    rows(INV, ep=epi(act=7))
+    zs.gemm_grouped_rows_bf16(4, FAKE, 0, 64, 64, FAKE, 64, FAKE, 64, zs.K_OUTER, 4096, FAKE, 64,
+                              stream=0)
+
+    def depth(status, n=4, off=FAKE, rows=101, M=64, N=64, lda=64, sc=4096, ldc=64):
+        refused(status, zs.gemm_grouped_depth_bf16, n, off, rows, M, N, FAKE, lda, FAKE, 64, FAKE,
+                ldc, sc)
+
+    depth(INV, n=0)
+    depth(INV, rows=-1)
+    depth(INV, off=None)
+    depth(ALIGN, off=FAKE + 4)
+    depth(UNSUP, M=60)
+    depth(INV, lda=56)
+    depth(INV, sc=4095)
+    depth(INV, ldc=56)
+    depth(UNSUP, sc=1 << 59)
+    depth(UNSUP, n=1 << 30)
+
+
+def test_layer_calls_refuse_before_the_gather():
+    L = zs.shard_init_rows("fsdp2", 2, 0, [(64, 32)])
+
+    def fwd(status, shards=(FAKE, FAKE), batch=5, ep=None, y=FAKE):
+        refused(status, zs.fsdp_linear_act_forward, L, 0, list(shards), batch, FAKE, FAKE, y, ep)
+
+    fwd(INV, shards=(FAKE, None))
+    fwd(INV, batch=-1)
+    fwd(INV, y=None)
+    fwd(INV, ep=epi(act=8))
+    fwd(INV, ep=epi(residual=FAKE, ldr=8))
+    with pytest.raises(ValueError):
+        zs.fsdp_linear_act_forward(L, 0, [FAKE], 5, FAKE, FAKE, FAKE, stream=0)
+
+    def bwd(status, x=None, act="gelu", z=None, dz=FAKE, dbias=None, work=None, batch=300):
+        refused(status, zs.fsdp_linear_act_backward, L, 0, [FAKE, FAKE], batch,
+                x or zs.Saved(FAKE, 64), act, z, FAKE, FAKE, dz, FAKE, FAKE, dbias, work)
+
+    z = zs.Saved(FAKE, 32)
+    bwd(INV, z=None)
+    bwd(INV, z=z, dz=None)
+    bwd(INV, z=z, dbias=FAKE)                       # no workspace
+    bwd(INV, z=z, x=zs.Saved(FAKE, 32))             # x too narrow
+    bwd(UNSUP, z=z, x=s8(ld=72, lds=72))
+    bwd(INV, z=z, act=6)
+    bwd(INV, z=z, batch=-1)
+
+    def experts(status, n=2, off=FAKE, ep=None):
+        refused(status, zs.fsdp_experts_forward, L, 0, n, [FAKE, FAKE], off, 10, FAKE, FAKE, FAKE, ep)
+        if ep is None:
+            refused(status, zs.fsdp_experts_backward, L, 0, n, [FAKE, FAKE], off, 10, FAKE, FAKE,
+                    FAKE, FAKE, FAKE)
+
+    experts(INV, n=0)
+    experts(INV, n=3)                               # 64 rows are not 3 experts'
+    experts(UNSUP, n=16)                            # 4 features each
+    experts(INV, off=None)
+    experts(UNSUP, ep=epi(bias=FAKE))
+
+
+def test_tensors_are_checked_before_the_call():
+    """Host tensors, wrong types and short buffers raise ValueError; two
+    devices in one call, or a device that is not the current one, too."""
+    host = torch.zeros(64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="GPU"):
+        zs.Saved(host, 8)
+    with pytest.raises(ValueError, match="GPU"):
+        zs.Epilogue(bias=host)
+
+    class OnDevice:
+        is_cuda = True
+
+        def __init__(self, n, dtype, dev=0, contiguous=True):
+            self.n, self.dtype, self.dev, self.c = n, dtype, dev, contiguous
+
+        def numel(self):
+            return self.n
+
+        def element_size(self):
+            return torch.empty(0, dtype=self.dtype).element_size()
+
+        def is_contiguous(self):
+            return self.c
+
+        def data_ptr(self):
+            return FAKE
+
+        def get_device(self):
+            return self.dev
+
+    bf = torch.bfloat16
+    good = zs.Saved(OnDevice(40 * 64, torch.uint8), 64, OnDevice(2 * 64, torch.uint8), 64)
+    short = zs.Saved(OnDevice(40 * 64 - 1, torch.uint8), 64, OnDevice(2 * 64, torch.uint8), 64)
+    few = zs.Saved(OnDevice(40 * 64, torch.uint8), 64, OnDevice(127, torch.uint8), 64)
+    kind = zs.Saved(OnDevice(40 * 64, torch.float32), 64, OnDevice(2 * 64, torch.uint8), 64)
+    x = OnDevice(40 * 64, bf)
+    for saved in (short, few, kind):
+        with pytest.raises(ValueError):
+            zs.saved_write(40, 64, x, 64, saved, stream=0)
+    with pytest.raises(ValueError):
+        zs.saved_write(40, 64, OnDevice(40 * 64 - 1, bf), 64, good, stream=0)
+    with pytest.raises(ValueError, match="contiguous"):
+        zs.saved_write(40, 64, OnDevice(40 * 64, bf, contiguous=False), 64, good, stream=0)
+    with pytest.raises(ValueError, match="two devices"):
+        zs.saved_write(40, 64, OnDevice(40 * 64, bf, dev=1), 64, good, stream=0)
+    with pytest.raises(ValueError):
+        zs.gemm_grouped_rows_bf16(4, OnDevice(4, torch.int64), 10, 8, 8, x, 8, x, 8, zs.K_OUTER, 64, x,
+                                  8, stream=0)
+    with pytest.raises(ValueError):
+        zs.gemm_grouped_depth_bf16(4, OnDevice(5, torch.int32), 10, 8, 8, x, 8, x, 8, x, 8, 64,
+                                   stream=0)
+    with pytest.raises(ValueError, match="workspace"):
+        zs.act_backward(300, 8, x, 8, "relu", zs.Saved(OnDevice(2400, bf), 8), x, 8,
+                        OnDevice(8, torch.float32), OnDevice(23, torch.float32), stream=0)
