@@ -68,12 +68,14 @@ __device__ __forceinline__ float normal_cdf(float z, float &g)
 }
 
 // -inf times a zero sigmoid would be NaN; the lowest finite value gives -0.
-__device__ __forceinline__ float finite_low(float z) { return z < -FLT_MAX ? -FLT_MAX : z; }
-// Past +-64 every slope's second term is 0; the bound keeps it from 0 * inf.
-__device__ __forceinline__ float bound64(float z)
+// (A NaN may come back as the bound: every caller multiplies it by a sigmoid
+// that is NaN then.)
+__device__ __forceinline__ float finite_low(float z)
 {
-    return z < -64.0f ? -64.0f : z > 64.0f ? 64.0f : z;
+    return __builtin_amdgcn_fmed3f(z, -FLT_MAX, __builtin_inff());
 }
+// Past +-64 every slope's second term is 0; the bound keeps it from 0 * inf.
+__device__ __forceinline__ float bound64(float z) { return __builtin_amdgcn_fmed3f(z, -64.0f, 64.0f); }
 
 constexpr float kTanhK = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kInvSqrt2Pi = 0.3989422804014327f;
@@ -104,9 +106,9 @@ __device__ __forceinline__ float act_slope(float z)
         const float c = normal_cdf(z, q);
         return __builtin_fmaf(bound64(z) * kInvSqrt2Pi, q, c);
     } else if constexpr (ACT == ZERO_ACT_GELU_TANH) {
-        const float b = bound64(z), b2 = 0.044715f * b * b;
-        const float s = sigmoid(kTanhK * b * (1.0f + b2), q);
-        return __builtin_fmaf(b * q, kTanhK * __builtin_fmaf(3.0f, b2, 1.0f), s);
+        const float b = bound64(z);
+        const float s = sigmoid(kTanhK * z * __builtin_fmaf(0.044715f * z, z, 1.0f), q);
+        return __builtin_fmaf(b * q, kTanhK * __builtin_fmaf(3.0f * 0.044715f * b, b, 1.0f), s);
     } else if constexpr (ACT == ZERO_ACT_SILU) {
         const float s = sigmoid(z, q);
         return __builtin_fmaf(bound64(z), q, s);
