@@ -465,21 +465,25 @@ __global__ __launch_bounds__(kGT) void grouped_depth_kernel(const int64_t *__res
 // ------------------------------------------- products from 8-bit operands --
 
 // C = A^T B with A a K x M checkpoint (codes and exponent bytes) and B bf16,
-// both K-outer.  As gemm_tile, except for A: a stage holds 32 k rows of BM
-// code bytes, and next to it the one row of BM exponent bytes that serves
-// them all -- the blocks run along k, so a lane, which holds one row of C,
+// both K-outer.  The pipeline is gemm_tile's; what differs is A.
+//
+// A stage holds 32 k rows of BM code bytes.  The blocks run along k, so one
+// row of exponent bytes serves a stage and a lane, which holds one row of C,
 // needs one exponent a stage.  A fragment is one ds_read_b64_tr_b8 (an 8 x 16
 // byte block transposed over 16 lanes: eight k of one row) and four
-// v_cvt_scalef32_pk_bf16_fp8, exact, on the vector unit beside the other
-// wave's MFMAs.
+// v_cvt_scalef32_pk_bf16_fp8, exact.  The 8 waves stand 4 x 2, each (BM / 4) x
+// (BN / 2): that halves the conversions of gemm_tile's 2 x 4 (each A fragment
+// is then widened by two waves instead of four) for the same accumulators.
 //
 // The 32-byte unit U of k row kr sits at U ^ (kr & 7) (BM = 256; for BM = 128,
 // whose rows are half as long, U ^ ((kr >> 1) & 3)), so that the eight k rows
 // a half wave reads at once fall into eight different bank ranges.
 //
-// The exponent row of tile kt is fetched by wave kt % 8 alone.  Each wave's
-// wait counts its own instructions back from the newest, and one more of them
-// only makes that wait stricter.
+// Exponents travel four tiles at a time, one 256-byte row a wave (waves 4-7
+// repeat 0-3): fetched in the first tile of a group behind its barrier, when
+// every wave has the present group's bytes in registers, read in the last.
+// A wave's wait counts its own instructions back from the newest; the extra
+// one makes it stricter, never laxer.
 template <int BM>
 __device__ __forceinline__ int a8_swz(int kr) { return BM == 256 ? kr & 7 : (kr >> 1) & 3; }
 
@@ -489,18 +493,16 @@ __device__ __forceinline__ void gemm_tile_a8(int64_t M, int64_t N, int64_t K,
                                              const uint8_t *__restrict__ E, int64_t lde,
                                              const uint16_t *__restrict__ B, int64_t ldb, const Epi &epi,
                                              int64_t m0, int64_t n0, ZS_LDS char *const (&As)[kStages],
-                                             ZS_LDS char *const (&Es)[kStages],
-                                             ZS_LDS char *const (&Bs)[kStages])
+                                             ZS_LDS char *Es, ZS_LDS char *const (&Bs)[kStages])
 {
     static_assert(BM == 256 || BM == 128, "");
-    constexpr int TM = BM / 64, TN = BN / 128;
-    constexpr int NF = TM + TN, NMF = TM * TN;
-    constexpr int NRD = TM + 2 * TN;
+    constexpr int TM = BM / 128, TN = BN / 64;
+    constexpr int NMF = TM * TN, NRD = TM + 2 * TN, NQ = NMF < NRD ? NMF : NRD;
     constexpr int NIB = Op<BN, true>::NI;
     constexpr int D = 1 + NIB;
 
     const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
-    const int wm = (wave >> 2) * (BM / 2), wn = (wave & 3) * (BN / 4);
+    const int wm = (wave >> 1) * (BM / 4), wn = (wave & 1) * (BN / 2);
     const int fr = lane & 31, fh = lane >> 5;
 
     // A's 1 KB instruction I: k rows KPI I .. of BM bytes.  A stage of 128
@@ -516,7 +518,7 @@ __device__ __forceinline__ void gemm_tile_a8(int64_t M, int64_t N, int64_t K,
 #pragma unroll
     for (int n = 0; n < 2; ++n)
         vb[n] = n < NIB ? dma_offset<BN, true>(ldb, wave, lane, n) : 0u;
-    int fa_off[TM][2], fb_off[TN][2], fe_off[TM];
+    int fa_off[TM][2], fb_off[TN][2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         const int j = lane & 15, kr = 16 * s + 8 * fh + (j >> 1);
@@ -528,9 +530,7 @@ __device__ __forceinline__ void gemm_tile_a8(int64_t M, int64_t N, int64_t K,
         for (int j2 = 0; j2 < TN; ++j2)
             fb_off[j2][s] = frag_offset<BN, true>(wn + 32 * j2, s, lane);
     }
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-        fe_off[i] = wm + 32 * i + fr;
+    const int fe_off = wm + fr;
 
     f32x16 acc[TM][TN];
 #pragma unroll
@@ -552,16 +552,18 @@ __device__ __forceinline__ void gemm_tile_a8(int64_t M, int64_t N, int64_t K,
         for (int n = 0; n < NIB; ++n)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (ZS_LDS void *)(Bs[S] + (wave + kNW * n) * 1024),
                                                      16, vb[n], 0, 0, 0);
-        if (wave == (int)(kt & 7)) {
-            const __amdgpu_buffer_rsrc_t re = rsrc(E + kt * lde + m0, M - m0);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(re, (ZS_LDS void *)Es[S], 4, 4 * lane, 0, 0, 0);
-        }
+    };
+    // Exponent rows kt .. kt + 3 (past the last: the last again).
+    auto dma_exps = [&](int64_t kt) {
+        const int64_t r = kt + (wave & 3) < kt_n ? kt + (wave & 3) : kt_n - 1;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(E + r * lde + m0, M - m0),
+                                                 (ZS_LDS void *)(Es + (wave & 3) * 256), 4, 4 * lane, 0, 0,
+                                                 0);
     };
     typedef int i32x2 __attribute__((ext_vector_type(2)));
     i32x2 ra0[TM], ra1[TM];
     bf16x8 fb0[TN], fb1[TN];
-    uint32_t e0[TM];
-    float sc[TM];
+    uint32_t ex[kStages][TM];
     auto frags = [&](auto st, int s, i32x2 (&fa)[TM], bf16x8 (&fb)[TN]) {
         constexpr int S = decltype(st)::value;
 #pragma unroll
@@ -571,30 +573,28 @@ __device__ __forceinline__ void gemm_tile_a8(int64_t M, int64_t N, int64_t K,
         for (int j = 0; j < TN; ++j)
             fb[j] = frag_read<BN, true>(Bs[S], fb_off[j][s]);
     };
-    auto exps = [&](auto st) {
-        constexpr int S = decltype(st)::value;
+    auto exps = [&]() {
 #pragma unroll
-        for (int i = 0; i < TM; ++i)
-            e0[i] = *reinterpret_cast<const ZS_LDS uint8_t *>(Es[S] + fe_off[i]);
+        for (int r = 0; r < kStages; ++r)
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+                ex[r][i] = *reinterpret_cast<const ZS_LDS uint8_t *>(Es + 256 * r + fe_off + 32 * i);
     };
-    auto widen = [&](i32x2 w, float s) {
+    auto widen = [&](i32x2 w, uint32_t byte) {
         typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+        const float s = __uint_as_float(byte << 23);
         const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)w[0], s, false);
         const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)w[0], s, true);
         const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)w[1], s, false);
         const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)w[1], s, true);
         return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
     };
-    auto mma = [&](const i32x2 (&fa)[TM], const bf16x8 (&fb)[TN], int lo, int hi) {
+    auto mma = [&](const bf16x8 (&fa)[TM], const bf16x8 (&fb)[TN], int lo, int hi) {
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            if (i < lo || i >= hi)
-                continue;
-            const bf16x8 a = widen(fa[i], sc[i]);
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, fb[j], acc[i][j], 0, 0, 0);
-        }
+        for (int q = 0; q < NMF; ++q)
+            if (q >= lo && q < hi)
+                acc[q / TN][q % TN] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                    fa[q / TN], fb[q % TN], acc[q / TN][q % TN], 0, 0, 0);
     };
     auto wait_for = [&](int64_t kt1) {
         const int64_t after = kt_n - 1 - kt1;
@@ -605,34 +605,44 @@ __device__ __forceinline__ void gemm_tile_a8(int64_t M, int64_t N, int64_t K,
         else
             wait_vm_lgkm0<0>();
     };
-    auto take_exps = [&]() {
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-            sc[i] = __uint_as_float(e0[i] << 23);
-    };
-    auto tile = [&](auto st, int64_t kt) {
+    // Tile kt in stage S, the S-th of its group of four, as in gemm_tile.
+    auto tile = [&](auto st, auto steady, int64_t kt) {
         constexpr int S = decltype(st)::value;
+        constexpr bool STEADY = decltype(steady)::value != 0;
         constexpr int SN = (S + kStages - 1) % kStages, S1 = (S + 1) % kStages;
         __builtin_amdgcn_sched_barrier(0);
-        take_exps();
-        if (kt + kStages - 1 < kt_n)
+        bf16x8 fa[TM], fc[TM];
+        if (STEADY || kt + kStages - 1 < kt_n)
             dma(IC<SN>{}, kt + kStages - 1);
         frags(IC<S>{}, 1, ra1, fb1);
-        mma(ra0, fb0, 0, TM);
-        seq<NF, NMF, NRD, 0>();
-        mma(ra1, fb1, 0, TM / 2);
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+            fa[i] = widen(ra0[i], ex[S][i]);
+        mma(fa, fb0, 0, NMF);
+        seq<NQ, NMF, NRD, STEADY ? D : 0>();
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+            fc[i] = widen(ra1[i], ex[S][i]);
+        mma(fc, fb1, 0, NMF / 2);
         __builtin_amdgcn_sched_barrier(0);
-        wait_for(kt + 1);
+        if constexpr (STEADY)
+            wait_vm_lgkm0<2 * D>();
+        else
+            wait_for(kt + 1);
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
-        if (kt + 1 < kt_n) {
+        if (S == 0 && (STEADY || kt + kStages < kt_n))
+            dma_exps(kt + kStages);
+        if (STEADY || kt + 1 < kt_n) {
             frags(IC<S1>{}, 0, ra0, fb0);
-            exps(IC<S1>{});
+            if (S == kStages - 1)
+                exps();
         }
-        mma(ra1, fb1, TM / 2, TM);
-        seq<NF, NMF / 2, NRD, 0>();
+        mma(fc, fb1, NMF / 2, NMF);
+        seq<NQ, NMF - NMF / 2, NRD, 0>();
     };
     if (kt_n > 0) {
+        dma_exps(0);
         dma(IC<0>{}, 0);
         if (kt_n > 1)
             dma(IC<1>{}, 1);
@@ -641,15 +651,23 @@ __device__ __forceinline__ void gemm_tile_a8(int64_t M, int64_t N, int64_t K,
         wait_for(0);
         __builtin_amdgcn_s_barrier();
         frags(IC<0>{}, 0, ra0, fb0);
-        exps(IC<0>{});
-        for (int64_t kt = 0; kt < kt_n; kt += kStages) {
-            tile(IC<0>{}, kt);
+        exps();
+        int64_t kt = 0;
+        // groups whose tiles kt + 3 .. kt + 6 exist
+        for (; kt + 2 * kStages - 1 <= kt_n; kt += kStages) {
+            tile(IC<0>{}, IC<1>{}, kt);
+            tile(IC<1>{}, IC<1>{}, kt + 1);
+            tile(IC<2>{}, IC<1>{}, kt + 2);
+            tile(IC<3>{}, IC<1>{}, kt + 3);
+        }
+        for (; kt < kt_n; kt += kStages) {
+            tile(IC<0>{}, IC<0>{}, kt);
             if (kt + 1 < kt_n)
-                tile(IC<1>{}, kt + 1);
+                tile(IC<1>{}, IC<0>{}, kt + 1);
             if (kt + 2 < kt_n)
-                tile(IC<2>{}, kt + 2);
+                tile(IC<2>{}, IC<0>{}, kt + 2);
             if (kt + 3 < kt_n)
-                tile(IC<3>{}, kt + 3);
+                tile(IC<3>{}, IC<0>{}, kt + 3);
         }
     }
     epi.template tile32<TM, TN>(acc, m0 + wm, n0 + wn, M, N, lane);
@@ -665,13 +683,12 @@ __global__ __launch_bounds__(kGT) void saved_kernel(int64_t M, int64_t N, int64_
 {
     __shared__ __attribute__((aligned(1024))) char a0[BM * 32], a1[BM * 32], a2[BM * 32], a3[BM * 32];
     __shared__ __attribute__((aligned(1024))) char b0[BN * 64], b1[BN * 64], b2[BN * 64], b3[BN * 64];
-    __shared__ __attribute__((aligned(256))) char e0[256], e1[256], e2[256], e3[256];
+    __shared__ __attribute__((aligned(256))) char es[1024];
     ZS_LDS char *const As[kStages] = {(ZS_LDS char *)a0, (ZS_LDS char *)a1, (ZS_LDS char *)a2,
                                       (ZS_LDS char *)a3};
     ZS_LDS char *const Bs[kStages] = {(ZS_LDS char *)b0, (ZS_LDS char *)b1, (ZS_LDS char *)b2,
                                       (ZS_LDS char *)b3};
-    ZS_LDS char *const Es[kStages] = {(ZS_LDS char *)e0, (ZS_LDS char *)e1, (ZS_LDS char *)e2,
-                                      (ZS_LDS char *)e3};
+    ZS_LDS char *const Es = (ZS_LDS char *)es;
     const PlainEpi<OUT_BF16> epi{C, ldc};
     int64_t m0, n0;
     if (place<BM, BN>(tiles_m, tiles_n, n_big, m0, n0))
