@@ -401,26 +401,34 @@ __device__ __forceinline__ int total_tiles(const int64_t *off, int n_groups, int
 
 // C[r] = epilogue(A[r] B_e) for the rows r of every group e.  The grid is the
 // most tiles the row count allows; blocks past the groups' real tiles leave.
+// A group's last tile of at most BM / 2 rows runs as a half tile, and so does
+// every tile of a last wave that would fill at most half the CUs (two blocks
+// a tile, as for the plain product; the tile count is the device's to know).
 template <int BM, int BN, bool B_KOUTER>
 __global__ __launch_bounds__(kGT) void grouped_rows_kernel(const int64_t *__restrict__ off, int n_groups,
                                                            int64_t rows, int64_t N, int64_t K,
                                                            const uint16_t *__restrict__ A, int64_t lda,
                                                            const uint16_t *__restrict__ B, int64_t ldb,
-                                                           int64_t stride_b, EpiArgs args, int tiles_n)
+                                                           int64_t stride_b, EpiArgs args, int tiles_n,
+                                                           int cus)
 {
     const int tiles_m = total_tiles<BM>(off, n_groups, rows);
-    const int T = tiles_m * tiles_n;
-    if ((int)blockIdx.x >= T)
+    const int T = tiles_m * tiles_n, rem = T % cus;
+    const int n_big = BM == kBM && rem > 0 && rem <= cus / 2 ? T - rem : T;
+    const int b = blockIdx.x, blocks = n_big + 2 * (T - n_big);
+    if (b >= blocks)
         return;
     int tm, tn, e, t;
-    grouped(xcd_order(blockIdx.x, T), tiles_m, tiles_n, tm, tn);
+    const int h = b < n_big ? 0 : xcd_order(b - n_big, blocks - n_big);
+    grouped(b < n_big ? xcd_order(b, n_big) : n_big + h / 2, tiles_m, tiles_n, tm, tn);
     if (!find_tile<BM>(off, n_groups, rows, tm, e, t))
         return;
     int64_t lo, hi;
     group_range(off, e, rows, lo, hi);
-    const int64_t M = hi - lo, m0 = (int64_t)t * BM, n0 = (int64_t)tn * BN;
-    if (t < 0 || m0 >= M)  // only with offsets that decrease
+    const int64_t M = hi - lo, m0 = (int64_t)t * BM + (h & 1) * (BM / 2), n0 = (int64_t)tn * BN;
+    if (t < 0 || m0 >= M)  // an empty half, or offsets that decrease
         return;
+    const bool half = BM == kBM && (b >= n_big || M - m0 <= BM / 2);
     args.C = static_cast<char *>(args.C) + lo * args.ldc * (args.c_bf16 ? 2 : 4);
     if (args.residual)
         args.residual = static_cast<const char *>(args.residual) + lo * args.ldr * (args.r_bf16 ? 2 : 4);
@@ -431,25 +439,38 @@ __global__ __launch_bounds__(kGT) void grouped_rows_kernel(const int64_t *__rest
     if constexpr (B_KOUTER) {
         ZS_STAGES(BM, BN);
         const LayerEpi epi{args, ZS_CORNER};
-        gemm_tile<BM, BN, false, true>(M, N, K, A, lda, B, ldb, epi, m0, n0, As, Bs);
+        if (half)
+            gemm_tile<kBM / 2, BN, false, true>(M, N, K, A, lda, B, ldb, epi, m0, n0, As, Bs);
+        else
+            gemm_tile<BM, BN, false, true>(M, N, K, A, lda, B, ldb, epi, m0, n0, As, Bs);
     } else {
         ZS_PAIRS(BM, BN);
         const LayerEpi epi{args, ZS_CORNER_KP((BM < BN ? BM : BN) * 64)};
-        gemm_tile_kp<BM, BN>(M, N, K, A, lda, B, ldb, epi, m0, n0, ZS_P);
+        if (half)
+            gemm_tile_kp<kBM / 2, BN>(M, N, K, A, lda, B, ldb, epi, m0, n0, ZS_P);
+        else
+            gemm_tile_kp<BM, BN>(M, N, K, A, lda, B, ldb, epi, m0, n0, ZS_P);
     }
 }
 
 // C_e = sum over the rows r of group e of A[r]^T B[r]; an empty group's C_e is
 // zeros.
 template <int BM, int BN, bool OUT_BF16>
-__global__ __launch_bounds__(kGT) void grouped_depth_kernel(const int64_t *__restrict__ off, int64_t rows,
-                                                            int64_t M, int64_t N,
-                                                            const uint16_t *__restrict__ A, int64_t lda,
-                                                            const uint16_t *__restrict__ B, int64_t ldb,
-                                                            void *__restrict__ C, int64_t ldc,
-                                                            int64_t stride_c, int tiles_m, int tiles_n)
+__global__ __launch_bounds__(kGT, BM == BN ? 2 : 4)
+void grouped_depth_kernel(const int64_t *__restrict__ off, int64_t rows, int64_t M, int64_t N,
+                          const uint16_t *__restrict__ A, int64_t lda, const uint16_t *__restrict__ B,
+                          int64_t ldb, void *__restrict__ C, int64_t ldc, int64_t stride_c, int tiles_m,
+                          int tiles_n)
 {
-    ZS_STAGES(BM, BN);
+    constexpr int ST = BM == BN ? 4 : 3;
+    __shared__ __attribute__((aligned(1024))) char a0[BM * 64], a1[BM * 64], a2[BM * 64];
+    __shared__ __attribute__((aligned(1024))) char b0[BN * 64], b1[BN * 64], b2[BN * 64];
+    __shared__ __attribute__((aligned(1024))) char a3[ST > 3 ? BM * 64 : 16], b3[ST > 3 ? BN * 64 : 16];
+    ZS_LDS char *As[ST], *Bs[ST];
+    As[0] = (ZS_LDS char *)a0, As[1] = (ZS_LDS char *)a1, As[2] = (ZS_LDS char *)a2;
+    Bs[0] = (ZS_LDS char *)b0, Bs[1] = (ZS_LDS char *)b1, Bs[2] = (ZS_LDS char *)b2;
+    if constexpr (ST > 3)
+        As[ST - 1] = (ZS_LDS char *)a3, Bs[ST - 1] = (ZS_LDS char *)b3;
     const int per = tiles_m * tiles_n;
     const int i = xcd_order(blockIdx.x, gridDim.x);
     const int e = i / per;
@@ -457,7 +478,7 @@ __global__ __launch_bounds__(kGT) void grouped_depth_kernel(const int64_t *__res
     grouped(i - e * per, tiles_m, tiles_n, tm, tn);
     int64_t lo, hi;
     group_range(off, e, rows, lo, hi);
-    const PlainEpi<OUT_BF16> epi{static_cast<char *>(C) + e * stride_c * (OUT_BF16 ? 2 : 4), ldc};
+    const PlainEpi<OUT_BF16, true> epi{static_cast<char *>(C) + e * stride_c * (OUT_BF16 ? 2 : 4), ldc};
     gemm_tile<BM, BN, true, true>(M, N, hi - lo, A + lo * lda, lda, B + lo * ldb, ldb, epi,
                                   (int64_t)tm * BM, (int64_t)tn * BN, As, Bs);
 }
@@ -689,7 +710,7 @@ __global__ __launch_bounds__(kGT) void saved_kernel(int64_t M, int64_t N, int64_
     ZS_LDS char *const Bs[kStages] = {(ZS_LDS char *)b0, (ZS_LDS char *)b1, (ZS_LDS char *)b2,
                                       (ZS_LDS char *)b3};
     ZS_LDS char *const Es = (ZS_LDS char *)es;
-    const PlainEpi<OUT_BF16> epi{C, ldc};
+    const PlainEpi<OUT_BF16, true> epi{C, ldc};
     int64_t m0, n0;
     if (place<BM, BN>(tiles_m, tiles_n, n_big, m0, n0))
         gemm_tile_a8<BM, BN>(M, N, K, A, lda, E, lde, B, ldb, epi, m0, n0, As, Es, Bs);
@@ -956,11 +977,12 @@ zero_status grouped_rows_run(int32_t n_groups, const int64_t *offsets, int64_t r
                                                      cu_count();
     const int bm = small ? 128 : kBM, bn = small ? 128 : kBN;
     const int tn = (int)((N + bn - 1) / bn);
-    const dim3 grid((unsigned)(most_tiles(n_groups, rows, bm) * tn));
+    const int cus = cu_count();
+    const dim3 grid((unsigned)(most_tiles(n_groups, rows, bm) * tn + (small ? 0 : cus / 2)));
     (void)hipGetLastError();
 #define ZS_ROWS(BM_, BN_, BO)                                                                      \
     hipLaunchKernelGGL((grouped_rows_kernel<BM_, BN_, BO>), grid, dim3(kGT), 0, s, offsets, n_groups, \
-                       rows, N, K, A, lda, B, ldb, stride_b, a, tn)
+                       rows, N, K, A, lda, B, ldb, stride_b, a, tn, cus)
     if (b_order == ZERO_K_OUTER) {
         if (small)
             ZS_ROWS(128, 128, true);
@@ -1006,24 +1028,32 @@ zero_status grouped_depth_run(int32_t n_groups, const int64_t *offsets, int64_t 
 {
     if (M == 0 || N == 0)
         return ZERO_OK;
-    const bool small = 2 * n_groups * ((M + kBM - 1) / kBM) * ((N + kBN - 1) / kBN) <= cu_count();
-    const int b = small ? 128 : kBM;
-    const int tm = (int)((M + b - 1) / b), tn = (int)((N + b - 1) / b);
+    // Two 256 x 128 blocks a CU, three stages each, where the sums are short
+    // (under 512 rows a group on average) and the stores weigh: one block's
+    // stores run under the other's products.  64 groups of 256 rows, 2048 x
+    // 1408: 212 us against 220 with 256 x 256 tiles; 32 of 512: 137 against 145;
+    // but 8 of 1024, 4096 x 14336: 1032 against 986, and of 2048 1988 against
+    // 1752.  Likewise where 256 x 256 tiles would leave half the CUs idle (4
+    // groups of 300 rows, 512 x 512: 13.4 against 17.4 us).
+    const int64_t wide = n_groups * ((M + kBM - 1) / kBM) * ((N + kBN - 1) / kBN);
+    const bool narrow = rows / n_groups < 512 || 2 * wide <= cu_count();
+    const int bn = narrow ? kBN / 2 : kBN;
+    const int tm = (int)((M + kBM - 1) / kBM), tn = (int)((N + bn - 1) / bn);
     const dim3 grid((unsigned)((int64_t)n_groups * tm * tn));
     (void)hipGetLastError();
-#define ZS_DEPTH(B_, BF)                                                                           \
-    hipLaunchKernelGGL((grouped_depth_kernel<B_, B_, BF>), grid, dim3(kGT), 0, s, offsets, rows, M, N, A, \
-                       lda, B, ldb, C, ldc, stride_c, tm, tn)
+#define ZS_DEPTH(BN_, BF)                                                                          \
+    hipLaunchKernelGGL((grouped_depth_kernel<kBM, BN_, BF>), grid, dim3(kGT), 0, s, offsets, rows, M, N, \
+                       A, lda, B, ldb, C, ldc, stride_c, tm, tn)
     if (c_dtype == ZERO_BF16) {
-        if (small)
-            ZS_DEPTH(128, true);
+        if (narrow)
+            ZS_DEPTH(kBN / 2, true);
         else
-            ZS_DEPTH(kBM, true);
+            ZS_DEPTH(kBN, true);
     } else {
-        if (small)
-            ZS_DEPTH(128, false);
+        if (narrow)
+            ZS_DEPTH(kBN / 2, false);
         else
-            ZS_DEPTH(kBM, false);
+            ZS_DEPTH(kBN, false);
     }
 #undef ZS_DEPTH
     return launched("gemm_grouped_depth");
