@@ -172,14 +172,15 @@ __device__ __forceinline__ int xcd_order(int i, int n)
     return x * per + (x < rem ? x : rem) + i / 8;
 }
 
-// Grouped order: big tile `logical` -> (tile row, tile column), kGroupM tile
+// Grouped order: big tile `logical` -> (tile row, tile column), `group` tile
 // rows at a time.
-__device__ __forceinline__ void grouped(int logical, int tiles_m, int tiles_n, int &tm, int &tn)
+__device__ __forceinline__ void grouped(int logical, int tiles_m, int tiles_n, int &tm, int &tn,
+                                        int group = kGroupM)
 {
-    const int gsz = kGroupM * tiles_n;
+    const int gsz = group * tiles_n;
     const int g = logical / gsz;
-    const int first_m = g * kGroupM;
-    const int gm = tiles_m - first_m < kGroupM ? tiles_m - first_m : kGroupM;
+    const int first_m = g * group;
+    const int gm = tiles_m - first_m < group ? tiles_m - first_m : group;
     const int in_g = logical - g * gsz;
     tm = first_m + in_g % gm;
     tn = in_g / gm;

@@ -37,7 +37,7 @@ struct EpiArgs {
     int64_t ldc, ldr, ldz, ldzs, ldo, ldos;
     int32_t act;
     bool c_bf16, bias_bf16, r_bf16;
-    bool c_vec, r_vec, z_vec;  // 16-byte aligned rows
+    bool vec;  // 16-byte aligned rows in every matrix but the checkpoints
 };
 
 // y = act(z) + residual with z = sum + bias, on the way from a wave's
@@ -110,73 +110,160 @@ struct LayerEpi {
         }
     }
 
-    template <int CW>
-    __device__ __forceinline__ void rows32(int64_t row0, int64_t col0, int64_t M, int64_t N, int lane) const
+    __device__ __forceinline__ float bf16_at(const void *q, int64_t i) const
     {
-        constexpr int LPR = CW / 8, RPI = 64 / LPR;  // lanes per row, rows per pass
-        wave_lds_order();
-        const int c = 8 * (lane % LPR);
-        const int64_t col = col0 + c;
-        const int n = (int)(N - col < 8 ? N - col : 8);
-        if (row0 < M && n > 0) {
+        return __uint_as_float((uint32_t)static_cast<const uint16_t *>(q)[i] << 16);
+    }
+
+    // Eight residual values as loaded: bf16 in lo, fp32 in lo and hi.
+    struct Res {
+        uint4 lo, hi;
+    };
+    __device__ __forceinline__ Res load_residual(int64_t i) const
+    {
+        Res r = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+        if (p.r_bf16) {
+            r.lo = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.residual) + i);
+        } else {
+            r.lo = *reinterpret_cast<const uint4 *>(static_cast<const float *>(p.residual) + i);
+            r.hi = *reinterpret_cast<const uint4 *>(static_cast<const float *>(p.residual) + i + 4);
+        }
+        return r;
+    }
+
+    // 32 whole rows x CW columns with every access 16 bytes: RPI rows a pass,
+    // a lane's 8 columns of one.  The passes are a loop, so that the epilogue
+    // stays a few KB of code (unrolled, its 28000 instructions cost more than
+    // they did), and the residual is fetched one pass ahead.
+    template <int CW, int ACT>
+    __device__ __forceinline__ void rows_fast(int64_t row0, int64_t col0, Res next, int lane) const
+    {
+        constexpr int LPR = CW / 8, RPI = 64 / LPR, NP = 32 / RPI;
+        int64_t row = row0 + lane / LPR;
+        const int64_t col = col0 + 8 * (lane % LPR);
+        ZS_LDS float *l = lds + (lane / LPR) * (CW + 4) + 8 * (lane % LPR);
+#pragma unroll 1
+        for (int it = 0; it < NP; ++it, row += RPI, l += RPI * (CW + 4)) {
+            const Res cur = next;
+            if (p.residual && it + 1 < NP)
+                next = load_residual((row + RPI) * p.ldr + col);
+            ZS_LDS f32x4 *q = reinterpret_cast<ZS_LDS f32x4 *>(l);
+            const f32x4 lo = q[0], hi = q[1];
+            float x[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            if (p.z && !p.z_scales)
+                store8(p.z, true, row * p.ldz + col, true, 8, x);
 #pragma unroll
-            for (int it = 0; it < 32 / RPI; ++it) {
-                const int r = it * RPI + lane / LPR;
-                const int64_t row = row0 + r;
-                if (row >= M)
-                    break;
-                ZS_LDS f32x4 *q = reinterpret_cast<ZS_LDS f32x4 *>(lds + r * (CW + 4) + c);
-                const f32x4 lo = q[0], hi = q[1];
-                float x[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-                if (p.z && !p.z_scales)
-                    store8(p.z, true, row * p.ldz + col, p.z_vec && n == 8, n, x);
-                by_act(p.act, [&](auto a) {
+            for (int k = 0; k < 8; ++k)
+                x[k] = act<ACT>(x[k]);
+            if (p.residual) {
+                float y[8];
+                if (p.r_bf16) {
+                    widen8(cur.lo, y);
+                } else {
+                    const uint32_t w[8] = {cur.lo.x, cur.lo.y, cur.lo.z, cur.lo.w,
+                                           cur.hi.x, cur.hi.y, cur.hi.z, cur.hi.w};
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        x[k] = act<decltype(a)::value>(x[k]);
-                });
-                if (p.residual) {
-                    float y[8];
-                    load8(p.residual, p.r_bf16, row * p.ldr + col, p.r_vec && n == 8, n, y);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        x[k] += y[k];
+                        y[k] = __uint_as_float(w[k]);
                 }
-                store8(p.C, p.c_bf16, row * p.ldc + col, p.c_vec && n == 8, n, x);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    x[k] += y[k];
+            }
+            store8(p.C, p.c_bf16, row * p.ldc + col, true, 8, x);
+            if (p.o) {
+                if (p.c_bf16)
+                    widen8(make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                                      pack_bf16(x[6], x[7])),
+                           x);
+                q[0] = f32x4{x[0], x[1], x[2], x[3]};
+                q[1] = f32x4{x[4], x[5], x[6], x[7]};
             }
         }
+    }
+
+    // The same element by element, for edges and unaligned matrices; a wave
+    // still covers neighbouring columns.
+    template <int CW>
+    __device__ __forceinline__ void rows_slow(int64_t row0, int64_t col0, int64_t M, int64_t N, int lane) const
+    {
+#pragma unroll 1
+        for (int e = lane; e < 32 * CW; e += 64) {
+            const int r = e / CW, c = e % CW;
+            const int64_t row = row0 + r, col = col0 + c;
+            if (row >= M || col >= N)
+                continue;
+            float x = lds[r * (CW + 4) + c];
+            if (p.z && !p.z_scales)
+                static_cast<uint16_t *>(p.z)[row * p.ldz + col] = (uint16_t)pack_bf16(x, x);
+            by_act(p.act, [&](auto a) { x = act<decltype(a)::value>(x); });
+            if (p.residual)
+                x += p.r_bf16 ? bf16_at(p.residual, row * p.ldr + col)
+                              : static_cast<const float *>(p.residual)[row * p.ldr + col];
+            if (p.c_bf16) {
+                const uint32_t h = pack_bf16(x, x);
+                static_cast<uint16_t *>(p.C)[row * p.ldc + col] = (uint16_t)h;
+                x = __uint_as_float(h << 16);
+            } else {
+                static_cast<float *>(p.C)[row * p.ldc + col] = x;
+            }
+            if (p.o)
+                lds[r * (CW + 4) + c] = x;
+        }
+    }
+
+    template <int CW>
+    __device__ __forceinline__ bool whole_rows(int64_t row0, int64_t col0, int64_t M, int64_t N) const
+    {
+        return p.vec && row0 + 32 <= M && col0 + CW <= N;
+    }
+
+    template <int CW>
+    __device__ __forceinline__ Res first_residual(int64_t row0, int64_t col0, int64_t M, int64_t N,
+                                                  int lane) const
+    {
+        if (!p.residual || !whole_rows<CW>(row0, col0, M, N))
+            return Res{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+        return load_residual((row0 + lane / (CW / 8)) * p.ldr + col0 + 8 * (lane % (CW / 8)));
+    }
+
+    // z of 32 rows x CW columns is in LDS.
+    template <int CW>
+    __device__ __forceinline__ void rows32(int64_t row0, int64_t col0, int64_t M, int64_t N, Res first,
+                                           int lane) const
+    {
+        wave_lds_order();
+        if (row0 >= M || col0 >= N)
+            return;
         if (p.z_scales)
             encode<CW>(static_cast<uint8_t *>(p.z), p.ldz, p.z_scales, p.ldzs, row0, col0, M, N, lane);
+        if (whole_rows<CW>(row0, col0, M, N))
+            by_act(p.act, [&](auto a) { rows_fast<CW, decltype(a)::value>(row0, col0, first, lane); });
+        else
+            rows_slow<CW>(row0, col0, M, N, lane);
+        // C in 8 bits is coded from C as stored, so it is what coding C
+        // afterwards would give.
         if (p.o) {
-            // C in 8 bits is coded from C as stored, so it is what coding C
-            // afterwards would give.
-            wave_lds_order();
-            if (row0 < M && n > 0) {
-#pragma unroll
-                for (int it = 0; it < 32 / RPI; ++it) {
-                    const int r = it * RPI + lane / LPR;
-                    const int64_t row = row0 + r;
-                    if (row >= M)
-                        break;
-                    float x[8];
-                    load8(p.C, p.c_bf16, row * p.ldc + col, p.c_vec && n == 8, n, x);
-                    ZS_LDS f32x4 *q = reinterpret_cast<ZS_LDS f32x4 *>(lds + r * (CW + 4) + c);
-                    q[0] = f32x4{x[0], x[1], x[2], x[3]};
-                    q[1] = f32x4{x[4], x[5], x[6], x[7]};
-                }
-            }
             wave_lds_order();
             encode<CW>(p.o, p.ldo, p.o_scales, p.ldos, row0, col0, M, N, lane);
         }
         wave_lds_order();
     }
 
-    __device__ __forceinline__ float bias_at(int64_t col, int64_t N) const
+    // The bias of TN columns W apart, the loads side by side.
+    template <int TN, int W>
+    __device__ __forceinline__ void load_bias(int64_t col, int64_t N, float (&b)[TN]) const
     {
-        if (!p.bias || col >= N)
-            return 0.0f;
-        return p.bias_bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t *>(p.bias)[col] << 16)
-                           : static_cast<const float *>(p.bias)[col];
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            b[j] = 0.0f;
+        if (!p.bias)
+            return;
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            const int64_t c = col + W * j < N ? col + W * j : N - 1;
+            b[j] = p.bias_bf16 ? bf16_at(p.bias, c) : static_cast<const float *>(p.bias)[c];
+        }
     }
 
     // Rows 32 I .. of the wave's tile; by recursion, so that every accumulator
@@ -188,12 +275,13 @@ struct LayerEpi {
         if constexpr (I < TM) {
             constexpr int CW = 32 * TN;
             const int fr = lane & 31, fh = lane >> 5;
+            const Res first = first_residual<CW>(row0 + 32 * I, col0, M, N, lane);
 #pragma unroll
             for (int j = 0; j < TN; ++j)
 #pragma unroll
                 for (int v = 0; v < 16; ++v)
                     lds[(8 * (v >> 2) + 4 * fh + (v & 3)) * (CW + 4) + 32 * j + fr] = acc[I][j][v] + b[j];
-            rows32<CW>(row0 + 32 * I, col0, M, N, lane);
+            rows32<CW>(row0 + 32 * I, col0, M, N, first, lane);
             step32<I + 1>(acc, b, row0, col0, M, N, lane);
         }
     }
@@ -205,6 +293,7 @@ struct LayerEpi {
         if constexpr (I < TM) {
             constexpr int CW = 16 * TN;
             const int r16 = lane & 15, g = lane >> 4;
+            const Res first = first_residual<CW>(row0 + 16 * I, col0, M, N, lane);
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -212,7 +301,7 @@ struct LayerEpi {
 #pragma unroll
                     for (int v = 0; v < 4; ++v)
                         lds[(16 * h + 4 * g + v) * (CW + 4) + 16 * j + r16] = acc[I + h][j][v] + b[j];
-            rows32<CW>(row0 + 16 * I, col0, M, N, lane);
+            rows32<CW>(row0 + 16 * I, col0, M, N, first, lane);
             step16<I + 2>(acc, b, row0, col0, M, N, lane);
         }
     }
@@ -221,11 +310,9 @@ struct LayerEpi {
     __device__ __forceinline__ void tile32(const f32x16 (&acc)[TM][TN], int64_t row0, int64_t col0,
                                            int64_t M, int64_t N, int lane) const
     {
-        __syncthreads();  // every wave is done with the K loop's LDS
         float b[TN];
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-            b[j] = bias_at(col0 + 32 * j + (lane & 31), N);
+        load_bias<TN, 32>(col0 + (lane & 31), N, b);
+        __syncthreads();  // every wave is done with the K loop's LDS
         step32<0>(acc, b, row0, col0, M, N, lane);
     }
 
@@ -233,11 +320,9 @@ struct LayerEpi {
     __device__ __forceinline__ void tile16(const f32x4 (&acc)[TM][TN], int64_t row0, int64_t col0,
                                            int64_t M, int64_t N, int lane) const
     {
-        __syncthreads();
         float b[TN];
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-            b[j] = bias_at(col0 + 16 * j + (lane & 15), N);
+        load_bias<TN, 16>(col0 + (lane & 15), N, b);
+        __syncthreads();
         step16<0>(acc, b, row0, col0, M, N, lane);
     }
 };
@@ -345,65 +430,94 @@ __device__ __forceinline__ void group_range(const int64_t *off, int e, int64_t r
     hi = hi < lo ? lo : hi > rows ? rows : hi;
 }
 
-// A group's tiles of BM rows, lane `lane` taking group c + lane (0 past the
-// last), and their inclusive sum over the lanes.
-template <int BM>
-__device__ __forceinline__ int lane_tiles(const int64_t *off, int n_groups, int c, int64_t rows, int lane,
-                                          int &sum)
+// Inclusive sum over the 64 lanes, in registers: within rows of 16 lanes, then
+// rows 0 and 2 into 1 and 3, then the lower half into the upper.  (Six
+// exchanges through LDS would cost more than the lookup's loads.)
+__device__ __forceinline__ int lane_sum(int x)
 {
+#define ZS_DPP(CTRL, ROWS) x += __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xf, false)
+    ZS_DPP(0x111, 0xf);  // row_shr:1
+    ZS_DPP(0x112, 0xf);
+    ZS_DPP(0x114, 0xf);
+    ZS_DPP(0x118, 0xf);
+    ZS_DPP(0x142, 0xa);  // row_bcast:15
+    ZS_DPP(0x143, 0xc);  // row_bcast:31
+#undef ZS_DPP
+    return x;
+}
+
+// Tiles of BM rows of group c + lane (0 past the last), and their running sum
+// over the lanes.
+template <int BM>
+__device__ __forceinline__ int lane_tiles(const int64_t *off, int n_groups, int c, int64_t rows, int &sum)
+{
+    const int lane = threadIdx.x & 63;
     int64_t lo = 0, hi = 0;
     if (c + lane < n_groups)
         group_range(off, c + lane, rows, lo, hi);
-    const int t = (int)((hi - lo + BM - 1) / BM);
-    sum = t;
-#pragma unroll
-    for (int s = 1; s < 64; s *= 2) {
-        const int x = __shfl_up(sum, s, 64);
-        sum += lane >= s ? x : 0;
-    }
+    const int t = (int)((uint64_t)(hi - lo + BM - 1) / BM);
+    sum = lane_sum(t);
     return t;
 }
 
-// Row tile `want` of all groups' tiles in order: its group and its number in
-// the group.  Every wave looks it up by itself, 64 groups at a time.
+struct Place {
+    int e, tile, row_tiles;  // group, tile number in the group, its row tiles
+    int half;                // -1: whole, or 0 / 1 of a tile split in two
+};
+
+// Which tile this block computes, looked up by every wave for itself.  Tiles
+// are numbered group after group; each XCD takes a contiguous run of them, so
+// that its L2 sees one stretch of weights, and a last wave of at most half
+// the CUs is split into half tiles, as in the plain product -- only that the
+// number of tiles is the device's to know.  The lookup is on every block's
+// path: with 64-bit scans through LDS it cost 8 us a block.
 template <int BM>
-__device__ __forceinline__ bool find_tile(const int64_t *off, int n_groups, int64_t rows, int want, int &e,
-                                          int &tile)
+__device__ __forceinline__ bool find_tile(const int64_t *off, int n_groups, int64_t rows, int tiles_n, int cus,
+                                          Place &p)
 {
-    const int lane = threadIdx.x & 63;
+    int sum;
+    int t = lane_tiles<BM>(off, n_groups, 0, rows, sum);
+    int total = __builtin_amdgcn_readlane(sum, 63);
+    for (int c = 64; c < n_groups; c += 64) {
+        int more;
+        lane_tiles<BM>(off, n_groups, c, rows, more);
+        total += __builtin_amdgcn_readlane(more, 63);
+    }
+    const int T = total * tiles_n, b = blockIdx.x, rem = (int)((unsigned)T % (unsigned)cus);
+    const int whole = BM == kBM && rem <= cus / 2 ? T - rem : T;
+    const int blocks = whole + 2 * (T - whole);
+    if (b >= blocks)
+        return false;
+    int want;
+    if (b < whole) {
+        want = xcd_order(b, whole);
+        p.half = -1;
+    } else {
+        const int h = xcd_order(b - whole, blocks - whole);
+        want = whole + h / 2;
+        p.half = h & 1;
+    }
     int before = 0;
-    for (int c = 0; c < n_groups; c += 64) {
-        int sum;
-        const int t = lane_tiles<BM>(off, n_groups, c, rows, lane, sum);
-        const uint64_t past = __ballot(before + sum > want);
+    for (int c = 0;;) {
+        const uint64_t past = __ballot((before + sum) * tiles_n > want);
         if (past) {
             const int l = __builtin_ctzll(past);
-            e = c + l;
-            tile = want - before - (__builtin_amdgcn_readlane(sum, l) - __builtin_amdgcn_readlane(t, l));
-            return true;
+            p.e = c + l;
+            p.row_tiles = __builtin_amdgcn_readlane(t, l);
+            p.tile = want - (before + __builtin_amdgcn_readlane(sum, l) - p.row_tiles) * tiles_n;
+            return p.tile >= 0;
         }
         before += __builtin_amdgcn_readlane(sum, 63);
+        if ((c += 64) >= n_groups)
+            return false;
+        t = lane_tiles<BM>(off, n_groups, c, rows, sum);
     }
-    return false;
 }
 
-template <int BM>
-__device__ __forceinline__ int total_tiles(const int64_t *off, int n_groups, int64_t rows)
-{
-    int n = 0;
-    for (int c = 0; c < n_groups; c += 64) {
-        int sum;
-        lane_tiles<BM>(off, n_groups, c, rows, threadIdx.x & 63, sum);
-        n += __builtin_amdgcn_readlane(sum, 63);
-    }
-    return n;
-}
+constexpr int kRunM = 6;
 
 // C[r] = epilogue(A[r] B_e) for the rows r of every group e.  The grid is the
-// most tiles the row count allows; blocks past the groups' real tiles leave.
-// A group's last tile of at most BM / 2 rows runs as a half tile, and so does
-// every tile of a last wave that would fill at most half the CUs (two blocks
-// a tile, as for the plain product; the tile count is the device's to know).
+// most blocks the row count allows; those past the real tiles leave.
 template <int BM, int BN, bool B_KOUTER>
 __global__ __launch_bounds__(kGT) void grouped_rows_kernel(const int64_t *__restrict__ off, int n_groups,
                                                            int64_t rows, int64_t N, int64_t K,
@@ -412,23 +526,21 @@ __global__ __launch_bounds__(kGT) void grouped_rows_kernel(const int64_t *__rest
                                                            int64_t stride_b, EpiArgs args, int tiles_n,
                                                            int cus)
 {
-    const int tiles_m = total_tiles<BM>(off, n_groups, rows);
-    const int T = tiles_m * tiles_n, rem = T % cus;
-    const int n_big = BM == kBM && rem > 0 && rem <= cus / 2 ? T - rem : T;
-    const int b = blockIdx.x, blocks = n_big + 2 * (T - n_big);
-    if (b >= blocks)
+    Place p;
+    if (!find_tile<BM>(off, n_groups, rows, tiles_n, cus, p))
         return;
-    int tm, tn, e, t;
-    const int h = b < n_big ? 0 : xcd_order(b - n_big, blocks - n_big);
-    grouped(b < n_big ? xcd_order(b, n_big) : n_big + h / 2, tiles_m, tiles_n, tm, tn);
-    if (!find_tile<BM>(off, n_groups, rows, tm, e, t))
-        return;
+    // A group's row tiles walk its columns together, in equal runs of at most
+    // kRunM, so that one fetch of a W column serves all of them.
+    int tm, tn;
+    const int e = p.e, runs = (p.row_tiles + kRunM - 1) / kRunM;
+    grouped(p.tile, p.row_tiles, tiles_n, tm, tn, (p.row_tiles + runs - 1) / runs);
     int64_t lo, hi;
     group_range(off, e, rows, lo, hi);
-    const int64_t M = hi - lo, m0 = (int64_t)t * BM + (h & 1) * (BM / 2), n0 = (int64_t)tn * BN;
-    if (t < 0 || m0 >= M)  // an empty half, or offsets that decrease
+    const int64_t M = hi - lo, n0 = (int64_t)tn * BN;
+    const int64_t m0 = (int64_t)tm * BM + (p.half > 0 ? BM / 2 : 0);
+    if (m0 >= M)  // an empty half, or offsets that decrease
         return;
-    const bool half = BM == kBM && (b >= n_big || M - m0 <= BM / 2);
+    const bool half = BM == kBM && (p.half >= 0 || M - m0 <= BM / 2);
     args.C = static_cast<char *>(args.C) + lo * args.ldc * (args.c_bf16 ? 2 : 4);
     if (args.residual)
         args.residual = static_cast<const char *>(args.residual) + lo * args.ldr * (args.r_bf16 ? 2 : 4);
@@ -765,7 +877,7 @@ EpiArgs epi_args(const zero_epilogue *ep, void *C, int64_t ldc, int32_t c_dtype)
     a.C = C;
     a.ldc = ldc;
     a.c_bf16 = c_dtype == ZERO_BF16;
-    a.c_vec = vec16(C, ldc, bytes_of(c_dtype));
+    a.vec = vec16(C, ldc, bytes_of(c_dtype));
     if (!ep)
         return a;
     a.act = ep->act;
@@ -774,15 +886,17 @@ EpiArgs epi_args(const zero_epilogue *ep, void *C, int64_t ldc, int32_t c_dtype)
     a.residual = ep->residual;
     a.ldr = ep->ldr;
     a.r_bf16 = ep->residual_dtype == ZERO_BF16;
-    a.r_vec = ep->residual && vec16(ep->residual, ep->ldr, bytes_of(ep->residual_dtype));
+    if (ep->residual)
+        a.vec = a.vec && vec16(ep->residual, ep->ldr, bytes_of(ep->residual_dtype));
     if (ep->preact) {
         a.z = ep->preact->data;
         a.ldz = ep->preact->ld;
         if (ep->preact->format == ZERO_SAVED_E4M3) {
             a.z_scales = ep->preact->scales;
             a.ldzs = ep->preact->ld_scales;
+        } else {
+            a.vec = a.vec && vec16(a.z, a.ldz, 2);
         }
-        a.z_vec = vec16(a.z, a.ldz, 2);
     }
     if (ep->output) {
         a.o = static_cast<uint8_t *>(ep->output->data);
