@@ -16,8 +16,9 @@ __all__ = ["zs", "build"]
 
 
 def __getattr__(name):
-    if name == "zs":
-        return importlib.import_module("._lib", __name__)
-    if name == "build":
-        return importlib.import_module(".build", __name__)
-    raise AttributeError(name)
+    modules = {"zs": "._lib", "build": ".build"}
+    if name not in modules:
+        raise AttributeError(name)
+    module = importlib.import_module(modules[name], __name__)
+    globals()[name] = module        # looked up once
+    return module

@@ -152,8 +152,7 @@ class _Saved(ctypes.Structure):
 
 
 class _Epilogue(ctypes.Structure):
-    _fields_ = [("bias", _P), ("residual", _P), ("ldr", _I64), ("preact", ctypes.POINTER(_Saved)),
-                ("output", ctypes.POINTER(_Saved)), ("bias_dtype", _I32), ("residual_dtype", _I32),
+    _fields_ = [("bias", _P), ("residual", _P), ("ldr", _I64), ("preact", _P), ("output", _P), ("bias_dtype", _I32), ("residual_dtype", _I32),
                 ("act", _I32)]
 
 
@@ -805,21 +804,43 @@ def fsdp_linear_backward(layout: Layout, unit: int, w_shards, batch: int, x, dy,
 
 # ------------------------------------------------------- layer operators --
 
-def _one_device(stream, *tensors) -> None:
-    """The tensors of a call share a device, and it is the one that the
-    default stream (the current device's) belongs to."""
-    at = None
-    for x in tensors:
-        if x is None or x.__class__ is int or not hasattr(x, "get_device"):
-            continue
-        d = x.get_device()
-        if at is None:
-            at = d
-        elif d != at:
-            raise ValueError(f"tensors of one call on two devices ({at} and {d})")
-    if at is not None and at >= 0 and stream is None and at != torch.cuda.current_device():
-        raise ValueError(f"tensors on device {at}, but the current device is "
-                         f"{torch.cuda.current_device()}: switch to it, or give a stream of it")
+class _Call:
+    """The buffers of one call: each checked like _need and turned into its
+    address, all on one device, which is the one that the default stream
+    belongs to.  Small calls last as long as their arguments' checks, so a
+    good tensor passes in a handful of lookups."""
+    __slots__ = ("device",)
+
+    def __init__(self):
+        self.device = None
+
+    def __call__(self, x, what: str, count: Optional[int], kind: str) -> Optional[int]:
+        if x is None or x.__class__ is int:
+            return x
+        if not (count is not None and x.is_cuda and x.dtype in _DTYPES[kind] and x.numel() >= count
+                and x.is_contiguous()):
+            _need(x, what, count, kind)
+        if self.device is None:
+            self.device = x.get_device()
+        elif x.get_device() != self.device:
+            raise ValueError(f"tensors of one call on two devices ({self.device} and "
+                             f"{x.get_device()})")
+        return x.data_ptr()
+
+    def stream(self, stream) -> Optional[int]:
+        if stream is not None:
+            return _stream(stream)
+        current = torch.cuda.current_device()
+        if self.device is not None and self.device != current:
+            raise ValueError(f"tensors on device {self.device}, but the current device is "
+                             f"{current}: switch to it, or give a stream of it")
+        return _raw_stream(current)
+
+
+# The current stream's handle without a Stream object around it, where this
+# torch has that; a Stream costs as much as the rest of a call's checks.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _extent(rows: int, ld: int, cols: int) -> Optional[int]:
@@ -834,12 +855,13 @@ class Saved:
     """A rows x cols activation matrix kept for the backward pass: bf16
     (`scales` None), or 8-bit codes with one exponent byte per 32 rows of a
     column.  Keeps its buffers alive."""
+    __slots__ = ("data", "scales", "format", "s", "ref")
 
     def __init__(self, data, ld: int, scales=None, ld_scales: int = 0):
         self.data, self.scales = data, scales
         self.format = SAVED_BF16 if scales is None else SAVED_E4M3
         self.s = _Saved(_addr(data), ld, _addr(scales), ld_scales, self.format)
-        self._checked = None
+        self.ref = ctypes.byref(self.s)
 
     @classmethod
     def empty(cls, rows: int, cols: int, device="cuda") -> "Saved":
@@ -848,25 +870,15 @@ class Saved:
         return cls(torch.empty((max(rows, 1), ld), dtype=torch.uint8, device=device), ld,
                    torch.empty((max(-(-rows // 32), 1), lds), dtype=torch.uint8, device=device), lds)
 
-    def ref(self):
-        return ctypes.byref(self.s)
-
-    def check(self, what: str, rows: int, cols: int) -> None:
-        if self._checked == (rows, cols):
-            return
-        n = _extent(rows, self.s.ld, cols)
+    def check(self, call: _Call, what: str, rows: int, cols: int):
+        """Checks the buffers for rows x cols; the C argument."""
+        s = self.s
         if self.format == SAVED_BF16:
-            _need(self.data, what, n, "bf16")
+            call(self.data, what, _extent(rows, s.ld, cols), "bf16")
         else:
-            _need(self.data, f"{what} codes", n, "codes")
-            _need(self.scales, f"{what} scales", _extent(-(-rows // 32), self.s.ld_scales, cols),
-                  "codes")
-        if n is not None:
-            self._checked = (rows, cols)
-
-
-def _saved_ref(s: Optional[Saved]):
-    return None if s is None else s.ref()
+            call(self.data, what, _extent(rows, s.ld, cols), "codes")
+            call(self.scales, what, _extent((rows + 31) // 32, s.ld_scales, cols), "codes")
+        return self.ref
 
 
 def _act(act) -> int:
@@ -877,44 +889,42 @@ def _act(act) -> int:
     return int(act)
 
 
+def _dtype_of(x, given: int) -> int:
+    """ZERO_FP32 for a float32 tensor, ZERO_BF16 for another tensor, `given`
+    for a raw address."""
+    if x is None or x.__class__ is int:
+        return given
+    return FP32 if x.dtype == torch.float32 else BF16
+
+
 class Epilogue:
     """C = act(z) + residual with z = A B + bias; `preact` keeps z, `output`
     keeps C in 8 bits.  `act` is a name of ACTIVATION or its number; the
     types of bias and residual are taken from tensors, else bias_dtype and
     residual_dtype (raw addresses).  Keeps its buffers alive."""
+    __slots__ = ("bias", "residual", "preact", "output", "s", "ref")
 
     def __init__(self, bias=None, act=ACT_NONE, residual=None, ldr: int = 0, preact: Optional[Saved] = None,
                  output: Optional[Saved] = None, bias_dtype: int = BF16, residual_dtype: int = BF16):
         self.bias, self.residual, self.preact, self.output = bias, residual, preact, output
-        kind = lambda x, given: (FP32 if x.dtype == torch.float32 else BF16) \
-            if hasattr(x, "dtype") else given
         self.s = _Epilogue(_addr(bias), _addr(residual), ldr,
-                           None if preact is None else ctypes.pointer(preact.s),
-                           None if output is None else ctypes.pointer(output.s),
-                           kind(bias, bias_dtype), kind(residual, residual_dtype), _act(act))
+                           None if preact is None else ctypes.addressof(preact.s),
+                           None if output is None else ctypes.addressof(output.s),
+                           _dtype_of(bias, bias_dtype), _dtype_of(residual, residual_dtype),
+                           _act(act))
+        self.ref = ctypes.byref(self.s)
 
-    def ref(self):
-        return ctypes.byref(self.s)
-
-    def check(self, M: int, N: int) -> None:
-        _need(self.bias, "bias", N if N >= 0 else None, _kind(self.s.bias_dtype))
-        _need(self.residual, "residual", _extent(M, self.s.ldr, N), _kind(self.s.residual_dtype))
+    def check(self, call: _Call, M: int, N: int):
+        """Checks the buffers for an M x N product; the C argument."""
+        if self.bias is not None:
+            call(self.bias, "bias", N if N >= 0 else None, _kind(self.s.bias_dtype))
+        if self.residual is not None:
+            call(self.residual, "residual", _extent(M, self.s.ldr, N), _kind(self.s.residual_dtype))
         if self.preact is not None:
-            self.preact.check("preact", M, N)
+            self.preact.check(call, "preact", M, N)
         if self.output is not None:
-            self.output.check("output", M, N)
-
-    def tensors(self):
-        kept = [x for s in (self.preact, self.output) if s is not None for x in (s.data, s.scales)]
-        return [self.bias, self.residual, *kept]
-
-
-def _check_epilogue(ep: Optional[Epilogue], M: int, N: int):
-    """(the C argument, the epilogue's tensors) of a call's M x N product."""
-    if ep is None:
-        return None, ()
-    ep.check(M, N)
-    return ep.ref(), ep.tensors()
+            self.output.check(call, "output", M, N)
+        return self.ref
 
 
 def saved_write(rows: int, cols: int, x, ldx: int, out: Saved, x_dtype: Optional[int] = None,
@@ -922,39 +932,39 @@ def saved_write(rows: int, cols: int, x, ldx: int, out: Saved, x_dtype: Optional
     """x (rows x cols, bf16 or fp32: taken from the tensor, BF16 for a raw
     address unless given) into the 8-bit checkpoint `out`."""
     if x_dtype is None:
-        x_dtype = FP32 if getattr(x, "dtype", None) == torch.float32 else BF16
-    _need(x, "x", _extent(rows, ldx, cols), _kind(x_dtype))
-    out.check("out", rows, cols)
-    _one_device(stream, x, out.data, out.scales)
-    _check(_lib.zero_saved_write(rows, cols, _addr(x), ldx, x_dtype, out.ref(), _stream(stream)),
-           "zero_saved_write")
+        x_dtype = _dtype_of(x, BF16)
+    call = _Call()
+    xp = call(x, "x", _extent(rows, ldx, cols), _kind(x_dtype))
+    _check(_lib.zero_saved_write(rows, cols, xp, ldx, x_dtype, out.check(call, "out", rows, cols),
+                                 call.stream(stream)), "zero_saved_write")
 
 
 def saved_read(rows: int, cols: int, saved: Saved, out, ldo: int, out_dtype: Optional[int] = None,
                stream=None) -> None:
     """The values of an 8-bit checkpoint, exact in bf16 and in fp32."""
     if out_dtype is None:
-        out_dtype = FP32 if getattr(out, "dtype", None) == torch.float32 else BF16
-    saved.check("saved", rows, cols)
-    _need(out, "out", _extent(rows, ldo, cols), _kind(out_dtype))
-    _one_device(stream, out, saved.data, saved.scales)
-    _check(_lib.zero_saved_read(rows, cols, saved.ref(), _addr(out), ldo, out_dtype,
-                                _stream(stream)), "zero_saved_read")
+        out_dtype = _dtype_of(out, BF16)
+    call = _Call()
+    op = call(out, "out", _extent(rows, ldo, cols), _kind(out_dtype))
+    _check(_lib.zero_saved_read(rows, cols, saved.check(call, "saved", rows, cols), op, ldo, out_dtype,
+                                call.stream(stream)), "zero_saved_read")
+
+
+def _operand_count(rows: int, K: int, ld: int, order: int) -> Optional[int]:
+    return _operand_extent(rows, K, ld, order) if K >= 0 else None
 
 
 def gemm_bf16_epilogue(M: int, N: int, K: int, A, lda: int, a_order: int, B, ldb: int, b_order: int,
                        C, ldc: int, c_dtype: int = FP32, epilogue: Optional[Epilogue] = None,
                        stream=None) -> None:
     """gemm_bf16 with bias, activation, residual and kept outputs."""
-    if M > 0 and N > 0 and K >= 0:
-        _need(A, "A", _operand_extent(M, K, lda, a_order), "bf16")
-        _need(B, "B", _operand_extent(N, K, ldb, b_order), "bf16")
-        _need(C, "C", (M - 1) * ldc + N, _kind(c_dtype))
-    ref, more = _check_epilogue(epilogue, M, N)
-    _one_device(stream, A, B, C, *more)
-    _check(_lib.zero_gemm_bf16_epilogue(M, N, K, _addr(A), lda, a_order, _addr(B), ldb, b_order,
-                                        _addr(C), ldc, c_dtype, ref, _stream(stream)),
-           "zero_gemm_bf16_epilogue")
+    call = _Call()
+    Ap = call(A, "A", _operand_count(M, K, lda, a_order), "bf16")
+    Bp = call(B, "B", _operand_count(N, K, ldb, b_order), "bf16")
+    Cp = call(C, "C", _extent(M, ldc, N), _kind(c_dtype))
+    ep = None if epilogue is None else epilogue.check(call, M, N)
+    _check(_lib.zero_gemm_bf16_epilogue(M, N, K, Ap, lda, a_order, Bp, ldb, b_order, Cp, ldc,
+                                        c_dtype, ep, call.stream(stream)), "zero_gemm_bf16_epilogue")
 
 
 def act_backward_workspace(rows: int, cols: int) -> int:
@@ -962,48 +972,51 @@ def act_backward_workspace(rows: int, cols: int) -> int:
     return _lib.zero_act_backward_workspace(rows, cols)
 
 
-def _check_act_backward(rows, cols, dy, ldy, dy_dtype, preact, dz, ldz, dbias, workspace):
-    _need(dy, "dy", _extent(rows, ldy, cols), _kind(dy_dtype))
-    if preact is not None:
-        preact.check("preact", rows, cols)
-    _need(dz, "dz", _extent(rows, ldz, cols), "bf16")
-    if dbias is not None:
-        _need(dbias, "dbias", max(cols, 0), "fp32")
-        _need(workspace, "workspace", act_backward_workspace(rows, cols), "fp32")
-
-
 def _numel(x) -> int:
     """Elements of a workspace; a raw address is taken at its caller's word."""
-    return 0 if x is None else x.numel() if hasattr(x, "numel") else (1 << 62)
+    return 0 if x is None else (1 << 62) if x.__class__ is int else x.numel()
+
+
+def _sums(call: _Call, rows: int, cols: int, dbias, workspace):
+    """dbias and its workspace, checked."""
+    if dbias is None:
+        return None, None
+    return (call(dbias, "dbias", max(cols, 0), "fp32"),
+            call(workspace, "workspace", act_backward_workspace(rows, cols), "fp32"))
 
 
 def act_backward(rows: int, cols: int, dy, ldy: int, act, preact: Optional[Saved], dz, ldz: int,
                  dbias=None, workspace=None, dy_dtype: Optional[int] = None, stream=None) -> None:
     """dz = dy act'(preact) in bf16 and dbias = its column sums in fp32."""
     if dy_dtype is None:
-        dy_dtype = FP32 if getattr(dy, "dtype", None) == torch.float32 else BF16
-    _check_act_backward(rows, cols, dy, ldy, dy_dtype, preact, dz, ldz, dbias, workspace)
-    more = () if preact is None else (preact.data, preact.scales)
-    _one_device(stream, dy, dz, dbias, workspace, *more)
-    _check(_lib.zero_act_backward(rows, cols, _addr(dy), ldy, dy_dtype, _act(act), _saved_ref(preact),
-                                  _addr(dz), ldz, _addr(dbias), _addr(workspace), _numel(workspace),
-                                  _stream(stream)), "zero_act_backward")
+        dy_dtype = _dtype_of(dy, BF16)
+    call = _Call()
+    dyp = call(dy, "dy", _extent(rows, ldy, cols), _kind(dy_dtype))
+    zp = None if preact is None else preact.check(call, "preact", rows, cols)
+    dzp = call(dz, "dz", _extent(rows, ldz, cols), "bf16")
+    dbp, wp = _sums(call, rows, cols, dbias, workspace)
+    _check(_lib.zero_act_backward(rows, cols, dyp, ldy, dy_dtype, _act(act), zp, dzp, ldz, dbp, wp,
+                                  _numel(workspace), call.stream(stream)), "zero_act_backward")
 
 
 def gemm_saved_bf16(M: int, N: int, K: int, A: Saved, B, ldb: int, C, ldc: int, c_dtype: int = FP32,
                     stream=None) -> None:
     """C = A^T B from a kept K x M operand and a K x N bf16 one."""
-    if M > 0 and N > 0 and K >= 0:
-        A.check("A", K, M)
-        _need(B, "B", _extent(K, ldb, N), "bf16")
-        _need(C, "C", (M - 1) * ldc + N, _kind(c_dtype))
-    _one_device(stream, A.data, A.scales, B, C)
-    _check(_lib.zero_gemm_saved_bf16(M, N, K, A.ref(), _addr(B), ldb, _addr(C), ldc, c_dtype,
-                                     _stream(stream)), "zero_gemm_saved_bf16")
+    call = _Call()
+    Ap = A.check(call, "A", K, M)
+    Bp = call(B, "B", _extent(K, ldb, N), "bf16")
+    Cp = call(C, "C", _extent(M, ldc, N), _kind(c_dtype))
+    _check(_lib.zero_gemm_saved_bf16(M, N, K, Ap, Bp, ldb, Cp, ldc, c_dtype, call.stream(stream)),
+           "zero_gemm_saved_bf16")
 
 
-def _group_count(n: int) -> Optional[int]:
-    return n + 1 if n >= 1 else None
+def _offsets(call: _Call, offsets, n_groups: int) -> Optional[int]:
+    return call(offsets, "offsets", n_groups + 1 if n_groups >= 1 else None, "int64")
+
+
+def _stacked(n: int, stride: int, each: Optional[int]) -> Optional[int]:
+    """Elements of n matrices `stride` apart, the last `each` long."""
+    return None if n < 1 or each is None else (n - 1) * stride + each
 
 
 def gemm_grouped_rows_bf16(n_groups: int, offsets, rows: int, N: int, K: int, A, lda: int, B,
@@ -1011,16 +1024,15 @@ def gemm_grouped_rows_bf16(n_groups: int, offsets, rows: int, N: int, K: int, A,
                            epilogue: Optional[Epilogue] = None, stream=None) -> None:
     """C[r] = epilogue(A[r] B_e) for the rows r of group e; `offsets` is a
     device int64 tensor of n_groups + 1."""
-    _need(offsets, "offsets", _group_count(n_groups), "int64")
-    if n_groups >= 1 and rows > 0 and N > 0 and K >= 0:
-        _need(A, "A", _operand_extent(rows, K, lda, K_INNER), "bf16")
-        _need(B, "B", (n_groups - 1) * stride_b + _operand_extent(N, K, ldb, b_order), "bf16")
-        _need(C, "C", (rows - 1) * ldc + N, _kind(c_dtype))
-    ref, more = _check_epilogue(epilogue, rows, N)
-    _one_device(stream, offsets, A, B, C, *more)
-    _check(_lib.zero_gemm_grouped_rows_bf16(n_groups, _addr(offsets), rows, N, K, _addr(A), lda,
-                                            _addr(B), ldb, b_order, stride_b, _addr(C), ldc, c_dtype,
-                                            ref, _stream(stream)),
+    call = _Call()
+    op = _offsets(call, offsets, n_groups)
+    Ap = call(A, "A", _operand_count(rows, K, lda, K_INNER), "bf16")
+    Bp = call(B, "B", _stacked(n_groups, stride_b, _operand_count(N, K, ldb, b_order))
+              if rows > 0 and N > 0 else 0, "bf16")
+    Cp = call(C, "C", _extent(rows, ldc, N), _kind(c_dtype))
+    ep = None if epilogue is None else epilogue.check(call, rows, N)
+    _check(_lib.zero_gemm_grouped_rows_bf16(n_groups, op, rows, N, K, Ap, lda, Bp, ldb, b_order,
+                                            stride_b, Cp, ldc, c_dtype, ep, call.stream(stream)),
            "zero_gemm_grouped_rows_bf16")
 
 
@@ -1028,67 +1040,72 @@ def gemm_grouped_depth_bf16(n_groups: int, offsets, rows: int, M: int, N: int, A
                             ldb: int, C, ldc: int, stride_c: int, c_dtype: int = FP32,
                             stream=None) -> None:
     """C_e = sum over the rows r of group e of A[r]^T B[r]."""
-    _need(offsets, "offsets", _group_count(n_groups), "int64")
-    if n_groups >= 1 and M > 0 and N > 0 and rows >= 0:
-        _need(A, "A", _extent(rows, lda, M), "bf16")
-        _need(B, "B", _extent(rows, ldb, N), "bf16")
-        _need(C, "C", (n_groups - 1) * stride_c + (M - 1) * ldc + N, _kind(c_dtype))
-    _one_device(stream, offsets, A, B, C)
-    _check(_lib.zero_gemm_grouped_depth_bf16(n_groups, _addr(offsets), rows, M, N, _addr(A), lda,
-                                             _addr(B), ldb, _addr(C), ldc, stride_c, c_dtype,
-                                             _stream(stream)), "zero_gemm_grouped_depth_bf16")
+    call = _Call()
+    op = _offsets(call, offsets, n_groups)
+    Ap = call(A, "A", _extent(rows, lda, M), "bf16")
+    Bp = call(B, "B", _extent(rows, ldb, N), "bf16")
+    Cp = call(C, "C", _stacked(n_groups, stride_c, _extent(M, ldc, N)), _kind(c_dtype))
+    _check(_lib.zero_gemm_grouped_depth_bf16(n_groups, op, rows, M, N, Ap, lda, Bp, ldb, Cp, ldc,
+                                             stride_c, c_dtype, call.stream(stream)),
+           "zero_gemm_grouped_depth_bf16")
+
+
+def _layer_buffers(call: _Call, layout: Layout, unit: int, w_shards, w_full):
+    """(the unit's (in, out, shard, padded) or None, the shards' pointers,
+    w_full's), checked."""
+    _need_len("w_shards", w_shards, _parts(layout))
+    d = _layer_dims(layout, unit)
+    shard, padded = (None, None) if d is None else d[2:]
+    ptrs = [call(x, f"W shard of rank {q}", shard, "bf16") for q, x in enumerate(w_shards)]
+    return d, (ctypes.c_void_p * max(1, len(ptrs)))(*ptrs), call(w_full, "w_full", padded, "bf16")
+
+
+def _times(rows: int, cols: Optional[int]) -> Optional[int]:
+    return None if cols is None or rows < 0 else rows * cols
 
 
 def fsdp_linear_act_forward(layout: Layout, unit: int, w_shards, batch: int, x, w_full, y,
                             epilogue: Optional[Epilogue] = None, y_dtype: int = BF16,
                             stream=None) -> None:
     """fsdp_linear_forward with an epilogue."""
-    _need_len("w_shards", w_shards, _parts(layout))
-    d = _check_layer(layout, unit, w_shards, w_full, batch)
-    ref, more = None, ()
-    if d is not None:
-        _need(x, "x", batch * d[0], "bf16")
-        _need(y, "y", batch * d[1], _kind(y_dtype))
-        ref, more = _check_epilogue(epilogue, batch, d[1])
-    elif epilogue is not None:
-        ref = epilogue.ref()
-    _one_device(stream, x, w_full, y, *w_shards, *more)
-    _check(_lib.zero_fsdp_linear_act_forward(layout.handle, unit, _ptrs(w_shards), batch, _addr(x),
-                                             _addr(w_full), ref, _addr(y), y_dtype,
-                                             _stream(stream)), "zero_fsdp_linear_act_forward")
+    call = _Call()
+    d, wp, wf = _layer_buffers(call, layout, unit, w_shards, w_full)
+    inf, out = (None, None) if d is None else d[:2]
+    xp = call(x, "x", _times(batch, inf), "bf16")
+    yp = call(y, "y", _times(batch, out), _kind(y_dtype))
+    ep = None if epilogue is None else epilogue.ref if d is None else epilogue.check(call, batch, out)
+    _check(_lib.zero_fsdp_linear_act_forward(layout.handle, unit, wp, batch, xp, wf, ep, yp, y_dtype,
+                                             call.stream(stream)), "zero_fsdp_linear_act_forward")
 
 
 def fsdp_linear_act_backward(layout: Layout, unit: int, w_shards, batch: int, x: Saved, act,
                              preact: Optional[Saved], dy, w_full, dz, dx, dw_full, dbias=None,
                              workspace=None, dx_dtype: int = BF16, stream=None) -> None:
     """fsdp_linear_backward through the epilogue, from the kept x and z."""
-    _need_len("w_shards", w_shards, _parts(layout))
-    d = _check_layer(layout, unit, w_shards, w_full, batch)
-    if d is not None:
-        x.check("x", batch, d[0])
-        _check_act_backward(batch, d[1], dy, d[1], BF16, preact, dz, d[1], dbias, workspace)
-        _need(dx, "dx", batch * d[0], _kind(dx_dtype))
-        _need(dw_full, "dw_full", d[3], "fp32")
-    more = () if preact is None else (preact.data, preact.scales)
-    _one_device(stream, x.data, x.scales, dy, w_full, dz, dx, dw_full, dbias, workspace, *w_shards,
-                *more)
-    _check(_lib.zero_fsdp_linear_act_backward(layout.handle, unit, _ptrs(w_shards), batch, x.ref(),
-                                              _act(act), _saved_ref(preact), _addr(dy),
-                                              _addr(w_full), _addr(dz), _addr(dx), dx_dtype,
-                                              _addr(dw_full), _addr(dbias), _addr(workspace),
-                                              _numel(workspace), _stream(stream)),
+    call = _Call()
+    d, wp, wf = _layer_buffers(call, layout, unit, w_shards, w_full)
+    inf, out, padded = (None, None, None) if d is None else (d[0], d[1], d[3])
+    xr = x.ref if d is None else x.check(call, "x", batch, inf)
+    zr = None if preact is None else \
+        preact.ref if d is None else preact.check(call, "preact", batch, out)
+    dyp = call(dy, "dy", _times(batch, out), "bf16")
+    dzp = call(dz, "dz", _times(batch, out), "bf16")
+    dxp = call(dx, "dx", _times(batch, inf), _kind(dx_dtype))
+    dwp = call(dw_full, "dw_full", padded, "fp32")
+    dbp, wsp = _sums(call, batch, 0 if d is None else out, dbias, workspace)
+    _check(_lib.zero_fsdp_linear_act_backward(layout.handle, unit, wp, batch, xr, _act(act), zr, dyp,
+                                              wf, dzp, dxp, dx_dtype, dwp, dbp, wsp,
+                                              _numel(workspace), call.stream(stream)),
            "zero_fsdp_linear_act_backward")
 
 
-def _check_experts(layout, unit, n_experts, w_shards, offsets, rows, w_full):
-    """(in, out, padded) of an expert layer's unit, or None if the library
-    will refuse it."""
-    _need_len("w_shards", w_shards, _parts(layout))
-    d = _check_layer(layout, unit, w_shards, w_full, rows)
-    _need(offsets, "offsets", _group_count(n_experts), "int64")
+def _expert_buffers(call: _Call, layout: Layout, unit: int, n_experts: int, w_shards, offsets, w_full):
+    """_layer_buffers with one expert's in, and the offsets' pointer."""
+    d, wp, wf = _layer_buffers(call, layout, unit, w_shards, w_full)
+    op = _offsets(call, offsets, n_experts)
     if d is None or n_experts < 1 or d[0] % n_experts:
-        return None
-    return d[0] // n_experts, d[1], d[3]
+        return None, wp, wf, op
+    return (d[0] // n_experts, *d[1:]), wp, wf, op
 
 
 def fsdp_experts_forward(layout: Layout, unit: int, n_experts: int, w_shards, offsets, rows: int, x,
@@ -1096,35 +1113,29 @@ def fsdp_experts_forward(layout: Layout, unit: int, n_experts: int, w_shards, of
                          stream=None) -> None:
     """The grouped forward of an expert layer whose weights (n_experts * in
     rows x out) are one row-sharded unit."""
-    d = _check_experts(layout, unit, n_experts, w_shards, offsets, rows, w_full)
-    ref, more = None, ()
-    if d is not None:
-        _need(x, "x", rows * d[0], "bf16")
-        _need(y, "y", rows * d[1], _kind(y_dtype))
-        ref, more = _check_epilogue(epilogue, rows, d[1])
-    elif epilogue is not None:
-        ref = epilogue.ref()
-    _one_device(stream, offsets, x, w_full, y, *w_shards, *more)
-    _check(_lib.zero_fsdp_experts_forward(layout.handle, unit, n_experts, _ptrs(w_shards),
-                                          _addr(offsets), rows, _addr(x), _addr(w_full), ref,
-                                          _addr(y), y_dtype, _stream(stream)),
-           "zero_fsdp_experts_forward")
+    call = _Call()
+    d, wp, wf, op = _expert_buffers(call, layout, unit, n_experts, w_shards, offsets, w_full)
+    inf, out = (None, None) if d is None else d[:2]
+    xp = call(x, "x", _times(rows, inf), "bf16")
+    yp = call(y, "y", _times(rows, out), _kind(y_dtype))
+    ep = None if epilogue is None else epilogue.ref if d is None else epilogue.check(call, rows, out)
+    _check(_lib.zero_fsdp_experts_forward(layout.handle, unit, n_experts, wp, op, rows, xp, wf, ep, yp,
+                                          y_dtype, call.stream(stream)), "zero_fsdp_experts_forward")
 
 
 def fsdp_experts_backward(layout: Layout, unit: int, n_experts: int, w_shards, offsets, rows: int,
                           x, dy, w_full, dx, dw_full, dx_dtype: int = BF16, stream=None) -> None:
     """The grouped dx and the experts' dW (dw_full: the padded unit, fp32)."""
-    d = _check_experts(layout, unit, n_experts, w_shards, offsets, rows, w_full)
-    if d is not None:
-        _need(x, "x", rows * d[0], "bf16")
-        _need(dy, "dy", rows * d[1], "bf16")
-        _need(dx, "dx", rows * d[0], _kind(dx_dtype))
-        _need(dw_full, "dw_full", d[2], "fp32")
-    _one_device(stream, offsets, x, dy, w_full, dx, dw_full, *w_shards)
-    _check(_lib.zero_fsdp_experts_backward(layout.handle, unit, n_experts, _ptrs(w_shards),
-                                           _addr(offsets), rows, _addr(x), _addr(dy),
-                                           _addr(w_full), _addr(dx), dx_dtype, _addr(dw_full),
-                                           _stream(stream)), "zero_fsdp_experts_backward")
+    call = _Call()
+    d, wp, wf, op = _expert_buffers(call, layout, unit, n_experts, w_shards, offsets, w_full)
+    inf, out, padded = (None, None, None) if d is None else (d[0], d[1], d[3])
+    xp = call(x, "x", _times(rows, inf), "bf16")
+    dyp = call(dy, "dy", _times(rows, out), "bf16")
+    dxp = call(dx, "dx", _times(rows, inf), _kind(dx_dtype))
+    dwp = call(dw_full, "dw_full", padded, "fp32")
+    _check(_lib.zero_fsdp_experts_backward(layout.handle, unit, n_experts, wp, op, rows, xp, dyp, wf,
+                                           dxp, dx_dtype, dwp, call.stream(stream)),
+           "zero_fsdp_experts_backward")
 
 
 def stream_mix(kind: int, grads, master, m, v, param, n: int, stream=None,

@@ -126,7 +126,7 @@ def test_act_backward_refusals():
     bad(INV, dbias=FAKE, text="workspace")
     bad(UNSUP, rows=1 << 41)
     with pytest.raises(zs.ZeroShardError):          # a workspace one float short
-        zs._check(zs.raw().zero_act_backward(200, 64, FAKE, 64, 0, 2, zs.Saved(FAKE, 64).ref(), FAKE,
+        zs._check(zs.raw().zero_act_backward(200, 64, FAKE, 64, 0, 2, zs.Saved(FAKE, 64).ref, FAKE,
                                              64, FAKE, FAKE, zs.act_backward_workspace(200, 64) - 1,
                                              0), "zero_act_backward")
     zs.act_backward(0, 64, None, 64, "gelu", None, None, 64, stream=0)
