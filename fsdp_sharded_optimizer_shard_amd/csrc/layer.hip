@@ -421,6 +421,208 @@ __global__ __launch_bounds__(kGT) void epi_kernel_kp(int64_t M, int64_t N, int64
         gemm_tile_kp<BM / 2, BN>(M, N, K, A, lda, B, ldb, epi, m0, n0, ZS_P);
 }
 
+// ------------------------------------------------- few tiles, long sums --
+
+// A 128 x 128 tile for products that have too few tiles to fill the CUs with
+// 256 x 256 ones, so that a CU runs one block: the two halves of its waves
+// take alternate K tiles of 32, each half a 2 x 2 grid of 64 x 64, and add
+// their sums at the end.  Against the 2 x 4 grid of gemm_tile on one K tile
+// at a time, a barrier stands between twice the products and a fragment
+// serves twice as many.  1000 x 4096 x 14336 (256 tiles, every block alone on
+// its CU): 153 -> 141 us with a K-outer B, 203 -> 169 with a K-inner one; one
+// row: 120 -> 95 and 201 -> 126.  What bounds it then is the fetch of operands
+// that no other block shares, 58 GB/s a CU.
+//
+// Each half has stages and loads of its own, in step with the other's through
+// the block's barriers: half h holds K tile 2 g + h in stage g % 4, at 16 KB h
+// of the stage's array, A first.  A K tile past the last reads as zeros.
+constexpr int kHalfBytes = 2 * 128 * kBK * 2;  // A and B of one half's stage
+
+template <bool A_KOUTER, bool B_KOUTER, class Epi>
+__device__ __forceinline__ void gemm_tile_k2(int64_t M, int64_t N, int64_t K,
+                                             const uint16_t *__restrict__ A, int64_t lda,
+                                             const uint16_t *__restrict__ B, int64_t ldb, const Epi &epi,
+                                             int64_t m0, int64_t n0, ZS_LDS char *const (&Ss)[kStages],
+                                             ZS_LDS float *mine, ZS_LDS float *partner)
+{
+    constexpr int BM = 128, BN = 128, TM = 2, TN = 2, NF = TM + TN, NMF = TM * TN;
+    constexpr int NRD = TM * Op<BM, A_KOUTER>::NRD + TN * Op<BN, B_KOUTER>::NRD;
+    constexpr int NI = 2, D = 2 * NI;  // loads of one operand, of both, per wave and stage
+
+    const int t = threadIdx.x, lane = t & 63, w8 = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int half = w8 >> 2, wave = w8 & 3;
+    const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
+
+    uint32_t va[NI], vb[NI];
+    int ka[NI];
+#pragma unroll
+    for (int n = 0; n < NI; ++n) {
+        va[n] = dma_offset<BM, A_KOUTER>(lda, wave + 4 * n, lane, 0);
+        vb[n] = dma_offset<BN, B_KOUTER>(ldb, wave + 4 * n, lane, 0);
+        ka[n] = dma_kofs(wave + 4 * n, lane, 0);
+    }
+    int fa_off[TM][2], fb_off[TN][2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+            fa_off[i][s] = half * kHalfBytes + frag_offset<BM, A_KOUTER>(wm + 32 * i, s, lane);
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            fb_off[j][s] = half * kHalfBytes + kHalfBytes / 2 + frag_offset<BN, B_KOUTER>(wn + 32 * j, s, lane);
+    }
+
+    f32x16 acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int v = 0; v < 16; ++v)
+                acc[i][j][v] = 0.0f;
+
+    const int64_t g_n = (K + 2 * kBK - 1) / (2 * kBK), g_full = K / (2 * kBK);
+    auto dma = [&](auto st, auto whole, int64_t g) {
+        constexpr int S = decltype(st)::value;
+        constexpr bool WHOLE = decltype(whole)::value != 0;
+        const int64_t k0 = (2 * g + half) * kBK;
+        const __amdgpu_buffer_rsrc_t ra = A_KOUTER ? rsrc(A + k0 * lda + m0, ((K - 1 - k0) * lda + M - m0) * 2)
+                                                   : rsrc(A + m0 * lda + k0, ((M - 1 - m0) * lda + K - k0) * 2);
+        const __amdgpu_buffer_rsrc_t rb = B_KOUTER ? rsrc(B + k0 * ldb + n0, ((K - 1 - k0) * ldb + N - n0) * 2)
+                                                   : rsrc(B + n0 * ldb + k0, ((N - 1 - n0) * ldb + K - k0) * 2);
+        ZS_LDS char *d = Ss[S] + half * kHalfBytes;
+#pragma unroll
+        for (int n = 0; n < NI; ++n) {
+            const uint32_t o = !WHOLE && !A_KOUTER && k0 + ka[n] >= K ? kOOB : va[n];
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (ZS_LDS void *)(d + (wave + 4 * n) * 1024), 16, o, 0,
+                                                     0, 0);
+        }
+#pragma unroll
+        for (int n = 0; n < NI; ++n) {
+            const uint32_t o = !WHOLE && !B_KOUTER && k0 + ka[n] >= K ? kOOB : vb[n];
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rb, (ZS_LDS void *)(d + kHalfBytes / 2 + (wave + 4 * n) * 1024), 16, o, 0, 0, 0);
+        }
+    };
+    bf16x8 fa0[TM], fb0[TN], fa1[TM], fb1[TN];
+    auto frags = [&](auto st, int s, bf16x8 (&fa)[TM], bf16x8 (&fb)[TN]) {
+        constexpr int S = decltype(st)::value;
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+            fa[i] = frag_read<BM, A_KOUTER>(Ss[S], fa_off[i][s]);
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            fb[j] = frag_read<BN, B_KOUTER>(Ss[S], fb_off[j][s]);
+    };
+    auto mma = [&](const bf16x8 (&fa)[TM], const bf16x8 (&fb)[TN], int lo, int hi) {
+#pragma unroll
+        for (int q = 0; q < NMF; ++q)
+            if (q >= lo && q < hi)
+                acc[q / TN][q % TN] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                    fa[q / TN], fb[q % TN], acc[q / TN][q % TN], 0, 0, 0);
+    };
+    auto wait_for = [&](int64_t g1) {
+        const int64_t after = g_n - 1 - g1;
+        if (after >= 2)
+            wait_vm_lgkm0<2 * D>();
+        else if (after == 1)
+            wait_vm_lgkm0<D>();
+        else
+            wait_vm_lgkm0<0>();
+    };
+    // Pair of K tiles g, as gemm_tile's tile.
+    auto tile = [&](auto st, auto steady, int64_t g) {
+        constexpr int S = decltype(st)::value;
+        constexpr bool STEADY = decltype(steady)::value != 0;
+        constexpr int SN = (S + kStages - 1) % kStages, S1 = (S + 1) % kStages;
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (STEADY)
+            dma(IC<SN>{}, IC<1>{}, g + kStages - 1);
+        else if (g + kStages - 1 < g_n)
+            dma(IC<SN>{}, IC<0>{}, g + kStages - 1);
+        frags(IC<S>{}, 1, fa1, fb1);
+        mma(fa0, fb0, 0, NMF);
+        seq<NF, NMF, NRD, STEADY ? D : 0>();
+        mma(fa1, fb1, 0, NMF / 2);
+        __builtin_amdgcn_sched_group_barrier(0x008, NMF / 2, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (STEADY)
+            wait_vm_lgkm0<2 * D>();
+        else
+            wait_for(g + 1);
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        if (STEADY || g + 1 < g_n)
+            frags(IC<S1>{}, 0, fa0, fb0);
+        mma(fa1, fb1, NMF / 2, NMF);
+        seq<NF, NMF / 2, NRD, 0>();
+    };
+    if (g_n > 0) {
+        dma(IC<0>{}, IC<0>{}, 0);
+        if (g_n > 1)
+            dma(IC<1>{}, IC<0>{}, 1);
+        if (g_n > 2)
+            dma(IC<2>{}, IC<0>{}, 2);
+        wait_for(0);
+        __builtin_amdgcn_s_barrier();
+        frags(IC<0>{}, 0, fa0, fb0);
+        int64_t g = 0;
+        for (; g + 2 * kStages - 1 <= g_full; g += kStages) {
+            tile(IC<0>{}, IC<1>{}, g);
+            tile(IC<1>{}, IC<1>{}, g + 1);
+            tile(IC<2>{}, IC<1>{}, g + 2);
+            tile(IC<3>{}, IC<1>{}, g + 3);
+        }
+        for (; g < g_n; g += kStages) {
+            tile(IC<0>{}, IC<0>{}, g);
+            if (g + 1 < g_n)
+                tile(IC<1>{}, IC<0>{}, g + 1);
+            if (g + 2 < g_n)
+                tile(IC<2>{}, IC<0>{}, g + 2);
+            if (g + 3 < g_n)
+                tile(IC<3>{}, IC<0>{}, g + 3);
+        }
+    }
+    // Wave (wave, half) hands its partner the rows 32 (1 - half) .. and keeps
+    // the others: the sum of the even K tiles plus that of the odd ones.
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+            partner[(16 * j + v) * 64 + lane] = half ? acc[0][j][v] : acc[1][j][v];
+    __syncthreads();
+    f32x16 sum[1][TN];
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+            const float other = mine[(16 * j + v) * 64 + lane];
+            sum[0][j][v] = half ? other + acc[1][j][v] : acc[0][j][v] + other;
+        }
+    epi.template tile32<1, TN>(sum, m0 + wm + 32 * half, n0 + wn, M, N, lane);
+}
+
+template <bool A_KOUTER, bool B_KOUTER>
+__global__ __launch_bounds__(kGT) void epi_kernel_k2(int64_t M, int64_t N, int64_t K,
+                                                     const uint16_t *__restrict__ A, int64_t lda,
+                                                     const uint16_t *__restrict__ B, int64_t ldb,
+                                                     EpiArgs args, int tiles_m, int tiles_n)
+{
+    __shared__ __attribute__((aligned(1024))) char s0[2 * kHalfBytes], s1[2 * kHalfBytes],
+        s2[2 * kHalfBytes], s3[2 * kHalfBytes];
+    ZS_LDS char *const Ss[kStages] = {(ZS_LDS char *)s0, (ZS_LDS char *)s1, (ZS_LDS char *)s2,
+                                      (ZS_LDS char *)s3};
+#define ZS_S(n) (ZS_LDS char *)s##n, (ZS_LDS char *)s##n + kHalfBytes
+    ZS_LDS float *mine = corner(ZS_S(0), ZS_S(1), ZS_S(2), ZS_S(3));
+    ZS_LDS float *partner = corner(ZS_S(2), ZS_S(3), ZS_S(0), ZS_S(1));
+#undef ZS_S
+    const LayerEpi epi{args, mine};
+    int64_t m0, n0;
+    place<128, 128>(tiles_m, tiles_n, tiles_m * tiles_n, m0, n0);
+    gemm_tile_k2<A_KOUTER, B_KOUTER>(M, N, K, A, lda, B, ldb, epi, m0, n0, Ss, mine, partner);
+}
+
 // Group e's rows [lo, hi), kept inside [0, rows] whatever the array holds.
 __device__ __forceinline__ void group_range(const int64_t *off, int e, int64_t rows, int64_t &lo, int64_t &hi)
 {
@@ -1008,11 +1210,17 @@ zero_status epilogue_gemm_run(int64_t M, int64_t N, int64_t K, const uint16_t *A
     const EpiArgs a = epi_args(ep, C, ldc, c_dtype);
     const bool ao = a_order == ZERO_K_OUTER, bo = b_order == ZERO_K_OUTER;
     const bool small = small_tiles(M, N);
+    // Under 1024 the halves' final exchange is not earned back: 1 x 520 x 256
+    // takes 8.9 us with it and 7.8 without, 256 x 1024 x 1024 12.0 and 13.0.
+    const bool k2 = small && K >= 1024;
     const Grid g = small ? tiles(M, N, 128, 128, false) : tiles(M, N, kBM, kBN, true);
     (void)hipGetLastError();
 #define ZS_EPI(AO, BO)                                                                             \
     do {                                                                                           \
-        if (small)                                                                                 \
+        if (k2)                                                                                    \
+            hipLaunchKernelGGL((epi_kernel_k2<AO, BO>), g.grid, dim3(kGT), 0, s, M, N, K, A, lda,  \
+                               B, ldb, a, g.tm, g.tn);                                             \
+        else if (small)                                                                                 \
             hipLaunchKernelGGL((epi_kernel<128, 128, AO, BO>), g.grid, dim3(kGT), 0, s, M, N, K, A, \
                                lda, B, ldb, a, g.tm, g.tn, g.n_big);                               \
         else                                                                                       \
@@ -1025,6 +1233,9 @@ zero_status epilogue_gemm_run(int64_t M, int64_t N, int64_t K, const uint16_t *A
         ZS_EPI(true, false);
     } else if (bo) {
         ZS_EPI(false, true);
+    } else if (k2) {
+        hipLaunchKernelGGL((epi_kernel_k2<false, false>), g.grid, dim3(kGT), 0, s, M, N, K, A, lda, B, ldb,
+                           a, g.tm, g.tn);
     } else if (small) {
         hipLaunchKernelGGL((epi_kernel_kp<128, 128>), g.grid, dim3(kGT), 0, s, M, N, K, A, lda, B, ldb, a,
                            g.tm, g.tn, g.n_big);
