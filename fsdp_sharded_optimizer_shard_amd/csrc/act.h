@@ -117,9 +117,10 @@ __device__ __forceinline__ float act_slope(float z)
     }
 }
 
-// ACT's functions over n values; `a` is the same in every lane.
+// f with the activation as a constant; on the device `a` is the same in every
+// lane.
 template <class F>
-__device__ __forceinline__ void by_act(int a, F f)
+__host__ __device__ __forceinline__ void by_act(int a, F f)
 {
     switch (a) {
     case ZERO_ACT_RELU: f(std::integral_constant<int, ZERO_ACT_RELU>{}); break;

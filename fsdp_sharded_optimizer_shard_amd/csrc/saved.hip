@@ -190,7 +190,7 @@ struct ActBackArgs {
     const uint8_t *z_scales;
     void *dz;
     float *sums;  // dbias when one block spans the rows, else one row of partial sums per block
-    int32_t act, units;  // units of 128 rows a block walks
+    int32_t units;  // of 128 rows, a block's walk
     bool y_bf16, y_vec, z_vec, zs_vec, d_vec;
     bool plain;  // bf16 dy, and every matrix's rows 16-byte aligned
 };
@@ -201,7 +201,8 @@ struct ActBackArgs {
 // 8 for codes.  The sums stay in registers over the units, then go through
 // LDS in row order and leave as one row per block, summed by sum_kernel in
 // row order too: no atomics, the same bits every time.
-template <int ZF>  // 0: no activation, 1: z in bf16, 2: z in 8 bits
+// ZF 0: no activation, 1: z in bf16, 2: z in 8 bits.
+template <int ZF, int ACT>
 __global__ __launch_bounds__(256) void act_backward_kernel(ActBackArgs p)
 {
     __shared__ float part[16][128 + 4];
@@ -218,15 +219,12 @@ __global__ __launch_bounds__(256) void act_backward_kernel(ActBackArgs p)
             if (ZF == 2)
                 b = load_bytes8(p.z_scales + (row >> 5) * p.ldzs + col, p.zs_vec && n == 8, n);
             auto finish = [&](int i, float (&y)[8], const float (&z)[8], bool vec) {
-                if (ZF != 0)
-                    by_act(p.act, [&](auto a) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            y[k] *= act_slope<decltype(a)::value>(z[k]);
-                    });
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
+                for (int k = 0; k < 8; ++k) {
+                    if (ZF != 0)
+                        y[k] *= act_slope<ACT>(z[k]);
                     sum[k] += y[k];
+                }
                 if (p.dz)
                     store8(p.dz, true, (row + i) * p.ldd + col, vec, n, y);
             };
@@ -257,7 +255,7 @@ __global__ __launch_bounds__(256) void act_backward_kernel(ActBackArgs p)
                 }
                 continue;
             }
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < 8; ++i) {
                 if (row + i >= p.rows)
                     break;
@@ -397,7 +395,6 @@ zero_status act_backward_run(int64_t rows, int64_t cols, const void *dy, int64_t
     p.ldy = ldy;
     p.y_bf16 = dy_dtype == ZERO_BF16;
     p.y_vec = vec16(dy, ldy, bytes_of(dy_dtype));
-    p.act = act;
     p.dz = dz;
     p.ldd = ldz;
     p.d_vec = vec16(dz, ldz, 2);
@@ -417,12 +414,15 @@ zero_status act_backward_run(int64_t rows, int64_t cols, const void *dy, int64_t
     p.sums = !dbias ? nullptr : blocks > 1 ? workspace : dbias;
     const dim3 grid((unsigned)((cols + 127) / 128), (unsigned)blocks);
     (void)hipGetLastError();
-    if (p.z_scales)
-        hipLaunchKernelGGL(act_backward_kernel<2>, grid, dim3(256), 0, s, p);
-    else if (p.z)
-        hipLaunchKernelGGL(act_backward_kernel<1>, grid, dim3(256), 0, s, p);
-    else
-        hipLaunchKernelGGL(act_backward_kernel<0>, grid, dim3(256), 0, s, p);
+    by_act(p.z ? act : ZERO_ACT_NONE, [&](auto a) {
+        constexpr int ACT = decltype(a)::value;
+        if (ACT == ZERO_ACT_NONE)
+            hipLaunchKernelGGL((act_backward_kernel<0, ZERO_ACT_NONE>), grid, dim3(256), 0, s, p);
+        else if (p.z_scales)
+            hipLaunchKernelGGL((act_backward_kernel<2, ACT>), grid, dim3(256), 0, s, p);
+        else
+            hipLaunchKernelGGL((act_backward_kernel<1, ACT>), grid, dim3(256), 0, s, p);
+    });
     zero_status st = launched("act_backward");
     if (st != ZERO_OK || !dbias || blocks == 1)
         return st;
