@@ -744,3 +744,154 @@ def test_calls_on_two_streams_at_once():
                         outs[2 + k][2])
         torch.cuda.synchronize()
         assert torch.equal(outs[k][0], outs[2 + k][0]) and torch.equal(outs[k][1], outs[2 + k][1])
+
+
+# ----------------------------------------- addresses that suit no vector load --
+
+@pytest.mark.parametrize("bo", [0, 1])
+def test_epilogue_on_unaligned_matrices(bo):
+    """C, residual and kept z two bytes off and with odd leading dimensions:
+    the element path, against the same call on aligned buffers, bit for bit."""
+    rng = np.random.default_rng(31)
+    M, N, K = 300, 264, 128
+    A, B, _, _ = product(rng, M, N, K, 0, bo, 0)
+    res = torch.from_numpy(val(rand_bf16(rng, (M, N))).astype(np.float32)).to(DEV).to(torch.bfloat16)
+    bias = torch.randn(N, device=DEV)
+    got = []
+    for off, ld in ((0, N), (1, N + 3), (0, N + 1), (3, N + 8)):
+        c, z, r = (torch.full((off + M * ld,), 7.0, dtype=torch.bfloat16, device=DEV)[off:] for _ in range(3))
+        r.view(M, ld)[:, :N] = res
+        o8 = new_saved(M, N)
+        zs.gemm_bf16_epilogue(M, N, K, dev16(A), K, 0, dev16(B), B.shape[1], bo, c, ld, zs.BF16,
+                              zs.Epilogue(bias=bias, act="gelu", residual=r, ldr=ld, preact=zs.Saved(z, ld),
+                                          output=o8))
+        torch.cuda.synchronize()
+        assert (c.view(M, ld)[:, N:] == 7.0).all() and (z.view(M, ld)[:, N:] == 7.0).all()
+        got.append((c.view(M, ld)[:, :N].clone(), z.view(M, ld)[:, :N].clone(), *saved_np(o8, M, N)))
+    for other in got[1:]:
+        assert torch.equal(got[0][0], other[0]) and torch.equal(got[0][1], other[1])
+        assert np.array_equal(got[0][2], other[2]) and np.array_equal(got[0][3], other[3])
+
+
+def test_act_backward_on_unaligned_matrices():
+    rng = np.random.default_rng(32)
+    rows, cols = 150, 264
+    dy0 = torch.from_numpy(val(rand_bf16(rng, (rows, cols))).astype(np.float32)).to(DEV).to(torch.bfloat16)
+    z0 = torch.from_numpy(val(rand_bf16(rng, (rows, cols))).astype(np.float32)).to(DEV).to(torch.bfloat16)
+    work = torch.empty(zs.act_backward_workspace(rows, cols), device=DEV)
+    got = []
+    for off, ld in ((0, cols), (1, cols), (0, cols + 3), (5, cols + 8)):
+        dy, z, dz = (torch.full((off + rows * ld,), 7.0, dtype=torch.bfloat16, device=DEV)[off:] for _ in range(3))
+        dy.view(rows, ld)[:, :cols] = dy0
+        z.view(rows, ld)[:, :cols] = z0
+        db = torch.empty(cols, device=DEV)
+        zs.act_backward(rows, cols, dy, ld, "gelu", zs.Saved(z, ld), dz, ld, db, work)
+        torch.cuda.synchronize()
+        assert (dz.view(rows, ld)[:, cols:] == 7.0).all()
+        got.append((dz.view(rows, ld)[:, :cols].clone(), db))
+    for other in got[1:]:
+        assert torch.equal(got[0][0], other[0]) and torch.equal(got[0][1], other[1])
+
+
+# --------------------------------------------------- offsets past 32 bits --
+
+def test_matrices_past_32_bits_of_offset():
+    """Leading dimensions of 2^26 over 70 rows: 9.4 GB matrices, whose last
+    rows lie past 2^32 bytes and past 2^32 elements."""
+    rng = np.random.default_rng(33)
+    M, N, K, ld = 70, 72, 64, 1 << 26
+    A, B, av, bv = product(rng, M, N, K, 0, 1, 0)
+    C = torch.empty(M * ld, dtype=torch.bfloat16, device=DEV)
+    Z = torch.empty(M * ld, dtype=torch.uint8, device=DEV)
+    zsc = torch.empty(3, 72, dtype=torch.uint8, device=DEV)
+    z8 = zs.Saved(Z, ld, zsc, 72)
+    small = new_saved(M, N)
+    c = torch.empty(M, N, dtype=torch.bfloat16, device=DEV)
+    for out, lo, keep in ((C, ld, z8), (c, N, small)):
+        zs.gemm_bf16_epilogue(M, N, K, dev16(A), K, 0, dev16(B), N, 1, out, lo, zs.BF16,
+                              zs.Epilogue(act="silu", preact=keep))
+    torch.cuda.synchronize()
+    assert torch.equal(C.view(M, ld)[:, :N], c)
+    codes, byte = saved_np(small, M, N)
+    assert np.array_equal(Z.view(M, ld)[:, :N].cpu().numpy(), codes) and np.array_equal(zsc.cpu().numpy(), byte)
+    # the gradient and the checkpoint calls over the same matrices
+    dz = torch.empty(M, N, dtype=torch.bfloat16, device=DEV)
+    want = torch.empty(M, N, dtype=torch.bfloat16, device=DEV)
+    db, dbw = torch.empty(N, device=DEV), torch.empty(N, device=DEV)
+    zs.act_backward(M, N, C, ld, "silu", z8, dz, N, db)
+    zs.act_backward(M, N, c, N, "silu", small, want, N, dbw)
+    again = new_saved(M, N)
+    zs.saved_write(M, N, C, ld, again)
+    first = new_saved(M, N)
+    zs.saved_write(M, N, c, N, first)
+    zs.saved_read(M, N, z8, C, ld)
+    back = torch.empty(M, N, dtype=torch.bfloat16, device=DEV)
+    zs.saved_read(M, N, small, back, N)
+    torch.cuda.synchronize()
+    assert torch.equal(dz, want) and torch.equal(db, dbw)
+    for a, b in zip(saved_np(again, M, N), saved_np(first, M, N)):
+        assert np.array_equal(a, b)
+    assert torch.equal(C.view(M, ld)[:, :N], back)
+    del C, Z
+    torch.cuda.empty_cache()
+
+
+def test_expert_weights_past_32_bits_of_offset():
+    """Three experts' weights 2^31 elements apart, and their dW as far."""
+    rng = np.random.default_rng(34)
+    G, inf, outf, counts, stride = 3, 64, 72, [5, 0, 40], 1 << 31
+    rows, off = sum(counts), np.cumsum([0] + counts)
+    W = torch.empty((G - 1) * stride + inf * outf, dtype=torch.bfloat16, device=DEV)
+    w = dev16(rand_bf16(rng, (G, inf, outf))).view(torch.bfloat16)
+    for e in range(G):
+        W[e * stride:e * stride + inf * outf] = w[e].reshape(-1)
+    x = dev16(rand_bf16(rng, (rows, inf)))
+    offd = torch.from_numpy(off.astype(np.int64)).to(DEV)
+    ys = [torch.empty(rows, outf, device=DEV) for _ in range(2)]
+    zs.gemm_grouped_rows_bf16(G, offd, rows, outf, inf, x, inf, W, outf, 1, stride, ys[0], outf, zs.FP32)
+    zs.gemm_grouped_rows_bf16(G, offd, rows, outf, inf, x, inf, w, outf, 1, inf * outf, ys[1], outf, zs.FP32)
+    dy = dev16(rand_bf16(rng, (rows, outf)))
+    far, near = W.view(torch.bfloat16), torch.empty(G, inf, outf, dtype=torch.bfloat16, device=DEV)
+    zs.gemm_grouped_depth_bf16(G, offd, rows, inf, outf, x, inf, dy, outf, far, outf, stride, zs.BF16)
+    zs.gemm_grouped_depth_bf16(G, offd, rows, inf, outf, x, inf, dy, outf, near, outf, inf * outf, zs.BF16)
+    torch.cuda.synchronize()
+    assert torch.equal(ys[0], ys[1])
+    for e in range(G):
+        assert torch.equal(far[e * stride:e * stride + inf * outf], near[e].reshape(-1))
+    del W, far
+    torch.cuda.empty_cache()
+
+
+def test_a_router_step_replayed_with_every_row_to_one_expert():
+    """Offsets read at replay: all rows to the first, the last, no expert."""
+    rng = np.random.default_rng(35)
+    rows, inf, outf, G = 300, 72, 136, 70
+    w = dev16(rand_bf16(rng, (G, inf, outf), inf ** -0.5))
+    x = dev16(rand_bf16(rng, (rows, inf)))
+    off = torch.zeros(G + 1, dtype=torch.int64, device=DEV)
+    y = torch.zeros(rows, outf, device=DEV)
+    dw = torch.zeros(G, inf, outf, device=DEV)
+    dy = dev16(rand_bf16(rng, (rows, outf)))
+
+    def step():
+        zs.gemm_grouped_rows_bf16(G, off, rows, outf, inf, x, inf, w, outf, 1, inf * outf, y, outf, zs.FP32)
+        zs.gemm_grouped_depth_bf16(G, off, rows, inf, outf, x, inf, dy, outf, dw, outf, inf * outf)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    xv, wv, dyv = val(host16(x)), val(host16(w)).reshape(G, inf, outf), val(host16(dy))
+    for cut in (0, G - 1, 35, None):
+        o = np.zeros(G + 1, np.int64)
+        if cut is not None:
+            o[cut + 1:] = rows
+        off.copy_(torch.from_numpy(o))
+        y.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = layer.grouped_rows(o, xv, wv, np.full((rows, outf), 7.0))
+        bound = linear.gamma(inf) * layer.grouped_rows(o, np.abs(xv), np.abs(wv), np.zeros((rows, outf)))
+        within(y.cpu().numpy(), want, bound, "y")
+        bd = linear.gamma(rows) * layer.grouped_depth(o, np.abs(xv), np.abs(dyv))
+        within(dw.cpu().numpy(), layer.grouped_depth(o, xv, dyv), bd, "dW")
