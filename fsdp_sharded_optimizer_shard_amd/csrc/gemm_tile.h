@@ -580,5 +580,174 @@ __device__ __forceinline__ void gemm_tile_kp(int64_t M, int64_t N, int64_t K,
     epi.template tile16<TM, TN>(acc, m0 + wm, n0 + wn, M, N, lane);
 }
 
+// A K-inner, B K-outer (X W), 256 columns: gemm_tile with A in the 64-k pairs
+// of gemm_tile_kp, whose DMA instructions move whole 128-byte rows of A where a
+// 32-k stage's touch 16 half lines each.  Two pair buffers for A, four stages
+// of 32 k for B, 128 KB as before; the MFMAs and their order are gemm_tile's,
+// so are the results.
+//
+// Tile kt reads half kt % 2 of pair kt / 2.  B of tile kt + 3 goes out at the
+// start of tile kt; a pair's successor in its buffer goes out behind the
+// barrier of its odd tile, when every wave has read it, two tiles ahead of its
+// own first read.  In order of issue: B(2p + 1), B(2p + 2), A(p + 1),
+// B(2p + 3), B(2p + 4), ...; so an even tile, waiting for B(kt + 1), may leave
+// B, A and B in flight, an odd one, waiting for A((kt + 1) / 2) too, two of B.
+template <int BM, class Epi>
+__device__ __forceinline__ void gemm_tile_ap(int64_t M, int64_t N, int64_t K,
+                                             const uint16_t *__restrict__ A, int64_t lda,
+                                             const uint16_t *__restrict__ B, int64_t ldb,
+                                             const Epi &epi, int64_t m0, int64_t n0, ZS_LDS char *A0,
+                                             ZS_LDS char *A1, ZS_LDS char *const (&Bs)[kStages])
+{
+    constexpr int TM = BM / 64, TN = 2, NF = TM + TN, NMF = TM * TN;
+    constexpr int NRD = TM + 2 * TN;
+    constexpr int NPA = BM / (8 * kNW), NIB = Op<kBN, true>::NI;
+
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int wm = (wave >> 2) * (BM / 2), wn = (wave & 3) * (kBN / 4);
+    const int fr = lane & 31, fh = lane >> 5;
+
+    auto Ab = [&](auto pb) -> ZS_LDS char * {
+        if constexpr (decltype(pb)::value == 0) return A0; else return A1;
+    };
+    uint32_t va[NPA], vb[NIB];
+#pragma unroll
+    for (int n = 0; n < NPA; ++n)
+        va[n] = kp_dma_offset(lda, wave, lane, n);
+#pragma unroll
+    for (int n = 0; n < NIB; ++n)
+        vb[n] = dma_offset<kBN, true>(ldb, wave, lane, n);
+    // 16-byte chunk 4 h + 2 s + fh of row wm + fr; 32 rows further the swizzle
+    // is the same.
+    int fa_off[2][2], fb_off[TN][2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            fa_off[h][s] = kp_pos(wm + fr, 4 * h + 2 * s + fh);
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            fb_off[j][s] = frag_offset<kBN, true>(wn + 32 * j, s, lane);
+    }
+
+    f32x16 acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int v = 0; v < 16; ++v)
+                acc[i][j][v] = 0.0f;
+
+    const int64_t kt_n = (K + kBK - 1) / kBK, np_n = (kt_n + 1) / 2, np_full = K / (2 * kBK);
+    auto dma_a = [&](auto pb, auto whole, int64_t p) {
+        constexpr int P = decltype(pb)::value;
+        constexpr bool WHOLE = decltype(whole)::value != 0;
+        const int64_t k0 = p * 2 * kBK;
+        const __amdgpu_buffer_rsrc_t ra = rsrc(A + m0 * lda + k0, ((M - 1 - m0) * lda + K - k0) * 2);
+#pragma unroll
+        for (int n = 0; n < NPA; ++n) {
+            const uint32_t o = !WHOLE && k0 + kp_kofs(wave, lane, n) >= K ? kOOB : va[n];
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                ra, (ZS_LDS void *)(Ab(IC<P>{}) + (wave + kNW * n) * 1024), 16, o, 0, 0, 0);
+        }
+    };
+    auto dma_b = [&](auto st, int64_t kt) {
+        constexpr int S = decltype(st)::value;
+        const int64_t k0 = kt * kBK;
+        const __amdgpu_buffer_rsrc_t rb = rsrc(B + k0 * ldb + n0, ((K - 1 - k0) * ldb + N - n0) * 2);
+#pragma unroll
+        for (int n = 0; n < NIB; ++n)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (ZS_LDS void *)(Bs[S] + (wave + kNW * n) * 1024),
+                                                     16, vb[n], 0, 0, 0);
+    };
+    bf16x8 fa0[TM], fb0[TN], fa1[TM], fb1[TN];
+    auto frags = [&](auto st, auto sub, bf16x8 (&fa)[TM], bf16x8 (&fb)[TN]) {
+        constexpr int S = decltype(st)::value, s = decltype(sub)::value;
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+            fa[i] = *reinterpret_cast<const ZS_LDS bf16x8 *>(Ab(IC<(S >> 1)>{}) + fa_off[S & 1][s] + i * 4096);
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            fb[j] = frag_read<kBN, true>(Bs[S], fb_off[j][s]);
+    };
+    auto mma = [&](const bf16x8 (&fa)[TM], const bf16x8 (&fb)[TN], int lo, int hi) {
+#pragma unroll
+        for (int q = 0; q < NMF; ++q)
+            if (q >= lo && q < hi)
+                acc[q / TN][q % TN] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                    fa[q / TN], fb[q % TN], acc[q / TN][q % TN], 0, 0, 0);
+    };
+    auto tile = [&](auto st, auto steady, int64_t kt) {
+        constexpr int S = decltype(st)::value;
+        constexpr bool STEADY = decltype(steady)::value != 0, ODD = S & 1;
+        constexpr int SN = (S + kStages - 1) % kStages, S1 = (S + 1) % kStages;
+        // what may stay in flight at this tile's wait
+        constexpr int FLY3 = ODD ? 2 * NIB : 2 * NIB + NPA, FLY2 = ODD ? NIB : NIB + NPA;
+        __builtin_amdgcn_sched_barrier(0);
+        if (STEADY || kt + kStages - 1 < kt_n)
+            dma_b(IC<SN>{}, kt + kStages - 1);
+        frags(IC<S>{}, IC<1>{}, fa1, fb1);
+        mma(fa0, fb0, 0, NMF);
+        seq<NF, NMF, NRD, STEADY ? NIB : 0>();
+        mma(fa1, fb1, 0, NMF / 2);
+        __builtin_amdgcn_sched_group_barrier(0x008, NMF / 2, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        if (STEADY || kt + 3 < kt_n)
+            wait_vm_lgkm0<FLY3>();
+        else if (kt + 2 < kt_n)
+            wait_vm_lgkm0<FLY2>();
+        else
+            wait_vm_lgkm0<0>();
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (ODD) {
+            const int64_t p = (kt + 3) / 2;
+            if constexpr (STEADY)
+                dma_a(IC<(S >> 1)>{}, IC<1>{}, p);
+            else if (p < np_n)
+                dma_a(IC<(S >> 1)>{}, IC<0>{}, p);
+        }
+        if (STEADY || kt + 1 < kt_n)
+            frags(IC<S1>{}, IC<0>{}, fa0, fb0);
+        mma(fa1, fb1, NMF / 2, NMF);
+        seq<NF, NMF / 2, NRD, STEADY && ODD ? NPA : 0>();
+    };
+    if (kt_n > 0) {
+        dma_a(IC<0>{}, IC<0>{}, 0);
+        dma_b(IC<0>{}, 0);
+        if (kt_n > 1)
+            dma_b(IC<1>{}, 1);
+        if (kt_n > 2) {
+            dma_b(IC<2>{}, 2);
+            dma_a(IC<1>{}, IC<0>{}, 1);
+            wait_vm_lgkm0<2 * NIB + NPA>();
+        } else {
+            wait_vm_lgkm0<0>();
+        }
+        __builtin_amdgcn_s_barrier();
+        frags(IC<0>{}, IC<0>{}, fa0, fb0);
+        int64_t kt = 0;
+        // steady: the pairs this group issues, (kt + 4) / 2 and (kt + 6) / 2,
+        // lie inside K
+        for (; (kt + 6) / 2 < np_full; kt += kStages) {
+            tile(IC<0>{}, IC<1>{}, kt);
+            tile(IC<1>{}, IC<1>{}, kt + 1);
+            tile(IC<2>{}, IC<1>{}, kt + 2);
+            tile(IC<3>{}, IC<1>{}, kt + 3);
+        }
+        for (; kt < kt_n; kt += kStages) {
+            tile(IC<0>{}, IC<0>{}, kt);
+            if (kt + 1 < kt_n)
+                tile(IC<1>{}, IC<0>{}, kt + 1);
+            if (kt + 2 < kt_n)
+                tile(IC<2>{}, IC<0>{}, kt + 2);
+            if (kt + 3 < kt_n)
+                tile(IC<3>{}, IC<0>{}, kt + 3);
+        }
+    }
+    epi.template tile32<TM, TN>(acc, m0 + wm, n0 + wn, M, N, lane);
+}
+
 }  // namespace
 }  // namespace zs

@@ -406,6 +406,31 @@ __global__ __launch_bounds__(kGT) void epi_kernel(int64_t M, int64_t N, int64_t 
         gemm_tile<BM / 2, BN, A_KOUTER, B_KOUTER>(M, N, K, A, lda, B, ldb, epi, m0, n0, As, Bs);
 }
 
+// X W on 256 x 256 tiles and their halves.
+#define ZS_AP                                                                                      \
+    __shared__ __attribute__((aligned(1024))) char pa0[kPair], pa1[kPair];                         \
+    __shared__ __attribute__((aligned(1024))) char b0[kStage], b1[kStage], b2[kStage], b3[kStage]; \
+    ZS_LDS char *const Bs[kStages] = {(ZS_LDS char *)b0, (ZS_LDS char *)b1, (ZS_LDS char *)b2,     \
+                                      (ZS_LDS char *)b3};                                          \
+    const LayerEpi epi{args, corner((ZS_LDS char *)pa0, (ZS_LDS char *)pa0 + kPair / 2,            \
+                                    (ZS_LDS char *)pa1, (ZS_LDS char *)pa1 + kPair / 2,            \
+                                    (ZS_LDS char *)b0, (ZS_LDS char *)b1, (ZS_LDS char *)b2,       \
+                                    (ZS_LDS char *)b3)}
+
+__global__ __launch_bounds__(kGT) void epi_kernel_ap(int64_t M, int64_t N, int64_t K,
+                                                     const uint16_t *__restrict__ A, int64_t lda,
+                                                     const uint16_t *__restrict__ B, int64_t ldb,
+                                                     EpiArgs args, int tiles_m, int tiles_n, int n_big)
+{
+    ZS_AP;
+    int64_t m0, n0;
+    if (place<kBM, kBN>(tiles_m, tiles_n, n_big, m0, n0))
+        gemm_tile_ap<kBM>(M, N, K, A, lda, B, ldb, epi, m0, n0, (ZS_LDS char *)pa0, (ZS_LDS char *)pa1, Bs);
+    else
+        gemm_tile_ap<kBM / 2>(M, N, K, A, lda, B, ldb, epi, m0, n0, (ZS_LDS char *)pa0, (ZS_LDS char *)pa1,
+                              Bs);
+}
+
 template <int BM, int BN>
 __global__ __launch_bounds__(kGT) void epi_kernel_kp(int64_t M, int64_t N, int64_t K,
                                                      const uint16_t *__restrict__ A, int64_t lda,
@@ -429,14 +454,16 @@ __global__ __launch_bounds__(kGT) void epi_kernel_kp(int64_t M, int64_t N, int64
 // their sums at the end.  Against the 2 x 4 grid of gemm_tile on one K tile
 // at a time, a barrier stands between twice the products and a fragment
 // serves twice as many.  1000 x 4096 x 14336 (256 tiles, every block alone on
-// its CU): 153 -> 141 us with a K-outer B, 203 -> 169 with a K-inner one; one
-// row: 120 -> 95 and 201 -> 126.  What bounds it then is the fetch of operands
-// that no other block shares, 58 GB/s a CU.
+// its CU): 153 -> 126 us with a K-outer B, 203 -> 139 with a K-inner one.  What
+// bounds it then is the fetch of operands that no other block shares, some 60
+// GB/s a CU: 141 us with 64-byte rows of a K-inner operand, 126 with 128.
 //
-// Each half has stages and loads of its own, in step with the other's through
-// the block's barriers: half h holds K tile 2 g + h in stage g % 4, at 16 KB h
-// of the stage's array, A first.  A K tile past the last reads as zeros.
-constexpr int kHalfBytes = 2 * 128 * kBK * 2;  // A and B of one half's stage
+// Stage g % 4 holds K tiles 2 g and 2 g + 1 of both operands, 16 KB each, A
+// first; half h of the waves reads tile 2 g + h.  A K-outer operand's tiles lie
+// one after the other, each fetched by the waves that read it; a K-inner
+// operand is one 64-k pair in gemm_tile_kp's layout, fetched by all waves in
+// whole 128-byte rows.  A K tile past the last reads as zeros.
+constexpr int kTwo = 2 * 128 * kBK * 2;  // bytes of one operand's two tiles
 
 template <bool A_KOUTER, bool B_KOUTER, class Epi>
 __device__ __forceinline__ void gemm_tile_k2(int64_t M, int64_t N, int64_t K,
@@ -457,19 +484,25 @@ __device__ __forceinline__ void gemm_tile_k2(int64_t M, int64_t N, int64_t K,
     int ka[NI];
 #pragma unroll
     for (int n = 0; n < NI; ++n) {
-        va[n] = dma_offset<BM, A_KOUTER>(lda, wave + 4 * n, lane, 0);
-        vb[n] = dma_offset<BN, B_KOUTER>(ldb, wave + 4 * n, lane, 0);
-        ka[n] = dma_kofs(wave + 4 * n, lane, 0);
+        va[n] = A_KOUTER ? dma_offset<BM, true>(lda, wave + 4 * n, lane, 0) : kp_dma_offset(lda, w8, lane, n);
+        vb[n] = B_KOUTER ? dma_offset<BN, true>(ldb, wave + 4 * n, lane, 0) : kp_dma_offset(ldb, w8, lane, n);
+        ka[n] = kp_kofs(w8, lane, n);
     }
+    auto frag_at = [&](auto outer, int w0, int s) {
+        if constexpr (decltype(outer)::value)
+            return half * (kTwo / 2) + frag_offset<128, true>(w0, s, lane);
+        else
+            return kp_pos(w0 + (lane & 31), 4 * half + 2 * s + (lane >> 5));
+    };
     int fa_off[TM][2], fb_off[TN][2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
 #pragma unroll
         for (int i = 0; i < TM; ++i)
-            fa_off[i][s] = half * kHalfBytes + frag_offset<BM, A_KOUTER>(wm + 32 * i, s, lane);
+            fa_off[i][s] = frag_at(IC<A_KOUTER>{}, wm + 32 * i, s);
 #pragma unroll
         for (int j = 0; j < TN; ++j)
-            fb_off[j][s] = half * kHalfBytes + kHalfBytes / 2 + frag_offset<BN, B_KOUTER>(wn + 32 * j, s, lane);
+            fb_off[j][s] = kTwo + frag_at(IC<B_KOUTER>{}, wn + 32 * j, s);
     }
 
     f32x16 acc[TM][TN];
@@ -485,23 +518,23 @@ __device__ __forceinline__ void gemm_tile_k2(int64_t M, int64_t N, int64_t K,
     auto dma = [&](auto st, auto whole, int64_t g) {
         constexpr int S = decltype(st)::value;
         constexpr bool WHOLE = decltype(whole)::value != 0;
-        const int64_t k0 = (2 * g + half) * kBK;
-        const __amdgpu_buffer_rsrc_t ra = A_KOUTER ? rsrc(A + k0 * lda + m0, ((K - 1 - k0) * lda + M - m0) * 2)
+        const int64_t k0 = 2 * g * kBK, kh = k0 + half * kBK;
+        const __amdgpu_buffer_rsrc_t ra = A_KOUTER ? rsrc(A + kh * lda + m0, ((K - 1 - kh) * lda + M - m0) * 2)
                                                    : rsrc(A + m0 * lda + k0, ((M - 1 - m0) * lda + K - k0) * 2);
-        const __amdgpu_buffer_rsrc_t rb = B_KOUTER ? rsrc(B + k0 * ldb + n0, ((K - 1 - k0) * ldb + N - n0) * 2)
+        const __amdgpu_buffer_rsrc_t rb = B_KOUTER ? rsrc(B + kh * ldb + n0, ((K - 1 - kh) * ldb + N - n0) * 2)
                                                    : rsrc(B + n0 * ldb + k0, ((N - 1 - n0) * ldb + K - k0) * 2);
-        ZS_LDS char *d = Ss[S] + half * kHalfBytes;
 #pragma unroll
         for (int n = 0; n < NI; ++n) {
             const uint32_t o = !WHOLE && !A_KOUTER && k0 + ka[n] >= K ? kOOB : va[n];
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (ZS_LDS void *)(d + (wave + 4 * n) * 1024), 16, o, 0,
-                                                     0, 0);
+            ZS_LDS char *d = Ss[S] + (A_KOUTER ? half * (kTwo / 2) + (wave + 4 * n) * 1024 : (w8 + 8 * n) * 1024);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (ZS_LDS void *)d, 16, o, 0, 0, 0);
         }
 #pragma unroll
         for (int n = 0; n < NI; ++n) {
             const uint32_t o = !WHOLE && !B_KOUTER && k0 + ka[n] >= K ? kOOB : vb[n];
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rb, (ZS_LDS void *)(d + kHalfBytes / 2 + (wave + 4 * n) * 1024), 16, o, 0, 0, 0);
+            ZS_LDS char *d = Ss[S] + kTwo +
+                             (B_KOUTER ? half * (kTwo / 2) + (wave + 4 * n) * 1024 : (w8 + 8 * n) * 1024);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (ZS_LDS void *)d, 16, o, 0, 0, 0);
         }
     };
     bf16x8 fa0[TM], fb0[TN], fa1[TM], fb1[TN];
@@ -609,11 +642,11 @@ __global__ __launch_bounds__(kGT) void epi_kernel_k2(int64_t M, int64_t N, int64
                                                      const uint16_t *__restrict__ B, int64_t ldb,
                                                      EpiArgs args, int tiles_m, int tiles_n)
 {
-    __shared__ __attribute__((aligned(1024))) char s0[2 * kHalfBytes], s1[2 * kHalfBytes],
-        s2[2 * kHalfBytes], s3[2 * kHalfBytes];
+    __shared__ __attribute__((aligned(1024))) char s0[2 * kTwo], s1[2 * kTwo],
+        s2[2 * kTwo], s3[2 * kTwo];
     ZS_LDS char *const Ss[kStages] = {(ZS_LDS char *)s0, (ZS_LDS char *)s1, (ZS_LDS char *)s2,
                                       (ZS_LDS char *)s3};
-#define ZS_S(n) (ZS_LDS char *)s##n, (ZS_LDS char *)s##n + kHalfBytes
+#define ZS_S(n) (ZS_LDS char *)s##n, (ZS_LDS char *)s##n + kTwo
     ZS_LDS float *mine = corner(ZS_S(0), ZS_S(1), ZS_S(2), ZS_S(3));
     ZS_LDS float *partner = corner(ZS_S(2), ZS_S(3), ZS_S(0), ZS_S(1));
 #undef ZS_S
@@ -750,13 +783,17 @@ __global__ __launch_bounds__(kGT) void grouped_rows_kernel(const int64_t *__rest
         args.z = static_cast<char *>(args.z) + lo * args.ldz * 2;
     A += lo * lda;
     B += e * stride_b;
-    if constexpr (B_KOUTER) {
+    if constexpr (B_KOUTER && BM == kBM) {
+        ZS_AP;
+        if (half)
+            gemm_tile_ap<kBM / 2>(M, N, K, A, lda, B, ldb, epi, m0, n0, (ZS_LDS char *)pa0, (ZS_LDS char *)pa1,
+                                  Bs);
+        else
+            gemm_tile_ap<kBM>(M, N, K, A, lda, B, ldb, epi, m0, n0, (ZS_LDS char *)pa0, (ZS_LDS char *)pa1, Bs);
+    } else if constexpr (B_KOUTER) {
         ZS_STAGES(BM, BN);
         const LayerEpi epi{args, ZS_CORNER};
-        if (half)
-            gemm_tile<kBM / 2, BN, false, true>(M, N, K, A, lda, B, ldb, epi, m0, n0, As, Bs);
-        else
-            gemm_tile<BM, BN, false, true>(M, N, K, A, lda, B, ldb, epi, m0, n0, As, Bs);
+        gemm_tile<BM, BN, false, true>(M, N, K, A, lda, B, ldb, epi, m0, n0, As, Bs);
     } else {
         ZS_PAIRS(BM, BN);
         const LayerEpi epi{args, ZS_CORNER_KP((BM < BN ? BM : BN) * 64)};
@@ -1231,8 +1268,15 @@ zero_status epilogue_gemm_run(int64_t M, int64_t N, int64_t K, const uint16_t *A
         ZS_EPI(true, true);
     } else if (ao) {
         ZS_EPI(true, false);
+    } else if (bo && !small) {
+        hipLaunchKernelGGL(epi_kernel_ap, g.grid, dim3(kGT), 0, s, M, N, K, A, lda, B, ldb, a, g.tm, g.tn,
+                           g.n_big);
+    } else if (bo && k2) {
+        hipLaunchKernelGGL((epi_kernel_k2<false, true>), g.grid, dim3(kGT), 0, s, M, N, K, A, lda, B, ldb, a,
+                           g.tm, g.tn);
     } else if (bo) {
-        ZS_EPI(false, true);
+        hipLaunchKernelGGL((epi_kernel<128, 128, false, true>), g.grid, dim3(kGT), 0, s, M, N, K, A, lda, B,
+                           ldb, a, g.tm, g.tn, g.n_big);
     } else if (k2) {
         hipLaunchKernelGGL((epi_kernel_k2<false, false>), g.grid, dim3(kGT), 0, s, M, N, K, A, lda, B, ldb,
                            a, g.tm, g.tn);
