@@ -656,6 +656,146 @@ __global__ __launch_bounds__(kGT) void epi_kernel_k2(int64_t M, int64_t N, int64
     gemm_tile_k2<A_KOUTER, B_KOUTER>(M, N, K, A, lda, B, ldb, epi, m0, n0, Ss, mine, partner);
 }
 
+// ------------------------------------------------------------- few rows --
+
+// 32 x 32 tiles for products of few rows, where the weights' bytes are the
+// work and 128 x 128 tiles would leave most CUs without a block: K is split
+// over the block's eight waves, 64 k at a time, each wave with two stages of
+// LDS and loads of its own and no barrier until the sums meet.  A stage of
+// the 32 A rows, or of 32 rows of a K-inner B, is gemm_tile_kp's pair (128-byte
+// rows, swizzled); of a K-outer B it is 64 k rows of 64 bytes as they come: the
+// transposing reads of a half wave take four whole rows, 256 bytes, so they
+// fall on all banks once.  Up to two stages, 128 KB a CU, are in flight.
+constexpr int kSkM = 32, kSkN = 32, kSkK = 64;
+constexpr int kSkOp = 32 * 128;  // bytes of one operand's stage of one wave
+
+template <bool B_KOUTER>
+__global__ __launch_bounds__(kGT) void skinny_kernel(int64_t M, int64_t N, int64_t K,
+                                                     const uint16_t *__restrict__ A, int64_t lda,
+                                                     const uint16_t *__restrict__ B, int64_t ldb,
+                                                     EpiArgs args, int tiles_m)
+{
+    __shared__ __attribute__((aligned(1024))) char s0[kNW * 2 * kSkOp], s1[kNW * 2 * kSkOp];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int b = xcd_order(blockIdx.x, gridDim.x);
+    const int64_t m0 = (int64_t)(b % tiles_m) * kSkM, n0 = (int64_t)(b / tiles_m) * kSkN;
+    const int fr = lane & 31, fh = lane >> 5;
+    auto stage = [&](auto st) -> ZS_LDS char * {
+        if constexpr (decltype(st)::value == 0)
+            return (ZS_LDS char *)s0 + wave * 2 * kSkOp;
+        else
+            return (ZS_LDS char *)s1 + wave * 2 * kSkOp;
+    };
+
+    // A's loads of eight rows; rows past M hold what LDS held and end in rows of
+    // C past M.
+    const int na = M - m0 >= 32 ? 4 : (int)((M - m0 + 7) / 8);
+    uint32_t va[4], vb[4];
+    int ka[4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+        va[n] = kp_dma_offset(lda, n, lane, 0);
+        ka[n] = kp_kofs(n, lane, 0);
+        vb[n] = B_KOUTER ? (uint32_t)(((16 * n + (lane >> 2)) * ldb + 8 * (lane & 3)) * 2)
+                         : kp_dma_offset(ldb, n, lane, 0);
+    }
+    // K tile t of 64 into a stage.
+    auto dma = [&](auto st, int64_t t) {
+        const int64_t k0 = t * kSkK;
+        const __amdgpu_buffer_rsrc_t ra = rsrc(A + m0 * lda + k0, ((M - 1 - m0) * lda + K - k0) * 2);
+        const __amdgpu_buffer_rsrc_t rb = B_KOUTER ? rsrc(B + k0 * ldb + n0, ((K - 1 - k0) * ldb + N - n0) * 2)
+                                                   : rsrc(B + n0 * ldb + k0, ((N - 1 - n0) * ldb + K - k0) * 2);
+        ZS_LDS char *d = stage(st);
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+            if (n < na)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (ZS_LDS void *)(d + n * 1024), 16,
+                                                         k0 + ka[n] >= K ? kOOB : va[n], 0, 0, 0);
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (ZS_LDS void *)(d + kSkOp + n * 1024), 16,
+                                                     !B_KOUTER && k0 + ka[n] >= K ? kOOB : vb[n], 0, 0, 0);
+    };
+    f32x16 acc;
+#pragma unroll
+    for (int v = 0; v < 16; ++v)
+        acc[v] = 0.0f;
+    auto step = [&](auto st, int64_t t, int64_t t_n) {
+        const ZS_LDS char *d = stage(st);
+        // the other stage's na + 4 loads may stay in flight
+        if (t + kNW >= t_n)
+            wait_vm_lgkm0<0>();
+        else if (na == 4)
+            wait_vm_lgkm0<8>();
+        else if (na == 3)
+            wait_vm_lgkm0<7>();
+        else if (na == 2)
+            wait_vm_lgkm0<6>();
+        else
+            wait_vm_lgkm0<5>();
+        bf16x8 fa[4], fb[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            fa[s] = *reinterpret_cast<const ZS_LDS bf16x8 *>(d + kp_pos(fr, 2 * s + fh));
+            if (!B_KOUTER) {
+                fb[s] = *reinterpret_cast<const ZS_LDS bf16x8 *>(d + kSkOp + kp_pos(fr, 2 * s + fh));
+            } else {
+                const int j = lane & 15, kr = 16 * s + 8 * fh + (j >> 2);
+                const int o = kr * 64 + 32 * ((lane >> 4) & 1) + 8 * (j & 3);
+                const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ZS_LDS s16x4 *)(d + kSkOp + o));
+                const s16x4 hi =
+                    __builtin_amdgcn_ds_read_tr16_b64_v4i16((ZS_LDS s16x4 *)(d + kSkOp + o + 4 * 64));
+                const s16x8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                fb[s] = __builtin_bit_cast(bf16x8, v);
+            }
+        }
+        // The stage is overwritten only after every read of it has returned.
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0) alone
+        __builtin_amdgcn_sched_barrier(0);
+        if (t + 2 * kNW < t_n)
+            dma(st, t + 2 * kNW);
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+            acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[s], fb[s], acc, 0, 0, 0);
+    };
+    const int64_t t_n = (K + kSkK - 1) / kSkK;
+    if (wave < t_n)
+        dma(IC<0>{}, wave);
+    if (wave + kNW < t_n)
+        dma(IC<1>{}, wave + kNW);
+    for (int64_t t = wave; t < t_n; t += 2 * kNW) {
+        step(IC<0>{}, t, t_n);
+        if (t + kNW < t_n)
+            step(IC<1>{}, t + kNW, t_n);
+    }
+    // The eight sums, added in the waves' order: 4 KB a wave, each wave adding
+    // two of the sixteen accumulators.
+    __syncthreads();
+    ZS_LDS float *part = (ZS_LDS float *)(ZS_LDS char *)s0;
+#pragma unroll
+    for (int v = 0; v < 16; ++v)
+        part[(wave * 16 + v) * 64 + lane] = acc[v];
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int v = 2 * wave + q;
+        float s = part[v * 64 + lane];
+#pragma unroll
+        for (int w = 1; w < kNW; ++w)
+            s += part[(w * 16 + v) * 64 + lane];
+        part[v * 64 + lane] = s;
+    }
+    __syncthreads();
+    f32x16 sum[1][1];
+#pragma unroll
+    for (int v = 0; v < 16; ++v)
+        sum[0][0][v] = part[v * 64 + lane];
+    // The first wave stores; for the others the tile lies past the last row.
+    const LayerEpi epi{args, (ZS_LDS float *)((ZS_LDS char *)s1 + wave * 2 * kSkOp)};
+    epi.tile32<1, 1>(sum, wave == 0 ? m0 : M, n0, M, N, lane);
+}
+
 // Group e's rows [lo, hi), kept inside [0, rows] whatever the array holds.
 __device__ __forceinline__ void group_range(const int64_t *off, int e, int64_t rows, int64_t &lo, int64_t &hi)
 {
@@ -1247,11 +1387,24 @@ zero_status epilogue_gemm_run(int64_t M, int64_t N, int64_t K, const uint16_t *A
     const EpiArgs a = epi_args(ep, C, ldc, c_dtype);
     const bool ao = a_order == ZERO_K_OUTER, bo = b_order == ZERO_K_OUTER;
     const bool small = small_tiles(M, N);
-    // Under 1024 the halves' final exchange is not earned back: 1 x 520 x 256
-    // takes 8.9 us with it and 7.8 without, 256 x 1024 x 1024 12.0 and 13.0.
+    // Under 1024 the halves' final exchange is not earned back: 1000 x 1000 x 600
+    // with a K-inner B takes 15.3 us with it and 13.9 without.
     const bool k2 = small && K >= 1024;
     const Grid g = small ? tiles(M, N, 128, 128, false) : tiles(M, N, kBM, kBN, true);
     (void)hipGetLastError();
+    // Up to two blocks a CU of 32 x 32 tiles: 1 x 4096 x 14336 takes 55 us so
+    // (K-inner B 31) and 95 in 128 x 128 tiles, 128 x 4096 x 4096 22 and 32,
+    // 256 x 1024 x 1024 7.2 and 13; past that, with 64 x 14336 x 4096, 60 and
+    // 44, 512 x 4096 x 4096 80 and 34.
+    const int64_t sm = (M + kSkM - 1) / kSkM, sn = (N + kSkN - 1) / kSkN;
+    if (!ao && sm <= 2 * cu_count() / sn) {
+        const dim3 grid((unsigned)(sm * sn));
+        if (bo)
+            hipLaunchKernelGGL(skinny_kernel<true>, grid, dim3(kGT), 0, s, M, N, K, A, lda, B, ldb, a, (int)sm);
+        else
+            hipLaunchKernelGGL(skinny_kernel<false>, grid, dim3(kGT), 0, s, M, N, K, A, lda, B, ldb, a, (int)sm);
+        return launched("gemm_epilogue");
+    }
 #define ZS_EPI(AO, BO)                                                                             \
     do {                                                                                           \
         if (k2)                                                                                    \

@@ -194,6 +194,11 @@ CASES = [  # M, N, K, pad, act, bias, residual, c, preact, output
     (1, 136, 1024, 0, "gelu", "bf16", None, "bf16", "bf16", False),
     (200, 328, 1048, 8, "silu", "fp32", "fp32", "bf16", "e4m3", True),
     (136, 120, 4160, 0, "relu", None, "bf16", "fp32", "e4m3", False),
+    (9, 200, 2120, 8, "silu", "bf16", "bf16", "bf16", "e4m3", True),
+    (1050, 1048, 1096, 8, "gelu", "bf16", "bf16", "bf16", "e4m3", True),
+    (1050, 1048, 96, 0, "silu", None, None, "bf16", "bf16", False),
+    (1050, 1048, 1048, 0, "gelu_tanh", "fp32", "bf16", "fp32", "bf16", True),
+    (1050, 1048, 4160, 0, "none", None, "fp32", "bf16", None, False),
     (3104, 2904, 136, 8, "gelu", "bf16", "bf16", "bf16", "e4m3", True),
     (2040, 9448, 72, 0, "silu", "bf16", None, "bf16", "bf16", False),
 ]
@@ -203,9 +208,10 @@ CASES = [  # M, N, K, pad, act, bias, residual, c, preact, output
 @pytest.mark.parametrize("case", CASES, ids=lambda c: f"{c[0]}x{c[1]}x{c[2]}-{c[4]}")
 def test_epilogue_within_bounds(case, ao, bo):
     """On a 256-CU part 3104 x 2904 runs whole 256 x 256 tiles, 2040 x 9448
-    whole and half tiles, the others 128 x 128 ones, from K = 1024 on with K
-    split over the waves: 1024 and 4160 are even numbers of 32 (4160 past the
-    steady loop's), 1048 and 1096 odd ones with a rest."""
+    whole and half tiles, 1050 x 1048 and a K-outer A 128 x 128 ones (from K =
+    1024 on with K split over the halves of a block: 1024 and 4160 are even
+    numbers of 32, 4160 past the steady loop's, 1048 and 1096 odd ones with a
+    rest), the others 32 x 32 ones with K split over the waves."""
     M, N, K, pad, act, bias, res, ct, pre, keep = case
     if ao and M % 8:
         M = -(-M // 8) * 8
