@@ -187,8 +187,9 @@ __device__ __forceinline__ void grouped(int logical, int tiles_m, int tiles_n, i
 }
 
 // The plain epilogue: C in fp32, or rounded to bf16.  STREAM stores fp32 past
-// the caches, for results that nothing reads soon: dW of 64 experts (738 MB)
-// 253 -> 204 us.  Each store of a wave covers whole 128-byte lines.
+// the caches, for results that nothing reads soon: dW of 64 experts of 256 rows
+// (738 MB) 247 -> 238 us, of 8, 4096 x 14336 (1.9 GB), 571 -> 459.  Each store of a
+// wave covers whole 128-byte lines.
 template <bool OUT_BF16, bool STREAM = false>
 struct PlainEpi {
     void *C;

@@ -1550,15 +1550,14 @@ zero_status grouped_depth_run(int32_t n_groups, const int64_t *offsets, int64_t 
 {
     if (M == 0 || N == 0)
         return ZERO_OK;
-    // Two 256 x 128 blocks a CU, three stages each, where the sums are short
-    // (under 512 rows a group on average) and the stores weigh: one block's
-    // stores run under the other's products.  64 groups of 256 rows, 2048 x
-    // 1408: 212 us against 220 with 256 x 256 tiles; 32 of 512: 137 against 145;
-    // but 8 of 1024, 4096 x 14336: 1032 against 986, and of 2048 1988 against
-    // 1752.  Likewise where 256 x 256 tiles would leave half the CUs idle (4
-    // groups of 300 rows, 512 x 512: 13.4 against 17.4 us).
+    // Two 256 x 128 blocks a CU, three stages each, where the sums are so short
+    // (128 rows a group on average) that a block is mostly its stores: 64 groups
+    // of 64 rows, 2048 x 1408: 143 us against 160 with 256 x 256 tiles; of 256
+    // rows 251 against 238, 8 of 512, 4096 x 14336, 707 against 670.  Likewise
+    // where 256 x 256 tiles would leave half the CUs idle (4 groups of 300
+    // rows, 512 x 512: 11.7 against 16.2 us).
     const int64_t wide = n_groups * ((M + kBM - 1) / kBM) * ((N + kBN - 1) / kBN);
-    const bool narrow = rows / n_groups < 512 || 2 * wide <= cu_count();
+    const bool narrow = rows / n_groups <= 128 || 2 * wide <= cu_count();
     const int bn = narrow ? kBN / 2 : kBN;
     const int tm = (int)((M + kBM - 1) / kBM), tn = (int)((N + bn - 1) / bn);
     const dim3 grid((unsigned)((int64_t)n_groups * tm * tn));
