@@ -1,7 +1,13 @@
 // What a linear layer does around its product: the product with bias,
 // activation and residual in its epilogue, the gradient of that epilogue,
 // activations kept in 8 bits for the backward pass, and products grouped by
-// expert.  The products run on the tiles of gemm_tile.h.
+// expert.  The products run on the tiles of gemm_tile.h and on two more for
+// shapes that those leave to a part of the CUs.
+//
+// All of them compute in fp32 from bf16 operands and leave through one
+// epilogue, LayerEpi; which tile a product takes depends on its sizes and on
+// how its operands are stored, and is decided where it is launched, with what
+// was measured on both sides.
 #include <hip/hip_runtime.h>
 
 #include <climits>
@@ -1495,8 +1501,15 @@ zero_status grouped_rows_run(int32_t n_groups, const int64_t *offsets, int64_t r
     if (rows == 0 || N == 0)
         return ZERO_OK;
     const EpiArgs a = epi_args(ep, C, ldc, c_dtype);
-    const bool small = rows / n_groups <= 128 || 2 * most_tiles(n_groups, rows, kBM) * ((N + kBN - 1) / kBN) <=
-                                                     cu_count();
+    // 128 x 128 tiles where 256 x 256 ones would leave half the CUs idle, and
+    // where groups are short and two blocks a CU hide what a tile's start and
+    // end cost.  Measured, 256 against 128: dX of 64 groups of 128 rows, 1408 ->
+    // 2048, 101 and 95 us, of 192 rows 116 and 131; forward (K-outer B, where
+    // gemm_tile_ap keeps up longer) 64 groups of 64 rows, 2048 -> 1408, 88 and 83,
+    // of 128 rows 97 and 103, but 32 of 64 at 4096 -> 4096 182 and 217.
+    const int64_t mean = rows / n_groups;
+    const bool few = 2 * most_tiles(n_groups, rows, kBM) * ((N + kBN - 1) / kBN) <= cu_count();
+    const bool small = few || (b_order == ZERO_K_INNER ? mean <= 128 : mean <= 64 && K <= 2048);
     const int bm = small ? 128 : kBM, bn = small ? 128 : kBN;
     const int tn = (int)((N + bn - 1) / bn);
     const int cus = cu_count();
