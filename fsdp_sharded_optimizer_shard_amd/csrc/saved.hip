@@ -203,6 +203,12 @@ struct ActBackArgs {
 // 8 for codes.  The sums stay in registers over the units, then go through
 // LDS in row order and leave as one row per block, summed by sum_kernel in
 // row order too: no atomics, the same bits every time.
+//
+// 4096 x 14336 with gelu and z in bf16: 71 us, 5.0 TB/s -- a plain copy on the
+// same part runs at 4.8 to 5.0 -- and 5 us for the sums of the 32 blocks.
+// Besides memory the vector unit bounds it: gelu's slope is some 30 issue slots
+// an element (its exponential and reciprocal go at a quarter of the rate), 42 us
+// of the 71.
 // ZF 0: no activation, 1: z in bf16, 2: z in 8 bits.
 template <int ZF, int ACT>
 __global__ __launch_bounds__(256) void act_backward_kernel(ActBackArgs p)
