@@ -1403,7 +1403,9 @@ zero_status epilogue_gemm_run(int64_t M, int64_t N, int64_t K, const uint16_t *A
     // 256 x 1024 x 1024 7.2 and 13; past that, with 64 x 14336 x 4096, 60 and
     // 44, 512 x 4096 x 4096 80 and 34.
     const int64_t sm = (M + kSkM - 1) / kSkM, sn = (N + kSkN - 1) / kSkN;
-    if (!ao && sm <= 2 * cu_count() / sn) {
+    // A stage of its K-outer B spans 64 k rows: half the leading dimension that
+    // 32-bit offsets allow the others.
+    if (!ao && sm <= 2 * cu_count() / sn && (!bo || ldb <= (int64_t(1) << 24))) {
         const dim3 grid((unsigned)(sm * sn));
         if (bo)
             hipLaunchKernelGGL(skinny_kernel<true>, grid, dim3(kGT), 0, s, M, N, K, A, lda, B, ldb, a, (int)sm);

@@ -901,3 +901,53 @@ def test_a_router_step_replayed_with_every_row_to_one_expert():
         within(y.cpu().numpy(), want, bound, "y")
         bd = linear.gamma(rows) * layer.grouped_depth(o, np.abs(xv), np.abs(dyv))
         within(dw.cpu().numpy(), layer.grouped_depth(o, xv, dyv), bd, "dW")
+
+
+@pytest.mark.parametrize("M,N,K,lda,bo,ldb", [
+    (40, 136, 72, 1 << 22, 1, 1 << 24),          # 32 x 32 tiles, B at their limit
+    (40, 136, 72, 1 << 22, 1, 1 << 25),          # past it
+    (40, 136, 72, 1 << 22, 0, 1 << 22),
+    (520, 1048, 1096, 1 << 22, 0, 1 << 22),      # K split over a block's halves
+    (2304, 9000, 72, 1 << 22, 1, 1 << 25),       # 256 x 256 tiles and halves
+])
+def test_epilogue_at_the_leading_dimension_limits(M, N, K, lda, bo, ldb):
+    """The largest leading dimensions that the host accepts, on every tile
+    that a product with an epilogue can take."""
+    rng = np.random.default_rng(M + K)
+    a, b = rand_bf16(rng, (M, K)), rand_bf16(rng, (N, K), K ** -0.5)
+    A = torch.empty((M, lda), dtype=torch.int16, device=DEV)
+    A[:, :K] = dev16(a)
+    B = torch.empty((K if bo else N, ldb), dtype=torch.int16, device=DEV)
+    if bo:
+        B[:, :N] = dev16(np.ascontiguousarray(b.T))
+    else:
+        B[:, :K] = dev16(b)
+    C = torch.full((M, N), 7.0, device=DEV)
+    zs.gemm_bf16_epilogue(M, N, K, A, lda, 0, B, ldb, bo, C, N, zs.FP32)
+    torch.cuda.synchronize()
+    got = C.cpu().numpy()
+    del A, B
+    torch.cuda.empty_cache()
+    av, bv = val(a), val(b)
+    within(got, av @ bv.T, linear.gemm_bound(av, bv.T), "C")
+
+
+def test_saved_product_at_the_leading_dimension_limits():
+    rng = np.random.default_rng(36)
+    for M, N, K in ((136, 264, 40), (2304, 9000, 40)):
+        x = rand_bf16(rng, (K, M))
+        b = rand_bf16(rng, (K, N))
+        ld = 1 << 25
+        codes = torch.empty((K, ld), dtype=torch.uint8, device=DEV)
+        s = zs.Saved(codes, ld, torch.empty((2, M), dtype=torch.uint8, device=DEV), M)
+        zs.saved_write(K, M, dev16(x), M, s)
+        B = torch.empty((K, ld), dtype=torch.int16, device=DEV)
+        B[:, :N] = dev16(b)
+        C = torch.empty((M, N), device=DEV)
+        zs.gemm_saved_bf16(M, N, K, s, B, ld, C, N)
+        torch.cuda.synchronize()
+        xv = layer.decode(codes[:, :M].cpu().numpy(), s.scales.cpu().numpy())
+        del codes, B, s
+        torch.cuda.empty_cache()
+        bv = val(b)
+        within(C.cpu().numpy(), xv.T @ bv, linear.gemm_bound(xv.T, bv), "C")
