@@ -1219,8 +1219,13 @@ __global__ __launch_bounds__(kGT) void saved_kernel(int64_t M, int64_t N, int64_
 
 // The epilogue of an M x N product, checked and translated; `grouped` refuses
 // what needs rows counted from a multiple of 32.
-zero_status epilogue_check(int64_t M, int64_t N, const zero_epilogue *ep, bool grouped)
+zero_status epilogue_check(int64_t M, int64_t N, const void *A, const void *B, const void *C, int64_t ldc,
+                           int32_t c_dtype, const zero_epilogue *ep, bool grouped)
 {
+    if (M == 0 || N == 0)
+        return ZERO_OK;
+    if (C == A || C == B)
+        return fail(ZERO_ERR_INVALID_ARG, "C must not be an operand");
     if (!ep)
         return ZERO_OK;
     if (ep->act < ZERO_ACT_NONE || ep->act > ZERO_ACT_SILU)
@@ -1236,10 +1241,19 @@ zero_status epilogue_check(int64_t M, int64_t N, const zero_epilogue *ep, bool g
         if ((st = check_matrix("residual", ep->residual, ep->ldr, N, ep->residual_dtype)) != ZERO_OK ||
             (st = check_extent(M, N, ep->ldr)) != ZERO_OK)
             return st;
+        if (ep->residual == C && (ep->residual_dtype != c_dtype || ep->ldr != ldc))
+            return fail(ZERO_ERR_INVALID_ARG, "a residual in place of C needs C's type and leading dimension");
     }
+    // What is kept must not lie where the product still reads or writes.
+    auto apart = [&](const zero_saved *s, const zero_saved *other) {
+        return s->data != C && s->data != A && s->data != B && s->data != ep->residual &&
+               s->data != ep->bias && (!other || s->data != other->data);
+    };
     if (ep->preact) {
         if ((st = saved_check("preact", ep->preact, M, N)) != ZERO_OK)
             return st;
+        if (!apart(ep->preact, ep->output))
+            return fail(ZERO_ERR_INVALID_ARG, "preact needs a buffer of its own");
         if (grouped && ep->preact->format != ZERO_SAVED_BF16)
             return fail(ZERO_ERR_UNSUPPORTED, "a grouped product keeps its pre-activation in bf16 only");
     }
@@ -1250,6 +1264,8 @@ zero_status epilogue_check(int64_t M, int64_t N, const zero_epilogue *ep, bool g
             return st;
         if (ep->output->format != ZERO_SAVED_E4M3)
             return fail(ZERO_ERR_UNSUPPORTED, "output is kept in 8 bits only");
+        if (!apart(ep->output, ep->preact))
+            return fail(ZERO_ERR_INVALID_ARG, "output needs a buffer of its own");
     }
     return ZERO_OK;
 }
@@ -1338,6 +1354,8 @@ zero_status gemm_saved_check(int64_t M, int64_t N, int64_t K, const zero_saved *
         (st = check_matrix("B", B, ldb, N, ZERO_BF16)) != ZERO_OK ||
         (st = check_matrix("C", C, ldc, N, c_dtype)) != ZERO_OK)
         return st;
+    if (C == A->data || C == B)
+        return fail(ZERO_ERR_INVALID_ARG, "C must not be an operand");
     if (M % 8 || N % 8 || ldb % 8 || A->ld % 8)
         return fail(ZERO_ERR_UNSUPPORTED, "a product from a kept operand needs M, N and the leading "
                     "dimensions multiples of 8");
@@ -1480,7 +1498,7 @@ zero_status grouped_rows_check(int32_t n_groups, const int64_t *offsets, int64_t
     zero_status st;
     if ((st = grouped_check(n_groups, offsets, rows)) != ZERO_OK ||
         (st = gemm_check(rows, N, K, A, lda, ZERO_K_INNER, B, ldb, b_order, C, ldc, c_dtype)) != ZERO_OK ||
-        (st = epilogue_check(rows, N, ep, true)) != ZERO_OK)
+        (st = epilogue_check(rows, N, A, B, C, ldc, c_dtype, ep, true)) != ZERO_OK)
         return st;
     if (rows == 0 || N == 0)
         return ZERO_OK;
@@ -1548,6 +1566,8 @@ zero_status grouped_depth_check(int32_t n_groups, const int64_t *offsets, int64_
         return st;
     if (M == 0 || N == 0)
         return ZERO_OK;
+    if (C == A || C == B)
+        return fail(ZERO_ERR_INVALID_ARG, "C must not be an operand");
     if (n_groups > 1 && stride_c < (M - 1) * ldc + N)
         return fail(ZERO_ERR_INVALID_ARG, "stride_c must be at least %lld (got %lld)",
                     (long long)((M - 1) * ldc + N), (long long)stride_c);
@@ -1606,7 +1626,7 @@ zero_status zero_gemm_bf16_epilogue(int64_t M, int64_t N, int64_t K, const uint1
 {
     zero_status st;
     if ((st = zs::gemm_check(M, N, K, A, lda, a_order, B, ldb, b_order, C, ldc, c_dtype)) != ZERO_OK ||
-        (st = zs::epilogue_check(M, N, epilogue, false)) != ZERO_OK)
+        (st = zs::epilogue_check(M, N, A, B, C, ldc, c_dtype, epilogue, false)) != ZERO_OK)
         return st;
     return zs::epilogue_gemm_run(M, N, K, A, lda, a_order, B, ldb, b_order, C, ldc, c_dtype, epilogue,
                                  static_cast<hipStream_t>(stream));

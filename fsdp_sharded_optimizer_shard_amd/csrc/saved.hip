@@ -378,6 +378,13 @@ zero_status act_backward_check(int64_t rows, int64_t cols, const void *dy, int64
             return fail(ZERO_ERR_INVALID_ARG, "dz is required");
         if (dz && (st = check_matrix("dz", dz, ldz, cols, ZERO_BF16)) != ZERO_OK)
             return st;
+        // In place of dy or of a bf16 z each element is read before it is
+        // written; with another type or row length it would not be.
+        if (dz && dz == dy && (dy_dtype != ZERO_BF16 || ldz != ldy))
+            return fail(ZERO_ERR_INVALID_ARG, "dz in place of dy needs bf16 and the same leading dimension");
+        if (dz && act != ZERO_ACT_NONE && dz == preact->data &&
+            (preact->format != ZERO_SAVED_BF16 || ldz != preact->ld))
+            return fail(ZERO_ERR_INVALID_ARG, "dz in place of preact needs bf16 and the same leading dimension");
     }
     if (!aligned(dbias, 4) || !aligned(workspace, 4))
         return fail(ZERO_ERR_ALIGNMENT, "dbias and workspace must be 4-byte aligned");
@@ -457,6 +464,8 @@ zero_status zero_saved_write(int64_t rows, int64_t cols, const void *x, int64_t 
         return st;
     if (out->format != ZERO_SAVED_E4M3)
         return fail(ZERO_ERR_UNSUPPORTED, "only the 8-bit format is written from a matrix");
+    if (out->data == x)
+        return fail(ZERO_ERR_INVALID_ARG, "a checkpoint needs a buffer of its own");
     const int64_t cw = (cols + 127) / 128, rb = (rows + 31) / 32;
     if (rb > int64_t(0x7fffffff) / 64 / cw)
         return fail(ZERO_ERR_UNSUPPORTED, "matrix too large for one launch");
@@ -489,6 +498,8 @@ zero_status zero_saved_read(int64_t rows, int64_t cols, const zero_saved *in, vo
         return st;
     if (in->format != ZERO_SAVED_E4M3)
         return fail(ZERO_ERR_UNSUPPORTED, "only the 8-bit format is read back");
+    if (in->data == out)
+        return fail(ZERO_ERR_INVALID_ARG, "a checkpoint is not read back in place");
     const int64_t cw = (cols + 127) / 128, rb = (rows + 31) / 32;
     if (rb > int64_t(0x7fffffff) / 64 / cw)
         return fail(ZERO_ERR_UNSUPPORTED, "matrix too large for one launch");

@@ -675,7 +675,9 @@ zero_status zero_saved_read(int64_t rows, int64_t cols, const zero_saved *in, vo
                (same type and leading dimension), else it must not overlap C;
      preact    receives z, in either format (E4M3: coded from the fp32 z);
      output    receives C in 8 bits (E4M3), coded from C as stored: the same
-               bytes that zero_saved_write of C would give. */
+               bytes that zero_saved_write of C would give.
+   What a call writes (C, preact, output) needs memory of its own, the
+   residual in place excepted; the same pointer twice is refused. */
 typedef struct zero_epilogue {
     const void *bias;
     const void *residual;
@@ -699,8 +701,8 @@ zero_status zero_gemm_bf16_epilogue(int64_t M, int64_t N, int64_t K, const uint1
        dz[i][j]  = dy[i][j] * act'(preact[i][j])     (bf16)
        dbias[j]  = sum over i of dz[i][j]            (fp32, of the unrounded
                                                       products; NULL: left out)
-   The residual's gradient is dy itself.  dy is bf16 or fp32; dz may be dy
-   (bf16, same leading dimension).  For ZERO_ACT_NONE preact is not read and
+   The residual's gradient is dy itself.  dy is bf16 or fp32; dz may be dy or
+   a bf16 preact (bf16, same leading dimension).  For ZERO_ACT_NONE preact is not read and
    dz may be NULL (dbias alone).  relu'(0) = 0.  The sum runs in a fixed
    order, so dbias has the same bits every time; it needs
    `workspace` of zero_act_backward_workspace(rows, cols) floats (at most

@@ -10,6 +10,8 @@ import torch
 from fsdp_sharded_optimizer_shard_amd import zs
 
 FAKE = 0x7f0000000000
+OUT = FAKE + (1 << 32)          # results, apart from the operands
+KEPT = FAKE + (2 << 32)
 HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
                       "include", "zero_shard.h")
 INV, ALIGN, UNSUP = zs.ERR_INVALID_ARG, zs.ERR_ALIGNMENT, zs.ERR_UNSUPPORTED
@@ -22,7 +24,7 @@ def refused(status, fn, *a, text="", **kw):
     assert text in str(e.value)
 
 
-def s8(ld=64, lds=64, data=FAKE, scales=FAKE):
+def s8(ld=64, lds=64, data=KEPT, scales=KEPT + (1 << 30)):
     return zs.Saved(data, ld, scales, lds)
 
 
@@ -61,7 +63,8 @@ def test_checkpoint_refusals(call):
     bad(UNSUP, saved=zs.Saved(FAKE, 64))            # bf16: nothing to code
     bad(ALIGN, x=FAKE + 1)
     bad(ALIGN, x=FAKE + 2, dtype=zs.FP32)
-    bad(ALIGN, saved=s8(data=FAKE + 8))
+    bad(ALIGN, saved=s8(data=KEPT + 8))
+    bad(INV, saved=s8(data=FAKE))                   # in place
     bad(UNSUP, rows=1 << 50)
     bad(UNSUP, rows=1 << 36, cols=64)               # one launch cannot hold it
     go(rows=0)                                      # nothing to do
@@ -73,7 +76,7 @@ def epi(**kw):
 
 
 def test_epilogue_refusals():
-    def bad(status, ep, M=64, N=64, K=64, C=FAKE, ldc=64, text="", **kw):
+    def bad(status, ep, M=64, N=64, K=64, C=OUT, ldc=64, text="", **kw):
         refused(status, zs.gemm_bf16_epilogue, M, N, K, FAKE, max(K, 64), zs.K_INNER, FAKE, 64,
                 zs.K_OUTER, C, ldc, zs.BF16, ep, text=text, **kw)
 
@@ -91,6 +94,14 @@ def test_epilogue_refusals():
     bad(INV, epi(preact=s8(lds=8)))
     bad(UNSUP, epi(output=zs.Saved(FAKE, 64)), text="8 bits")
     bad(ALIGN, epi(output=s8(data=FAKE + 4)))
+    # one buffer for two things
+    bad(INV, epi(), C=FAKE, text="operand")
+    bad(INV, epi(residual=OUT, ldr=72), text="in place")
+    bad(INV, epi(residual=OUT, ldr=64, residual_dtype=zs.FP32), text="in place")
+    bad(INV, epi(preact=zs.Saved(OUT, 64)), text="its own")
+    bad(INV, epi(preact=zs.Saved(KEPT, 64), residual=KEPT, ldr=64), text="its own")
+    bad(INV, epi(output=s8(data=OUT)), text="its own")
+    bad(INV, epi(preact=s8(), output=s8()), text="its own")
     # the product's own limits still hold
     bad(UNSUP, epi(), K=60)
     bad(INV, epi(), C=None)
@@ -103,9 +114,9 @@ def test_epilogue_refusals():
 
 
 def test_act_backward_refusals():
-    def bad(status, rows=200, cols=64, dy=FAKE, ldy=64, act="gelu", z="bf16", dz=FAKE, ldz=64,
+    def bad(status, rows=200, cols=64, dy=FAKE, ldy=64, act="gelu", z="bf16", dz=OUT, ldz=64,
             dbias=None, work=None, text="", **kw):
-        z = zs.Saved(FAKE, 64) if z == "bf16" else z
+        z = zs.Saved(KEPT, 64) if z == "bf16" else z
         refused(status, zs.act_backward, rows, cols, dy, ldy, act, z, dz, ldz, dbias, work,
                 text=text, **kw)
 
@@ -120,7 +131,11 @@ def test_act_backward_refusals():
     bad(INV, dz=None)
     bad(INV, dz=None, act="none", z=None)           # neither dz nor dbias
     bad(INV, ldz=8)
-    bad(ALIGN, dz=FAKE + 1)
+    bad(ALIGN, dz=OUT + 1)
+    bad(INV, dz=FAKE, ldy=72, text="in place")
+    bad(INV, dz=FAKE, dy_dtype=zs.FP32, text="in place")
+    bad(INV, dz=KEPT, z=s8(), text="in place")
+    bad(INV, dz=KEPT, ldz=72, text="in place")
     bad(ALIGN, dbias=FAKE + 2, work=FAKE)
     bad(ALIGN, dbias=FAKE, work=FAKE + 2)
     bad(INV, dbias=FAKE, text="workspace")
@@ -144,7 +159,7 @@ def test_workspace_size():
 
 
 def test_saved_product_refusals():
-    def bad(status, M=64, N=64, K=100, A=None, B=FAKE, ldb=64, C=FAKE, ldc=64, dt=zs.FP32):
+    def bad(status, M=64, N=64, K=100, A=None, B=FAKE, ldb=64, C=OUT, ldc=64, dt=zs.FP32):
         refused(status, zs.gemm_saved_bf16, M, N, K, A or s8(), B, ldb, C, ldc, dt)
 
     bad(INV, M=-8)
@@ -162,8 +177,10 @@ def test_saved_product_refusals():
     bad(UNSUP, ldb=1 << 26)
     bad(UNSUP, A=s8(ld=1 << 26))
     bad(ALIGN, B=FAKE + 8)
-    bad(ALIGN, C=FAKE + 2)
-    bad(ALIGN, A=s8(data=FAKE + 8))
+    bad(ALIGN, C=OUT + 2)
+    bad(INV, C=FAKE)                                # an operand
+    bad(INV, C=KEPT)
+    bad(ALIGN, A=s8(data=KEPT + 8))
     bad(ALIGN, A=zs.Saved(FAKE + 2, 64))
     bad(UNSUP, A=zs.Saved(FAKE, 68))
     zs.gemm_saved_bf16(0, 64, 100, s8(), FAKE, 64, FAKE, 64, stream=0)
@@ -171,9 +188,9 @@ def test_saved_product_refusals():
 
 def test_grouped_refusals():
     def rows(status, n=4, off=FAKE, rows=100, N=64, K=64, sb=4096, ldb=64, order=zs.K_OUTER, ep=None,
-             lda=64):
+             lda=64, C=OUT):
         refused(status, zs.gemm_grouped_rows_bf16, n, off, rows, N, K, FAKE, lda, FAKE, ldb, order,
-                sb, FAKE, 64, zs.BF16, ep)
+                sb, C, 64, zs.BF16, ep)
 
     rows(INV, n=0)
     rows(INV, rows=-1)
@@ -189,11 +206,12 @@ def test_grouped_refusals():
     rows(UNSUP, ep=epi(preact=s8()))
     rows(UNSUP, ep=epi(output=s8()))
     rows(INV, ep=epi(act=7))
+    rows(INV, C=FAKE)
     zs.gemm_grouped_rows_bf16(4, FAKE, 0, 64, 64, FAKE, 64, FAKE, 64, zs.K_OUTER, 4096, FAKE, 64,
                               stream=0)
 
-    def depth(status, n=4, off=FAKE, rows=101, M=64, N=64, lda=64, sc=4096, ldc=64):
-        refused(status, zs.gemm_grouped_depth_bf16, n, off, rows, M, N, FAKE, lda, FAKE, 64, FAKE,
+    def depth(status, n=4, off=FAKE, rows=101, M=64, N=64, lda=64, sc=4096, ldc=64, C=OUT):
+        refused(status, zs.gemm_grouped_depth_bf16, n, off, rows, M, N, FAKE, lda, FAKE, 64, C,
                 ldc, sc)
 
     depth(INV, n=0)
@@ -206,12 +224,13 @@ def test_grouped_refusals():
     depth(INV, ldc=56)
     depth(UNSUP, sc=1 << 59)
     depth(UNSUP, n=1 << 30)
+    depth(INV, C=FAKE)
 
 
 def test_layer_calls_refuse_before_the_gather():
     L = zs.shard_init_rows("fsdp2", 2, 0, [(64, 32)])
 
-    def fwd(status, shards=(FAKE, FAKE), batch=5, ep=None, y=FAKE):
+    def fwd(status, shards=(FAKE, FAKE), batch=5, ep=None, y=OUT):
         refused(status, zs.fsdp_linear_act_forward, L, 0, list(shards), batch, FAKE, FAKE, y, ep)
 
     fwd(INV, shards=(FAKE, None))
@@ -222,11 +241,11 @@ def test_layer_calls_refuse_before_the_gather():
     with pytest.raises(ValueError):
         zs.fsdp_linear_act_forward(L, 0, [FAKE], 5, FAKE, FAKE, FAKE, stream=0)
 
-    def bwd(status, x=None, act="gelu", z=None, dz=FAKE, dbias=None, work=None, batch=300):
+    def bwd(status, x=None, act="gelu", z=None, dz=KEPT, dbias=None, work=None, batch=300):
         refused(status, zs.fsdp_linear_act_backward, L, 0, [FAKE, FAKE], batch,
-                x or zs.Saved(FAKE, 64), act, z, FAKE, FAKE, dz, FAKE, FAKE, dbias, work)
+                x or zs.Saved(FAKE, 64), act, z, FAKE, FAKE, dz, OUT, OUT, dbias, work)
 
-    z = zs.Saved(FAKE, 32)
+    z = zs.Saved(KEPT + 64, 32)
     bwd(INV, z=None)
     bwd(INV, z=z, dz=None)
     bwd(INV, z=z, dbias=FAKE)                       # no workspace
@@ -236,10 +255,10 @@ def test_layer_calls_refuse_before_the_gather():
     bwd(INV, z=z, batch=-1)
 
     def experts(status, n=2, off=FAKE, ep=None):
-        refused(status, zs.fsdp_experts_forward, L, 0, n, [FAKE, FAKE], off, 10, FAKE, FAKE, FAKE, ep)
+        refused(status, zs.fsdp_experts_forward, L, 0, n, [FAKE, FAKE], off, 10, FAKE, FAKE, OUT, ep)
         if ep is None:
             refused(status, zs.fsdp_experts_backward, L, 0, n, [FAKE, FAKE], off, 10, FAKE, FAKE,
-                    FAKE, FAKE, FAKE)
+                    FAKE, OUT, OUT)
 
     experts(INV, n=0)
     experts(INV, n=3)                               # 64 rows are not 3 experts'

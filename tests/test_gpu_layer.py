@@ -951,3 +951,64 @@ def test_saved_product_at_the_leading_dimension_limits():
         torch.cuda.empty_cache()
         bv = val(b)
         within(C.cpu().numpy(), xv.T @ bv, linear.gemm_bound(xv.T, bv), "C")
+
+
+@pytest.mark.parametrize("batch,with_bias", [(1, True), (70, False), (133, True)])
+def test_layer_without_activation_uses_dy(batch, with_bias):
+    """act = none, bf16 x: no dz buffer, dbias alone from the elementwise pass."""
+    rng = np.random.default_rng(batch)
+    n, inf, outf = 2, 72, 136
+    L = zs.shard_init_rows("fsdp2", n, 0, [(inf, outf)])
+    c, Lu = L.shard_len // outf, L.query(0)["padded_len"]
+    w = rand_bf16(rng, (inf, outf))
+    shards = _shards(rng, w, n, c, outf)
+    x, dy = rand_bf16(rng, (batch, inf)), rand_bf16(rng, (batch, outf))
+    w_full = torch.empty(Lu, dtype=torch.int16, device=DEV)
+    dx, dw = torch.empty(batch, inf, device=DEV), torch.full((Lu,), 9.0, device=DEV)
+    db = torch.full((outf,), 9.0, device=DEV) if with_bias else None
+    work = torch.empty(max(1, zs.act_backward_workspace(batch, outf)), device=DEV)
+    zs.fsdp_linear_act_backward(L, 0, shards, batch, zs.Saved(dev16(x), inf), "none", None, dev16(dy), w_full,
+                                None, dx, dw, db, work, zs.FP32)
+    torch.cuda.synchronize()
+    xv, dyv, wv = val(x), val(dy), val(w)
+    within(dx.cpu().numpy(), dyv @ wv.T, linear.gemm_bound(dyv, wv.T), "dx")
+    within(dw.cpu().numpy().reshape(-1, outf)[:inf], xv.T @ dyv, linear.gemm_bound(xv.T, dyv), "dW")
+    if with_bias:
+        within(db.cpu().numpy(), dyv.sum(0), linear.gamma(batch) * np.abs(dyv).sum(0), "dbias")
+
+
+def test_gradient_in_place_of_the_kept_z():
+    rng = np.random.default_rng(41)
+    rows, cols = 333, 200
+    dy = dev16(rand_bf16(rng, (rows, cols)))
+    z = dev16(rand_bf16(rng, (rows, cols)))
+    apart = torch.empty(rows, cols, dtype=torch.int16, device=DEV)
+    zs.act_backward(rows, cols, dy, cols, "gelu", zs.Saved(z, cols), apart, cols)
+    zs.act_backward(rows, cols, dy, cols, "gelu", zs.Saved(z, cols), z, cols)
+    torch.cuda.synchronize()
+    assert torch.equal(apart, z)
+
+
+def test_empty_batches_and_experts_without_rows():
+    """batch 0 and rows 0: dW and dbias are zeros, nothing else is written."""
+    n, inf, outf = 2, 64, 72
+    L = zs.shard_init_rows("fsdp2", n, 1, [(inf, outf)])
+    Lu = L.query(0)["padded_len"]
+    shards = [torch.zeros(L.shard_len, dtype=torch.int16, device=DEV) for _ in range(n)]
+    one = torch.full((8,), 7, dtype=torch.int16, device=DEV)
+    w_full = torch.empty(Lu, dtype=torch.int16, device=DEV)
+    dw, db = torch.full((Lu,), 9.0, device=DEV), torch.full((outf,), 9.0, device=DEV)
+    out = torch.full((8,), 7.0, device=DEV)
+    zs.fsdp_linear_act_forward(L, 0, shards, 0, one, w_full, out, zs.Epilogue(act="silu"), zs.FP32)
+    zs.fsdp_linear_act_backward(L, 0, shards, 0, zs.Saved(one, inf), "silu", zs.Saved(one, outf), one, w_full,
+                                torch.empty(8, dtype=torch.int16, device=DEV), out, dw, db, None, zs.FP32)
+    torch.cuda.synchronize()
+    assert not dw.cpu().numpy().any() and not db.cpu().numpy().any()
+    off = torch.zeros(3, dtype=torch.int64, device=DEV)
+    dw.fill_(9.0)
+    E = zs.shard_init_rows("fsdp2", n, 1, [(2 * 32, outf)])
+    zs.fsdp_experts_forward(E, 0, 2, shards, off, 0, one, w_full, out, None, zs.FP32)
+    zs.fsdp_experts_backward(E, 0, 2, shards, off, 0, one, one, w_full, out, dw, zs.FP32)
+    torch.cuda.synchronize()
+    assert not dw.cpu().numpy().any()
+    assert (out == 7.0).all() and (one == 7).all()
