@@ -37,7 +37,8 @@ HBM_PEAK_GBPS = 8000.0
 COUNTERS = os.path.join(ROOT, "profiles", "fused_step_7b_n8_counters.md")
 KERNELS_SRC = os.path.join(ROOT, "fsdp_sharded_optimizer_shard_amd", "csrc", "kernels.hip")
 GEMM_COUNTERS = os.path.join(ROOT, "profiles", "gemm_fsdp_linear_mistral_up_counters.md")
-GEMM_SRC = os.path.join(ROOT, "fsdp_sharded_optimizer_shard_amd", "csrc", "gemm.hip")
+GEMM_SRC = tuple(os.path.join(ROOT, "fsdp_sharded_optimizer_shard_amd", "csrc", f)
+                 for f in ("gemm.hip", "gemm_tile.h"))
 HEADLINE_METRIC = "shard optimizer-step params/sec at 7B N=8; achieved HBM GB/s vs peak"
 
 
@@ -1070,12 +1071,14 @@ def counter_traffic(path=COUNTERS, src=KERNELS_SRC, sha_key="kernels_hip_sha256"
                     key="fused_traffic_bytes_per_launch"):
     """HBM bytes from a committed rocprofv3 FETCH_SIZE / WRITE_SIZE summary
     (already scaled by the copy calibration), or None if that summary was
-    taken on a different version of the kernel source."""
+    taken on a different version of the kernel source (a file, or several
+    hashed one after the other)."""
     import hashlib
+    files = (src,) if isinstance(src, str) else src
     try:
         kv = dict(line.split(": ", 1) for line in open(path).read().splitlines()
                   if line.startswith((sha_key + ": ", key + ": ")))
-        sha = hashlib.sha256(open(src, "rb").read()).hexdigest()
+        sha = hashlib.sha256(b"".join(open(f, "rb").read() for f in files)).hexdigest()
         if kv.get(sha_key) != sha:
             return None
         return float(kv[key])
