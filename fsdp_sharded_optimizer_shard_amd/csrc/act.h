@@ -101,7 +101,7 @@ __device__ __forceinline__ float act_slope(float z)
 {
     float q;
     if constexpr (ACT == ZERO_ACT_RELU) {
-        return z > 0.0f ? 1.0f : 0.0f;
+        return z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z;
     } else if constexpr (ACT == ZERO_ACT_GELU) {
         const float c = normal_cdf(z, q);
         return __builtin_fmaf(bound64(z) * kInvSqrt2Pi, q, c);

@@ -1247,7 +1247,9 @@ zero_status epilogue_check(int64_t M, int64_t N, const void *A, const void *B, c
     // What is kept must not lie where the product still reads or writes.
     auto apart = [&](const zero_saved *s, const zero_saved *other) {
         return s->data != C && s->data != A && s->data != B && s->data != ep->residual &&
-               s->data != ep->bias && (!other || s->data != other->data);
+               s->data != ep->bias && (!other || s->data != other->data) &&
+               !(other && s->format == ZERO_SAVED_E4M3 && other->format == ZERO_SAVED_E4M3 &&
+                 s->scales == other->scales);
     };
     if (ep->preact) {
         if ((st = saved_check("preact", ep->preact, M, N)) != ZERO_OK)

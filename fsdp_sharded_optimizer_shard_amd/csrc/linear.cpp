@@ -200,6 +200,9 @@ zero_status zero_fsdp_linear_act_backward(const zero_layout *L, int32_t unit,
         (st = zs::gemm_saved_check(d.in, d.out, batch, x, g, d.out, dw_full, d.out,
                                    ZERO_FP32)) != ZERO_OK)
         return st;
+    if (batch > 0 && (dx == g || dx == x->data || dx == w_full ||
+                      (g == dz && (dz == x->data || dz == w_full))))
+        return zs::fail(ZERO_ERR_INVALID_ARG, "dx and dz must not lie where x, w_full or dz is still read");
     const hipStream_t s = static_cast<hipStream_t>(stream);
     if ((st = zero_gather_params(L, unit, unit + 1, w_shards, L->parts, w_full, stream)) != ZERO_OK)
         return st;
@@ -267,6 +270,8 @@ zero_status zero_fsdp_experts_backward(const zero_layout *L, int32_t unit, int32
         (st = zs::grouped_depth_check(n_experts, offsets, rows, d.in, d.out, x, d.in, dy, d.out,
                                       dw_full, d.out, stride, ZERO_FP32)) != ZERO_OK)
         return st;
+    if (rows > 0 && dx == x)
+        return zs::fail(ZERO_ERR_INVALID_ARG, "dx must not lie where x is still read");
     const hipStream_t s = static_cast<hipStream_t>(stream);
     if ((st = zero_gather_params(L, unit, unit + 1, w_shards, L->parts, w_full, stream)) != ZERO_OK)
         return st;

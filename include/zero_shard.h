@@ -702,9 +702,9 @@ zero_status zero_gemm_bf16_epilogue(int64_t M, int64_t N, int64_t K, const uint1
        dbias[j]  = sum over i of dz[i][j]            (fp32, of the unrounded
                                                       products; NULL: left out)
    The residual's gradient is dy itself.  dy is bf16 or fp32; dz may be dy or
-   a bf16 preact (bf16, same leading dimension).  For ZERO_ACT_NONE preact is not read and
-   dz may be NULL (dbias alone).  relu'(0) = 0.  The sum runs in a fixed
-   order, so dbias has the same bits every time; it needs
+   a bf16 preact (bf16, same leading dimension).  For ZERO_ACT_NONE preact is
+   not read and dz may be NULL (dbias alone).  relu'(0) = 0; act'(NaN) is NaN.
+   The sum runs in a fixed order, so dbias has the same bits every time; it needs
    `workspace` of zero_act_backward_workspace(rows, cols) floats (at most
    64 cols; 0 up to 128 rows, and the workspace may then be NULL), used
    until the call's work has run: calls that overlap in time, and captured
@@ -757,8 +757,10 @@ zero_status zero_gemm_grouped_depth_bf16(int32_t n_groups, const int64_t *offset
                keeping what the epilogue names.
      backward: w_full again; dz = dy act'(preact); dbias; dx = dz W^T;
                dw_full = x^T dz from the kept x (bf16 or 8 bits), padding
-               rows zeroed.  dz is a batch x out bf16 buffer (it may be dy);
-               for ZERO_ACT_NONE it may be NULL and dy is used as it is.
+               rows zeroed.  dz is a batch x out bf16 buffer (it may be dy or a
+               bf16 preact); for ZERO_ACT_NONE it may be NULL and dy is used as
+               it is.  x and dz are read last, for dW: dz needs memory apart
+               from x, dx from both.
                dbias may be NULL; workspace as zero_act_backward.
    batch is any number here; otherwise as zero_fsdp_linear_*. */
 zero_status zero_fsdp_linear_act_forward(const zero_layout *layout, int32_t unit,
@@ -781,7 +783,8 @@ zero_status zero_fsdp_linear_act_backward(const zero_layout *layout, int32_t uni
      backward: w_full again; dx = grouped dy W_e^T; dw_full = the experts' dW
                one after the other (fp32, the padded unit), ready for
                zero_reduce_shard and zero_adam_step.
-   in and out multiples of 8.  Rows in no group keep their y and dx. */
+   in and out multiples of 8; dx needs memory apart from x and dy.  Rows in no
+   group keep their y and dx. */
 zero_status zero_fsdp_experts_forward(const zero_layout *layout, int32_t unit,
                                       int32_t n_experts, const uint16_t *const *w_shards,
                                       const int64_t *offsets, int64_t rows, const uint16_t *x,

@@ -54,7 +54,7 @@ def slope(name: str, z: np.ndarray) -> np.ndarray:
     if name == "none":
         return np.ones_like(z)
     if name == "relu":
-        return np.where(z > 0, 1.0, 0.0)
+        return np.where(z > 0, 1.0, np.where(z <= 0, 0.0, z))
     if name == "gelu":
         return 0.5 * erfc(-c / math.sqrt(2)) + c * np.exp(-c * c / 2) / math.sqrt(2 * math.pi)
     if name == "gelu_tanh":

@@ -321,3 +321,36 @@ def test_tensors_are_checked_before_the_call():
     with pytest.raises(ValueError, match="workspace"):
         zs.act_backward(300, 8, x, 8, "relu", zs.Saved(OnDevice(2400, bf), 8), x, 8,
                         OnDevice(8, torch.float32), OnDevice(23, torch.float32), stream=0)
+
+
+def test_layer_gradients_refuse_results_over_what_is_still_read():
+    """dx and dz of a layer's backward pass in the buffer of the kept x: dW
+    reads x after both are written.  fsdp2 of (64, 64): all shapes agree."""
+    L = zs.shard_init_rows("fsdp2", 2, 0, [(64, 64)])
+    W, X, DY, DZ, Z = (FAKE + (i << 28) for i in range(5))
+
+    def bwd(x=zs.Saved(X, 64), act="gelu", z=zs.Saved(Z, 64), dy=DY, dz=DZ, dx=OUT, w=W):
+        refused(INV, zs.fsdp_linear_act_backward, L, 0, [KEPT, KEPT + 4096], 40, x, act, z, dy, w, dz,
+                dx, OUT + (1 << 28), text="still read")
+
+    bwd(dx=X)
+    bwd(dx=DZ)
+    bwd(dx=W)
+    bwd(dx=DY, act="none", z=None, dz=None)
+    bwd(dz=X)
+    bwd(dz=W)
+    bwd(dz=DY, dx=DY)
+
+    def experts(dx=OUT, x=X, w=W):
+        refused(INV, zs.fsdp_experts_backward, L, 0, 2, [KEPT, KEPT + 4096], FAKE - 4096, 40, x, DY, w,
+                dx, OUT + (1 << 28), text="dx must" if dx == X else "operand")
+
+    experts(dx=X)
+    experts(dx=DY)
+    experts(dx=W)
+
+
+def test_kept_matrices_do_not_share_their_scales():
+    ep = epi(preact=s8(data=KEPT), output=s8(data=KEPT + (1 << 20)))
+    refused(INV, zs.gemm_bf16_epilogue, 64, 64, 64, FAKE, 64, zs.K_INNER, FAKE, 64, zs.K_OUTER, OUT, 64,
+            zs.BF16, ep, text="its own")

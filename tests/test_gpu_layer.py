@@ -1012,3 +1012,26 @@ def test_empty_batches_and_experts_without_rows():
     torch.cuda.synchronize()
     assert not dw.cpu().numpy().any()
     assert (out == 7.0).all() and (one == 7).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("act", layer.ACTS)
+def test_a_pre_activation_that_is_not_a_number_gives_no_gradient(act, fmt):
+    """NaN in z is NaN in dz and in its column's dbias, and nowhere else,
+    under every activation with a slope; without one z is not read."""
+    rows, cols = 40, 24
+    rng = np.random.default_rng(5)
+    zb, dyb = rand_bf16(rng, (rows, cols), 2.0), rand_bf16(rng, (rows, cols), 1.0)
+    bad = np.zeros((rows, cols), bool)
+    bad[3, 5] = bad[39, 23] = True
+    zb[bad] = 0x7FC0
+    kept = zs.Saved(dev16(zb), cols)
+    if fmt == "e4m3":
+        kept = new_saved(rows, cols, 0, 0)
+        zs.saved_write(rows, cols, dev16(zb), cols, kept)
+    dz = torch.empty(rows, cols, dtype=torch.bfloat16, device=DEV)
+    db = torch.empty(cols, device=DEV)
+    zs.act_backward(rows, cols, dev16(dyb).view(torch.bfloat16), cols, act, kept, dz, cols, db)
+    want = bad if act != "none" else np.zeros_like(bad)
+    assert np.array_equal(np.isnan(dz.float().cpu().numpy()), want)
+    assert np.array_equal(np.isnan(db.cpu().numpy()), want.any(0))
