@@ -802,6 +802,164 @@ __global__ __launch_bounds__(kGT) void skinny_kernel(int64_t M, int64_t N, int64
     epi.tile32<1, 1>(sum, wave == 0 ? m0 : M, n0, M, N, lane);
 }
 
+// The same for a K-outer B of many columns: 64 of them, so that its k rows come
+// in whole 128-byte lines, 32 k at a time, three stages a wave (6 KB each, 144 KB
+// a CU).  A's rows lie as in gemm_tile's 32-k stage; the 64-byte half h of B's k
+// row r sits at h ^ ((r >> 1) & 1), so that the four rows a half wave reads at
+// once fall on all banks.  1 x 14336 x 4096: 27 us, 4.3 TB/s of weights, against 37
+// in 32 columns; 32 rows 31 and 42, 64 x 8192 x 8192 46 and 60, 128 x 4096 x 4096 16
+// and 21.  With fewer blocks than that makes, 32 columns keep more CUs loading: 1
+// x 4096 x 14336 (64 blocks) 60 and 54, 64 x 4096 x 4096 (128) 16.1 and 13.4, 1 x
+// 8192 x 28672 (128) 125 and 113.
+constexpr int kOuN = 64, kOuStages = 3;
+constexpr int kOuA = 32 * kBK * 2, kOuStage = kOuA + kBK * kOuN * 2;  // bytes of one wave
+
+__global__ __launch_bounds__(kGT) void skinny_outer_kernel(int64_t M, int64_t N, int64_t K,
+                                                           const uint16_t *__restrict__ A, int64_t lda,
+                                                           const uint16_t *__restrict__ B, int64_t ldb,
+                                                           EpiArgs args, int tiles_m)
+{
+    __shared__ __attribute__((aligned(1024))) char s0[kNW * kOuStage], s1[kNW * kOuStage], s2[kNW * kOuStage];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int b = xcd_order(blockIdx.x, gridDim.x);
+    const int64_t m0 = (int64_t)(b % tiles_m) * kSkM, n0 = (int64_t)(b / tiles_m) * kOuN;
+    const int fr = lane & 31, fh = lane >> 5;
+    auto stage = [&](auto st) -> ZS_LDS char * {
+        if constexpr (decltype(st)::value == 0)
+            return (ZS_LDS char *)s0 + wave * kOuStage;
+        else if constexpr (decltype(st)::value == 1)
+            return (ZS_LDS char *)s1 + wave * kOuStage;
+        else
+            return (ZS_LDS char *)s2 + wave * kOuStage;
+    };
+
+    // A's loads of sixteen rows; rows past M hold what LDS held and end in rows
+    // of C past M.
+    const int na = M - m0 > 16 ? 2 : 1;
+    uint32_t va[2], vb[4];
+    int ka[2];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        va[n] = dma_offset<128, false>(lda, n, lane, 0);
+        ka[n] = dma_kofs(n, lane, 0);
+    }
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+        const int r = 8 * n + (lane >> 3), c = (lane & 7) ^ (((r >> 1) & 1) << 2);
+        vb[n] = (uint32_t)((r * ldb + 8 * c) * 2);
+    }
+    // K tile t of 32 into a stage.
+    auto dma = [&](auto st, int64_t t) {
+        const int64_t k0 = t * kBK;
+        const __amdgpu_buffer_rsrc_t ra = rsrc(A + m0 * lda + k0, ((M - 1 - m0) * lda + K - k0) * 2);
+        const __amdgpu_buffer_rsrc_t rb = rsrc(B + k0 * ldb + n0, ((K - 1 - k0) * ldb + N - n0) * 2);
+        ZS_LDS char *d = stage(st);
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+            if (n < na)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (ZS_LDS void *)(d + n * 1024), 16,
+                                                         k0 + ka[n] >= K ? kOOB : va[n], 0, 0, 0);
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (ZS_LDS void *)(d + kOuA + n * 1024), 16, vb[n], 0, 0,
+                                                     0);
+    };
+    f32x16 acc[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+            acc[j][v] = 0.0f;
+    const int64_t t_n = (K + kBK - 1) / kBK;
+    auto step = [&](auto st, int64_t t) {
+        const ZS_LDS char *d = stage(st);
+        // the later stages' na + 4 loads each may stay in flight
+        if (t + kNW >= t_n) {
+            wait_vm_lgkm0<0>();
+        } else if (t + 2 * kNW >= t_n) {
+            if (na == 2)
+                wait_vm_lgkm0<6>();
+            else
+                wait_vm_lgkm0<5>();
+        } else {
+            if (na == 2)
+                wait_vm_lgkm0<12>();
+            else
+                wait_vm_lgkm0<10>();
+        }
+        bf16x8 fa[2], fb[2][2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            fa[s] = *reinterpret_cast<const ZS_LDS bf16x8 *>(d + ki_pos(fr, 2 * s + fh));
+            const int j4 = lane & 15, kr = 16 * s + 8 * fh + (j4 >> 2);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int o = kr * 128 + 64 * (j ^ (j4 >> 3)) + 32 * ((lane >> 4) & 1) + 8 * (j4 & 3);
+                const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ZS_LDS s16x4 *)(d + kOuA + o));
+                const s16x4 hi =
+                    __builtin_amdgcn_ds_read_tr16_b64_v4i16((ZS_LDS s16x4 *)(d + kOuA + o + 4 * 128));
+                const s16x8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                fb[s][j] = __builtin_bit_cast(bf16x8, v);
+            }
+        }
+        // The stage is overwritten only after every read of it has returned.
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0) alone
+        __builtin_amdgcn_sched_barrier(0);
+        if (t + kOuStages * kNW < t_n)
+            dma(st, t + kOuStages * kNW);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[s], fb[s][j], acc[j], 0, 0, 0);
+    };
+    if (wave < t_n)
+        dma(IC<0>{}, wave);
+    if (wave + kNW < t_n)
+        dma(IC<1>{}, wave + kNW);
+    if (wave + 2 * kNW < t_n)
+        dma(IC<2>{}, wave + 2 * kNW);
+    for (int64_t t = wave; t < t_n; t += kOuStages * kNW) {
+        step(IC<0>{}, t);
+        if (t + kNW < t_n)
+            step(IC<1>{}, t + kNW);
+        if (t + 2 * kNW < t_n)
+            step(IC<2>{}, t + 2 * kNW);
+    }
+    // The eight sums, added in the waves' order: 4 KB a wave and 32 columns, each
+    // wave adding two of the sixteen accumulators of both.
+    __syncthreads();
+    ZS_LDS float *part0 = (ZS_LDS float *)(ZS_LDS char *)s0, *part1 = (ZS_LDS float *)(ZS_LDS char *)s1;
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+        part0[(wave * 16 + v) * 64 + lane] = acc[0][v];
+        part1[(wave * 16 + v) * 64 + lane] = acc[1][v];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int v = 2 * wave + q;
+        float x = part0[v * 64 + lane], y = part1[v * 64 + lane];
+#pragma unroll
+        for (int w = 1; w < kNW; ++w) {
+            x += part0[(w * 16 + v) * 64 + lane];
+            y += part1[(w * 16 + v) * 64 + lane];
+        }
+        part0[v * 64 + lane] = x;
+        part1[v * 64 + lane] = y;
+    }
+    __syncthreads();
+    f32x16 sum[1][1];
+#pragma unroll
+    for (int v = 0; v < 16; ++v)
+        sum[0][0][v] = wave & 1 ? part1[v * 64 + lane] : part0[v * 64 + lane];
+    // Two waves store, 32 columns each; for the others the tile lies past the
+    // last row.
+    const LayerEpi epi{args, (ZS_LDS float *)((ZS_LDS char *)s2 + wave * kOuStage)};
+    epi.tile32<1, 1>(sum, wave < 2 ? m0 : M, n0 + 32 * (wave & 1), M, N, lane);
+}
+
 // Group e's rows [lo, hi), kept inside [0, rows] whatever the array holds.
 __device__ __forceinline__ void group_range(const int64_t *off, int e, int64_t rows, int64_t &lo, int64_t &hi)
 {
@@ -1421,16 +1579,21 @@ zero_status epilogue_gemm_run(int64_t M, int64_t N, int64_t K, const uint16_t *A
     // Up to two blocks a CU of 32 x 32 tiles: 1 x 4096 x 14336 takes 55 us so
     // (K-inner B 31) and 95 in 128 x 128 tiles, 128 x 4096 x 4096 22 and 32,
     // 256 x 1024 x 1024 7.2 and 13; past that, with 64 x 14336 x 4096, 60 and
-    // 44, 512 x 4096 x 4096 80 and 34.
+    // 44, 512 x 4096 x 4096 80 and 34.  Of a K-outer B more than one block a CU
+    // becomes 32 x 64 tiles, up to one a CU (with two, 448 blocks, 64 x 14336 x 4096
+    // takes 48 us and 44 in 128 x 128 ones, 1 x 28672 x 8192 103 and 85); so do
+    // leading dimensions for which the 64 k rows of a 32-column stage would pass
+    // 32-bit offsets.
     const int64_t sm = (M + kSkM - 1) / kSkM, sn = (N + kSkN - 1) / kSkN;
-    // A stage of its K-outer B spans 64 k rows: half the leading dimension that
-    // 32-bit offsets allow the others.
-    if (!ao && sm <= 2 * cu_count() / sn && (!bo || ldb <= (int64_t(1) << 24))) {
+    if (!ao && sm <= 2 * cu_count() / sn) {
         const dim3 grid((unsigned)(sm * sn));
-        if (bo)
+        if (!bo)
+            hipLaunchKernelGGL(skinny_kernel<false>, grid, dim3(kGT), 0, s, M, N, K, A, lda, B, ldb, a, (int)sm);
+        else if (sm * sn <= cu_count() && ldb <= (int64_t(1) << 24))
             hipLaunchKernelGGL(skinny_kernel<true>, grid, dim3(kGT), 0, s, M, N, K, A, lda, B, ldb, a, (int)sm);
         else
-            hipLaunchKernelGGL(skinny_kernel<false>, grid, dim3(kGT), 0, s, M, N, K, A, lda, B, ldb, a, (int)sm);
+            hipLaunchKernelGGL(skinny_outer_kernel, dim3((unsigned)(sm * ((N + kOuN - 1) / kOuN))), dim3(kGT), 0,
+                               s, M, N, K, A, lda, B, ldb, a, (int)sm);
         return launched("gemm_epilogue");
     }
 #define ZS_EPI(AO, BO)                                                                             \

@@ -195,6 +195,10 @@ CASES = [  # M, N, K, pad, act, bias, residual, c, preact, output
     (200, 328, 1048, 8, "silu", "fp32", "fp32", "bf16", "e4m3", True),
     (136, 120, 4160, 0, "relu", None, "bf16", "fp32", "e4m3", False),
     (9, 200, 2120, 8, "silu", "bf16", "bf16", "bf16", "e4m3", True),
+    (1, 8200, 40, 8, "gelu", "bf16", "bf16", "bf16", "bf16", True),
+    (40, 4168, 1096, 0, "silu", None, "fp32", "fp32", "e4m3", False),
+    (500, 520, 200, 8, "gelu_tanh", "fp32", "bf16", "bf16", "e4m3", True),
+    (17, 8224, 808, 0, "none", "bf16", None, "fp32", None, False),
     (1050, 1048, 1096, 8, "gelu", "bf16", "bf16", "bf16", "e4m3", True),
     (1050, 1048, 96, 0, "silu", None, None, "bf16", "bf16", False),
     (1050, 1048, 1048, 0, "gelu_tanh", "fp32", "bf16", "fp32", "bf16", True),
@@ -211,7 +215,8 @@ def test_epilogue_within_bounds(case, ao, bo):
     whole and half tiles, 1050 x 1048 and a K-outer A 128 x 128 ones (from K =
     1024 on with K split over the halves of a block: 1024 and 4160 are even
     numbers of 32, 4160 past the steady loop's, 1048 and 1096 odd ones with a
-    rest), the others 32 x 32 ones with K split over the waves."""
+    rest), the others 32 x 32 ones with K split over the waves -- 32 x 64 ones
+    where a K-outer B makes more than 256 of 32 x 32: the four from 1 x 8200 on."""
     M, N, K, pad, act, bias, res, ct, pre, keep = case
     if ao and M % 8:
         M = -(-M // 8) * 8
@@ -905,7 +910,8 @@ def test_a_router_step_replayed_with_every_row_to_one_expert():
 
 @pytest.mark.parametrize("M,N,K,lda,bo,ldb", [
     (40, 136, 72, 1 << 22, 1, 1 << 24),          # 32 x 32 tiles, B at their limit
-    (40, 136, 72, 1 << 22, 1, 1 << 25),          # past it
+    (40, 136, 72, 1 << 22, 1, 1 << 25),          # past it: 32 x 64 ones
+    (1, 8200, 72, 1 << 22, 1, 1 << 25),
     (40, 136, 72, 1 << 22, 0, 1 << 22),
     (520, 1048, 1096, 1 << 22, 0, 1 << 22),      # K split over a block's halves
     (2304, 9000, 72, 1 << 22, 1, 1 << 25),       # 256 x 256 tiles and halves
