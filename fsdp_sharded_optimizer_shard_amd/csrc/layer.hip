@@ -676,15 +676,12 @@ constexpr int kSkM = 32, kSkN = 32, kSkK = 64;
 constexpr int kSkOp = 32 * 128;  // bytes of one operand's stage of one wave
 
 template <bool B_KOUTER>
-__global__ __launch_bounds__(kGT) void skinny_kernel(int64_t M, int64_t N, int64_t K,
-                                                     const uint16_t *__restrict__ A, int64_t lda,
-                                                     const uint16_t *__restrict__ B, int64_t ldb,
-                                                     EpiArgs args, int tiles_m)
+__device__ __forceinline__ void skinny_tile(int64_t M, int64_t N, int64_t K, const uint16_t *__restrict__ A,
+                                            int64_t lda, const uint16_t *__restrict__ B, int64_t ldb,
+                                            const EpiArgs &args, int64_t m0, int64_t n0)
 {
     __shared__ __attribute__((aligned(1024))) char s0[kNW * 2 * kSkOp], s1[kNW * 2 * kSkOp];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int b = xcd_order(blockIdx.x, gridDim.x);
-    const int64_t m0 = (int64_t)(b % tiles_m) * kSkM, n0 = (int64_t)(b / tiles_m) * kSkN;
     const int fr = lane & 31, fh = lane >> 5;
     auto stage = [&](auto st) -> ZS_LDS char * {
         if constexpr (decltype(st)::value == 0)
@@ -814,15 +811,13 @@ __global__ __launch_bounds__(kGT) void skinny_kernel(int64_t M, int64_t N, int64
 constexpr int kOuN = 64, kOuStages = 3;
 constexpr int kOuA = 32 * kBK * 2, kOuStage = kOuA + kBK * kOuN * 2;  // bytes of one wave
 
-__global__ __launch_bounds__(kGT) void skinny_outer_kernel(int64_t M, int64_t N, int64_t K,
-                                                           const uint16_t *__restrict__ A, int64_t lda,
-                                                           const uint16_t *__restrict__ B, int64_t ldb,
-                                                           EpiArgs args, int tiles_m)
+__device__ __forceinline__ void skinny_outer_tile(int64_t M, int64_t N, int64_t K,
+                                                  const uint16_t *__restrict__ A, int64_t lda,
+                                                  const uint16_t *__restrict__ B, int64_t ldb,
+                                                  const EpiArgs &args, int64_t m0, int64_t n0)
 {
     __shared__ __attribute__((aligned(1024))) char s0[kNW * kOuStage], s1[kNW * kOuStage], s2[kNW * kOuStage];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int b = xcd_order(blockIdx.x, gridDim.x);
-    const int64_t m0 = (int64_t)(b % tiles_m) * kSkM, n0 = (int64_t)(b / tiles_m) * kOuN;
     const int fr = lane & 31, fh = lane >> 5;
     auto stage = [&](auto st) -> ZS_LDS char * {
         if constexpr (decltype(st)::value == 0)
@@ -960,6 +955,20 @@ __global__ __launch_bounds__(kGT) void skinny_outer_kernel(int64_t M, int64_t N,
     epi.tile32<1, 1>(sum, wave < 2 ? m0 : M, n0 + 32 * (wave & 1), M, N, lane);
 }
 
+template <int BN, bool B_KOUTER>
+__global__ __launch_bounds__(kGT) void skinny_kernel(int64_t M, int64_t N, int64_t K,
+                                                     const uint16_t *__restrict__ A, int64_t lda,
+                                                     const uint16_t *__restrict__ B, int64_t ldb,
+                                                     EpiArgs args, int tiles_m)
+{
+    const int b = xcd_order(blockIdx.x, gridDim.x);
+    const int64_t m0 = (int64_t)(b % tiles_m) * kSkM, n0 = (int64_t)(b / tiles_m) * BN;
+    if constexpr (BN == kOuN)
+        skinny_outer_tile(M, N, K, A, lda, B, ldb, args, m0, n0);
+    else
+        skinny_tile<B_KOUTER>(M, N, K, A, lda, B, ldb, args, m0, n0);
+}
+
 // Group e's rows [lo, hi), kept inside [0, rows] whatever the array holds.
 __device__ __forceinline__ void group_range(const int64_t *off, int e, int64_t rows, int64_t &lo, int64_t &hi)
 {
@@ -1053,6 +1062,16 @@ __device__ __forceinline__ bool find_tile(const int64_t *off, int n_groups, int6
     }
 }
 
+// The epilogue's matrices from row lo on.
+__device__ __forceinline__ void from_row(EpiArgs &args, int64_t lo)
+{
+    args.C = static_cast<char *>(args.C) + lo * args.ldc * (args.c_bf16 ? 2 : 4);
+    if (args.residual)
+        args.residual = static_cast<const char *>(args.residual) + lo * args.ldr * (args.r_bf16 ? 2 : 4);
+    if (args.z)
+        args.z = static_cast<char *>(args.z) + lo * args.ldz * 2;
+}
+
 constexpr int kRunM = 6;
 
 // C[r] = epilogue(A[r] B_e) for the rows r of every group e.  The grid is the
@@ -1077,14 +1096,10 @@ __global__ __launch_bounds__(kGT) void grouped_rows_kernel(const int64_t *__rest
     group_range(off, e, rows, lo, hi);
     const int64_t M = hi - lo, n0 = (int64_t)tn * BN;
     const int64_t m0 = (int64_t)tm * BM + (p.half > 0 ? BM / 2 : 0);
-    if (m0 >= M)  // an empty half, or offsets that decrease
+    if (m0 >= M || n0 >= N)  // an empty half, or offsets that decrease
         return;
     const bool half = BM == kBM && (p.half >= 0 || M - m0 <= BM / 2);
-    args.C = static_cast<char *>(args.C) + lo * args.ldc * (args.c_bf16 ? 2 : 4);
-    if (args.residual)
-        args.residual = static_cast<const char *>(args.residual) + lo * args.ldr * (args.r_bf16 ? 2 : 4);
-    if (args.z)
-        args.z = static_cast<char *>(args.z) + lo * args.ldz * 2;
+    from_row(args, lo);
     A += lo * lda;
     B += e * stride_b;
     if constexpr (B_KOUTER && BM == kBM) {
@@ -1106,6 +1121,33 @@ __global__ __launch_bounds__(kGT) void grouped_rows_kernel(const int64_t *__rest
         else
             gemm_tile_kp<BM, BN>(M, N, K, A, lda, B, ldb, epi, m0, n0, ZS_P);
     }
+}
+
+// The same with few rows in all, in 32-row tiles.
+template <int BN, bool B_KOUTER>
+__global__ __launch_bounds__(kGT) void grouped_skinny_kernel(const int64_t *__restrict__ off, int n_groups,
+                                                             int64_t rows, int64_t N, int64_t K,
+                                                             const uint16_t *__restrict__ A, int64_t lda,
+                                                             const uint16_t *__restrict__ B, int64_t ldb,
+                                                             int64_t stride_b, EpiArgs args, int tiles_n,
+                                                             int cus)
+{
+    Place p;
+    if (!find_tile<kSkM>(off, n_groups, rows, tiles_n, cus, p))
+        return;
+    const int64_t m0 = (int64_t)(p.tile % p.row_tiles) * kSkM, n0 = (int64_t)(p.tile / p.row_tiles) * BN;
+    int64_t lo, hi;
+    group_range(off, p.e, rows, lo, hi);
+    const int64_t M = hi - lo;
+    if (m0 >= M || n0 >= N)
+        return;
+    from_row(args, lo);
+    A += lo * lda;
+    B += p.e * stride_b;
+    if constexpr (BN == kOuN)
+        skinny_outer_tile(M, N, K, A, lda, B, ldb, args, m0, n0);
+    else
+        skinny_tile<B_KOUTER>(M, N, K, A, lda, B, ldb, args, m0, n0);
 }
 
 // C_e = sum over the rows r of group e of A[r]^T B[r]; an empty group's C_e is
@@ -1562,6 +1604,29 @@ zero_status gemm_saved_run(int64_t M, int64_t N, int64_t K, const zero_saved *A,
     return launched("gemm_saved");
 }
 
+// Up to two blocks a CU of 32 x 32 tiles: 1 x 4096 x 14336 takes 55 us so
+// (K-inner B 31) and 95 in 128 x 128 tiles, 128 x 4096 x 4096 22 and 32,
+// 256 x 1024 x 1024 7.2 and 13; past that, with 64 x 14336 x 4096, 60 and
+// 44, 512 x 4096 x 4096 80 and 34.  Of a K-outer B more than one block a CU
+// becomes 32 x 64 tiles, up to one a CU (with two, 448 blocks, 64 x 14336 x 4096
+// takes 48 us and 44 in 128 x 128 ones, 1 x 28672 x 8192 103 and 85); so do
+// leading dimensions for which the 64 k rows of a 32-column stage would pass
+// 32-bit offsets.
+//
+// Grouped products by the same rule, with the row tiles that the groups may
+// have, against 128 x 128 tiles (K-outer and K-inner B): 2 groups of a row, 14336 ->
+// 4096, 60 and 48 us against 124 and 207; 16 of one, 4096 -> 1024, 34 and 43
+// against 46 and 65; 4 of 100, 2048 -> 512, 9.1 and 8.0 against 22 and 26.
+//
+// Columns of a few-row tile, 0 where the product takes larger ones.
+static int skinny_columns(int64_t row_tiles, int64_t N, bool b_kouter, int64_t ldb)
+{
+    const int64_t sn = (N + kSkN - 1) / kSkN, cus = cu_count();
+    if (row_tiles > 2 * cus / sn)
+        return 0;
+    return !b_kouter || (row_tiles * sn <= cus && ldb <= (int64_t(1) << 24)) ? kSkN : kOuN;
+}
+
 zero_status epilogue_gemm_run(int64_t M, int64_t N, int64_t K, const uint16_t *A, int64_t lda,
                               int32_t a_order, const uint16_t *B, int64_t ldb, int32_t b_order, void *C,
                               int64_t ldc, int32_t c_dtype, const zero_epilogue *ep, hipStream_t s)
@@ -1576,24 +1641,18 @@ zero_status epilogue_gemm_run(int64_t M, int64_t N, int64_t K, const uint16_t *A
     const bool k2 = small && K >= 1024;
     const Grid g = small ? tiles(M, N, 128, 128, false) : tiles(M, N, kBM, kBN, true);
     (void)hipGetLastError();
-    // Up to two blocks a CU of 32 x 32 tiles: 1 x 4096 x 14336 takes 55 us so
-    // (K-inner B 31) and 95 in 128 x 128 tiles, 128 x 4096 x 4096 22 and 32,
-    // 256 x 1024 x 1024 7.2 and 13; past that, with 64 x 14336 x 4096, 60 and
-    // 44, 512 x 4096 x 4096 80 and 34.  Of a K-outer B more than one block a CU
-    // becomes 32 x 64 tiles, up to one a CU (with two, 448 blocks, 64 x 14336 x 4096
-    // takes 48 us and 44 in 128 x 128 ones, 1 x 28672 x 8192 103 and 85); so do
-    // leading dimensions for which the 64 k rows of a 32-column stage would pass
-    // 32-bit offsets.
-    const int64_t sm = (M + kSkM - 1) / kSkM, sn = (N + kSkN - 1) / kSkN;
-    if (!ao && sm <= 2 * cu_count() / sn) {
-        const dim3 grid((unsigned)(sm * sn));
+    if (const int bn = ao ? 0 : skinny_columns((M + kSkM - 1) / kSkM, N, bo, ldb)) {
+        const int64_t sm = (M + kSkM - 1) / kSkM;
+        const dim3 grid((unsigned)(sm * ((N + bn - 1) / bn)));
+#define ZS_SKINNY(BN_, BO)                                                                         \
+    hipLaunchKernelGGL((skinny_kernel<BN_, BO>), grid, dim3(kGT), 0, s, M, N, K, A, lda, B, ldb, a, (int)sm)
         if (!bo)
-            hipLaunchKernelGGL(skinny_kernel<false>, grid, dim3(kGT), 0, s, M, N, K, A, lda, B, ldb, a, (int)sm);
-        else if (sm * sn <= cu_count() && ldb <= (int64_t(1) << 24))
-            hipLaunchKernelGGL(skinny_kernel<true>, grid, dim3(kGT), 0, s, M, N, K, A, lda, B, ldb, a, (int)sm);
+            ZS_SKINNY(kSkN, false);
+        else if (bn == kSkN)
+            ZS_SKINNY(kSkN, true);
         else
-            hipLaunchKernelGGL(skinny_outer_kernel, dim3((unsigned)(sm * ((N + kOuN - 1) / kOuN))), dim3(kGT), 0,
-                               s, M, N, K, A, lda, B, ldb, a, (int)sm);
+            ZS_SKINNY(kOuN, true);
+#undef ZS_SKINNY
         return launched("gemm_epilogue");
     }
 #define ZS_EPI(AO, BO)                                                                             \
@@ -1692,14 +1751,31 @@ zero_status grouped_rows_run(int32_t n_groups, const int64_t *offsets, int64_t r
     // 2048, 101 and 95 us, of 192 rows 116 and 131; forward (K-outer B, where
     // gemm_tile_ap keeps up longer) 64 groups of 64 rows, 2048 -> 1408, 88 and 83,
     // of 128 rows 97 and 103, but 32 of 64 at 4096 -> 4096 182 and 217.
+    const int cus = cu_count();
+    const bool bo = b_order == ZERO_K_OUTER;
+    (void)hipGetLastError();
+    const int64_t sm = most_tiles(n_groups, rows, kSkM);
+    if (const int bn = skinny_columns(sm, N, bo, ldb)) {
+        const int tn = (int)((N + bn - 1) / bn);
+        const dim3 grid((unsigned)(sm * tn));
+#define ZS_SKINNY(BN_, BO)                                                                         \
+    hipLaunchKernelGGL((grouped_skinny_kernel<BN_, BO>), grid, dim3(kGT), 0, s, offsets, n_groups, rows, N, K, \
+                       A, lda, B, ldb, stride_b, a, tn, cus)
+        if (!bo)
+            ZS_SKINNY(kSkN, false);
+        else if (bn == kSkN)
+            ZS_SKINNY(kSkN, true);
+        else
+            ZS_SKINNY(kOuN, true);
+#undef ZS_SKINNY
+        return launched("gemm_grouped_rows");
+    }
     const int64_t mean = rows / n_groups;
     const bool few = 2 * most_tiles(n_groups, rows, kBM) * ((N + kBN - 1) / kBN) <= cu_count();
     const bool small = few || (b_order == ZERO_K_INNER ? mean <= 128 : mean <= 64 && K <= 2048);
     const int bm = small ? 128 : kBM, bn = small ? 128 : kBN;
     const int tn = (int)((N + bn - 1) / bn);
-    const int cus = cu_count();
     const dim3 grid((unsigned)(most_tiles(n_groups, rows, bm) * tn + (small ? 0 : cus / 2)));
-    (void)hipGetLastError();
 #define ZS_ROWS(BM_, BN_, BO)                                                                      \
     hipLaunchKernelGGL((grouped_rows_kernel<BM_, BN_, BO>), grid, dim3(kGT), 0, s, offsets, n_groups, \
                        rows, N, K, A, lda, B, ldb, stride_b, a, tn, cus)

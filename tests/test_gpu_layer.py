@@ -452,6 +452,8 @@ GROUPS = [  # counts (first entry: rows before the first group, last: rows behin
     [0, 300, 0, 257, 31, 1, 0],
     [2] + [k % 5 for k in range(70)] + [9],
     [0, 600, 40, 700, 0, 520, 12],
+    [3, 300, 0, 70, 129, 1, 12],        # with 520 columns 32 x 64 tiles of a K-outer B
+    [0] + [9, 0, 31, 1, 33, 2] * 3 + [5],
     [0] + [0] * 6 + [20],
 ]
 
