@@ -3,6 +3,8 @@
 
 #include <hip/hip_runtime_api.h>
 
+#include <initializer_list>
+
 #include "internal.h"
 
 namespace zs {
@@ -13,6 +15,24 @@ bool vec16(const void *p, int64_t ld, int es) { return aligned(p, 16) && ld * es
 
 bool known_dtype(int32_t d) { return d == ZERO_BF16 || d == ZERO_FP32; }
 int bytes_of(int32_t d) { return d == ZERO_BF16 ? 2 : 4; }
+
+// Whether p is one of `others`; NULL is nothing.  What a call writes must not
+// be an address that it uses for something else: only equal addresses are
+// looked for, since matrices with leading dimensions may share a range.
+bool is_one_of(const void *p, std::initializer_list<const void *> others)
+{
+    for (const void *o : others)
+        if (p && p == o)
+            return true;
+    return false;
+}
+
+// The exponent bytes of a kept matrix that has them.
+const void *scales_of(const zero_saved *s)
+{
+    return s && s->format == ZERO_SAVED_E4M3 ? s->scales : nullptr;
+}
+const void *data_of(const zero_saved *s) { return s ? s->data : nullptr; }
 
 zero_status launched(const char *what)
 {

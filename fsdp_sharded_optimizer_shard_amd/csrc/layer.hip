@@ -1426,14 +1426,15 @@ __global__ __launch_bounds__(kGT) void saved_kernel(int64_t M, int64_t N, int64_
 
 }  // namespace
 
-// The epilogue of an M x N product, checked and translated; `grouped` refuses
-// what needs rows counted from a multiple of 32.
+// The epilogue of an M x N product, checked and translated.  `offsets` (NULL: no
+// groups) refuses what needs rows counted from a multiple of 32.
 zero_status epilogue_check(int64_t M, int64_t N, const void *A, const void *B, const void *C, int64_t ldc,
-                           int32_t c_dtype, const zero_epilogue *ep, bool grouped)
+                           int32_t c_dtype, const zero_epilogue *ep, const int64_t *offsets)
 {
     if (M == 0 || N == 0)
         return ZERO_OK;
-    if (C == A || C == B)
+    const bool grouped = offsets != nullptr;
+    if (is_one_of(C, {A, B, offsets}))
         return fail(ZERO_ERR_INVALID_ARG, "C must not be an operand");
     if (!ep)
         return ZERO_OK;
@@ -1445,6 +1446,8 @@ zero_status epilogue_check(int64_t M, int64_t N, const void *A, const void *B, c
             return fail(ZERO_ERR_UNSUPPORTED, "a grouped product takes no bias");
         if ((st = check_matrix("bias", ep->bias, N, N, ep->bias_dtype)) != ZERO_OK)
             return st;
+        if (ep->bias == C)
+            return fail(ZERO_ERR_INVALID_ARG, "bias must not lie where C is written");
     }
     if (ep->residual) {
         if ((st = check_matrix("residual", ep->residual, ep->ldr, N, ep->residual_dtype)) != ZERO_OK ||
@@ -1455,10 +1458,10 @@ zero_status epilogue_check(int64_t M, int64_t N, const void *A, const void *B, c
     }
     // What is kept must not lie where the product still reads or writes.
     auto apart = [&](const zero_saved *s, const zero_saved *other) {
-        return s->data != C && s->data != A && s->data != B && s->data != ep->residual &&
-               s->data != ep->bias && (!other || s->data != other->data) &&
-               !(other && s->format == ZERO_SAVED_E4M3 && other->format == ZERO_SAVED_E4M3 &&
-                 s->scales == other->scales);
+        for (const void *p : {data_of(s), scales_of(s)})
+            if (is_one_of(p, {C, A, B, offsets, ep->residual, ep->bias, data_of(other), scales_of(other)}))
+                return false;
+        return data_of(s) != scales_of(s);
     };
     if (ep->preact) {
         if ((st = saved_check("preact", ep->preact, M, N)) != ZERO_OK)
@@ -1565,7 +1568,7 @@ zero_status gemm_saved_check(int64_t M, int64_t N, int64_t K, const zero_saved *
         (st = check_matrix("B", B, ldb, N, ZERO_BF16)) != ZERO_OK ||
         (st = check_matrix("C", C, ldc, N, c_dtype)) != ZERO_OK)
         return st;
-    if (C == A->data || C == B)
+    if (is_one_of(C, {A->data, scales_of(A), B}))
         return fail(ZERO_ERR_INVALID_ARG, "C must not be an operand");
     if (M % 8 || N % 8 || ldb % 8 || A->ld % 8)
         return fail(ZERO_ERR_UNSUPPORTED, "a product from a kept operand needs M, N and the leading "
@@ -1743,7 +1746,7 @@ zero_status grouped_rows_check(int32_t n_groups, const int64_t *offsets, int64_t
     zero_status st;
     if ((st = grouped_check(n_groups, offsets, rows)) != ZERO_OK ||
         (st = gemm_check(rows, N, K, A, lda, ZERO_K_INNER, B, ldb, b_order, C, ldc, c_dtype)) != ZERO_OK ||
-        (st = epilogue_check(rows, N, A, B, C, ldc, c_dtype, ep, true)) != ZERO_OK)
+        (st = epilogue_check(rows, N, A, B, C, ldc, c_dtype, ep, offsets)) != ZERO_OK)
         return st;
     if (rows == 0 || N == 0)
         return ZERO_OK;
@@ -1828,7 +1831,7 @@ zero_status grouped_depth_check(int32_t n_groups, const int64_t *offsets, int64_
         return st;
     if (M == 0 || N == 0)
         return ZERO_OK;
-    if (C == A || C == B)
+    if (is_one_of(C, {A, B, offsets}))
         return fail(ZERO_ERR_INVALID_ARG, "C must not be an operand");
     if (n_groups > 1 && stride_c < (M - 1) * ldc + N)
         return fail(ZERO_ERR_INVALID_ARG, "stride_c must be at least %lld (got %lld)",
@@ -1894,7 +1897,7 @@ zero_status zero_gemm_bf16_epilogue(int64_t M, int64_t N, int64_t K, const uint1
 {
     zero_status st;
     if ((st = zs::gemm_check(M, N, K, A, lda, a_order, B, ldb, b_order, C, ldc, c_dtype)) != ZERO_OK ||
-        (st = zs::epilogue_check(M, N, A, B, C, ldc, c_dtype, epilogue, false)) != ZERO_OK)
+        (st = zs::epilogue_check(M, N, A, B, C, ldc, c_dtype, epilogue, nullptr)) != ZERO_OK)
         return st;
     return zs::epilogue_gemm_run(M, N, K, A, lda, a_order, B, ldb, b_order, C, ldc, c_dtype, epilogue,
                                  static_cast<hipStream_t>(stream));

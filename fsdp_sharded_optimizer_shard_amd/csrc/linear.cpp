@@ -156,7 +156,7 @@ zero_status zero_fsdp_linear_act_forward(const zero_layout *L, int32_t unit,
     if ((st = zs::gemm_check(batch, d.out, d.in, x, d.in, ZERO_K_INNER, w_full, d.out,
                              ZERO_K_OUTER, y, d.out, y_dtype)) != ZERO_OK ||
         (st = zs::epilogue_check(batch, d.out, x, w_full, y, d.out, y_dtype, epilogue,
-                                 false)) != ZERO_OK)
+                                 nullptr)) != ZERO_OK)
         return st;
     if ((st = zero_gather_params(L, unit, unit + 1, w_shards, L->parts, w_full, stream)) != ZERO_OK)
         return st;

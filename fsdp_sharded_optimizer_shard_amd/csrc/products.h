@@ -27,7 +27,7 @@ zero_status zero_rows_fill(float *p, int64_t ld, int64_t r0, int64_t r1, int64_t
                            hipStream_t s);
 
 zero_status epilogue_check(int64_t M, int64_t N, const void *A, const void *B, const void *C, int64_t ldc,
-                           int32_t c_dtype, const zero_epilogue *ep, bool grouped);
+                           int32_t c_dtype, const zero_epilogue *ep, const int64_t *offsets);
 zero_status epilogue_gemm_run(int64_t M, int64_t N, int64_t K, const uint16_t *A, int64_t lda,
                               int32_t a_order, const uint16_t *B, int64_t ldb, int32_t b_order, void *C,
                               int64_t ldc, int32_t c_dtype, const zero_epilogue *ep, hipStream_t s);

@@ -676,8 +676,10 @@ zero_status zero_saved_read(int64_t rows, int64_t cols, const zero_saved *in, vo
      preact    receives z, in either format (E4M3: coded from the fp32 z);
      output    receives C in 8 bits (E4M3), coded from C as stored: the same
                bytes that zero_saved_write of C would give.
-   What a call writes (C, preact, output) needs memory of its own, the
-   residual in place excepted; the same pointer twice is refused. */
+   What a call writes (C, preact, output, with their scales) needs memory apart
+   from everything else that the call uses, the residual in place excepted; an
+   address given twice is refused.  That holds for the scales and the offsets
+   of the products below, too. */
 typedef struct zero_epilogue {
     const void *bias;
     const void *residual;

@@ -354,3 +354,58 @@ def test_kept_matrices_do_not_share_their_scales():
     ep = epi(preact=s8(data=KEPT), output=s8(data=KEPT + (1 << 20)))
     refused(INV, zs.gemm_bf16_epilogue, 64, 64, 64, FAKE, 64, zs.K_INNER, FAKE, 64, zs.K_OUTER, OUT, 64,
             zs.BF16, ep, text="its own")
+
+
+# One buffer for two things: with every address of its own each call below
+# passes its checks and fails at the launch (no GPU here), so a refusal is the
+# shared address's.
+A_, B_, C_, R_, BIAS, Z_, ZS, O_, OS, OFF = (FAKE + (i << 33) for i in range(1, 11))
+
+
+def shared_address_is_refused(call, base, *pairs):
+    """`call(**addresses)`: accepted as far as a launch with `base`, refused
+    with each (written, other) pair of names at the written one's address."""
+    for w, o in pairs:
+        with pytest.raises(zs.ZeroShardError) as e:
+            call(**{**base, o: base[w]})
+        assert e.value.status == INV, (w, o, str(e.value))
+    if not torch.cuda.is_available():
+        with pytest.raises(zs.ZeroShardError) as e:
+            call(**base)
+        assert e.value.status == zs.ERR_HIP, str(e.value)
+
+
+@pytest.mark.parametrize("preact", ["bf16", "e4m3"])
+def test_a_product_writes_over_nothing_that_it_uses(preact):
+    def call(a, b, c, r, bias, z, zsc, o, os_):
+        z8 = zs.Saved(z, 64, zsc, 64) if preact == "e4m3" else zs.Saved(z, 64)
+        zs.gemm_bf16_epilogue(64, 64, 64, a, 64, zs.K_INNER, b, 64, zs.K_OUTER, c, 64, zs.BF16,
+                              zs.Epilogue(bias=bias, residual=r, ldr=72, preact=z8,
+                                          output=zs.Saved(o, 64, os_, 64)), stream=0)
+
+    base = dict(a=A_, b=B_, c=C_, r=R_, bias=BIAS, z=Z_, zsc=ZS, o=O_, os_=OS)
+    written = ["c", "z", "o", "os_"] + ["zsc"] * (preact == "e4m3")
+    shared_address_is_refused(call, base, *[(w, o) for w in written for o in base
+                                            if o != w and (o != "zsc" or preact == "e4m3")])
+
+
+def test_grouped_products_write_over_nothing_that_they_use():
+    def rows(a, b, c, r, z, off):
+        zs.gemm_grouped_rows_bf16(4, off, 100, 64, 64, a, 64, b, 64, zs.K_OUTER, 4096, c, 64, zs.BF16,
+                                  zs.Epilogue(residual=r, ldr=72, preact=zs.Saved(z, 64)), stream=0)
+
+    base = dict(a=A_, b=B_, c=C_, r=R_, z=Z_, off=OFF)
+    shared_address_is_refused(rows, base, *[(w, o) for w in ("c", "z") for o in base if o != w])
+
+    def depth(a, b, c, off):
+        zs.gemm_grouped_depth_bf16(4, off, 100, 64, 64, a, 64, b, 64, c, 64, 4096, stream=0)
+
+    base = dict(a=A_, b=B_, c=C_, off=OFF)
+    shared_address_is_refused(depth, base, ("c", "a"), ("c", "b"), ("c", "off"))
+
+
+def test_a_saved_product_does_not_write_over_its_scales():
+    def call(a, asc, b, c):
+        zs.gemm_saved_bf16(64, 64, 100, zs.Saved(a, 64, asc, 64), b, 64, c, 64, stream=0)
+
+    shared_address_is_refused(call, dict(a=A_, asc=ZS, b=B_, c=C_), ("c", "a"), ("c", "asc"), ("c", "b"))
