@@ -464,7 +464,7 @@ zero_status zero_saved_write(int64_t rows, int64_t cols, const void *x, int64_t 
         return st;
     if (out->format != ZERO_SAVED_E4M3)
         return fail(ZERO_ERR_UNSUPPORTED, "only the 8-bit format is written from a matrix");
-    if (out->data == x)
+    if (is_one_of(out->data, {x, out->scales}) || out->scales == x)
         return fail(ZERO_ERR_INVALID_ARG, "a checkpoint needs a buffer of its own");
     const int64_t cw = (cols + 127) / 128, rb = (rows + 31) / 32;
     if (rb > int64_t(0x7fffffff) / 64 / cw)
@@ -498,7 +498,7 @@ zero_status zero_saved_read(int64_t rows, int64_t cols, const zero_saved *in, vo
         return st;
     if (in->format != ZERO_SAVED_E4M3)
         return fail(ZERO_ERR_UNSUPPORTED, "only the 8-bit format is read back");
-    if (in->data == out)
+    if (is_one_of(out, {in->data, in->scales}))
         return fail(ZERO_ERR_INVALID_ARG, "a checkpoint is not read back in place");
     const int64_t cw = (cols + 127) / 128, rb = (rows + 31) / 32;
     if (rb > int64_t(0x7fffffff) / 64 / cw)

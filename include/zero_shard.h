@@ -659,7 +659,9 @@ typedef struct zero_saved {
 } zero_saved;
 
 /* *out = x (rows x cols, bf16 or fp32, leading dimension ldx) in 8 bits
-   (E4M3 only).  Bytes past column cols of a row are not written. */
+   (E4M3 only).  Bytes past column cols of a row are not written.  The matrix,
+   the codes and the scales need memory each, here and in zero_saved_read; an
+   address given twice is refused. */
 zero_status zero_saved_write(int64_t rows, int64_t cols, const void *x, int64_t ldx,
                              int32_t x_dtype, const zero_saved *out, void *stream);
 

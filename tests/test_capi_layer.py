@@ -409,3 +409,16 @@ def test_a_saved_product_does_not_write_over_its_scales():
         zs.gemm_saved_bf16(64, 64, 100, zs.Saved(a, 64, asc, 64), b, 64, c, 64, stream=0)
 
     shared_address_is_refused(call, dict(a=A_, asc=ZS, b=B_, c=C_), ("c", "a"), ("c", "asc"), ("c", "b"))
+
+
+@pytest.mark.parametrize("call", ["write", "read"])
+def test_a_checkpoint_shares_no_address(call):
+    def go(x, data, sc):
+        s = zs.Saved(data, 64, sc, 64)
+        if call == "write":
+            zs.saved_write(40, 64, x, 64, s, zs.BF16, stream=0)
+        else:
+            zs.saved_read(40, 64, s, x, 64, zs.BF16, stream=0)
+
+    pairs = [("data", "x"), ("sc", "x"), ("data", "sc")] if call == "write" else [("x", "data"), ("x", "sc")]
+    shared_address_is_refused(go, dict(x=A_, data=Z_, sc=ZS), *pairs)
