@@ -392,6 +392,15 @@ zero_status act_backward_check(int64_t rows, int64_t cols, const void *dy, int64
     if (need > 0 && (!workspace || n_workspace < need))
         return fail(ZERO_ERR_INVALID_ARG, "dbias of %lld x %lld needs a workspace of %lld floats",
                     (long long)rows, (long long)cols, (long long)need);
+    if (rows > 0) {
+        const bool kept = act != ZERO_ACT_NONE;
+        const void *z = kept ? data_of(preact) : nullptr, *z_scales = kept ? scales_of(preact) : nullptr;
+        const void *w = need > 0 ? workspace : nullptr;
+        if (is_one_of(dbias, {dy, z, z_scales, dz, w}) || is_one_of(w, {dy, z, z_scales, dz}) ||
+            is_one_of(dz, {z_scales}))
+            return fail(ZERO_ERR_INVALID_ARG, "dz, dbias and the workspace need memory apart from what the "
+                        "call reads and from each other");
+    }
     if ((cols + 127) / 128 > int64_t(0x7fffffff) / 256)
         return fail(ZERO_ERR_UNSUPPORTED, "too many columns for one launch");
     return ZERO_OK;

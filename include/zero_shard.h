@@ -712,7 +712,8 @@ zero_status zero_gemm_bf16_epilogue(int64_t M, int64_t N, int64_t K, const uint1
    `workspace` of zero_act_backward_workspace(rows, cols) floats (at most
    64 cols; 0 up to 128 rows, and the workspace may then be NULL), used
    until the call's work has run: calls that overlap in time, and captured
-   graphs that do, need one each.  rows = 0 writes zeros to dbias. */
+   graphs that do, need one each.  But for dz in place, one address for two
+   things is refused.  rows = 0 writes zeros to dbias. */
 zero_status zero_act_backward(int64_t rows, int64_t cols, const void *dy, int64_t ldy,
                               int32_t dy_dtype, int32_t act, const zero_saved *preact,
                               uint16_t *dz, int64_t ldz, float *dbias, float *workspace,

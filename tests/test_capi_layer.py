@@ -422,3 +422,24 @@ def test_a_checkpoint_shares_no_address(call):
 
     pairs = [("data", "x"), ("sc", "x"), ("data", "sc")] if call == "write" else [("x", "data"), ("x", "sc")]
     shared_address_is_refused(go, dict(x=A_, data=Z_, sc=ZS), *pairs)
+
+
+def test_the_epilogue_gradient_writes_over_nothing_that_it_uses():
+    """dz over dy or a bf16 z is allowed; all else is apart."""
+    def call(dy, z, zsc, dz, db, work, rows=300):
+        zs.act_backward(rows, 64, dy, 64, "gelu", zs.Saved(z, 64, zsc, 64), dz, 64, db, work, stream=0)
+
+    base = dict(dy=A_, z=Z_, zsc=ZS, dz=C_, db=BIAS, work=O_)
+    shared_address_is_refused(call, base, ("dz", "z"), ("dz", "zsc"), ("dz", "db"), ("dz", "work"),
+                              ("db", "dy"), ("db", "z"), ("db", "zsc"), ("db", "work"),
+                              ("work", "dy"), ("work", "z"), ("work", "zsc"))
+
+    def alone(dy, db, work):
+        zs.act_backward(300, 64, dy, 64, "none", None, None, 0, db, work, stream=0)
+
+    shared_address_is_refused(alone, dict(dy=A_, db=BIAS, work=O_), ("db", "dy"), ("db", "work"),
+                              ("work", "dy"))
+    if not torch.cuda.is_available():       # up to 128 rows the workspace is not used
+        with pytest.raises(zs.ZeroShardError) as e:
+            call(**{**base, "work": base["db"]}, rows=100)
+        assert e.value.status == zs.ERR_HIP
