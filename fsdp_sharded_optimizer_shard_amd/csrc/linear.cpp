@@ -13,9 +13,14 @@
 // multiple-of-8 rule on it.
 #include <hip/hip_runtime.h>
 
+#include "checks.h"
 #include "products.h"
 
 namespace {
+
+using zs::data_of;
+using zs::is_one_of;
+using zs::scales_of;
 
 struct Dims {
     int64_t in, out, in_pad;
@@ -60,6 +65,16 @@ zero_status expert_dims(const zero_layout *L, int32_t unit, int32_t n_experts, D
     if (d->in % 8 || d->out % 8)
         return zs::fail(ZERO_ERR_UNSUPPORTED, "in_features and out_features must be "
                         "multiples of 8");
+    return ZERO_OK;
+}
+
+// The gather writes w_full before a forward product reads anything else; what
+// the product writes over w_full is its own checks' to find.
+zero_status check_gathered(const uint16_t *w_full, const uint16_t *x, const int64_t *offsets,
+                           const zero_epilogue *ep)
+{
+    if (is_one_of(w_full, {x, offsets, ep ? ep->bias : nullptr, ep ? ep->residual : nullptr}))
+        return zs::fail(ZERO_ERR_INVALID_ARG, "w_full must not lie where the call reads something else");
     return ZERO_OK;
 }
 
@@ -156,7 +171,8 @@ zero_status zero_fsdp_linear_act_forward(const zero_layout *L, int32_t unit,
     if ((st = zs::gemm_check(batch, d.out, d.in, x, d.in, ZERO_K_INNER, w_full, d.out,
                              ZERO_K_OUTER, y, d.out, y_dtype)) != ZERO_OK ||
         (st = zs::epilogue_check(batch, d.out, x, w_full, y, d.out, y_dtype, epilogue,
-                                 nullptr)) != ZERO_OK)
+                                 nullptr)) != ZERO_OK ||
+        (batch > 0 && (st = check_gathered(w_full, x, nullptr, epilogue)) != ZERO_OK))
         return st;
     if ((st = zero_gather_params(L, unit, unit + 1, w_shards, L->parts, w_full, stream)) != ZERO_OK)
         return st;
@@ -200,9 +216,20 @@ zero_status zero_fsdp_linear_act_backward(const zero_layout *L, int32_t unit,
         (st = zs::gemm_saved_check(d.in, d.out, batch, x, g, d.out, dw_full, d.out,
                                    ZERO_FP32)) != ZERO_OK)
         return st;
-    if (batch > 0 && (dx == g || dx == x->data || dx == w_full ||
-                      (g == dz && (dz == x->data || dz == w_full))))
-        return zs::fail(ZERO_ERR_INVALID_ARG, "dx and dz must not lie where x, w_full or dz is still read");
+    // In the order of the work: w_full is gathered over nothing that is read
+    // later; dz, dbias and the workspace leave x and w_full to the products (and
+    // dbias is a result), dx leaves x, dz and dbias, dW the results.
+    const bool kept = act != ZERO_ACT_NONE;
+    const void *z = kept ? data_of(preact) : nullptr, *z_scales = kept ? scales_of(preact) : nullptr;
+    const void *x8 = scales_of(x);
+    const void *w = dbias && zero_act_backward_workspace(batch, d.out) > 0 ? workspace : nullptr;
+    if (batch > 0 &&
+        (is_one_of(w_full, {x->data, x8, dy, z, z_scales, g, dx, dbias, w}) ||
+         (kept && is_one_of(dz, {x->data, x8})) || is_one_of(w, {x->data, x8}) ||
+         is_one_of(dbias, {x->data, x8}) || is_one_of(dx, {x->data, x8, g, dbias}) ||
+         is_one_of(dw_full, {x->data, x8, g, dx, dbias})))
+        return zs::fail(ZERO_ERR_INVALID_ARG, "w_full, dz, dbias, the workspace, dx and dw_full must not lie "
+                        "where x, w_full, dz or a result is still read or kept");
     const hipStream_t s = static_cast<hipStream_t>(stream);
     if ((st = zero_gather_params(L, unit, unit + 1, w_shards, L->parts, w_full, stream)) != ZERO_OK)
         return st;
@@ -241,7 +268,8 @@ zero_status zero_fsdp_experts_forward(const zero_layout *L, int32_t unit, int32_
         return st;
     const int64_t stride = d.in * d.out;
     if ((st = zs::grouped_rows_check(n_experts, offsets, rows, d.out, d.in, x, d.in, w_full, d.out,
-                                     ZERO_K_OUTER, stride, y, d.out, y_dtype, epilogue)) != ZERO_OK)
+                                     ZERO_K_OUTER, stride, y, d.out, y_dtype, epilogue)) != ZERO_OK ||
+        (rows > 0 && (st = check_gathered(w_full, x, offsets, epilogue)) != ZERO_OK))
         return st;
     if ((st = zero_gather_params(L, unit, unit + 1, w_shards, L->parts, w_full, stream)) != ZERO_OK)
         return st;
@@ -270,8 +298,9 @@ zero_status zero_fsdp_experts_backward(const zero_layout *L, int32_t unit, int32
         (st = zs::grouped_depth_check(n_experts, offsets, rows, d.in, d.out, x, d.in, dy, d.out,
                                       dw_full, d.out, stride, ZERO_FP32)) != ZERO_OK)
         return st;
-    if (rows > 0 && dx == x)
-        return zs::fail(ZERO_ERR_INVALID_ARG, "dx must not lie where x is still read");
+    if (rows > 0 && (is_one_of(dx, {x, dw_full}) || is_one_of(w_full, {x, dy, offsets})))
+        return zs::fail(ZERO_ERR_INVALID_ARG, "dx must not lie where x is still read or dw_full is written, nor "
+                        "w_full where x, dy or the offsets are still read");
     const hipStream_t s = static_cast<hipStream_t>(stream);
     if ((st = zero_gather_params(L, unit, unit + 1, w_shards, L->parts, w_full, stream)) != ZERO_OK)
         return st;

@@ -764,8 +764,11 @@ zero_status zero_gemm_grouped_depth_bf16(int32_t n_groups, const int64_t *offset
                dw_full = x^T dz from the kept x (bf16 or 8 bits), padding
                rows zeroed.  dz is a batch x out bf16 buffer (it may be dy or a
                bf16 preact); for ZERO_ACT_NONE it may be NULL and dy is used as
-               it is.  x and dz are read last, for dW: dz needs memory apart
-               from x, dx from both.
+               it is.  The steps run in this order, and a buffer may be
+               written again once nothing later reads it (dx over dy, dw_full
+               over w_full); one address for two things that are needed at
+               once is refused.  w_full comes before all that the call reads,
+               x and dz are read last, for dW.
                dbias may be NULL; workspace as zero_act_backward.
    batch is any number here; otherwise as zero_fsdp_linear_*. */
 zero_status zero_fsdp_linear_act_forward(const zero_layout *layout, int32_t unit,
@@ -788,8 +791,9 @@ zero_status zero_fsdp_linear_act_backward(const zero_layout *layout, int32_t uni
      backward: w_full again; dx = grouped dy W_e^T; dw_full = the experts' dW
                one after the other (fp32, the padded unit), ready for
                zero_reduce_shard and zero_adam_step.
-   in and out multiples of 8; dx needs memory apart from x and dy.  Rows in no
-   group keep their y and dx. */
+   in and out multiples of 8; w_full needs memory apart from all that a call
+   reads, dx apart from x, dy and dw_full.  Rows in no group keep their y and
+   dx. */
 zero_status zero_fsdp_experts_forward(const zero_layout *layout, int32_t unit,
                                       int32_t n_experts, const uint16_t *const *w_shards,
                                       const int64_t *offsets, int64_t rows, const uint16_t *x,

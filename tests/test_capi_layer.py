@@ -443,3 +443,70 @@ def test_the_epilogue_gradient_writes_over_nothing_that_it_uses():
         with pytest.raises(zs.ZeroShardError) as e:
             call(**{**base, "work": base["db"]}, rows=100)
         assert e.value.status == zs.ERR_HIP
+
+
+W_, X_, XS, DY, DZ, DX, DW = (FAKE + (i << 33) for i in range(11, 18))
+SHARDS = [FAKE + (20 << 33), FAKE + (21 << 33)]
+
+
+def test_a_layer_gathers_its_weight_over_nothing_that_it_uses():
+    """w_full is written first: over x, bias, residual or what is kept it
+    would be read, or written, as the weight."""
+    L = zs.shard_init_rows("fsdp2", 2, 0, [(64, 64)])
+
+    def call(w, x, y, r, bias, z, zsc):
+        zs.fsdp_linear_act_forward(L, 0, SHARDS, 40, x, w, y,
+                                   zs.Epilogue(bias=bias, residual=r, ldr=72, preact=zs.Saved(z, 64, zsc, 64)),
+                                   stream=0)
+
+    base = dict(w=W_, x=X_, y=C_, r=R_, bias=BIAS, z=Z_, zsc=ZS)
+    shared_address_is_refused(call, base, *[("w", o) for o in base if o != "w"])
+
+    def experts(w, x, y, r, z, off):
+        zs.fsdp_experts_forward(L, 0, 2, SHARDS, off, 40, x, w, y,
+                                zs.Epilogue(residual=r, ldr=72, preact=zs.Saved(z, 64)), stream=0)
+
+    base = dict(w=W_, x=X_, y=C_, r=R_, z=Z_, off=OFF)
+    shared_address_is_refused(experts, base, *[("w", o) for o in base if o != "w"])
+
+
+def test_layer_gradients_lie_over_nothing_that_is_still_used():
+    L = zs.shard_init_rows("fsdp2", 2, 0, [(64, 64)])
+
+    def call(w, x, xs, z, zsc, dy, dz, dx, dw, db, work, act="gelu", batch=300):
+        zs.fsdp_linear_act_backward(L, 0, SHARDS, batch, zs.Saved(x, 64, xs, 64), act, zs.Saved(z, 64, zsc, 64),
+                                    dy, w, dz, dx, dw, db, work, stream=0)
+
+    base = dict(w=W_, x=X_, xs=XS, z=Z_, zsc=ZS, dy=DY, dz=DZ, dx=DX, dw=DW, db=BIAS, work=O_)
+    pairs = [("w", o) for o in base if o not in ("w", "dw")]
+    pairs += [("dz", o) for o in ("x", "xs", "zsc", "dx", "dw", "db", "work")]
+    pairs += [("dx", o) for o in ("x", "xs", "dw", "db")]
+    pairs += [("dw", o) for o in ("x", "xs", "db")]
+    pairs += [("db", o) for o in ("x", "xs", "dy", "work")]
+    pairs += [("work", o) for o in ("x", "xs", "dy", "z")]
+    shared_address_is_refused(call, base, *pairs)
+    plain = dict(base, act="none", dz=None)
+    shared_address_is_refused(call, plain, ("dx", "dy"), ("dw", "dy"), ("w", "dy"), ("w", "x"))
+
+    def experts(w, x, dy, dx, dw, off):
+        zs.fsdp_experts_backward(L, 0, 2, SHARDS, off, 40, x, dy, w, dx, dw, stream=0)
+
+    base = dict(w=W_, x=X_, dy=DY, dx=DX, dw=DW, off=OFF)
+    shared_address_is_refused(experts, base, *[("w", o) for o in ("x", "dy", "dx", "off")],
+                              *[("dx", o) for o in ("x", "dy", "dw", "off")],
+                              *[("dw", o) for o in ("x", "dy", "off")])
+
+
+def test_layer_buffers_that_are_done_with_may_be_used_again():
+    """What a step no longer reads is a later step's to write: dW over the
+    gathered weight, dx over dy or the kept z."""
+    if torch.cuda.is_available():
+        pytest.skip("fake addresses would be launched on")
+    L = zs.shard_init_rows("fsdp2", 2, 0, [(64, 64)])
+    for kw in (dict(dw=W_), dict(dx=DY), dict(dx=Z_), dict(dw=DY), dict(dw=Z_), dict(dz=DY), dict(dz=Z_)):
+        a = dict(dz=DZ, dx=DX, dw=DW, **{})
+        a.update(kw)
+        with pytest.raises(zs.ZeroShardError) as e:
+            zs.fsdp_linear_act_backward(L, 0, SHARDS, 40, zs.Saved(X_, 64), "gelu", zs.Saved(Z_, 64), DY, W_,
+                                        a["dz"], a["dx"], a["dw"], stream=0)
+        assert e.value.status == zs.ERR_HIP, kw
