@@ -1565,7 +1565,7 @@ zero_status gemm_saved_check(int64_t M, int64_t N, int64_t K, const zero_saved *
         return ZERO_OK;
     zero_status st;
     if ((st = saved_check("A", A, K, M)) != ZERO_OK ||
-        (st = check_matrix("B", B, ldb, N, ZERO_BF16)) != ZERO_OK ||
+        (st = check_matrix("B", operand(B, K > 0), ldb, N, ZERO_BF16)) != ZERO_OK ||
         (st = check_matrix("C", C, ldc, N, c_dtype)) != ZERO_OK)
         return st;
     if (is_one_of(C, {A->data, scales_of(A), B}))
@@ -1745,7 +1745,8 @@ zero_status grouped_rows_check(int32_t n_groups, const int64_t *offsets, int64_t
 {
     zero_status st;
     if ((st = grouped_check(n_groups, offsets, rows)) != ZERO_OK ||
-        (st = gemm_check(rows, N, K, A, lda, ZERO_K_INNER, B, ldb, b_order, C, ldc, c_dtype)) != ZERO_OK ||
+        (st = gemm_check(rows, N, K, operand(A, K > 0), lda, ZERO_K_INNER, operand(B, K > 0), ldb, b_order, C,
+                         ldc, c_dtype)) != ZERO_OK ||
         (st = epilogue_check(rows, N, A, B, C, ldc, c_dtype, ep, offsets)) != ZERO_OK)
         return st;
     if (rows == 0 || N == 0)
@@ -1826,8 +1827,8 @@ zero_status grouped_depth_check(int32_t n_groups, const int64_t *offsets, int64_
     // K rounded down to gemm_check's multiple of 8: with both operands
     // K-outer any number of rows will do.
     if ((st = grouped_check(n_groups, offsets, rows)) != ZERO_OK ||
-        (st = gemm_check(M, N, rows / 8 * 8, A, lda, ZERO_K_OUTER, B, ldb, ZERO_K_OUTER, C, ldc,
-                         c_dtype)) != ZERO_OK)
+        (st = gemm_check(M, N, rows / 8 * 8, operand(A, rows > 0), lda, ZERO_K_OUTER, operand(B, rows > 0),
+                         ldb, ZERO_K_OUTER, C, ldc, c_dtype)) != ZERO_OK)
         return st;
     if (M == 0 || N == 0)
         return ZERO_OK;
@@ -1896,7 +1897,8 @@ zero_status zero_gemm_bf16_epilogue(int64_t M, int64_t N, int64_t K, const uint1
                                     void *stream)
 {
     zero_status st;
-    if ((st = zs::gemm_check(M, N, K, A, lda, a_order, B, ldb, b_order, C, ldc, c_dtype)) != ZERO_OK ||
+    if ((st = zs::gemm_check(M, N, K, zs::operand(A, K > 0), lda, a_order, zs::operand(B, K > 0), ldb, b_order,
+                             C, ldc, c_dtype)) != ZERO_OK ||
         (st = zs::epilogue_check(M, N, A, B, C, ldc, c_dtype, epilogue, nullptr)) != ZERO_OK)
         return st;
     return zs::epilogue_gemm_run(M, N, K, A, lda, a_order, B, ldb, b_order, C, ldc, c_dtype, epilogue,

@@ -160,7 +160,7 @@ zero_status zero_fsdp_linear_act_forward(const zero_layout *L, int32_t unit,
     zero_status st = layer_dims(L, unit, &d);
     if (st != ZERO_OK)
         return st;
-    if (!w_shards || !x || !w_full || !y || batch < 0)
+    if (!w_shards || !w_full || batch < 0 || (batch > 0 && (!x || !y)))
         return zs::fail(ZERO_ERR_INVALID_ARG, "w_shards, x, w_full, y and batch >= 0 are "
                         "required");
     if ((st = check_shards(L, w_shards)) != ZERO_OK)
@@ -193,7 +193,7 @@ zero_status zero_fsdp_linear_act_backward(const zero_layout *L, int32_t unit,
     zero_status st = layer_dims(L, unit, &d);
     if (st != ZERO_OK)
         return st;
-    if (!w_shards || !x || !dy || !w_full || !dx || !dw_full || batch < 0)
+    if (!w_shards || !x || !w_full || !dw_full || batch < 0 || (batch > 0 && (!dy || !dx)))
         return zs::fail(ZERO_ERR_INVALID_ARG, "w_shards, x, dy, w_full, dx, dw_full and batch >= 0 "
                         "are required");
     if ((st = check_shards(L, w_shards)) != ZERO_OK)
@@ -201,7 +201,7 @@ zero_status zero_fsdp_linear_act_backward(const zero_layout *L, int32_t unit,
     if (d.in % 8 || d.out % 8)
         return zs::fail(ZERO_ERR_UNSUPPORTED, "in_features and out_features must be "
                         "multiples of 8");
-    if (act != ZERO_ACT_NONE && !dz)
+    if (act != ZERO_ACT_NONE && !dz && batch > 0)
         return zs::fail(ZERO_ERR_INVALID_ARG, "dz is required for an activation");
     // Without an activation dz is dy itself.
     const uint16_t *g = act == ZERO_ACT_NONE ? dy : dz;
@@ -262,7 +262,7 @@ zero_status zero_fsdp_experts_forward(const zero_layout *L, int32_t unit, int32_
     zero_status st = expert_dims(L, unit, n_experts, &d);
     if (st != ZERO_OK)
         return st;
-    if (!w_shards || !x || !w_full || !y || rows < 0)
+    if (!w_shards || !w_full || rows < 0 || (rows > 0 && (!x || !y)))
         return zs::fail(ZERO_ERR_INVALID_ARG, "w_shards, x, w_full, y and rows >= 0 are required");
     if ((st = check_shards(L, w_shards)) != ZERO_OK)
         return st;
@@ -288,7 +288,7 @@ zero_status zero_fsdp_experts_backward(const zero_layout *L, int32_t unit, int32
     zero_status st = expert_dims(L, unit, n_experts, &d);
     if (st != ZERO_OK)
         return st;
-    if (!w_shards || !x || !dy || !w_full || !dx || !dw_full || rows < 0)
+    if (!w_shards || !w_full || !dw_full || rows < 0 || (rows > 0 && (!x || !dy || !dx)))
         return zs::fail(ZERO_ERR_INVALID_ARG, "every buffer and rows >= 0 are required");
     if ((st = check_shards(L, w_shards)) != ZERO_OK)
         return st;

@@ -18,6 +18,13 @@ int cu_count();
 zero_status gemm_check(int64_t M, int64_t N, int64_t K, const uint16_t *A, int64_t lda,
                        int32_t a_order, const uint16_t *B, int64_t ldb, int32_t b_order,
                        const void *C, int64_t ldc, int32_t c_dtype);
+// An operand for gemm_check: one that is never read, as in a product of K = 0, may
+// be NULL, which an empty tensor's address is; gemm_check wants an address.
+inline const uint16_t *operand(const uint16_t *p, bool read)
+{
+    alignas(16) static const uint16_t unread[8] = {};
+    return p || read ? p : unread;
+}
 zero_status gemm_run(int64_t M, int64_t N, int64_t K, const uint16_t *A, int64_t lda, int32_t a_order,
                      const uint16_t *B, int64_t ldb, int32_t b_order, void *C, int64_t ldc,
                      int32_t c_dtype, hipStream_t s);

@@ -327,6 +327,8 @@ zero_status saved_check(const char *what, const zero_saved *s, int64_t rows, int
     zero_status st;
     if ((st = check_extent(rows, cols, s->ld)) != ZERO_OK)
         return st;
+    if (rows == 0 && !s->data)
+        return ZERO_OK;
     if (s->format == ZERO_SAVED_BF16)
         return check_matrix(what, s->data, s->ld, cols, ZERO_BF16);
     if (!s->data || !s->scales)

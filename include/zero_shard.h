@@ -633,6 +633,9 @@ typedef enum zero_activation {
     ZERO_ACT_SILU = 4
 } zero_activation;
 
+/* In all of these calls a matrix without rows (or a product's operand with
+   K = 0) is never read, and its address may be NULL. */
+
 /* A rows x cols activation matrix kept for the backward pass.
      ZERO_SAVED_BF16  data: rows x cols bf16, leading dimension ld.
      ZERO_SAVED_E4M3  data: rows x cols e4m3 codes of one byte, leading

@@ -510,3 +510,50 @@ def test_layer_buffers_that_are_done_with_may_be_used_again():
             zs.fsdp_linear_act_backward(L, 0, SHARDS, 40, zs.Saved(X_, 64), "gelu", zs.Saved(Z_, 64), DY, W_,
                                         a["dz"], a["dx"], a["dw"], stream=0)
         assert e.value.status == zs.ERR_HIP, kw
+
+
+def test_empty_matrices_have_no_address():
+    """torch.empty((0, n)).data_ptr() is 0: a matrix of no rows is accepted
+    without an address by every call that documents such a size."""
+    if torch.cuda.is_available():
+        pytest.skip("fake addresses would be launched on")
+    L = zs.shard_init_rows("fsdp2", 2, 0, [(64, 64)])
+    none8 = zs.Saved(0, 64, 0, 64)
+    none16 = zs.Saved(0, 64)
+    calls = [
+        lambda: zs.gemm_bf16_epilogue(64, 64, 0, 0, 64, zs.K_INNER, 0, 64, zs.K_OUTER, C_, 64, stream=0),
+        lambda: zs.gemm_saved_bf16(64, 64, 0, none8, 0, 64, C_, 64, stream=0),
+        lambda: zs.gemm_saved_bf16(64, 64, 0, none16, 0, 64, C_, 64, stream=0),
+        lambda: zs.gemm_grouped_rows_bf16(2, OFF, 5, 64, 0, 0, 64, 0, 64, zs.K_OUTER, 0, C_, 64, stream=0),
+        lambda: zs.gemm_grouped_depth_bf16(2, OFF, 0, 64, 64, 0, 64, 0, 64, C_, 64, 4096, stream=0),
+        lambda: zs.act_backward(0, 64, 0, 64, "gelu", none8, 0, 64, BIAS, 0, stream=0),
+        lambda: zs.fsdp_linear_act_forward(L, 0, SHARDS, 0, 0, W_, 0,
+                                           zs.Epilogue(bias=BIAS, act="gelu", preact=none8), stream=0),
+        lambda: zs.fsdp_linear_act_backward(L, 0, SHARDS, 0, none8, "gelu", none8, 0, W_, 0, 0, DW, BIAS, 0,
+                                            stream=0),
+        lambda: zs.fsdp_linear_act_backward(L, 0, SHARDS, 0, none16, "none", None, 0, W_, None, 0, DW,
+                                            stream=0),
+        lambda: zs.fsdp_experts_forward(L, 0, 2, SHARDS, OFF, 0, 0, W_, 0, stream=0),
+        lambda: zs.fsdp_experts_backward(L, 0, 2, SHARDS, OFF, 0, 0, 0, W_, 0, DW, stream=0),
+    ]
+    for k, call in enumerate(calls):
+        with pytest.raises(zs.ZeroShardError) as e:
+            call()
+        assert e.value.status == zs.ERR_HIP, (k, str(e.value))
+    zs.gemm_grouped_rows_bf16(2, OFF, 0, 64, 64, 0, 64, 0, 64, zs.K_OUTER, 4096, 0, 64, stream=0)
+    # with rows to read the address is required still
+    refused(INV, zs.gemm_grouped_depth_bf16, 2, OFF, 1, 64, 64, 0, 64, B_, 64, C_, 64, 4096)
+    refused(INV, zs.gemm_grouped_depth_bf16, 2, OFF, 1, 64, 64, A_, 64, 0, 64, C_, 64, 4096)
+    refused(INV, zs.gemm_saved_bf16, 64, 64, 1, none8, B_, 64, C_, 64)
+    refused(INV, zs.gemm_saved_bf16, 64, 64, 1, zs.Saved(A_, 64), 0, 64, C_, 64)
+    refused(INV, zs.gemm_bf16_epilogue, 64, 64, 8, 0, 64, zs.K_INNER, B_, 64, zs.K_OUTER, C_, 64)
+    refused(INV, zs.gemm_grouped_rows_bf16, 2, OFF, 5, 64, 8, A_, 64, 0, 64, zs.K_OUTER, 4096, C_, 64)
+    for x, dy, dz, dx in ((none8, DY, DZ, DX), (zs.Saved(X_, 64), 0, DZ, DX), (zs.Saved(X_, 64), DY, 0, DX),
+                          (zs.Saved(X_, 64), DY, DZ, 0)):
+        refused(INV, zs.fsdp_linear_act_backward, L, 0, SHARDS, 1, x, "gelu", zs.Saved(Z_, 64), dy, W_, dz, dx,
+                DW)
+    for x, y in ((0, C_), (X_, 0)):
+        refused(INV, zs.fsdp_linear_act_forward, L, 0, SHARDS, 1, x, W_, y)
+        refused(INV, zs.fsdp_experts_forward, L, 0, 2, SHARDS, OFF, 1, x, W_, y)
+    for x, dy, dx in ((0, DY, DX), (X_, 0, DX), (X_, DY, 0)):
+        refused(INV, zs.fsdp_experts_backward, L, 0, 2, SHARDS, OFF, 1, x, dy, W_, dx, DW)

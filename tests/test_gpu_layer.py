@@ -1043,3 +1043,49 @@ def test_a_pre_activation_that_is_not_a_number_gives_no_gradient(act, fmt):
     want = bad if act != "none" else np.zeros_like(bad)
     assert np.array_equal(np.isnan(dz.float().cpu().numpy()), want)
     assert np.array_equal(np.isnan(db.cpu().numpy()), want.any(0))
+
+
+def test_empty_tensors_are_empty_matrices():
+    """A rank without tokens passes torch.empty((0, n)), whose address is 0:
+    dW and dbias are zeros, a product of K = 0 is its bias."""
+    n, inf, outf = 2, 64, 72
+    L = zs.shard_init_rows("fsdp2", n, 1, [(inf, outf)])
+    Lu = L.query(0)["padded_len"]
+    shards = [torch.zeros(L.shard_len, dtype=torch.int16, device=DEV) for _ in range(n)]
+    w_full = torch.empty(Lu, dtype=torch.int16, device=DEV)
+
+    def rows0(k, dt=torch.bfloat16):
+        return torch.empty((0, k), dtype=dt, device=DEV)
+    assert rows0(inf).data_ptr() == 0
+    z8 = zs.Saved(rows0(80, torch.uint8), 80, rows0(outf, torch.uint8), outf)
+    zs.fsdp_linear_act_forward(L, 0, shards, 0, rows0(inf), w_full, rows0(outf),
+                               zs.Epilogue(act="silu", residual=rows0(outf), ldr=outf, preact=z8))
+    for x in (zs.Saved(rows0(inf), inf), zs.Saved(rows0(inf, torch.uint8), inf, rows0(inf, torch.uint8), inf)):
+        dw, db = torch.full((Lu,), 9.0, device=DEV), torch.full((outf,), 9.0, device=DEV)
+        zs.fsdp_linear_act_backward(L, 0, shards, 0, x, "silu", z8, rows0(outf), w_full, rows0(outf), rows0(inf),
+                                    dw, db, torch.empty(0, device=DEV))
+        torch.cuda.synchronize()
+        assert not dw.cpu().numpy().any() and not db.cpu().numpy().any()
+    off = torch.zeros(3, dtype=torch.int64, device=DEV)
+    E = zs.shard_init_rows("fsdp2", n, 1, [(2 * 32, outf)])
+    dw = torch.full((Lu,), 9.0, device=DEV)
+    zs.fsdp_experts_forward(E, 0, 2, shards, off, 0, rows0(32), w_full, rows0(outf))
+    zs.fsdp_experts_backward(E, 0, 2, shards, off, 0, rows0(32), rows0(outf), w_full, rows0(32), dw)
+    torch.cuda.synchronize()
+    assert not dw.cpu().numpy().any()
+    for M, N in ((5, 72), (300, 520), (3104, 2904)):
+        bias = torch.arange(N, dtype=torch.float32, device=DEV)
+        A, B = (torch.empty(s, dtype=torch.bfloat16, device=DEV) for s in ((M, 0), (0, N)))
+        C, D, G = (torch.full((M, N), 9.0, device=DEV) for _ in range(3))
+        zs.gemm_bf16_epilogue(M, N, 0, A, 0, zs.K_INNER, B, N, zs.K_OUTER, C, N, zs.FP32, zs.Epilogue(bias=bias))
+        one = torch.tensor([0, M], dtype=torch.int64, device=DEV)
+        zs.gemm_grouped_rows_bf16(1, one, M, N, 0, A, 0, B, N, zs.K_OUTER, 0, G, N, zs.FP32)
+        torch.cuda.synchronize()
+        assert torch.equal(C, bias.expand(M, N)) and not G.cpu().numpy().any()
+        if M % 8 == 0:
+            for a in (zs.Saved(rows0(M), M), zs.Saved(rows0(-(-M // 16) * 16, torch.uint8), -(-M // 16) * 16,
+                                                      rows0(M, torch.uint8), M)):
+                D.fill_(9.0)
+                zs.gemm_saved_bf16(M, N, 0, a, rows0(N), N, D, N)
+                torch.cuda.synchronize()
+                assert not D.cpu().numpy().any()
