@@ -17,6 +17,9 @@
 // z > -4 and within 3e-6 down to -8, where the rounding of z^2 in the
 // exponent decides.
 //
+// An exponential below fp32's normal numbers comes as 0, so values and slopes
+// under 2^-117 may: silu past -87, gelu_tanh past -10, gelu past -13.
+//
 // Infinities: every activation takes its limit (gelu(-inf) = silu(-inf) = -0,
 // slopes 0 and 1); NaN stays NaN.
 #pragma once
@@ -74,8 +77,9 @@ __device__ __forceinline__ float finite_low(float z)
 {
     return __builtin_amdgcn_fmed3f(z, -FLT_MAX, __builtin_inff());
 }
-// Past +-64 every slope's second term is 0; the bound keeps it from 0 * inf.
-__device__ __forceinline__ float bound64(float z) { return __builtin_amdgcn_fmed3f(z, -64.0f, 64.0f); }
+// Past +-128 every slope's second term is 0 -- silu's e^-|z|, the slowest to
+// go, leaves fp32 at 104 -- and the bound keeps it from 0 * inf.
+__device__ __forceinline__ float bound128(float z) { return __builtin_amdgcn_fmed3f(z, -128.0f, 128.0f); }
 
 constexpr float kTanhK = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kInvSqrt2Pi = 0.3989422804014327f;
@@ -104,14 +108,14 @@ __device__ __forceinline__ float act_slope(float z)
         return z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z;
     } else if constexpr (ACT == ZERO_ACT_GELU) {
         const float c = normal_cdf(z, q);
-        return __builtin_fmaf(bound64(z) * kInvSqrt2Pi, q, c);
+        return __builtin_fmaf(bound128(z) * kInvSqrt2Pi, q, c);
     } else if constexpr (ACT == ZERO_ACT_GELU_TANH) {
-        const float b = bound64(z);
+        const float b = bound128(z);
         const float s = sigmoid(kTanhK * z * __builtin_fmaf(0.044715f * z, z, 1.0f), q);
         return __builtin_fmaf(b * q, kTanhK * __builtin_fmaf(3.0f * 0.044715f * b, b, 1.0f), s);
     } else if constexpr (ACT == ZERO_ACT_SILU) {
         const float s = sigmoid(z, q);
-        return __builtin_fmaf(bound64(z), q, s);
+        return __builtin_fmaf(bound128(z), q, s);
     } else {
         return 1.0f;
     }

@@ -64,6 +64,21 @@ def slope(name: str, z: np.ndarray) -> np.ndarray:
     return s + c * s * (1 - s)
 
 
+def slope_terms(name: str, z: np.ndarray):
+    """(first, second, weight): the slope is first + second, second being its
+    exponential's weight times that exponential (below 1 in both terms)."""
+    z = np.asarray(z, np.float64)
+    if name == "gelu":
+        w = z / math.sqrt(2 * math.pi)
+        return 0.5 * erfc(-z / math.sqrt(2)), w * np.exp(-z * z / 2), w
+    if name == "gelu_tanh":
+        s, w = _sigmoid(_tanh_arg(z)), z * 2 * math.sqrt(2 / math.pi) * (1 + 3 * 0.044715 * z * z)
+        return s, w * s * _sigmoid(-_tanh_arg(z)), w
+    if name == "silu":
+        return _sigmoid(z), z * _sigmoid(z) * _sigmoid(-z), z
+    return slope(name, z), np.zeros_like(z), np.zeros_like(z)
+
+
 def act_rel(name: str, z: np.ndarray) -> np.ndarray:
     """Relative error allowed to an fp32 evaluation of act(z) at an fp32 z,
     and of each of the terms of its slope.  The exponential e^-a carries the

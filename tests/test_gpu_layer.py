@@ -1089,3 +1089,28 @@ def test_empty_tensors_are_empty_matrices():
                 zs.gemm_saved_bf16(M, N, 0, a, rows0(N), N, D, N)
                 torch.cuda.synchronize()
                 assert not D.cpu().numpy().any()
+
+
+@pytest.mark.parametrize("act", layer.ACTS)
+def test_slopes_of_far_values(act):
+    """The slope's two terms, each to its own size, out to where fp32 ends.
+    The exponent's argument a carries at most 8 roundings (its constants' three
+    among them), 8 a 2^-24 in e^-a; everything else is below 24 of them, as in
+    oracle.layer.act_rel.  An e^-a below fp32's normal numbers may come as 0:
+    2^-126 of each term's weight."""
+    z = np.concatenate([np.arange(-112, -4, 0.0625), np.arange(4, 112, 0.0625)])
+    z = np.unique(val(_c.f32_to_bf16(z.astype(np.float32))))
+    N = z.size
+    kept = zs.Saved(dev16(_c.f32_to_bf16(z.astype(np.float32))), N)
+    dz, db = torch.empty(1, N, dtype=torch.bfloat16, device=DEV), torch.empty(N, device=DEV)
+    zs.act_backward(1, N, torch.ones(1, N, device=DEV), N, act, kept, dz, N, db)
+    torch.cuda.synchronize()
+    first, second, weight = layer.slope_terms(act, z)
+    a = {"gelu": z * z / 2, "gelu_tanh": np.abs(layer._tanh_arg(z)), "silu": np.abs(z)}.get(act, 0 * z)
+    rel = (24 + 8 * np.minimum(a, 200.0)) * U32
+    bound = rel * (np.abs(first) + np.abs(second)) + 2.0 ** -126 * (1 + np.abs(weight))
+    bound = bound if act not in ("none", "relu") else np.zeros_like(z)
+    got, want = db.cpu().numpy().astype(np.float64), first + second
+    within(got, want, bound, "slope")
+    half = UB * (np.abs(want) + bound) + 2.0 ** -134        # a subnormal's half step
+    within(dz.float().cpu().numpy()[0], want, bound + half, "slope in bf16")

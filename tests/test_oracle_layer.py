@@ -132,3 +132,13 @@ def test_grouped_products_are_the_groups_products():
     d = layer.grouped_depth(off, a, out)
     assert not d[0].any() and not d[2].any()
     assert np.allclose(d[1] + d[3], a[2:12].T @ out[2:12], rtol=0, atol=1e-10)
+
+
+@pytest.mark.parametrize("act", layer.ACTS)
+def test_slope_terms_add_up(act):
+    z = np.linspace(-150, 150, 6001)
+    a, b, _ = layer.slope_terms(act, z)
+    # far out the terms' own exponentials are the more precise form
+    assert np.abs(a + b - layer.slope(act, z)).max() < 1e-13
+    if act == "silu":
+        assert np.allclose((a + b)[z < -40], (np.exp(z) * (1 + z))[z < -40], rtol=1e-12, atol=0)
