@@ -1114,3 +1114,87 @@ def test_slopes_of_far_values(act):
     within(got, want, bound, "slope")
     half = UB * (np.abs(want) + bound) + 2.0 ** -134        # a subnormal's half step
     within(dz.float().cpu().numpy()[0], want, bound + half, "slope in bf16")
+
+
+# ------------------------------------- the tiles that large products take --
+
+@pytest.mark.parametrize("ao,bo", [(0, 0), (0, 1), (1, 0), (1, 1)])
+@pytest.mark.parametrize("case", [
+    (2040, 9448, 600, 0, "silu", "bf16", None, "bf16", "bf16", False),
+    (3104, 2904, 616, 8, "gelu", "bf16", "bf16", "fp32", "bf16", True),
+], ids=lambda c: f"{c[0]}x{c[1]}x{c[2]}")
+def test_epilogue_of_large_products(case, ao, bo):
+    """256 x 256 tiles past the steady loop's start: an odd and an even number
+    of 32-k tiles, each with a rest."""
+    test_epilogue_within_bounds(case, ao, bo)
+
+
+def test_epilogue_of_a_large_product_in_8_bits():
+    test_epilogue_within_bounds((3104, 2904, 424, 8, "silu", None, "bf16", "bf16", "e4m3", True), 0, 1)
+
+
+# 13 row tiles of 256, tails of 1, 44, 100, 128, 129 and 255 rows
+LARGE = [5, 300, 129, 0, 640, 100, 256, 511, 1, 385, 3]
+
+
+@pytest.mark.parametrize("N,K,bo,act", [(2056, 584, 0, "silu"), (2056, 584, 1, "gelu"), (4104, 328, 0, "none"),
+                                        (4104, 328, 1, "relu"), (5128, 264, 0, "gelu_tanh"),
+                                        (5128, 264, 1, "silu")])
+def test_grouped_rows_of_large_groups(N, K, bo, act):
+    """256 x 256 tiles: with 256 CUs 2056 columns run as half tiles, 4104 as
+    whole ones, 5128 as 256 whole ones and the rest halves."""
+    test_grouped_rows_within_bounds(LARGE, N, K, bo, act)
+
+
+@pytest.mark.parametrize("counts,M,N", [([3, 300, 33, 0, 641, 200, 9], 1288, 1544),    # 256 x 256 tiles
+                                        ([0, 30, 130, 0, 224, 200, 0], 392, 1000),      # 256 x 128
+                                        ([2, 100, 7, 0, 255, 1, 12], 1288, 1544)])
+@pytest.mark.parametrize("store", ["lines", "fp32", "bf16"])
+def test_grouped_depth_of_large_groups(counts, M, N, store):
+    """Past the steady loops' start, with fp32 rows of whole 128-byte lines
+    (stored past the caches), others and bf16."""
+    off, rows = offsets_of(counts)
+    G = len(off) - 1
+    rng = np.random.default_rng(rows + M + N)
+    a, b = rand_bf16(rng, (rows, M)), rand_bf16(rng, (rows, N))
+    ldc = -(-N // 32) * 32 if store == "lines" else N + 5
+    dt = torch.bfloat16 if store == "bf16" else torch.float32
+    C = torch.full((G, M + 1, ldc), 7.0, dtype=dt, device=DEV)
+    assert C.data_ptr() % 128 == 0
+    zs.gemm_grouped_depth_bf16(G, torch.from_numpy(off.astype(np.int64)).to(DEV), rows, M, N, dev16(a), M,
+                               dev16(b), N, C, ldc, (M + 1) * ldc, zs.BF16 if store == "bf16" else zs.FP32)
+    torch.cuda.synchronize()
+    av, bv = val(a), val(b)
+    want = layer.grouped_depth(off, av, bv)
+    bound = np.stack([linear.gamma(max(1, hi - lo)) * (np.abs(av[lo:hi]).T @ np.abs(bv[lo:hi]))
+                      for lo, hi in zip(off[:-1], off[1:])])
+    if store == "bf16":
+        bound = bound + UB * (np.abs(want) + bound)
+    got = C.float().cpu().numpy()
+    within(got[:, :M, :N], want, bound, "C")
+    assert (got[:, :, N:] == 7.0).all() and (got[:, M:] == 7.0).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(1000, 1024, 1097), (2040, 9448, 301), (3104, 2904, 421)])
+@pytest.mark.parametrize("store", ["lines", "fp32", "bf16"])
+def test_large_products_from_a_kept_operand(M, N, K, store):
+    """128 x 128 tiles, 256 x 256 ones and halves, and whole ones alone, past
+    the steady loop's start and several refills of the exponents."""
+    rng = np.random.default_rng(M + N + K)
+    x = _c.f32_to_bf16((rng.standard_normal((K, M)) * np.exp(rng.uniform(-4, 4, (1, M)))).astype(np.float32))
+    b = rand_bf16(rng, (K, N))
+    s = zs.Saved.empty(K, M, DEV)
+    s.data.fill_(0x7F)                      # NaN codes around the matrix
+    zs.saved_write(K, M, dev16(x), M, s)
+    ldc = -(-N // 32) * 32 if store == "lines" else N + 3
+    C = torch.full((M, ldc), 7.0, dtype=torch.bfloat16 if store == "bf16" else torch.float32, device=DEV)
+    zs.gemm_saved_bf16(M, N, K, s, dev16(b), N, C, ldc, zs.BF16 if store == "bf16" else zs.FP32)
+    torch.cuda.synchronize()
+    xv = layer.decode(s.data.cpu().numpy()[:K, :M], s.scales.cpu().numpy()[:, :M])
+    bv = val(b)
+    exact, bound = xv.T @ bv, linear.gemm_bound(xv.T, bv)
+    if store == "bf16":
+        bound = bound + UB * (np.abs(exact) + bound)
+    got = C.float().cpu().numpy()
+    within(got[:, :N], exact, bound, "C")
+    assert (got[:, N:] == 7.0).all()
