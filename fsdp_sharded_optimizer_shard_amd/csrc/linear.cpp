@@ -13,6 +13,8 @@
 // multiple-of-8 rule on it.
 #include <hip/hip_runtime.h>
 
+#include <initializer_list>
+
 #include "checks.h"
 #include "products.h"
 
@@ -51,6 +53,16 @@ zero_status check_shards(const zero_layout *L, const uint16_t *const *w_shards)
     return ZERO_OK;
 }
 
+// No result over a shard, which is some rank's weight after the call too.
+zero_status check_results(const zero_layout *L, const uint16_t *const *w_shards,
+                          std::initializer_list<const void *> results)
+{
+    for (int32_t q = 0; q < L->parts; ++q)
+        if (is_one_of(w_shards[q], results))
+            return zs::fail(ZERO_ERR_INVALID_ARG, "a result must not lie over the W shard of rank %d", q);
+    return ZERO_OK;
+}
+
 // An expert unit's dimensions: in is one expert's, in_pad the whole unit's
 // padded rows.
 zero_status expert_dims(const zero_layout *L, int32_t unit, int32_t n_experts, Dims *d)
@@ -69,13 +81,14 @@ zero_status expert_dims(const zero_layout *L, int32_t unit, int32_t n_experts, D
 }
 
 // The gather writes w_full before a forward product reads anything else; what
-// the product writes over w_full is its own checks' to find.
-zero_status check_gathered(const uint16_t *w_full, const uint16_t *x, const int64_t *offsets,
-                           const zero_epilogue *ep)
+// the product writes over w_full is its own checks' to find, over a shard not.
+zero_status check_gathered(const zero_layout *L, const uint16_t *const *w_shards, const uint16_t *w_full,
+                           const uint16_t *x, const int64_t *offsets, const zero_epilogue *ep, const void *y)
 {
     if (is_one_of(w_full, {x, offsets, ep ? ep->bias : nullptr, ep ? ep->residual : nullptr}))
         return zs::fail(ZERO_ERR_INVALID_ARG, "w_full must not lie where the call reads something else");
-    return ZERO_OK;
+    const zero_saved *z = ep ? ep->preact : nullptr, *o = ep ? ep->output : nullptr;
+    return check_results(L, w_shards, {y, data_of(z), scales_of(z), data_of(o), scales_of(o)});
 }
 
 }  // namespace
@@ -172,7 +185,8 @@ zero_status zero_fsdp_linear_act_forward(const zero_layout *L, int32_t unit,
                              ZERO_K_OUTER, y, d.out, y_dtype)) != ZERO_OK ||
         (st = zs::epilogue_check(batch, d.out, x, w_full, y, d.out, y_dtype, epilogue,
                                  nullptr)) != ZERO_OK ||
-        (batch > 0 && (st = check_gathered(w_full, x, nullptr, epilogue)) != ZERO_OK))
+        (batch > 0 &&
+         (st = check_gathered(L, w_shards, w_full, x, nullptr, epilogue, y)) != ZERO_OK))
         return st;
     if ((st = zero_gather_params(L, unit, unit + 1, w_shards, L->parts, w_full, stream)) != ZERO_OK)
         return st;
@@ -230,6 +244,9 @@ zero_status zero_fsdp_linear_act_backward(const zero_layout *L, int32_t unit,
          is_one_of(dw_full, {x->data, x8, g, dx, dbias})))
         return zs::fail(ZERO_ERR_INVALID_ARG, "w_full, dz, dbias, the workspace, dx and dw_full must not lie "
                         "where x, w_full, dz or a result is still read or kept");
+    if ((st = check_results(L, w_shards, {batch > 0 && kept ? dz : nullptr, batch > 0 ? dx : nullptr, dw_full,
+                                          dbias, w})) != ZERO_OK)
+        return st;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     if ((st = zero_gather_params(L, unit, unit + 1, w_shards, L->parts, w_full, stream)) != ZERO_OK)
         return st;
@@ -269,7 +286,8 @@ zero_status zero_fsdp_experts_forward(const zero_layout *L, int32_t unit, int32_
     const int64_t stride = d.in * d.out;
     if ((st = zs::grouped_rows_check(n_experts, offsets, rows, d.out, d.in, x, d.in, w_full, d.out,
                                      ZERO_K_OUTER, stride, y, d.out, y_dtype, epilogue)) != ZERO_OK ||
-        (rows > 0 && (st = check_gathered(w_full, x, offsets, epilogue)) != ZERO_OK))
+        (rows > 0 &&
+         (st = check_gathered(L, w_shards, w_full, x, offsets, epilogue, y)) != ZERO_OK))
         return st;
     if ((st = zero_gather_params(L, unit, unit + 1, w_shards, L->parts, w_full, stream)) != ZERO_OK)
         return st;
@@ -301,6 +319,8 @@ zero_status zero_fsdp_experts_backward(const zero_layout *L, int32_t unit, int32
     if (rows > 0 && (is_one_of(dx, {x, dw_full}) || is_one_of(w_full, {x, dy, offsets})))
         return zs::fail(ZERO_ERR_INVALID_ARG, "dx must not lie where x is still read or dw_full is written, nor "
                         "w_full where x, dy or the offsets are still read");
+    if ((st = check_results(L, w_shards, {rows > 0 ? dx : nullptr, dw_full})) != ZERO_OK)
+        return st;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     if ((st = zero_gather_params(L, unit, unit + 1, w_shards, L->parts, w_full, stream)) != ZERO_OK)
         return st;

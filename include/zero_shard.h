@@ -770,8 +770,8 @@ zero_status zero_gemm_grouped_depth_bf16(int32_t n_groups, const int64_t *offset
                it is.  The steps run in this order, and a buffer may be
                written again once nothing later reads it (dx over dy, dw_full
                over w_full); one address for two things that are needed at
-               once is refused.  w_full comes before all that the call reads,
-               x and dz are read last, for dW.
+               once, or for a result and a shard, is refused.  w_full comes
+               before all that the call reads, x and dz are read last, for dW.
                dbias may be NULL; workspace as zero_act_backward.
    batch is any number here; otherwise as zero_fsdp_linear_*. */
 zero_status zero_fsdp_linear_act_forward(const zero_layout *layout, int32_t unit,

@@ -557,3 +557,37 @@ def test_empty_matrices_have_no_address():
         refused(INV, zs.fsdp_experts_forward, L, 0, 2, SHARDS, OFF, 1, x, W_, y)
     for x, dy, dx in ((0, DY, DX), (X_, 0, DX), (X_, DY, 0)):
         refused(INV, zs.fsdp_experts_backward, L, 0, 2, SHARDS, OFF, 1, x, dy, W_, dx, DW)
+
+
+def test_layer_results_lie_over_no_shard():
+    """A result over a rank's shard would be that rank's weight from then on."""
+    L = zs.shard_init_rows("fsdp2", 2, 0, [(64, 64)])
+
+    def forward(y, z, zsc, o, os_, s0, s1):
+        zs.fsdp_linear_act_forward(L, 0, [s0, s1], 40, X_, W_, y,
+                                   zs.Epilogue(preact=zs.Saved(z, 64, zsc, 64), output=zs.Saved(o, 64, os_, 64)),
+                                   stream=0)
+
+    base = dict(y=C_, z=Z_, zsc=ZS, o=O_, os_=OS, s0=SHARDS[0], s1=SHARDS[1])
+    shared_address_is_refused(forward, base, *[(w, s) for w in ("y", "z", "zsc", "o", "os_") for s in ("s0", "s1")])
+
+    def backward(dz, dx, dw, db, work, s0, s1):
+        zs.fsdp_linear_act_backward(L, 0, [s0, s1], 300, zs.Saved(X_, 64), "silu", zs.Saved(Z_, 64), DY, W_, dz, dx,
+                                    dw, db, work, stream=0)
+
+    base = dict(dz=DZ, dx=DX, dw=DW, db=BIAS, work=O_, s0=SHARDS[0], s1=SHARDS[1])
+    shared_address_is_refused(backward, base, *[(w, s) for w in ("dz", "dx", "dw", "db", "work")
+                                                for s in ("s0", "s1")])
+
+    def experts(y, z, s0, s1):
+        zs.fsdp_experts_forward(L, 0, 2, [s0, s1], OFF, 40, X_, W_, y, zs.Epilogue(preact=zs.Saved(z, 64)),
+                                stream=0)
+
+    base = dict(y=C_, z=Z_, s0=SHARDS[0], s1=SHARDS[1])
+    shared_address_is_refused(experts, base, *[(w, s) for w in ("y", "z") for s in ("s0", "s1")])
+
+    def gradients(dx, dw, s0, s1):
+        zs.fsdp_experts_backward(L, 0, 2, [s0, s1], OFF, 40, X_, DY, W_, dx, dw, stream=0)
+
+    base = dict(dx=DX, dw=DW, s0=SHARDS[0], s1=SHARDS[1])
+    shared_address_is_refused(gradients, base, *[(w, s) for w in ("dx", "dw") for s in ("s0", "s1")])
