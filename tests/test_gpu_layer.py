@@ -1198,3 +1198,55 @@ def test_large_products_from_a_kept_operand(M, N, K, store):
     got = C.float().cpu().numpy()
     within(got[:, :N], exact, bound, "C")
     assert (got[:, N:] == 7.0).all()
+
+
+@pytest.mark.parametrize("batch", [40, 300])
+def test_layer_gradients_over_buffers_that_are_done_with(batch):
+    """dz over z, dx over dy, dW over the gathered weight: the bits of the same
+    call with buffers of its own."""
+    rng = np.random.default_rng(batch)
+    n, inf, outf = 2, 72, 136
+    L = zs.shard_init_rows("fsdp2", n, 0, [(inf, outf)])
+    c, Lu = L.shard_len // outf, L.query(0)["padded_len"]
+    shards = _shards(rng, rand_bf16(rng, (inf, outf)), n, c, outf)
+    x, dy, z = (dev16(rand_bf16(rng, (batch, k))) for k in (inf, outf, outf))
+    work = torch.empty(zs.act_backward_workspace(batch, outf), device=DEV)
+
+    def run(dy, z, w_full, dz, dx, dw):
+        db = torch.empty(outf, device=DEV)
+        zs.fsdp_linear_act_backward(L, 0, shards, batch, zs.Saved(x, inf), "gelu", zs.Saved(z, outf), dy, w_full, dz,
+                                    dx, dw, db, work)
+        torch.cuda.synchronize()
+        return db
+    dz, dx = torch.empty_like(z), torch.empty(batch, inf, dtype=torch.int16, device=DEV)
+    dw = torch.full((Lu,), 9.0, device=DEV)
+    db = run(dy, z, torch.empty(Lu, dtype=torch.int16, device=DEV), dz, dx, dw)
+    dy2, z2, dw2 = dy.clone(), z.clone(), torch.full((Lu,), 9.0, device=DEV)
+    db2 = run(dy2, z2, dw2.view(torch.int16), z2, dy2, dw2)
+    assert torch.equal(db, db2) and torch.equal(dz, z2) and torch.equal(dw, dw2)
+    assert torch.equal(dx.view(-1), dy2.view(-1)[:batch * inf])
+
+
+@pytest.mark.parametrize("ct", ["bf16", "fp32"])
+@pytest.mark.parametrize("M,N", [(40, 72), (300, 520), (3104, 2904)])
+def test_kept_outputs_that_are_not_finite(M, N, ct):
+    """z and C in 8 bits, from the epilogue, where columns hold NaN, infinities,
+    the largest numbers and subnormals: the bytes that writing them gives."""
+    odd = np.array([np.nan, np.inf, -np.inf, 3.4e38, -3.2e38, 3.0e38, 2.0 ** -126, 2.0 ** -140, -0.0, 0.0, 449.0,
+                    448.0], np.float32)
+    bias = np.ones(N, np.float32)
+    bias[::5] = np.resize(odd, bias[::5].size)
+    z8, o8, zc, oc = (new_saved(M, N) for _ in range(4))
+    dt, kind = (torch.bfloat16, zs.BF16) if ct == "bf16" else (torch.float32, zs.FP32)
+    C, unread = torch.empty(M, N, dtype=dt, device=DEV), torch.empty(0, dtype=torch.bfloat16, device=DEV)
+    b = torch.from_numpy(bias).to(DEV)
+    zs.gemm_bf16_epilogue(M, N, 0, unread, 0, zs.K_INNER, unread, N, zs.K_OUTER, C, N, kind,
+                          zs.Epilogue(bias=b, preact=z8, output=o8))
+    z = b + torch.zeros_like(b)             # an empty sum is +0, and +0 + -0 is +0
+    zs.saved_write(M, N, z.expand(M, N).contiguous(), N, zc)
+    zs.saved_write(M, N, C, N, oc)
+    torch.cuda.synchronize()
+    for got, want in ((z8, zc), (o8, oc)):
+        (gc, gb), (wc, wb) = saved_np(got, M, N), saved_np(want, M, N)
+        assert same_codes(gc, wc) and np.array_equal(gb, wb)
+    assert (np.isnan(C.float().cpu().numpy()) == np.isnan(bias)).all()
