@@ -203,13 +203,13 @@ def prepare(case, seed):
         s["targets"][pad] = -100
         s["loss"], s["lse"] = new(r), new(r)
         s["dloss"] = (~pad).float() / (~pad).sum()
-        s["piece"] = min(16384, _up(v, 256))
         tiles = _up(v, 128) // 128
         n = r * (2 * tiles + 2)
         if c["pass"] == "both":
             s["dx"] = new(r, h, dtype=torch.bfloat16)
             s["dw"] = new(*s["w"].shape, dtype=torch.bfloat16)
-            n = max(n, r * s["piece"] // 2 + r * h)
+            # the logits' gradient of a piece of the vocabulary, 128 MB of it, and dx
+            n = max(n, r * min(_up(v, 8), max(4096, (1 << 26) // r)) // 2 + r * h)
         s["work"] = new(n)
     else:
         sizes = _sizes(c)
@@ -494,7 +494,7 @@ def _own(s):
         if c["pass"] == "loss":
             return s["loss"], s["lse"]
         zs.linear_xent_backward(r, v, h, s["x"], h, s["w"], ldw, order, s["targets"], s["lse"],
-                                s["dloss"], s["dx"], h, s["dw"], ldw, s["piece"], s["work"])
+                                s["dloss"], s["dx"], h, s["dw"], ldw, 0, s["work"])
         return s["loss"], s["lse"], s["dx"], s["dw"]
     small = c["state"] == "e4m3"
     if not s["kept"]:       # the list of tensors, which a program makes once
