@@ -38,18 +38,23 @@ INDEX_FULL, INDEX_SHARD = 0, 1
 K_INNER, K_OUTER = 0, 1
 ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = range(5)
 SAVED_BF16, SAVED_E4M3 = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+STATE_FP32, STATE_E4M3 = 0, 1
 MIX_STEP_STREAMS, MIX_READS, MIX_WRITES = 0, 1, 2
 MAX_RANKS_PER_CALL = 64
 NOALLOC_MAX_PARTIALS = 524288
 STATE_CHUNK_MIN, STATE_CHUNK_MAX = 4, 1 << 24     # zero_layout_chunk_state bounds
 STATE_CHUNK_DEFAULT = 8192                         # the measured best on MI355X
 GRAD_CHUNK_DEFAULT = 16384                         # chunked gradients, likewise
+XENT_PIECE_ELEMS = 67108864                        # dz elements of a head's piece, by default
 
 STRATEGY = {"ddp": DDP, "zero1": STAGE1, "zero1_allreduce": STAGE1, "zero2": STAGE2,
             "zero3": STAGE3, "fsdp": FSDP, "fsdp2": FSDP, "megatron_do": MEGATRON_DO}
 
 ACTIVATION = {"none": ACT_NONE, "relu": ACT_RELU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH,
               "silu": ACT_SILU}
+
+SCORE = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
 
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
@@ -188,6 +193,66 @@ _lib.zero_fsdp_experts_forward.restype = _I32
 _lib.zero_fsdp_experts_backward.argtypes = [_P, _I32, _I32, _PP, _P, _I64, _P, _P, _P, _P, _I32, _P,
                                             _P]
 _lib.zero_fsdp_experts_backward.restype = _I32
+
+
+class _Router(ctypes.Structure):
+    _fields_ = [(k, _I32) for k in ("n_experts", "top_k", "n_groups", "top_groups", "group_best",
+                                    "score", "renormalize")] + [("scale", ctypes.c_float)]
+
+
+class _Tensor(ctypes.Structure):
+    _fields_ = [("n", _I64)] + [(k, _P) for k in ("master", "grad", "param", "m", "v", "m_scales",
+                                                  "v_scales")] + [("decay", _I32)]
+
+
+_RP = ctypes.POINTER(_Router)
+_TP = ctypes.POINTER(_Tensor)
+_F32, _U64 = ctypes.c_float, ctypes.c_uint64
+_lib.zero_layer_norm_forward.argtypes = [_I64, _I64, _P, _I64, _I32, _P, _P, _I32, _F32, _P, _I64,
+                                         _I32, _P, _P, _P]
+_lib.zero_layer_norm_forward.restype = _I32
+_lib.zero_layer_norm_backward.argtypes = [_I64, _I64, _P, _I64, _I32, _P, _I64, _I32, _P, _I32, _P,
+                                          _P, _P, _I64, _P, _I64, _I32, _P, _P, _P, _I64, _P]
+_lib.zero_layer_norm_backward.restype = _I32
+_lib.zero_layer_norm_workspace.argtypes = [_I64, _I64]
+_lib.zero_layer_norm_workspace.restype = _I64
+_lib.zero_route_forward.argtypes = [_RP, _I64, _P, _I64, _I32, _P, _P, _P, _P, _P, _P, _P, _I64, _P]
+_lib.zero_route_forward.restype = _I32
+_lib.zero_route_workspace.argtypes = [_RP, _I64]
+_lib.zero_route_workspace.restype = _I64
+_lib.zero_route_backward.argtypes = [_RP, _I64, _P, _I64, _I32, _P, _P, _P, _I64, _I32, _P]
+_lib.zero_route_backward.restype = _I32
+_lib.zero_experts_dispatch.argtypes = [_I64, _I32, _I64, _P, _I64, _P, _P, _I64, _P, _I64, _P]
+_lib.zero_experts_dispatch.restype = _I32
+_lib.zero_experts_combine.argtypes = [_I64, _I32, _I64, _P, _I64, _I64, _P, _P, _P, _I64, _P, _I64,
+                                      _I32, _P]
+_lib.zero_experts_combine.restype = _I32
+_lib.zero_experts_combine_backward.argtypes = [_I64, _I32, _I64, _P, _I64, _I64, _P, _P, _P, _I64, _P,
+                                               _I64, _P, _P]
+_lib.zero_experts_combine_backward.restype = _I32
+_lib.zero_linear_xent_forward.argtypes = [_I64, _I64, _I64, _P, _I64, _P, _I64, _I32, _P, _P, _P, _P,
+                                          _I64, _P]
+_lib.zero_linear_xent_forward.restype = _I32
+_lib.zero_linear_xent_backward.argtypes = [_I64, _I64, _I64, _P, _I64, _P, _I64, _I32, _P, _P, _P, _P,
+                                           _I64, _I32, _P, _I64, _I32, _I64, _P, _I64, _P]
+_lib.zero_linear_xent_backward.restype = _I32
+_lib.zero_linear_xent_workspace.argtypes = [_I64, _I64, _I64, _I32, _I64]
+_lib.zero_linear_xent_workspace.restype = _I64
+_lib.zero_fsdp_head_forward.argtypes = [_P, _I32, _PP, _I32, _I64, _P, _P, _P, _P, _P, _P, _I64, _P]
+_lib.zero_fsdp_head_forward.restype = _I32
+_lib.zero_fsdp_head_backward.argtypes = [_P, _I32, _PP, _I32, _I64, _P, _P, _P, _P, _P, _P, _I32, _P,
+                                         _I64, _P, _I64, _P]
+_lib.zero_fsdp_head_backward.restype = _I32
+_lib.zero_adam_tensors.argtypes = [_I32, _TP, _I32, _I32, ctypes.POINTER(AdamCfg), _U64, _P, _P]
+_lib.zero_adam_tensors.restype = _I32
+_lib.zero_adam_tensors_table.argtypes = [_I32, _TP, _I32, _I32, _P, _I64, _P, _U64, _P, _P]
+_lib.zero_adam_tensors_table.restype = _I32
+_lib.zero_tensors_sumsq.argtypes = [_I32, _TP, _I32, _P, _I64, _P]
+_lib.zero_tensors_sumsq.restype = _I32
+_lib.zero_tensors_partials_count.argtypes = [_I32, _TP]
+_lib.zero_tensors_partials_count.restype = _I64
+_lib.zero_adam_state_read.argtypes = [_I64, _P, _P, _I32, _P, _I32, _P]
+_lib.zero_adam_state_read.restype = _I32
 _lib.zero_stream_mix.argtypes = [_I32, ctypes.POINTER(ctypes.c_void_p), _I32, _P, _P, _P, _P,
                                  _I64, _I64, _I64, _P]
 _lib.zero_stream_mix.restype = _I32
@@ -212,6 +277,13 @@ EXPORTS = ("zero_shard_init", "zero_shard_init_rows", "zero_layout_rows", "zero_
            "zero_gemm_grouped_depth_bf16", "zero_fsdp_linear_act_forward",
            "zero_fsdp_linear_act_backward", "zero_fsdp_experts_forward",
            "zero_fsdp_experts_backward",
+           "zero_layer_norm_forward", "zero_layer_norm_backward", "zero_layer_norm_workspace",
+           "zero_route_forward", "zero_route_workspace", "zero_route_backward",
+           "zero_experts_dispatch", "zero_experts_combine", "zero_experts_combine_backward",
+           "zero_linear_xent_forward", "zero_linear_xent_backward", "zero_linear_xent_workspace",
+           "zero_fsdp_head_forward", "zero_fsdp_head_backward",
+           "zero_adam_tensors", "zero_adam_tensors_table", "zero_tensors_sumsq",
+           "zero_tensors_partials_count", "zero_adam_state_read",
            "zero_status_str", "zero_last_error")
 
 
@@ -246,6 +318,8 @@ _DTYPES = {
     "fp64": (torch.float64,),
     "bf16": (torch.int16, torch.uint16, torch.bfloat16),   # bf16 bit patterns
     "int64": (torch.int64,),
+    "int32": (torch.int32,),
+    "bytes8": (torch.uint8, torch.bool),
     "codes": (torch.uint8, torch.float8_e4m3fn),           # one byte each
 }
 
@@ -1136,6 +1210,361 @@ def fsdp_experts_backward(layout: Layout, unit: int, n_experts: int, w_shards, o
     _check(_lib.zero_fsdp_experts_backward(layout.handle, unit, n_experts, wp, op, rows, xp, dyp, wf,
                                            dxp, dx_dtype, dwp, call.stream(stream)),
            "zero_fsdp_experts_backward")
+
+
+# ---------------------------------------------------- training operators --
+
+def layer_norm_forward(rows: int, cols: int, x, ldx: int, gain, bias, eps: float, y, ldy: int,
+                       mean=None, rstd=None, x_dtype: int = BF16, param_dtype: int = BF16,
+                       y_dtype: int = BF16, stream=None) -> None:
+    """y = (x - mean) rstd gain + bias, row by row; mean and rstd (fp32) are kept for the
+    backward pass if given.  Types are taken from tensors; the *_dtype arguments
+    are those of raw addresses."""
+    call = _Call()
+    xt, yt = _dtype_of(x, x_dtype), _dtype_of(y, y_dtype)
+    pt = _dtype_of(bias if gain is None or gain.__class__ is int else gain, param_dtype)
+    n = max(cols, 0)
+    xp = call(x, "x", _extent(rows, ldx, cols), _kind(xt))
+    gp = call(gain, "gain", n, _kind(pt))
+    bp = call(bias, "bias", n, _kind(pt))
+    yp = call(y, "y", _extent(rows, ldy, cols), _kind(yt))
+    mp = call(mean, "mean", max(rows, 0), "fp32")
+    rp = call(rstd, "rstd", max(rows, 0), "fp32")
+    _check(_lib.zero_layer_norm_forward(rows, cols, xp, ldx, xt, gp, bp, pt, eps, yp, ldy, yt, mp, rp,
+                                        call.stream(stream)), "zero_layer_norm_forward")
+
+
+def layer_norm_workspace(rows: int, cols: int) -> int:
+    """Floats of workspace that dgain and dbias need."""
+    return _lib.zero_layer_norm_workspace(rows, cols)
+
+
+def layer_norm_backward(rows: int, cols: int, dy, lddy: int, x, ldx: int, gain, mean, rstd, dx,
+                        lddx: int, dgain=None, dbias=None, workspace=None, residual=None,
+                        ldr: int = 0, dy_dtype: int = BF16, x_dtype: int = BF16,
+                        param_dtype: int = BF16, dx_dtype: int = BF16, stream=None) -> None:
+    """dx, with the gradient `residual` that reaches x past the norm added, and the sums
+    dgain and dbias."""
+    call = _Call()
+    yt, xt, pt, dt = (_dtype_of(t, d) for t, d in ((dy, dy_dtype), (x, x_dtype), (gain, param_dtype),
+                                                   (dx, dx_dtype)))
+    n, r = max(cols, 0), max(rows, 0)
+    yp = call(dy, "dy", _extent(rows, lddy, cols), _kind(yt))
+    xp = call(x, "x", _extent(rows, ldx, cols), _kind(xt))
+    gp = call(gain, "gain", n, _kind(pt))
+    mp = call(mean, "mean", r, "fp32")
+    rp = call(rstd, "rstd", r, "fp32")
+    sp = call(residual, "residual", _extent(rows, ldr, cols), _kind(dt))
+    dp = call(dx, "dx", _extent(rows, lddx, cols), _kind(dt))
+    dgp = call(dgain, "dgain", n, "fp32")
+    dbp = call(dbias, "dbias", n, "fp32")
+    need = layer_norm_workspace(rows, cols) if dgain is not None or dbias is not None else 0
+    wp = call(workspace, "workspace", need, "fp32")
+    _check(_lib.zero_layer_norm_backward(rows, cols, yp, lddy, yt, xp, ldx, xt, gp, pt, mp, rp, sp, ldr,
+                                         dp, lddx, dt, dgp, dbp, wp, _numel(workspace),
+                                         call.stream(stream)), "zero_layer_norm_backward")
+
+
+class Router:
+    """How tokens choose experts: `top_k` of `n_experts` by softmax or sigmoid scores,
+    from the `top_groups` best of `groups` equal runs of experts, a group ranked by
+    its `group_best` (1 or 2) best experts; weights renormalised and scaled."""
+    __slots__ = ("s", "ref")
+
+    def __init__(self, n_experts: int, top_k: int, score="softmax", groups: int = 1,
+                 top_groups: int = 1, group_best: int = 1, renormalize: bool = True,
+                 scale: float = 1.0):
+        if isinstance(score, str):
+            if score not in SCORE:
+                raise ValueError(f"unknown score {score!r} (one of {', '.join(SCORE)})")
+            score = SCORE[score]
+        self.s = _Router(n_experts, top_k, groups, top_groups, group_best, score,
+                         int(bool(renormalize)), scale)
+        self.ref = ctypes.byref(self.s)
+
+
+def route_workspace(router: Router, tokens: int) -> int:
+    """int32 of workspace that routing `tokens` tokens needs."""
+    return _lib.zero_route_workspace(router.ref, tokens)
+
+
+def route_forward(router: Router, tokens: int, logits, ldl: int, experts, weights, offsets, rows_of,
+                  workspace=None, bias=None, active=None, logits_dtype: int = BF16,
+                  stream=None) -> None:
+    """Each token's experts and weights (tokens x top_k), the experts' offsets for the
+    grouped products and each choice's row when sorted by expert."""
+    call = _Call()
+    lt, E = _dtype_of(logits, logits_dtype), router.s.n_experts
+    n, e = max(tokens, 0) * max(router.s.top_k, 0), max(E, 0)
+    lp = call(logits, "logits", _extent(tokens, ldl, E), _kind(lt))
+    ep = call(experts, "experts", n, "int32")
+    wp = call(weights, "weights", n, "fp32")
+    op = call(offsets, "offsets", e + 1, "int64")
+    rp = call(rows_of, "rows_of", n, "int32")
+    sp = call(workspace, "workspace", route_workspace(router, tokens), "int32")
+    bp = call(bias, "bias", e, "fp32")
+    ap = call(active, "active", max(tokens, 0), "bytes8")
+    _check(_lib.zero_route_forward(router.ref, tokens, lp, ldl, lt, bp, ap, ep, wp, op, rp, sp,
+                                   _numel(workspace), call.stream(stream)), "zero_route_forward")
+
+
+def route_backward(router: Router, tokens: int, logits, ldl: int, experts, dweights, dlogits,
+                   ldd: int, logits_dtype: int = BF16, dlogits_dtype: int = BF16,
+                   stream=None) -> None:
+    """dlogits from dweights, the choice held fixed."""
+    call = _Call()
+    lt, dt, E = _dtype_of(logits, logits_dtype), _dtype_of(dlogits, dlogits_dtype), router.s.n_experts
+    n = max(tokens, 0) * max(router.s.top_k, 0)
+    lp = call(logits, "logits", _extent(tokens, ldl, E), _kind(lt))
+    ep = call(experts, "experts", n, "int32")
+    wp = call(dweights, "dweights", n, "fp32")
+    dp = call(dlogits, "dlogits", _extent(tokens, ldd, E), _kind(dt))
+    _check(_lib.zero_route_backward(router.ref, tokens, lp, ldl, lt, ep, wp, dp, ldd, dt,
+                                    call.stream(stream)), "zero_route_backward")
+
+
+def experts_dispatch(tokens: int, top_k: int, cols: int, x, ldx: int, rows_of, rows: int, out, ldo: int,
+                     weights=None, stream=None) -> None:
+    """out[rows_of[t, j]] = (weights[t, j]) x[t], bf16."""
+    call = _Call()
+    n = max(tokens, 0) * max(top_k, 0)
+    xp = call(x, "x", _extent(tokens, ldx, cols), "bf16")
+    rp = call(rows_of, "rows_of", n, "int32")
+    wp = call(weights, "weights", n, "fp32")
+    op = call(out, "out", _extent(rows, ldo, cols), "bf16")
+    _check(_lib.zero_experts_dispatch(tokens, top_k, cols, xp, ldx, rp, wp, rows, op, ldo,
+                                      call.stream(stream)), "zero_experts_dispatch")
+
+
+def experts_combine(tokens: int, top_k: int, cols: int, src, lds: int, rows: int, rows_of, y, ldy: int,
+                    weights=None, residual=None, ldr: int = 0, y_dtype: int = BF16,
+                    stream=None) -> None:
+    """y[t] = sum over j of (weights[t, j]) src[rows_of[t, j]] (+ residual[t])."""
+    call = _Call()
+    yt, n = _dtype_of(y, y_dtype), max(tokens, 0) * max(top_k, 0)
+    sp = call(src, "src", _extent(rows, lds, cols), "bf16")
+    rp = call(rows_of, "rows_of", n, "int32")
+    wp = call(weights, "weights", n, "fp32")
+    ep = call(residual, "residual", _extent(tokens, ldr, cols), "bf16")
+    yp = call(y, "y", _extent(tokens, ldy, cols), _kind(yt))
+    _check(_lib.zero_experts_combine(tokens, top_k, cols, sp, lds, rows, rp, wp, ep, ldr, yp, ldy, yt,
+                                     call.stream(stream)), "zero_experts_combine")
+
+
+def experts_combine_backward(tokens: int, top_k: int, cols: int, dy, lddy: int, rows: int, rows_of,
+                             weights, src, lds: int, dsrc, ldds: int, dweights, stream=None) -> None:
+    """dsrc[rows_of[t, j]] = weights[t, j] dy[t] and dweights[t, j] = dy[t] . src[rows_of[t, j]]."""
+    call = _Call()
+    n = max(tokens, 0) * max(top_k, 0)
+    yp = call(dy, "dy", _extent(tokens, lddy, cols), "bf16")
+    rp = call(rows_of, "rows_of", n, "int32")
+    wp = call(weights, "weights", n, "fp32")
+    sp = call(src, "src", _extent(rows, lds, cols), "bf16")
+    dp = call(dsrc, "dsrc", _extent(rows, ldds, cols), "bf16")
+    dwp = call(dweights, "dweights", n, "fp32")
+    _check(_lib.zero_experts_combine_backward(tokens, top_k, cols, yp, lddy, rows, rp, wp, sp, lds, dp,
+                                              ldds, dwp, call.stream(stream)),
+           "zero_experts_combine_backward")
+
+
+def linear_xent_workspace(rows: int, vocab: int, hidden: int, backward: bool = False,
+                          piece: int = 0) -> int:
+    """Floats of workspace of the loss, or of its gradient."""
+    return _lib.zero_linear_xent_workspace(rows, vocab, hidden, int(bool(backward)), piece)
+
+
+def _head_extent(vocab: int, hidden: int, ld: int, order: int) -> Optional[int]:
+    return _extent(hidden, ld, vocab) if order == K_OUTER else _extent(vocab, ld, hidden)
+
+
+def linear_xent_forward(rows: int, vocab: int, hidden: int, x, ldx: int, w, ldw: int, w_order: int,
+                        targets, loss, lse, workspace, stream=None) -> None:
+    """loss and lse of softmax(x W) against targets (int64; one outside [0, vocab) is none)."""
+    call = _Call()
+    r = max(rows, 0)
+    xp = call(x, "x", _extent(rows, ldx, hidden), "bf16")
+    wp = call(w, "w", _head_extent(vocab, hidden, ldw, w_order), "bf16")
+    tp = call(targets, "targets", r, "int64")
+    lp = call(loss, "loss", r, "fp32")
+    ep = call(lse, "lse", r, "fp32")
+    sp = call(workspace, "workspace", linear_xent_workspace(rows, vocab, hidden), "fp32")
+    _check(_lib.zero_linear_xent_forward(rows, vocab, hidden, xp, ldx, wp, ldw, w_order, tp, lp, ep, sp,
+                                         _numel(workspace), call.stream(stream)),
+           "zero_linear_xent_forward")
+
+
+def linear_xent_backward(rows: int, vocab: int, hidden: int, x, ldx: int, w, ldw: int, w_order: int,
+                         targets, lse, dloss, dx, lddx: int, dw, lddw: int, piece: int, workspace,
+                         dx_dtype: int = BF16, dw_dtype: int = FP32, stream=None) -> None:
+    """dx and dw from the rows' dloss; piece 0: the default pieces of the vocabulary."""
+    call = _Call()
+    dxt, dwt, r = _dtype_of(dx, dx_dtype), _dtype_of(dw, dw_dtype), max(rows, 0)
+    xp = call(x, "x", _extent(rows, ldx, hidden), "bf16")
+    wp = call(w, "w", _head_extent(vocab, hidden, ldw, w_order), "bf16")
+    tp = call(targets, "targets", r, "int64")
+    ep = call(lse, "lse", r, "fp32")
+    lp = call(dloss, "dloss", r, "fp32")
+    dxp = call(dx, "dx", _extent(rows, lddx, hidden), _kind(dxt))
+    dwp = call(dw, "dw", _head_extent(vocab, hidden, lddw, w_order), _kind(dwt))
+    sp = call(workspace, "workspace", linear_xent_workspace(rows, vocab, hidden, True, piece), "fp32")
+    _check(_lib.zero_linear_xent_backward(rows, vocab, hidden, xp, ldx, wp, ldw, w_order, tp, ep, lp, dxp,
+                                          lddx, dxt, dwp, lddw, dwt, piece, sp, _numel(workspace),
+                                          call.stream(stream)), "zero_linear_xent_backward")
+
+
+def _head(call: _Call, layout: Layout, unit: int, w_shards, w_full, w_order: int, batch: int, x, targets):
+    """(vocab, hidden, the padded unit's elements; None where the unit does not exist), and the
+    arguments every head call begins with, checked."""
+    d, wp, wf = _layer_buffers(call, layout, unit, w_shards, w_full)
+    hidden, vocab, padded = (None, None, None) if d is None else (d[0], d[1], d[3])
+    if d is not None and w_order == K_INNER:
+        hidden, vocab = vocab, hidden
+    xp = call(x, "x", _times(batch, hidden), "bf16")
+    tp = call(targets, "targets", max(batch, 0), "int64")
+    return vocab, hidden, padded, wp, wf, xp, tp
+
+
+def fsdp_head_forward(layout: Layout, unit: int, w_shards, w_order: int, batch: int, x, w_full, targets,
+                      loss, lse, workspace, stream=None) -> None:
+    """The loss of a head whose W is a row-sharded unit."""
+    call = _Call()
+    vocab, hidden, _, wp, wf, xp, tp = _head(call, layout, unit, w_shards, w_full, w_order, batch, x,
+                                             targets)
+    r = max(batch, 0)
+    lp = call(loss, "loss", r, "fp32")
+    ep = call(lse, "lse", r, "fp32")
+    sp = call(workspace, "workspace",
+              None if vocab is None else linear_xent_workspace(batch, vocab, hidden), "fp32")
+    _check(_lib.zero_fsdp_head_forward(layout.handle, unit, wp, w_order, batch, xp, wf, tp, lp, ep, sp,
+                                       _numel(workspace), call.stream(stream)),
+           "zero_fsdp_head_forward")
+
+
+def fsdp_head_backward(layout: Layout, unit: int, w_shards, w_order: int, batch: int, x, w_full, targets,
+                       lse, dloss, dx, dw_full, piece: int, workspace, dx_dtype: int = BF16,
+                       stream=None) -> None:
+    """dx, and dW as the padded unit in fp32."""
+    call = _Call()
+    vocab, hidden, padded, wp, wf, xp, tp = _head(call, layout, unit, w_shards, w_full, w_order, batch,
+                                                  x, targets)
+    dxt, r = _dtype_of(dx, dx_dtype), max(batch, 0)
+    ep = call(lse, "lse", r, "fp32")
+    lp = call(dloss, "dloss", r, "fp32")
+    dxp = call(dx, "dx", _times(batch, hidden), _kind(dxt))
+    dwp = call(dw_full, "dw_full", padded, "fp32")
+    sp = call(workspace, "workspace",
+              None if vocab is None else linear_xent_workspace(batch, vocab, hidden, True, piece), "fp32")
+    _check(_lib.zero_fsdp_head_backward(layout.handle, unit, wp, w_order, batch, xp, wf, tp, ep, lp, dxp,
+                                        dxt, dwp, piece, sp, _numel(workspace), call.stream(stream)),
+           "zero_fsdp_head_backward")
+
+
+class TensorList:
+    """The tensors of one optimizer step, described once: a list each of masters (fp32),
+    gradients (all bf16 or all fp32; None until set_grads), parameters (bf16, or None), m
+    and v (fp32, or 8-bit codes with m_scales and v_scales), and whether weight decay
+    applies (default: to all).  Tensors are contiguous, of any shape; no two may share
+    memory.  Keeps its buffers alive."""
+    __slots__ = ("s", "n", "state", "grad_dtype", "device", "sizes", "_keep")
+
+    def __init__(self, masters, grads, params, m, v, m_scales=None, v_scales=None, decay=None):
+        self.n = len(masters)
+        self.state = STATE_FP32 if m_scales is None else STATE_E4M3
+        none = [None] * self.n
+        lists = {"master": masters, "param": none if params is None else params, "m": m, "v": v,
+                 "m_scales": none if m_scales is None else m_scales,
+                 "v_scales": none if v_scales is None else v_scales}
+        for name, x in lists.items():
+            _need_len(name, x, self.n)
+        decay = [True] * self.n if decay is None else decay
+        _need_len("decay", decay, self.n)
+        self.s = (_Tensor * max(1, self.n))()
+        call, seen = _Call(), set()
+        kinds = {"master": "fp32", "param": "bf16", "m": "fp32", "v": "fp32"}
+        if self.state == STATE_E4M3:
+            kinds.update({"m": "codes", "v": "codes", "m_scales": "codes", "v_scales": "codes"})
+        self.sizes = [x.numel() for x in masters]
+        for i, size in enumerate(self.sizes):
+            d = self.s[i]
+            d.n, d.decay = size, int(bool(decay[i]))
+            for name, kind in kinds.items():
+                x = lists[name][i]
+                if x is None and name != "param":
+                    raise ValueError(f"tensor {i}: {name} is required")
+                count = -(-size // 32) if name.endswith("scales") else size
+                p = call(x, f"{name} of tensor {i}", count, kind)
+                if p and size:
+                    if p in seen:
+                        raise ValueError(f"{name} of tensor {i} is given twice")
+                    seen.add(p)
+                setattr(d, name, p)
+        self.device, self.grad_dtype, self._keep = call.device, BF16, [lists]
+        if grads is not None:
+            self.set_grads(grads)
+
+    def set_grads(self, grads) -> None:
+        """Other gradient tensors for the next steps."""
+        _need_len("grads", grads, self.n)
+        call = _Call()
+        call.device = self.device
+        kind = None
+        for i, x in enumerate(grads):
+            if kind is None:
+                kind = _dtype_of(x, BF16)
+            self.s[i].grad = call(x, f"gradient of tensor {i}", self.sizes[i], _kind(kind))
+        self.grad_dtype = BF16 if kind is None else kind
+        self._keep[1:] = [grads]
+
+    def partials_count(self) -> int:
+        """fp64 partial sums that tensors_sumsq writes."""
+        return _lib.zero_tensors_partials_count(self.n, self.s)
+
+    def _call(self) -> _Call:
+        call = _Call()
+        call.device = self.device
+        return call
+
+
+def adam_tensors(tensors: TensorList, cfg: AdamCfg, seed: int = 0, clip_coef=None, stream=None) -> None:
+    """One Adam / AdamW step of every tensor of the list."""
+    call = tensors._call()
+    cp = call(clip_coef, "clip_coef", 1, "fp32")
+    _check(_lib.zero_adam_tensors(tensors.n, tensors.s, tensors.state, tensors.grad_dtype,
+                                  ctypes.byref(cfg), seed & (2 ** 64 - 1), cp, call.stream(stream)),
+           "zero_adam_tensors")
+
+
+def adam_tensors_table(tensors: TensorList, table, n_entries: int, step_counter, seed: int = 0,
+                       clip_coef=None, stream=None) -> None:
+    """adam_tensors with the scalars of table[*step_counter - 1] (device table and counter)."""
+    call = tensors._call()
+    _need(table, "table", n_entries * ctypes.sizeof(AdamTableEntry), "bytes")
+    sp = call(step_counter, "step_counter", 1, "int64")
+    cp = call(clip_coef, "clip_coef", 1, "fp32")
+    _check(_lib.zero_adam_tensors_table(tensors.n, tensors.s, tensors.state, tensors.grad_dtype,
+                                        _addr(table), n_entries, sp, seed & (2 ** 64 - 1), cp,
+                                        call.stream(stream)), "zero_adam_tensors_table")
+
+
+def tensors_sumsq(tensors: TensorList, partials, stream=None) -> None:
+    """The gradients' sums of squares, for clip_coef: partials_count() fp64."""
+    call = tensors._call()
+    n = tensors.partials_count()
+    pp = call(partials, "partials", n, "fp64")
+    _check(_lib.zero_tensors_sumsq(tensors.n, tensors.s, tensors.grad_dtype, pp, _numel(partials),
+                                   call.stream(stream)), "zero_tensors_sumsq")
+
+
+def adam_state_read(n: int, codes, scales, out, second: bool = False, out_dtype: int = BF16,
+                    stream=None) -> None:
+    """What n 8-bit state codes stand for: m, or with `second` v."""
+    call = _Call()
+    ot, k = _dtype_of(out, out_dtype), max(n, 0)
+    cp = call(codes, "codes", k, "codes")
+    sp = call(scales, "scales", -(-k // 32), "codes")
+    op = call(out, "out", k, _kind(ot))
+    _check(_lib.zero_adam_state_read(n, cp, sp, int(bool(second)), op, ot, call.stream(stream)),
+           "zero_adam_state_read")
 
 
 def stream_mix(kind: int, grads, master, m, v, param, n: int, stream=None,

@@ -23,6 +23,8 @@ LIB = os.path.join(PKG, "libzeroshard.so")
 SOURCES = [os.path.join(CSRC, "layout.cpp"), os.path.join(CSRC, "kernels.hip"),
            os.path.join(CSRC, "sweep.cpp"), os.path.join(CSRC, "gemm.hip"),
            os.path.join(CSRC, "layer.hip"), os.path.join(CSRC, "saved.hip"),
+           os.path.join(CSRC, "norm.hip"), os.path.join(CSRC, "route.hip"),
+           os.path.join(CSRC, "xent.hip"), os.path.join(CSRC, "tensors.hip"),
            os.path.join(CSRC, "linear.cpp")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

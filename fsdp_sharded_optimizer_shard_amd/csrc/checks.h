@@ -10,16 +10,16 @@
 namespace zs {
 namespace {
 
-bool aligned(const void *p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-bool vec16(const void *p, int64_t ld, int es) { return aligned(p, 16) && ld * es % 16 == 0; }
+inline bool aligned(const void *p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+inline bool vec16(const void *p, int64_t ld, int es) { return aligned(p, 16) && ld * es % 16 == 0; }
 
-bool known_dtype(int32_t d) { return d == ZERO_BF16 || d == ZERO_FP32; }
-int bytes_of(int32_t d) { return d == ZERO_BF16 ? 2 : 4; }
+inline bool known_dtype(int32_t d) { return d == ZERO_BF16 || d == ZERO_FP32; }
+inline int bytes_of(int32_t d) { return d == ZERO_BF16 ? 2 : 4; }
 
 // Whether p is one of `others`; NULL is nothing.  What a call writes must not
 // be an address that it uses for something else: only equal addresses are
 // looked for, since matrices with leading dimensions may share a range.
-bool is_one_of(const void *p, std::initializer_list<const void *> others)
+inline bool is_one_of(const void *p, std::initializer_list<const void *> others)
 {
     for (const void *o : others)
         if (p && p == o)
@@ -28,13 +28,13 @@ bool is_one_of(const void *p, std::initializer_list<const void *> others)
 }
 
 // The exponent bytes of a kept matrix that has them.
-const void *scales_of(const zero_saved *s)
+inline const void *scales_of(const zero_saved *s)
 {
     return s && s->format == ZERO_SAVED_E4M3 ? s->scales : nullptr;
 }
-const void *data_of(const zero_saved *s) { return s ? s->data : nullptr; }
+inline const void *data_of(const zero_saved *s) { return s ? s->data : nullptr; }
 
-zero_status launched(const char *what)
+inline zero_status launched(const char *what)
 {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess)
@@ -43,7 +43,7 @@ zero_status launched(const char *what)
 }
 
 // A matrix argument: pointer, leading dimension and alignment.
-zero_status check_matrix(const char *what, const void *p, int64_t ld, int64_t cols, int32_t dtype)
+inline zero_status check_matrix(const char *what, const void *p, int64_t ld, int64_t cols, int32_t dtype)
 {
     if (!known_dtype(dtype))
         return fail(ZERO_ERR_INVALID_ARG, "%s: unknown dtype %d", what, dtype);
@@ -61,7 +61,7 @@ zero_status check_matrix(const char *what, const void *p, int64_t ld, int64_t co
 // products of two of them, and byte offsets, then fit 63 bits.
 constexpr int64_t kMaxDim = int64_t(1) << 40, kMaxElems = int64_t(1) << 60;
 
-zero_status check_extent(int64_t rows, int64_t cols, int64_t ld)
+inline zero_status check_extent(int64_t rows, int64_t cols, int64_t ld)
 {
     if (rows < 0 || cols < 0)
         return fail(ZERO_ERR_INVALID_ARG, "negative size");

@@ -334,4 +334,79 @@ zero_status zero_fsdp_experts_backward(const zero_layout *L, int32_t unit, int32
     return zs::zero_rows_fill(dw_full, d.out, total, d.in_pad, d.out, s);
 }
 
+// The head: a unit of hidden x vocab (K_OUTER) or vocab x hidden (K_INNER).
+static zero_status head_dims(const zero_layout *L, int32_t unit, int32_t w_order, Dims *d, int64_t *vocab,
+                             int64_t *hidden)
+{
+    const zero_status st = layer_dims(L, unit, d);
+    if (st != ZERO_OK)
+        return st;
+    if (w_order != ZERO_K_INNER && w_order != ZERO_K_OUTER)
+        return zs::fail(ZERO_ERR_INVALID_ARG, "unknown operand order %d", w_order);
+    *vocab = w_order == ZERO_K_OUTER ? d->out : d->in;
+    *hidden = w_order == ZERO_K_OUTER ? d->in : d->out;
+    return ZERO_OK;
+}
+
+zero_status zero_fsdp_head_forward(const zero_layout *L, int32_t unit, const uint16_t *const *w_shards,
+                                   int32_t w_order, int64_t batch, const uint16_t *x, uint16_t *w_full,
+                                   const int64_t *targets, float *loss, float *lse, float *workspace,
+                                   int64_t n_workspace, void *stream)
+{
+    Dims d;
+    int64_t vocab, hidden;
+    zero_status st = head_dims(L, unit, w_order, &d, &vocab, &hidden);
+    if (st != ZERO_OK)
+        return st;
+    if (!w_shards || !w_full || batch < 0)
+        return zs::fail(ZERO_ERR_INVALID_ARG, "w_shards, w_full and batch >= 0 are required");
+    if ((st = check_shards(L, w_shards)) != ZERO_OK ||
+        (st = zs::xent_forward_check(batch, vocab, hidden, x, hidden, w_full, d.out, w_order, targets, loss, lse,
+                                     workspace, n_workspace)) != ZERO_OK)
+        return st;
+    if (batch > 0) {
+        if (is_one_of(w_full, {x, targets}))
+            return zs::fail(ZERO_ERR_INVALID_ARG, "w_full must not lie where the call reads something else");
+        if ((st = check_results(L, w_shards, {loss, lse, workspace})) != ZERO_OK)
+            return st;
+    }
+    if ((st = zero_gather_params(L, unit, unit + 1, w_shards, L->parts, w_full, stream)) != ZERO_OK)
+        return st;
+    return zs::xent_forward_run(batch, vocab, hidden, x, hidden, w_full, d.out, w_order, targets, loss, lse, workspace,
+                                static_cast<hipStream_t>(stream));
+}
+
+zero_status zero_fsdp_head_backward(const zero_layout *L, int32_t unit, const uint16_t *const *w_shards,
+                                    int32_t w_order, int64_t batch, const uint16_t *x, uint16_t *w_full,
+                                    const int64_t *targets, const float *lse, const float *dloss, void *dx,
+                                    int32_t dx_dtype, float *dw_full, int64_t piece, float *workspace,
+                                    int64_t n_workspace, void *stream)
+{
+    Dims d;
+    int64_t vocab, hidden;
+    zero_status st = head_dims(L, unit, w_order, &d, &vocab, &hidden);
+    if (st != ZERO_OK)
+        return st;
+    if (!w_shards || !w_full || !dw_full || batch < 0)
+        return zs::fail(ZERO_ERR_INVALID_ARG, "w_shards, w_full, dw_full and batch >= 0 are required");
+    if ((st = check_shards(L, w_shards)) != ZERO_OK ||
+        (st = zs::xent_backward_check(batch, vocab, hidden, x, hidden, w_full, d.out, w_order, targets, lse, dloss, dx,
+                                      hidden, dx_dtype, dw_full, d.out, ZERO_FP32, piece, workspace,
+                                      n_workspace)) != ZERO_OK)
+        return st;
+    // W is read in every piece, dw_full written in every one.
+    if (is_one_of(dw_full, {w_full}) || (batch > 0 && is_one_of(w_full, {x, targets, lse, dloss})))
+        return zs::fail(ZERO_ERR_INVALID_ARG, "w_full must not lie where the call reads something else, nor dw_full "
+                        "over w_full");
+    if ((st = check_results(L, w_shards, {batch > 0 ? dx : nullptr, dw_full, batch > 0 ? workspace : nullptr})) !=
+        ZERO_OK)
+        return st;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    if ((st = zero_gather_params(L, unit, unit + 1, w_shards, L->parts, w_full, stream)) != ZERO_OK ||
+        (st = zs::xent_backward_run(batch, vocab, hidden, x, hidden, w_full, d.out, w_order, targets, lse, dloss, dx,
+                                    hidden, dx_dtype, dw_full, d.out, ZERO_FP32, piece, workspace, s)) != ZERO_OK)
+        return st;
+    return zs::zero_rows_fill(dw_full, d.out, d.in, d.in_pad, d.out, s);
+}
+
 }  // extern "C"

@@ -66,4 +66,21 @@ zero_status grouped_depth_run(int32_t n_groups, const int64_t *offsets, int64_t 
                               const uint16_t *A, int64_t lda, const uint16_t *B, int64_t ldb, void *C,
                               int64_t ldc, int64_t stride_c, int32_t c_dtype, hipStream_t s);
 
+// The cross entropy of a linear head (zero_linear_xent_*).
+zero_status xent_forward_check(int64_t rows, int64_t vocab, int64_t hidden, const uint16_t *x, int64_t ldx,
+                               const uint16_t *w, int64_t ldw, int32_t w_order, const int64_t *targets,
+                               const float *loss, const float *lse, const float *workspace, int64_t n_workspace);
+zero_status xent_forward_run(int64_t rows, int64_t vocab, int64_t hidden, const uint16_t *x, int64_t ldx,
+                             const uint16_t *w, int64_t ldw, int32_t w_order, const int64_t *targets, float *loss,
+                             float *lse, float *workspace, hipStream_t s);
+zero_status xent_backward_check(int64_t rows, int64_t vocab, int64_t hidden, const uint16_t *x, int64_t ldx,
+                                const uint16_t *w, int64_t ldw, int32_t w_order, const int64_t *targets,
+                                const float *lse, const float *dloss, const void *dx, int64_t lddx, int32_t dx_dtype,
+                                const void *dw, int64_t lddw, int32_t dw_dtype, int64_t piece, const float *workspace,
+                                int64_t n_workspace);
+zero_status xent_backward_run(int64_t rows, int64_t vocab, int64_t hidden, const uint16_t *x, int64_t ldx,
+                              const uint16_t *w, int64_t ldw, int32_t w_order, const int64_t *targets,
+                              const float *lse, const float *dloss, void *dx, int64_t lddx, int32_t dx_dtype, void *dw,
+                              int64_t lddw, int32_t dw_dtype, int64_t piece, float *workspace, hipStream_t s);
+
 }  // namespace zs

@@ -1,0 +1,498 @@
+// Adam / AdamW over many tensors at once, with fp32 states or states in 8 bits,
+// and what belongs to it: the sum of squares of the tensors' gradients (for a
+// global-norm clip) and the values of 8-bit states.
+//
+// A launch takes up to kTensors tensors from its arguments and walks their
+// concatenated tiles of 2048 elements, a lane eight neighbouring ones, so that
+// many small tensors cost one launch between them.  An element costs 2 or 4
+// bytes of gradient, 8 of master, 2 of parameter and 16 (fp32) or 4 1/8 bytes of
+// state, and no product: memory bounds it.
+//
+// 8-bit states.  m and the root of v are kept as e4m3 codes, 32 neighbouring
+// elements of a tensor under one power of two: the least 2^e, e in [-117, 120],
+// with the block's largest finite magnitude at most 448 * 2^e.  The root halves
+// v's range of exponents, so that a block whose gradients span five decades
+// still has a code for each.  The codes' step is 1/16 to 1/8 of a value and an
+// exponential average moves v by (1 - beta2) of itself a step, so rounding to
+// nearest would leave v where it is for good; a new state is therefore rounded
+// up or down at random, up with the probability of the part that rounding down
+// would lose, which keeps the average right.  A v that is not 0 keeps a code
+// that is not 0: it would else be missing under a later m.  The step itself uses
+// m and v before they are rounded.
+//
+// The random bits are a hash of the element's number in the list, the seed and
+// the step number, so a step has the same bits whatever the launch, and needs no
+// state of its own.
+#include <hip/hip_runtime.h>
+
+#include <cstring>
+
+#include "act.h"
+#include "adam.h"
+#include "checks.h"
+#include "vec.h"
+
+#pragma clang fp contract(off)
+
+namespace zs {
+namespace {
+
+constexpr int kTensors = 36;     // tensors of one launch: its arguments stay below 4 KB
+constexpr int kTensorTile = 2048;
+constexpr int kSumTile = 8192;   // elements of one sum of squares
+
+struct Tensor {
+    float *master;
+    const void *grad;
+    uint16_t *param;
+    void *m, *v;
+    uint8_t *ms, *vs;
+    int64_t n, number, tile0;  // elements, the first one's number in the list, first tile
+    int32_t decay, vec;        // vec: 16-byte aligned values and 8-byte aligned codes
+};
+
+struct TensorArgs {
+    AdamScalars sc;
+    const AdamScalars *table;  // non-null: scalars of table[*counter - 1]
+    const int64_t *counter;
+    int64_t n_table, step, first_sum;
+    uint64_t seed;
+    const float *clip;
+    double *sums;
+    int32_t n_tensors, g_bf16;
+    Tensor t[kTensors];
+};
+static_assert(sizeof(TensorArgs) <= 4096, "kernel arguments");
+
+__device__ __forceinline__ const Tensor &tensor_of(const TensorArgs &a, int64_t tile)
+{
+    int lo = 0, hi = a.n_tensors - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (a.t[mid].tile0 <= tile)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return a.t[lo];
+}
+
+// The step's two keys: three rounds of xor-shift and multiplication over the
+// seed and the step number.
+__device__ __forceinline__ uint2 step_keys(uint64_t seed, int64_t step)
+{
+    uint64_t z = seed + (uint64_t)step * 0x9E3779B97F4A7C15ull;
+    z = (z ^ (z >> 31)) * 0xD6E8FEB86659FD93ull;
+    z = (z ^ (z >> 29)) * 0xA0761D6478BD642Full;
+    z ^= z >> 32;
+    return make_uint2((uint32_t)z, (uint32_t)(z >> 32));
+}
+
+// 32 random bits of element number i.
+__device__ __forceinline__ uint32_t random_bits(uint2 key, int64_t i)
+{
+    uint32_t h = (uint32_t)i * 0x9E3779B1u + (uint32_t)((uint64_t)i >> 32) * 0x85EBCA77u + key.x;
+    h ^= h >> 16;
+    h = h * 0x7FEB352Du + key.y;
+    h ^= h >> 15;
+    h *= 0x6C8E9CF5u;
+    return h ^ (h >> 16);
+}
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t quad_max(uint32_t x)
+{
+    const uint32_t y = (uint32_t)__builtin_amdgcn_mov_dpp((int)x, CTRL, 0xf, 0xf, true);
+    return x > y ? x : y;
+}
+
+// The exponent byte of a block of 32: the largest of the four lanes' eight values.
+__device__ __forceinline__ uint32_t block_of(const float (&x)[8])
+{
+    uint32_t mx = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const uint32_t b = mag_bits(x[k]);
+        mx = b > mx ? b : mx;
+    }
+    mx = quad_max<0xB1>(mx);  // lanes 1 0 3 2
+    mx = quad_max<0x4E>(mx);  // lanes 2 3 0 1
+    return block_byte(mx);
+}
+
+// x / 2^e as a code, rounded up where the 16 random bits `r` and the part of a
+// step above the code below sum to a whole step.  Under 2^-6 the codes are 2^-9
+// apart, as they are from 2^-6 to 2^-5, so 2^-6 is added there.
+template <bool ROOT>
+__device__ __forceinline__ uint32_t code_random(float x, float inv, uint32_t r)
+{
+    const uint32_t u = __float_as_uint(x), mag = u & 0x7fffffffu;
+    const float lim = 0x1.ep127f, a = __builtin_fabsf(x), q = (a > lim ? lim : a) * inv;
+    const bool low = q < 0x1p-6f;
+    const uint32_t t = __float_as_uint(low ? q + 0x1p-6f : q) + (r << 4);
+    uint32_t c = (t >> 20) - (low ? 968u : 960u);
+    if (ROOT)
+        c = c == 0 && q > 0.0f ? 1u : c;
+    c = mag < kInf ? c : 0x7fu;
+    return ROOT ? c : c | ((u >> 24) & 0x80u);
+}
+
+template <bool ROOT>
+__device__ __forceinline__ void code8(const float (&x)[8], const uint32_t (&r)[8], uint32_t byte, uint32_t (&w)[2])
+{
+    const float inv = inv_scale(byte);
+    w[0] = w[1] = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        w[k >> 2] |= code_random<ROOT>(x[k], inv, ROOT ? r[k] >> 16 : r[k] & 0xffffu) << (8 * (k & 3));
+}
+
+template <bool SMALL>
+__global__ __launch_bounds__(256) void tensors_kernel(const TensorArgs a)
+{
+    AdamScalars sc = a.sc;
+    int64_t step = a.step;
+    if (a.table) {
+        // a counter outside the table leaves every buffer as it is
+        step = *a.counter;
+        if (step < 1 || step > a.n_table)
+            return;
+        sc = a.table[step - 1];
+    }
+    const float coef = a.clip ? *a.clip : 1.0f;
+    const Tensor &t = tensor_of(a, blockIdx.x);
+    sc.has_wd = sc.has_wd && t.decay;
+    const int64_t i = ((int64_t)blockIdx.x - t.tile0) * kTensorTile + threadIdx.x * 8;
+    const int64_t left = t.n - i;
+    const int n = left <= 0 ? 0 : left < 8 ? (int)left : 8;
+    const bool vec = t.vec && n == 8;
+    float g[8], p[8], m[8], v[8];
+    load8(t.grad, a.g_bf16, i, vec, n, g);
+    load8(t.master, false, i, vec, n, p);
+    if (SMALL) {
+        // the codes of a lane are of one block
+        uint32_t bm = 0, bv = 0;
+        uint2 cm = make_uint2(0, 0), cv = cm;
+        if (n > 0) {
+            cm = load_bytes8(static_cast<const uint8_t *>(t.m) + i, vec, n);
+            cv = load_bytes8(static_cast<const uint8_t *>(t.v) + i, vec, n);
+            bm = t.ms[i >> 5];
+            bv = t.vs[i >> 5];
+        }
+        bm *= 0x01010101u;
+        bv *= 0x01010101u;
+        decode8(cm, make_uint2(bm, bm), m);
+        decode8(cv, make_uint2(bv, bv), v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            v[k] = v[k] * v[k];
+    } else {
+        load8(t.m, false, i, vec, n, m);
+        load8(t.v, false, i, vec, n, v);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        adam1(sc, g[k] * coef, p[k], m[k], v[k]);
+    if (SMALL) {
+        const uint2 key = step_keys(a.seed, step);
+        uint32_t r[8], w[2];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            r[k] = random_bits(key, t.number + i + k);
+            v[k] = sqrtf(v[k]);
+            if (k >= n)
+                m[k] = v[k] = 0.0f;
+        }
+        const uint32_t bm = block_of(m), bv = block_of(v);
+        if (n == 0)
+            return;
+        code8<false>(m, r, bm, w);
+        store_bytes8(static_cast<uint8_t *>(t.m) + i, vec, n, make_uint2(w[0], w[1]));
+        code8<true>(v, r, bv, w);
+        store_bytes8(static_cast<uint8_t *>(t.v) + i, vec, n, make_uint2(w[0], w[1]));
+        if ((threadIdx.x & 3) == 0) {
+            t.ms[i >> 5] = (uint8_t)bm;
+            t.vs[i >> 5] = (uint8_t)bv;
+        }
+    } else if (n > 0) {
+        store8(t.m, false, i, vec, n, m);
+        store8(t.v, false, i, vec, n, v);
+    }
+    if (n == 0)
+        return;
+    store8(t.master, false, i, vec, n, p);
+    if (t.param)
+        store8(t.param, true, i, vec, n, p);
+}
+
+// The sum of squares of 8192 elements of a tensor's gradient, in fp64, where each
+// square is exact.
+__global__ __launch_bounds__(256) void tensors_sum_kernel(const TensorArgs a)
+{
+    __shared__ double part[4];
+    const Tensor &t = tensor_of(a, blockIdx.x);
+    const int64_t i0 = ((int64_t)blockIdx.x - t.tile0) * kSumTile + threadIdx.x * 8;
+    double s = 0.0;
+#pragma unroll
+    for (int j = 0; j < kSumTile / 2048; ++j) {
+        const int64_t i = i0 + 2048 * j, left = t.n - i;
+        if (left <= 0)
+            break;
+        const int n = left < 8 ? (int)left : 8;
+        float g[8];
+        load8(t.grad, a.g_bf16, i, t.vec && n == 8, n, g);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            s += (double)g[k] * (double)g[k];
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2)
+        s += __shfl_xor(s, d, 64);
+    if ((threadIdx.x & 63) == 0)
+        part[threadIdx.x >> 6] = s;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        a.sums[a.first_sum + blockIdx.x] = ((part[0] + part[1]) + part[2]) + part[3];
+}
+
+// What 8-bit states stand for; `second`: the square, which is v.  Exact in bf16
+// (a root has four bits, its square eight) down to fp32's smallest numbers.
+__global__ __launch_bounds__(256) void state_read_kernel(int64_t n_all, const uint8_t *codes, const uint8_t *scales,
+                                                         bool second, void *out, bool bf16, bool vec)
+{
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8, left = n_all - i;
+    if (left <= 0)
+        return;
+    const int n = left < 8 ? (int)left : 8;
+    const uint32_t b = scales[i >> 5] * 0x01010101u;
+    float x[8];
+    decode8(load_bytes8(codes + i, vec && n == 8, n), make_uint2(b, b), x);
+    if (second)
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            x[k] *= x[k];
+    store8(out, bf16, i, vec && n == 8, n, x);
+}
+
+int64_t tensor_tiles(int64_t n, int tile) { return (n + tile - 1) / tile; }
+
+zero_status check_tensors(int32_t n_tensors, const zero_tensor *ts, int32_t format, int32_t grad_dtype)
+{
+    if (n_tensors < 0 || (n_tensors > 0 && !ts))
+        return fail(ZERO_ERR_INVALID_ARG, "a list of %d tensors is required", n_tensors);
+    if (format != ZERO_STATE_FP32 && format != ZERO_STATE_E4M3)
+        return fail(ZERO_ERR_INVALID_ARG, "unknown state format %d", format);
+    if (!known_dtype(grad_dtype))
+        return fail(ZERO_ERR_INVALID_ARG, "unknown gradient dtype %d", grad_dtype);
+    const bool small = format == ZERO_STATE_E4M3;
+    for (int32_t k = 0; k < n_tensors; ++k) {
+        const zero_tensor &t = ts[k];
+        if (t.n < 0)
+            return fail(ZERO_ERR_INVALID_ARG, "tensor %d: negative length", k);
+        if (t.n > kMaxDim)
+            return fail(ZERO_ERR_UNSUPPORTED, "tensor %d: too long", k);
+        if (t.n == 0)
+            continue;
+        if (!t.master || !t.grad || !t.m || !t.v || (small && (!t.m_scales || !t.v_scales)))
+            return fail(ZERO_ERR_INVALID_ARG, "tensor %d: master, grad, m, v%s are required", k,
+                        small ? " and the scales" : "");
+        if (!aligned(t.master, 4) || !aligned(t.grad, bytes_of(grad_dtype)) || !aligned(t.param, 2) ||
+            (!small && (!aligned(t.m, 4) || !aligned(t.v, 4))))
+            return fail(ZERO_ERR_ALIGNMENT, "tensor %d: a buffer is misaligned", k);
+        const void *ms = small ? t.m_scales : nullptr, *vs = small ? t.v_scales : nullptr;
+        if (is_one_of(t.master, {t.grad, t.param, t.m, t.v, ms, vs}) || is_one_of(t.grad, {t.param, t.m, t.v, ms, vs}) ||
+            is_one_of(t.param, {t.m, t.v, ms, vs}) || is_one_of(t.m, {t.v, ms, vs}) || is_one_of(t.v, {ms, vs}) ||
+            is_one_of(ms, {vs}))
+            return fail(ZERO_ERR_INVALID_ARG, "tensor %d: its buffers need memory each", k);
+    }
+    return ZERO_OK;
+}
+
+// Launches `go(args, blocks)` for kTensors tensors at a time, the empty ones left
+// out.
+template <class F>
+zero_status each_launch(int32_t n_tensors, const zero_tensor *ts, bool small, int32_t grad_dtype, int tile,
+                        TensorArgs &a, const char *what, F go)
+{
+    constexpr int64_t kMost = int64_t(0xffffffffu) / 256;
+    int64_t number = 0, tiles = 0, before = 0;
+    a.g_bf16 = grad_dtype == ZERO_BF16;
+    a.n_tensors = 0;
+    (void)hipGetLastError();
+    for (int32_t k = 0; k <= n_tensors; ++k) {
+        const bool end = k == n_tensors;
+        if (a.n_tensors > 0 && (end || a.n_tensors == kTensors || tiles + tensor_tiles(ts[k].n, tile) > kMost)) {
+            a.first_sum = before;
+            go(a, (unsigned)tiles);
+            const zero_status st = launched(what);
+            if (st != ZERO_OK)
+                return st;
+            before += tiles;
+            tiles = 0;
+            a.n_tensors = 0;
+        }
+        if (end)
+            break;
+        const zero_tensor &t = ts[k];
+        if (t.n > 0) {
+            Tensor &d = a.t[a.n_tensors++];
+            d.master = t.master, d.grad = t.grad, d.param = t.param, d.m = t.m, d.v = t.v;
+            d.ms = t.m_scales, d.vs = t.v_scales, d.n = t.n, d.number = number, d.tile0 = tiles;
+            d.decay = t.decay;
+            const int sa = small ? 8 : 16;
+            d.vec = aligned(t.master, 16) && aligned(t.grad, 16) && aligned(t.param, 16) && aligned(t.m, sa) &&
+                    aligned(t.v, sa);
+            tiles += tensor_tiles(t.n, tile);
+        }
+        number += (t.n + 31) / 32 * 32;
+    }
+    return ZERO_OK;
+}
+
+// No tensor may need more blocks than one launch has.
+zero_status check_tiles(int32_t n_tensors, const zero_tensor *ts)
+{
+    for (int32_t k = 0; k < n_tensors; ++k)
+        if (tensor_tiles(ts[k].n, kTensorTile) > int64_t(0xffffffffu) / 256)
+            return fail(ZERO_ERR_UNSUPPORTED, "tensor %d: too long for one launch", k);
+    return ZERO_OK;
+}
+
+zero_status run_tensors(int32_t n_tensors, const zero_tensor *ts, int32_t format, int32_t grad_dtype, TensorArgs &a,
+                        hipStream_t s)
+{
+    const bool small = format == ZERO_STATE_E4M3;
+    return each_launch(n_tensors, ts, small, grad_dtype, kTensorTile, a, "adam_tensors",
+                       [&](const TensorArgs &args, unsigned blocks) {
+                           if (small)
+                               hipLaunchKernelGGL(tensors_kernel<true>, dim3(blocks), dim3(256), 0, s, args);
+                           else
+                               hipLaunchKernelGGL(tensors_kernel<false>, dim3(blocks), dim3(256), 0, s, args);
+                       });
+}
+
+}  // namespace
+}  // namespace zs
+
+extern "C" {
+
+zero_status zero_adam_tensors(int32_t n_tensors, const zero_tensor *tensors, int32_t state_format,
+                              int32_t grad_dtype, const zero_adam_cfg *cfg, uint64_t seed,
+                              const float *clip_coef, void *stream)
+{
+    using namespace zs;
+    zero_status st;
+    if (!cfg)
+        return fail(ZERO_ERR_INVALID_ARG, "cfg is NULL");
+    TensorArgs a;
+    std::memset(&a, 0, offsetof(TensorArgs, t));
+    zero_adam_table_entry e;
+    if ((st = zero_adam_table_fill(cfg, 1, &e)) != ZERO_OK ||
+        (st = check_tensors(n_tensors, tensors, state_format, grad_dtype)) != ZERO_OK ||
+        (st = check_tiles(n_tensors, tensors)) != ZERO_OK)
+        return st;
+    if (!aligned(clip_coef, 4))
+        return fail(ZERO_ERR_ALIGNMENT, "clip_coef is misaligned");
+    std::memcpy(&a.sc, &e, sizeof e);
+    a.step = cfg->step;
+    a.seed = seed;
+    a.clip = clip_coef;
+    return run_tensors(n_tensors, tensors, state_format, grad_dtype, a, static_cast<hipStream_t>(stream));
+}
+
+zero_status zero_adam_tensors_table(int32_t n_tensors, const zero_tensor *tensors, int32_t state_format,
+                                    int32_t grad_dtype, const zero_adam_table_entry *table, int64_t n_entries,
+                                    const int64_t *step_counter, uint64_t seed, const float *clip_coef,
+                                    void *stream)
+{
+    using namespace zs;
+    zero_status st;
+    if (!table || !step_counter || n_entries < 1)
+        return fail(ZERO_ERR_INVALID_ARG, "table, step_counter and n_entries >= 1 are required");
+    if (!aligned(table, 4) || !aligned(step_counter, 8) || !aligned(clip_coef, 4))
+        return fail(ZERO_ERR_ALIGNMENT, "misaligned step table, counter or clip_coef");
+    if ((st = check_tensors(n_tensors, tensors, state_format, grad_dtype)) != ZERO_OK ||
+        (st = check_tiles(n_tensors, tensors)) != ZERO_OK)
+        return st;
+    TensorArgs a;
+    std::memset(&a, 0, offsetof(TensorArgs, t));
+    a.table = reinterpret_cast<const AdamScalars *>(table);
+    a.counter = step_counter;
+    a.n_table = n_entries;
+    a.seed = seed;
+    a.clip = clip_coef;
+    return run_tensors(n_tensors, tensors, state_format, grad_dtype, a, static_cast<hipStream_t>(stream));
+}
+
+int64_t zero_tensors_partials_count(int32_t n_tensors, const zero_tensor *tensors)
+{
+    int64_t n = 0;
+    for (int32_t k = 0; tensors && k < n_tensors; ++k)
+        n += tensors[k].n > 0 ? zs::tensor_tiles(tensors[k].n, zs::kSumTile) : 0;
+    return n;
+}
+
+zero_status zero_tensors_sumsq(int32_t n_tensors, const zero_tensor *tensors, int32_t grad_dtype, double *partials,
+                               int64_t n_partials, void *stream)
+{
+    using namespace zs;
+    zero_status st;
+    if (n_tensors < 0 || (n_tensors > 0 && !tensors))
+        return fail(ZERO_ERR_INVALID_ARG, "a list of %d tensors is required", n_tensors);
+    if (!known_dtype(grad_dtype))
+        return fail(ZERO_ERR_INVALID_ARG, "unknown gradient dtype %d", grad_dtype);
+    for (int32_t k = 0; k < n_tensors; ++k) {
+        const zero_tensor &t = tensors[k];
+        if (t.n < 0 || t.n > kMaxDim || (t.n > 0 && !t.grad))
+            return fail(ZERO_ERR_INVALID_ARG, "tensor %d: a length in [0, 2^40] and a gradient are required", k);
+        if (!aligned(t.grad, bytes_of(grad_dtype)))
+            return fail(ZERO_ERR_ALIGNMENT, "tensor %d: the gradient is misaligned", k);
+        if (t.grad && t.grad == partials)
+            return fail(ZERO_ERR_INVALID_ARG, "tensor %d: the partial sums need memory of their own", k);
+    }
+    if ((st = check_tiles(n_tensors, tensors)) != ZERO_OK)
+        return st;
+    const int64_t need = zero_tensors_partials_count(n_tensors, tensors);
+    if (need == 0)
+        return ZERO_OK;
+    if (!partials || n_partials < need)
+        return fail(ZERO_ERR_INVALID_ARG, "%lld partial sums are required", (long long)need);
+    if (!aligned(partials, 8))
+        return fail(ZERO_ERR_ALIGNMENT, "partials is misaligned");
+    TensorArgs a;
+    std::memset(&a, 0, offsetof(TensorArgs, t));
+    a.sums = partials;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    return each_launch(n_tensors, tensors, true, grad_dtype, kSumTile, a, "tensors_sumsq",
+                       [&](const TensorArgs &args, unsigned blocks) {
+                           hipLaunchKernelGGL(tensors_sum_kernel, dim3(blocks), dim3(256), 0, s, args);
+                       });
+}
+
+zero_status zero_adam_state_read(int64_t n, const uint8_t *codes, const uint8_t *scales, int32_t second, void *out,
+                                 int32_t out_dtype, void *stream)
+{
+    using namespace zs;
+    if (n < 0)
+        return fail(ZERO_ERR_INVALID_ARG, "negative length");
+    if (!known_dtype(out_dtype))
+        return fail(ZERO_ERR_INVALID_ARG, "out: unknown dtype %d", out_dtype);
+    if (n == 0)
+        return ZERO_OK;
+    if (!codes || !scales || !out)
+        return fail(ZERO_ERR_INVALID_ARG, "codes, scales and out are required");
+    if (!aligned(out, bytes_of(out_dtype)))
+        return fail(ZERO_ERR_ALIGNMENT, "out is misaligned");
+    if (is_one_of(out, {codes, scales}))
+        return fail(ZERO_ERR_INVALID_ARG, "a state is not read back in place");
+    const int64_t blocks = tensor_tiles(n, kTensorTile);
+    if (blocks > int64_t(0xffffffffu) / 256)
+        return fail(ZERO_ERR_UNSUPPORTED, "too long for one launch");
+    (void)hipGetLastError();
+    hipLaunchKernelGGL(state_read_kernel, dim3((unsigned)blocks), dim3(256), 0, static_cast<hipStream_t>(stream), n,
+                       codes, scales, second != 0, out, out_dtype == ZERO_BF16,
+                       aligned(codes, 8) && aligned(out, 16));
+    return launched("adam_state_read");
+}
+
+}  // extern "C"

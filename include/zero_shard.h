@@ -808,6 +808,229 @@ zero_status zero_fsdp_experts_backward(const zero_layout *layout, int32_t unit,
                                        const uint16_t *dy, uint16_t *w_full, void *dx,
                                        int32_t dx_dtype, float *dw_full, void *stream);
 
+/* --------------------------------------------- training operators -- */
+
+/* What a rank's training pass does between its linear layers and around them:
+   layer norm, routing to experts and moving their rows, the loss of a linear head,
+   and the optimizer step of parameters that are tensors of their own, as FSDP2
+   keeps them.  Everything under CONVENTIONS holds here; a matrix without rows or
+   columns is never read, and its address may be NULL.  One address for two
+   things that a call needs at once is refused, the in-place forms named below
+   excepted. */
+
+/* Layer norm of rows of `cols` values: with mu and var a row's mean and variance
+   (about the mean, over cols) and r = 1 / sqrt(var + eps),
+       y = (x - mu) r gain + bias.
+   x and y bf16 or fp32; gain and bias cols values of param_dtype, each may be NULL
+   (1, 0); mean and rstd receive mu and r (fp32, rows each; may be NULL).  y may be
+   x (same type and leading dimension).  eps >= 0. */
+zero_status zero_layer_norm_forward(int64_t rows, int64_t cols, const void *x, int64_t ldx,
+                                    int32_t x_dtype, const void *gain, const void *bias,
+                                    int32_t param_dtype, float eps, void *y, int64_t ldy,
+                                    int32_t y_dtype, float *mean, float *rstd, void *stream);
+
+/* Its gradient, from the kept x, mean and rstd: with xh = (x - mu) r, h = dy gain,
+       dx    = r (h - mean(h) - xh mean(h xh)) + residual   (means over the row)
+       dgain = sum over rows of dy xh,  dbias = sum over rows of dy   (fp32).
+   residual (rows x cols of dx's type, leading dimension ldr; NULL: 0) is the
+   gradient that reaches x past the norm.  dx may be dy, x or the residual (same type
+   and leading dimension).  dgain and dbias may be NULL; either needs `workspace` of
+   zero_layer_norm_workspace(rows, cols) floats (at most 512 cols), used until the
+   call's work has run: calls that overlap in time, and captured graphs that do, need
+   one each.  The sums run in a fixed order.  rows = 0 writes zeros to both. */
+zero_status zero_layer_norm_backward(int64_t rows, int64_t cols, const void *dy, int64_t lddy,
+                                     int32_t dy_dtype, const void *x, int64_t ldx,
+                                     int32_t x_dtype, const void *gain, int32_t param_dtype,
+                                     const float *mean, const float *rstd, const void *residual,
+                                     int64_t ldr, void *dx, int64_t lddx, int32_t dx_dtype,
+                                     float *dgain, float *dbias, float *workspace,
+                                     int64_t n_workspace, void *stream);
+int64_t zero_layer_norm_workspace(int64_t rows, int64_t cols);
+
+/* How tokens choose experts.  s = softmax or sigmoid of a token's n_experts logits.
+   Experts are ranked by s + bias, or by the logit where there is no bias (which
+   ranks as s does), the lower number first among equals, NaN last.  With n_groups
+   > 1 the experts fall into that many runs of equal length; a group is ranked by its
+   best expert (group_best 1) or by the sum of its two best (2; of s where there is
+   no bias), and only the top_groups best groups' experts are left.  The token
+   takes the top_k best, with weights
+       w_j = scale s_j,   or   scale s_j / (sum of the chosen s + 1e-20)
+   with `renormalize`.  The bias ranks and does not weigh.  A row of -inf alone has
+   scores of 0.  Sums that rank are compared in fp64, to 42 bits.  At most 1024
+   experts, 16 of them for a token, 64 groups. */
+typedef enum zero_score { ZERO_SCORE_SOFTMAX = 0, ZERO_SCORE_SIGMOID = 1 } zero_score;
+
+typedef struct zero_router {
+    int32_t n_experts;
+    int32_t top_k;
+    int32_t n_groups;   /* 1: no groups; divides n_experts */
+    int32_t top_groups; /* 1 .. n_groups; their experts are at least top_k */
+    int32_t group_best; /* 1 or 2 */
+    int32_t score;      /* zero_score */
+    int32_t renormalize;
+    float scale;
+} zero_router;
+
+/* Routes `tokens` rows of logits (tokens x n_experts, bf16 or fp32).  bias: n_experts
+   fp32 or NULL; active: one byte a token or NULL; a token whose byte is 0 takes no
+   expert.  Results:
+     experts  tokens x top_k int32, the best first; -1 for a token that is not active;
+     weights  tokens x top_k fp32; 0 there;
+     offsets  n_experts + 1 int64: expert e's rows are offsets[e] .. offsets[e + 1] - 1,
+              as the grouped products take them;
+     rows_of  tokens x top_k int32: each choice's row when the rows are sorted by expert
+              and, within an expert, by token; -1 there.
+   workspace: zero_route_workspace int32 (0 for one block's tokens, when it may be
+   NULL), used until the call's work has run.  tokens x top_k is below 2^31.
+   tokens = 0 writes zero offsets. */
+zero_status zero_route_forward(const zero_router *router, int64_t tokens, const void *logits,
+                               int64_t ldl, int32_t logits_dtype, const float *bias,
+                               const uint8_t *active, int32_t *experts, float *weights,
+                               int64_t *offsets, int32_t *rows_of, int32_t *workspace,
+                               int64_t n_workspace, void *stream);
+int64_t zero_route_workspace(const zero_router *router, int64_t tokens);
+
+/* The gradient of the weights with respect to the logits, the choice held fixed:
+   dlogits (tokens x n_experts, bf16 or fp32; it may be logits) from dweights
+   (tokens x top_k).  `experts` as zero_route_forward left them; numbers outside
+   [0, n_experts) count as none, and a token without experts has a gradient of 0. */
+zero_status zero_route_backward(const zero_router *router, int64_t tokens, const void *logits,
+                                int64_t ldl, int32_t logits_dtype, const int32_t *experts,
+                                const float *dweights, void *dlogits, int64_t ldd,
+                                int32_t dlogits_dtype, void *stream);
+
+/* Tokens' rows to their experts and back.  rows_of is tokens x top_k (top_k at most
+   16); numbers outside [0, rows) are none.
+     dispatch          out[rows_of[t][j]] = w[t][j] x[t]   (bf16; weights NULL: copies).
+                       Rows that no token has are left as they were.
+     combine           y[t] = sum over j of w[t][j] in[rows_of[t][j]] + residual[t], in
+                       fp32, rounded once (y bf16 or fp32; weights NULL: 1; residual
+                       bf16 or NULL, it may be y).  With weights NULL it is the gradient
+                       of dispatch.
+     combine_backward  din[rows_of[t][j]] = w[t][j] dy[t] (it may be in) and
+                       dweights[t][j] = sum over the columns of dy[t] in[rows_of[t][j]]
+                       (fp32; 0 for none), in one pass. */
+zero_status zero_experts_dispatch(int64_t tokens, int32_t top_k, int64_t cols, const uint16_t *x,
+                                  int64_t ldx, const int32_t *rows_of, const float *weights,
+                                  int64_t rows, uint16_t *out, int64_t ldo, void *stream);
+zero_status zero_experts_combine(int64_t tokens, int32_t top_k, int64_t cols, const uint16_t *in,
+                                 int64_t ldi, int64_t rows, const int32_t *rows_of,
+                                 const float *weights, const uint16_t *residual, int64_t ldr,
+                                 void *y, int64_t ldy, int32_t y_dtype, void *stream);
+zero_status zero_experts_combine_backward(int64_t tokens, int32_t top_k, int64_t cols,
+                                          const uint16_t *dy, int64_t lddy, int64_t rows,
+                                          const int32_t *rows_of, const float *weights,
+                                          const uint16_t *in, int64_t ldi, uint16_t *din,
+                                          int64_t lddi, float *dweights, void *stream);
+
+/* Softmax cross entropy of a linear head: z = x W over `vocab` words, x rows x hidden
+   bf16, W hidden x vocab (w_order ZERO_K_OUTER, as a linear layer keeps it) or vocab x
+   hidden (ZERO_K_INNER, as an embedding does) bf16.  The logits never reach memory.
+     lse[r]  = log(sum over c of exp z[r][c]),  loss[r] = lse[r] - z[r][targets[r]];
+     dz      = (exp(z - lse) - [c = target]) dloss[r], rounded to bf16 (a piece of the
+               vocabulary at a time, in the workspace);
+     dx      = dz W^T (rows x hidden), dw = x^T dz (as W lies), fp32 sums, bf16 or fp32.
+   A target outside [0, vocab) is none: loss 0, no gradient.  hidden and the leading
+   dimensions of x and W are multiples of 8, a vocabulary stored as columns too; x and
+   W 16-byte aligned; limits of zero_gemm_bf16.  loss, lse and dloss are fp32, one a
+   row; lse is what the loss left.  piece: words at a time, 0 or a multiple of 256; 0
+   takes the widest pieces of at most ZERO_XENT_PIECE_ELEMS dz (and at least 4096
+   words).  workspace: zero_linear_xent_workspace floats of the pass (`backward`;
+   16-byte aligned), used until the call's work has run.  rows = 0 writes zeros to
+   dw. */
+#define ZERO_XENT_PIECE_ELEMS 67108864
+zero_status zero_linear_xent_forward(int64_t rows, int64_t vocab, int64_t hidden,
+                                     const uint16_t *x, int64_t ldx, const uint16_t *w,
+                                     int64_t ldw, int32_t w_order, const int64_t *targets,
+                                     float *loss, float *lse, float *workspace,
+                                     int64_t n_workspace, void *stream);
+zero_status zero_linear_xent_backward(int64_t rows, int64_t vocab, int64_t hidden,
+                                      const uint16_t *x, int64_t ldx, const uint16_t *w,
+                                      int64_t ldw, int32_t w_order, const int64_t *targets,
+                                      const float *lse, const float *dloss, void *dx,
+                                      int64_t lddx, int32_t dx_dtype, void *dw, int64_t lddw,
+                                      int32_t dw_dtype, int64_t piece, float *workspace,
+                                      int64_t n_workspace, void *stream);
+int64_t zero_linear_xent_workspace(int64_t rows, int64_t vocab, int64_t hidden, int32_t backward,
+                                   int64_t piece);
+
+/* The head as an FSDP unit: unit `unit` of a row layout is W (hidden x vocab rows x
+   cols for ZERO_K_OUTER, vocab x hidden for ZERO_K_INNER).  Both gather w_full
+   first; the backward pass leaves dw_full as the padded unit in fp32 (padding rows
+   zeroed), ready for zero_reduce_shard and zero_adam_step.  x, dx: batch x hidden. */
+zero_status zero_fsdp_head_forward(const zero_layout *layout, int32_t unit,
+                                   const uint16_t *const *w_shards, int32_t w_order,
+                                   int64_t batch, const uint16_t *x, uint16_t *w_full,
+                                   const int64_t *targets, float *loss, float *lse,
+                                   float *workspace, int64_t n_workspace, void *stream);
+zero_status zero_fsdp_head_backward(const zero_layout *layout, int32_t unit,
+                                    const uint16_t *const *w_shards, int32_t w_order,
+                                    int64_t batch, const uint16_t *x, uint16_t *w_full,
+                                    const int64_t *targets, const float *lse,
+                                    const float *dloss, void *dx, int32_t dx_dtype,
+                                    float *dw_full, int64_t piece, float *workspace,
+                                    int64_t n_workspace, void *stream);
+
+/* Adam / AdamW over many tensors at once: per element the update of zero_adam_step
+   (the same bits, with fp32 states), each tensor with buffers of its own.  A host
+   array of descriptions, read during the call:
+     n           elements (0: nothing, the pointers may be NULL);
+     master      fp32; grad: grad_dtype, multiplied by *clip_coef (device float, NULL:
+                 1); param: bf16, receives the new master (NULL: left out);
+     m, v        fp32 (ZERO_STATE_FP32), or one code a byte (ZERO_STATE_E4M3) with
+                 m_scales, v_scales of ceil(n / 32) bytes;
+     decay       0: weight decay is left out for this tensor.
+   Different tensors' buffers must not overlap.
+   ZERO_STATE_E4M3 keeps m, and the root of v, as e4m3 codes of blocks of 32
+   neighbouring elements: a byte b stands for 2^(b - 127), b - 127 the least e in
+   [-117, 120] for which the block's largest finite magnitude is at most 448 * 2^e; NaN
+   and infinities become NaN.  All-zero buffers are zero states.  A new state is
+   rounded to one of the two codes around it at random, by 16 random bits, so that
+   averages that move by less than a code's step keep moving; a v above 0 keeps a
+   code above 0.  The update itself uses the unrounded m and v.  The random bits
+   depend on `seed`, the step's number and the element's number alone (elements are
+   numbered through the list, each tensor from the next multiple of 32): another
+   seed for each rank is a good choice.  24 bytes fewer of traffic and 5.9 fewer of
+   memory an element than fp32 states: 16 against 28, 14.06 against 20 with bf16
+   gradients. */
+typedef enum zero_state_format { ZERO_STATE_FP32 = 0, ZERO_STATE_E4M3 = 1 } zero_state_format;
+
+typedef struct zero_tensor {
+    int64_t n;
+    float *master;
+    const void *grad;
+    uint16_t *param;
+    void *m;
+    void *v;
+    uint8_t *m_scales;
+    uint8_t *v_scales;
+    int32_t decay;
+} zero_tensor;
+
+zero_status zero_adam_tensors(int32_t n_tensors, const zero_tensor *tensors, int32_t state_format,
+                              int32_t grad_dtype, const zero_adam_cfg *cfg, uint64_t seed,
+                              const float *clip_coef, void *stream);
+
+/* zero_adam_tensors with the scalars of table[*step_counter - 1] and *step_counter as
+   the step's number, both on the device, as zero_adam_step_table takes them: for
+   captured steps.  A counter outside [1, n_entries] leaves every buffer untouched. */
+zero_status zero_adam_tensors_table(int32_t n_tensors, const zero_tensor *tensors,
+                                    int32_t state_format, int32_t grad_dtype,
+                                    const zero_adam_table_entry *table, int64_t n_entries,
+                                    const int64_t *step_counter, uint64_t seed,
+                                    const float *clip_coef, void *stream);
+
+/* The tensors' gradients' sums of squares for zero_clip_coef: fp64 partial sums, one
+   for each 8192 elements of a tensor, zero_tensors_partials_count of them. */
+zero_status zero_tensors_sumsq(int32_t n_tensors, const zero_tensor *tensors, int32_t grad_dtype,
+                               double *partials, int64_t n_partials, void *stream);
+int64_t zero_tensors_partials_count(int32_t n_tensors, const zero_tensor *tensors);
+
+/* What n 8-bit state codes and their scales stand for: m, or with `second` v (the
+   square of what is kept), bf16 or fp32, both exact. */
+zero_status zero_adam_state_read(int64_t n, const uint8_t *codes, const uint8_t *scales,
+                                 int32_t second, void *out, int32_t out_dtype, void *stream);
+
 /* ---------------------------------------------------------- errors -- */
 
 const char *zero_status_str(zero_status status);
