@@ -120,66 +120,78 @@ struct NormArgs {
     bool x_vec, p_vec, y_vec;
 };
 
-// TPR threads a row, each NC chunks of eight columns, TPR chunks apart.
-template <int TPR, int NC>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_forward_kernel(const NormArgs p)
+// TPR threads a row, each NC chunks of eight columns, TPR chunks apart.  A block of
+// THREADS takes rows blockIdx.x, + gridDim.x, ... of groups of THREADS / TPR rows: the
+// gain and the bias stay in registers, and the next row's loads go out before the
+// present one's sums meet.
+template <int THREADS, int TPR, int NC, bool W>
+__global__ __launch_bounds__(THREADS) void norm_forward_kernel(const NormArgs p)
 {
-    constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
-    __shared__ float slots[2][RPB][32];
+    constexpr int RPB = THREADS / TPR;
+    __shared__ float slots[2][2][RPB][32];
     const int t = threadIdx.x % TPR, g = threadIdx.x / TPR;
-    const int64_t row = (int64_t)blockIdx.x * RPB + g;
-    const bool here = row < p.rows;
-    Raw8<true> raw[NC];
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    Raw8<W> raw[NC], rg[NC], rb[NC];
     int n[NC];
+    auto fetch = [&](int64_t row) {
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+            raw[j] = raw8<W>(p.x, p.x_bf16, row * p.ldx + (int64_t)(t + j * TPR) * 8, p.x_vec, row < p.rows ? n[j] : 0);
+    };
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-        const int64_t col = (int64_t)(t + j * TPR) * 8;
-        const int64_t left = here ? p.cols - col : 0;
+        const int64_t left = p.cols - (int64_t)(t + j * TPR) * 8;
         n[j] = left < 0 ? 0 : left < 8 ? (int)left : 8;
-        raw[j] = raw8<true>(p.x, p.x_bf16, row * p.ldx + col, p.x_vec, n[j]);
     }
-    float x[NC][8], s = 0.0f, none = 0.0f;
+    fetch((int64_t)blockIdx.x * RPB + g);
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-        unraw8(raw[j], p.x_bf16, x[j]);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            s += x[j][k];
-    }
-    row_sums<TPR>(s, none, slots[0][g]);
-    const float mu = s * p.inv_n;
-    float q = 0.0f;
-#pragma unroll
-    for (int j = 0; j < NC; ++j)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            x[j][k] -= mu;
-            q += k < n[j] ? x[j][k] * x[j][k] : 0.0f;
-        }
-    row_sums<TPR>(q, none, slots[1][g]);
-    const float r = 1.0f / sqrtf(q * p.inv_n + p.eps);
-    if (!here)
-        return;
-    if (t == 0) {
-        if (p.mean)
-            p.mean[row] = mu;
-        if (p.rstd)
-            p.rstd[row] = r;
-    }
-#pragma unroll
-    for (int j = 0; j < NC; ++j) {
-        if (n[j] == 0)
-            break;
         const int64_t col = (int64_t)(t + j * TPR) * 8;
-        float gain[8], bias[8];
-        unraw8(raw8<true>(p.gain, p.p_bf16, col, p.p_vec, p.gain ? n[j] : 0), p.p_bf16, gain);
-        unraw8(raw8<true>(p.bias, p.p_bf16, col, p.p_vec, p.bias ? n[j] : 0), p.p_bf16, bias);
+        rg[j] = raw8<W>(p.gain, p.p_bf16, col, p.p_vec, p.gain ? n[j] : 0);
+        rb[j] = raw8<W>(p.bias, p.p_bf16, col, p.p_vec, p.bias ? n[j] : 0);
+    }
+    int turn = 0;
+    for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < p.rows; row0 += step, turn ^= 1) {
+        const int64_t row = row0 + g;
+        const bool here = row < p.rows;
+        float x[NC][8], s = 0.0f, q = 0.0f, none = 0.0f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            x[j][k] *= r;
-            x[j][k] = __builtin_fmaf(x[j][k], p.gain ? gain[k] : 1.0f, bias[k]);
+        for (int j = 0; j < NC; ++j) {
+            unraw8(raw[j], p.x_bf16, x[j]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                s += x[j][k];
         }
-        store8(p.y, p.y_bf16, row * p.ldy + col, p.y_vec && n[j] == 8, n[j], x[j]);
+        fetch(row + step);
+        row_sums<TPR>(s, none, slots[turn][0][g]);
+        const float mu = s * p.inv_n;
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                x[j][k] -= mu;
+                q += k < n[j] ? x[j][k] * x[j][k] : 0.0f;
+            }
+        row_sums<TPR>(q, none, slots[turn][1][g]);
+        const float r = 1.0f / sqrtf(q * p.inv_n + p.eps);
+        if (here && t == 0) {
+            if (p.mean)
+                p.mean[row] = mu;
+            if (p.rstd)
+                p.rstd[row] = r;
+        }
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+            if (!here || n[j] == 0)
+                break;
+            float gain[8], bias[8];
+            unraw8(rg[j], p.p_bf16, gain);
+            unraw8(rb[j], p.p_bf16, bias);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                x[j][k] = __builtin_fmaf(x[j][k] * r, p.gain ? gain[k] : 1.0f, bias[k]);
+            store8(p.y, p.y_bf16, row * p.ldy + (int64_t)(t + j * TPR) * 8, p.y_vec && n[j] == 8, n[j], x[j]);
+        }
     }
 }
 
@@ -535,22 +547,32 @@ zero_status zero_layer_norm_forward(int64_t rows, int64_t cols, const void *x, i
     p.p_vec = vec_or_null(gain) && vec_or_null(bias);
     const hipStream_t s = static_cast<hipStream_t>(stream);
     (void)hipGetLastError();
-#define ZS_NORM(TPR, NC)                                                                           \
-    hipLaunchKernelGGL((norm_forward_kernel<TPR, NC>),                                             \
-                       dim3((unsigned)((rows + (TPR < 256 ? 256 / TPR : 1) - 1) / (TPR < 256 ? 256 / TPR : 1))), \
-                       dim3(TPR < 256 ? 256 : TPR), 0, s, p)
+#define ZS_NORM(THREADS, TPR, NC)                                                                  \
+    do {                                                                                           \
+        const int64_t groups = (rows + THREADS / TPR - 1) / (THREADS / TPR);                       \
+        const dim3 grid((unsigned)(groups < most / THREADS ? groups : most / THREADS));            \
+        if (wide)                                                                                  \
+            hipLaunchKernelGGL((norm_forward_kernel<THREADS, TPR, NC, true>), grid, dim3(THREADS), 0, s, p); \
+        else                                                                                       \
+            hipLaunchKernelGGL((norm_forward_kernel<THREADS, TPR, NC, false>), grid, dim3(THREADS), 0, s, p); \
+    } while (0)
+    const bool wide = !(p.x_bf16 && p.p_bf16);
+    // Two chunks a thread and 1024 threads a CU: 128 MB through rows of 8192 in 27 us
+    // (a copy: 26.5), one chunk a thread 44, four 31; twice the threads 29 to 32.  Rows
+    // of up to 512, of one chunk, take 27.6 us with 2048 threads a CU and 33 with 1024.
+    const int64_t most = (cols <= 512 ? 512 : 256) * 1024;
     if (cols <= 512)
-        ZS_NORM(64, 1);
+        ZS_NORM(256, 64, 1);
     else if (cols <= 1024)
-        ZS_NORM(64, 2);
+        ZS_NORM(256, 64, 2);
     else if (cols <= 2048)
-        ZS_NORM(256, 1);
+        ZS_NORM(256, 128, 2);
     else if (cols <= 4096)
-        ZS_NORM(256, 2);
+        ZS_NORM(256, 256, 2);
     else if (cols <= 8192)
-        ZS_NORM(256, 4);
+        ZS_NORM(512, 512, 2);
     else if (cols <= kHeld)
-        ZS_NORM(1024, 2);
+        ZS_NORM(1024, 1024, 2);
     else
         hipLaunchKernelGGL(norm_forward_long_kernel, dim3((unsigned)rows), dim3(1024), 0, s, p);
 #undef ZS_NORM

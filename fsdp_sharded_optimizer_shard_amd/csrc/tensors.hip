@@ -25,6 +25,7 @@
 // state of its own.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <cstring>
 
 #include "act.h"
@@ -53,6 +54,7 @@ struct Tensor {
 
 struct TensorArgs {
     AdamScalars sc;
+    float rate, per;           // 8-bit states: lr / bias1, 1 / sqrt(bias2)
     const AdamScalars *table;  // non-null: scalars of table[*counter - 1]
     const int64_t *counter;
     int64_t n_table, step, first_sum;
@@ -106,51 +108,104 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t x)
     return x > y ? x : y;
 }
 
-// The exponent byte of a block of 32: the largest of the four lanes' eight values.
-__device__ __forceinline__ uint32_t block_of(const float (&x)[8])
+// Largest of the four lanes of a block of 32.
+__device__ __forceinline__ uint32_t over_block(uint32_t mx)
+{
+    mx = quad_max<0xB1>(mx);  // lanes 1 0 3 2
+    return quad_max<0x4E>(mx);  // lanes 2 3 0 1
+}
+
+constexpr uint32_t kLimBits = 0x7f700000u;  // 240 * 2^120
+
+// x / 2^e as a code (ROOT: x is not negative), rounded up where the 16 random bits
+// `r` and the part of a step above the code below sum to a whole step.  Under 2^-6
+// the codes are 2^-9 apart, as they are from 2^-6 to 2^-5, so 2^-6 is added there.
+// PLAIN: x is finite and at most 240 * 2^120.
+template <bool ROOT, bool PLAIN>
+__device__ __forceinline__ uint32_t code_random(float x, float inv, uint32_t r)
+{
+    const uint32_t u = __float_as_uint(x), mag = u & 0x7fffffffu;
+    float a = __builtin_fabsf(x);
+    if (!PLAIN)
+        a = mag > kLimBits ? __uint_as_float(kLimBits) : a;
+    const float q = a * inv;
+    const uint32_t t = (q < 0x1p-6f ? __float_as_uint(q + 0x1p-6f) - (8u << 20) : __float_as_uint(q)) + (r << 4);
+    uint32_t c = (t >> 20) - 960u;
+    if (ROOT) {
+        const uint32_t some = __float_as_uint(q) < 1u ? __float_as_uint(q) : 1u;
+        c = c > some ? c : some;
+    }
+    if (!PLAIN)
+        c = mag < kInf ? c : 0x7fu;
+    return ROOT ? c : c | ((u >> 24) & 0x80u);
+}
+
+template <bool ROOT, bool PLAIN>
+__device__ __forceinline__ uint2 code8(const float (&x)[8], const uint32_t (&r)[8], uint32_t byte)
+{
+    const float inv = inv_scale(byte);
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        w[k >> 2] |= code_random<ROOT, PLAIN>(x[k], inv, ROOT ? r[k] >> 16 : r[k] & 0xffffu) << (8 * (k & 3));
+    return make_uint2(w[0], w[1]);
+}
+
+// The codes of a lane's eight values and their block's exponent byte.
+template <bool ROOT>
+__device__ __forceinline__ uint2 encode(const float (&x)[8], const uint32_t (&r)[8], uint32_t &byte)
 {
     uint32_t mx = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const uint32_t b = ROOT ? __float_as_uint(x[k]) : __float_as_uint(x[k]) & 0x7fffffffu;
+        mx = b > mx ? b : mx;
+    }
+    // all of a wave's values are numbers that bf16 holds, but for a step gone wrong
+    if (__ballot(mx > kLimBits) == 0) {
+        byte = block_byte(over_block(mx));
+        return code8<ROOT, true>(x, r, byte);
+    }
+    mx = 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         const uint32_t b = mag_bits(x[k]);
         mx = b > mx ? b : mx;
     }
-    mx = quad_max<0xB1>(mx);  // lanes 1 0 3 2
-    mx = quad_max<0x4E>(mx);  // lanes 2 3 0 1
-    return block_byte(mx);
+    byte = block_byte(over_block(mx));
+    return code8<ROOT, false>(x, r, byte);
 }
 
-// x / 2^e as a code, rounded up where the 16 random bits `r` and the part of a
-// step above the code below sum to a whole step.  Under 2^-6 the codes are 2^-9
-// apart, as they are from 2^-6 to 2^-5, so 2^-6 is added there.
-template <bool ROOT>
-__device__ __forceinline__ uint32_t code_random(float x, float inv, uint32_t r)
-{
-    const uint32_t u = __float_as_uint(x), mag = u & 0x7fffffffu;
-    const float lim = 0x1.ep127f, a = __builtin_fabsf(x), q = (a > lim ? lim : a) * inv;
-    const bool low = q < 0x1p-6f;
-    const uint32_t t = __float_as_uint(low ? q + 0x1p-6f : q) + (r << 4);
-    uint32_t c = (t >> 20) - (low ? 968u : 960u);
-    if (ROOT)
-        c = c == 0 && q > 0.0f ? 1u : c;
-    c = mag < kInf ? c : 0x7fu;
-    return ROOT ? c : c | ((u >> 24) & 0x80u);
-}
+// The scalars of a step with 8-bit states.
+struct SmallScalars {
+    float b1, omb1, b2, omb2, eps, decay, wd;
+    float rate;   // lr / bias1
+    float per;    // 1 / sqrt(bias2)
+    bool l2;
+};
 
-template <bool ROOT>
-__device__ __forceinline__ void code8(const float (&x)[8], const uint32_t (&r)[8], uint32_t byte, uint32_t (&w)[2])
+// adam1 with the quotient from the reciprocal and from the root that the state needs
+// anyway: m_hat / (sqrt(v_hat) + eps) with v_hat = v / bias2 as m rate / (sqrt(v) per
+// + eps).  m and v have adam1's bits; the quotient carries at most 8 roundings more
+// (2^-21 of the update, which its codes' steps of 1/16 drown), and costs 40 issue slots
+// less of 175 an element, where 126 keep up with memory.
+__device__ __forceinline__ void adam_small(const SmallScalars &s, float g, float &p, float &m, float &v, float &root)
 {
-    const float inv = inv_scale(byte);
-    w[0] = w[1] = 0;
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-        w[k >> 2] |= code_random<ROOT>(x[k], inv, ROOT ? r[k] >> 16 : r[k] & 0xffffu) << (8 * (k & 3));
+    p = p * s.decay;
+    if (s.l2)
+        g = g + s.wd * p;
+    m = s.b1 * m + s.omb1 * g;
+    v = s.b2 * v + s.omb2 * (g * g);
+    root = sqrtf(v);
+    const float r = __builtin_amdgcn_rcpf(__builtin_fmaf(root, s.per, s.eps));
+    p = __builtin_fmaf(-(m * s.rate), r, p);
 }
 
 template <bool SMALL>
 __global__ __launch_bounds__(256) void tensors_kernel(const TensorArgs a)
 {
     AdamScalars sc = a.sc;
+    float rate = a.rate, per = a.per;
     int64_t step = a.step;
     if (a.table) {
         // a counter outside the table leaves every buffer as it is
@@ -158,6 +213,10 @@ __global__ __launch_bounds__(256) void tensors_kernel(const TensorArgs a)
         if (step < 1 || step > a.n_table)
             return;
         sc = a.table[step - 1];
+        if (SMALL) {
+            rate = sc.lr / sc.bias1;
+            per = 1.0f / sqrtf(sc.bias2);
+        }
     }
     const float coef = a.clip ? *a.clip : 1.0f;
     const Tensor &t = tensor_of(a, blockIdx.x);
@@ -190,31 +249,37 @@ __global__ __launch_bounds__(256) void tensors_kernel(const TensorArgs a)
         load8(t.m, false, i, vec, n, m);
         load8(t.v, false, i, vec, n, v);
     }
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-        adam1(sc, g[k] * coef, p[k], m[k], v[k]);
     if (SMALL) {
+        SmallScalars ss;
+        ss.b1 = sc.b1, ss.omb1 = sc.omb1, ss.b2 = sc.b2, ss.omb2 = sc.omb2, ss.eps = sc.eps, ss.wd = sc.wd;
+        ss.decay = sc.has_wd && sc.decoupled ? sc.decay : 1.0f;
+        ss.l2 = sc.has_wd && !sc.decoupled;
+        ss.rate = rate, ss.per = per;
         const uint2 key = step_keys(a.seed, step);
-        uint32_t r[8], w[2];
+        uint32_t r[8], bm, bv;
+        float root[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
+            adam_small(ss, g[k] * coef, p[k], m[k], v[k], root[k]);
             r[k] = random_bits(key, t.number + i + k);
-            v[k] = sqrtf(v[k]);
             if (k >= n)
-                m[k] = v[k] = 0.0f;
+                m[k] = root[k] = 0.0f;
         }
-        const uint32_t bm = block_of(m), bv = block_of(v);
+        const uint2 wm = encode<false>(m, r, bm), wv = encode<true>(root, r, bv);
         if (n == 0)
             return;
-        code8<false>(m, r, bm, w);
-        store_bytes8(static_cast<uint8_t *>(t.m) + i, vec, n, make_uint2(w[0], w[1]));
-        code8<true>(v, r, bv, w);
-        store_bytes8(static_cast<uint8_t *>(t.v) + i, vec, n, make_uint2(w[0], w[1]));
+        store_bytes8(static_cast<uint8_t *>(t.m) + i, vec, n, wm);
+        store_bytes8(static_cast<uint8_t *>(t.v) + i, vec, n, wv);
         if ((threadIdx.x & 3) == 0) {
             t.ms[i >> 5] = (uint8_t)bm;
             t.vs[i >> 5] = (uint8_t)bv;
         }
-    } else if (n > 0) {
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            adam1(sc, g[k] * coef, p[k], m[k], v[k]);
+        if (n == 0)
+            return;
         store8(t.m, false, i, vec, n, m);
         store8(t.v, false, i, vec, n, v);
     }
@@ -394,6 +459,8 @@ zero_status zero_adam_tensors(int32_t n_tensors, const zero_tensor *tensors, int
     if (!aligned(clip_coef, 4))
         return fail(ZERO_ERR_ALIGNMENT, "clip_coef is misaligned");
     std::memcpy(&a.sc, &e, sizeof e);
+    a.rate = a.sc.lr / a.sc.bias1;
+    a.per = 1.0f / std::sqrt(a.sc.bias2);
     a.step = cfg->step;
     a.seed = seed;
     a.clip = clip_coef;

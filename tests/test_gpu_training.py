@@ -5,8 +5,8 @@ Bounds, from the arithmetic (u = 2^-24, gamma_k = k u / (1 - k u)):
   * a division, root, product or difference: u of its value; v_exp_f32 and the
     reciprocals within 4 u, an exponential's argument a carrying 3 u |a| besides;
   * an output in bf16: half a step, 2^-8 of the value;
-  * choices, offsets and rows: the oracle's; codes of 8-bit states and everything
-    that the optimizer step leaves: the oracle's bits.
+  * choices, offsets and rows: the oracle's; codes of 8-bit states, and all that a step
+    with fp32 states leaves: the oracle's bits.
 """
 import numpy as np
 import pytest
@@ -693,8 +693,8 @@ CFG = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.1, decouple
 
 
 def adam_oracle(ref, sizes, state, cfg, step, seed, decay, coef):
-    """One step on numpy's values, in place; returns the bf16 parameters."""
-    first, params = 0, []
+    """One step on numpy's values, in place; returns the masters before it."""
+    first, before = 0, [x.copy() for x in ref["master"]]
     for i, n in enumerate(sizes):
         hp = dict(cfg, step=step)
         if not decay[i]:
@@ -713,19 +713,27 @@ def adam_oracle(ref, sizes, state, cfg, step, seed, decay, coef):
             bits = training.random_bits(first, n, seed, step)
             ref["m"][i], ref["ms"][i] = training.encode_random(m, bits & np.uint64(0xffff), False)
             ref["v"][i], ref["vs"][i] = training.encode_random(np.sqrt(v), bits >> np.uint64(16), True)
-        params.append(_c.f32_to_bf16(ref["master"][i]))
         first += -(-n // 32) * 32
-    return params
+    return before
 
 
-def same_state(out, ref, params, state):
-    for i, p in enumerate(params):
-        assert np.array_equal(out["master"][i].cpu().numpy().view(np.uint32), ref["master"][i].view(np.uint32)), i
-        assert np.array_equal(out["param"][i].view(torch.int16).cpu().numpy().view(np.uint16), p), i
+def same_state(out, ref, before, state):
+    """What a step leaves: the oracle's bits.  With 8-bit states the master is the oracle's
+    within a rounding and 8 more of its move (the quotient's: rate, per and their
+    products, the root, the sum with eps, the reciprocal's two); it is taken over for the
+    next step, which weight decay makes depend on it."""
+    for i, old in enumerate(before):
+        got, want = out["master"][i].cpu().numpy(), ref["master"][i]
+        if state == "fp32":
+            assert np.array_equal(got.view(np.uint32), want.view(np.uint32)), i
+        else:
+            w, o = want.astype(np.float64), old.astype(np.float64)
+            move = np.abs(w - o) + CFG["lr"] * CFG["weight_decay"] * np.abs(o)
+            within(got, w, 2 * U * np.abs(w) + 2.0 ** -20 * move, f"master of tensor {i}")
+            ref["master"][i] = got.copy()
+        assert np.array_equal(out["param"][i].view(torch.int16).cpu().numpy().view(np.uint16), _c.f32_to_bf16(got)), i
         for k in ("m", "v") if state == "fp32" else ("m", "v", "ms", "vs"):
-            got = out[k][i].cpu().numpy()
-            want = ref[k][i]
-            assert np.array_equal(got.view(np.uint8), want.view(np.uint8)), (i, k)
+            assert np.array_equal(out[k][i].cpu().numpy().view(np.uint8), ref[k][i].view(np.uint8)), (i, k)
 
 
 def tensor_list(out, state, decay):
@@ -750,8 +758,8 @@ def test_adam_of_many_tensors(state, grad, shift, decoupled):
     for step in (1, 2, 3):
         zs.adam_tensors(ts, zs.adam_cfg(step=step, **cfg), seed=seed, clip_coef=clip if step == 2 else None)
         torch.cuda.synchronize()
-        params = adam_oracle(ref, SIZES, state, cfg, step, seed, decay, np.float32(0.7) if step == 2 else None)
-        same_state(out, ref, params, state)
+        before = adam_oracle(ref, SIZES, state, cfg, step, seed, decay, np.float32(0.7) if step == 2 else None)
+        same_state(out, ref, before, state)
 
 
 @pytest.mark.parametrize("state", ["fp32", "e4m3"])
