@@ -2,15 +2,20 @@
 // rows' order by expert, the gradient of the weights, and the rows' way to their
 // experts and back.
 //
-// Choice.  Experts are ranked by a 64-bit key, the largest first: the value's bits
-// in an order of unsigned numbers, its lowest 11 bits given to the expert's
-// number so that no two keys are equal and the lower number wins a tie.  Without
-// a bias the value is the logit itself, which ranks as its score does; where keys
-// are sums (a bias, or a group's two best) the scores are taken in fp64, so that
-// which expert is chosen does not hang on how an fp32 score was rounded (the
-// 42 bits that are left decide).  A token's LPT lanes hold VPL neighbouring
-// experts each, so one wave routes 64 / LPT tokens, and a maximum is a scan of
-// VPL registers and log2 LPT exchanges, four of them without LDS.
+// Choice.  Experts are ranked by a 64-bit key, the largest first: the value as a double,
+// its lowest 11 bits given to the expert's number so that no two keys are equal and the
+// lower number wins a tie.  Without a bias the value is the logit itself, which ranks as
+// its score does; where keys are sums (a bias, or a group's two best) the scores are
+// taken in fp64, so that which expert is chosen does not hang on how an fp32 score was
+// rounded (the 42 bits that are left decide).  A token's LPT lanes hold VPL neighbouring
+// experts each, so one wave routes 64 / LPT tokens.  A lane sorts its keys once, by
+// fp64 minima and maxima; each of the top_k steps is then a maximum of the lanes' first
+// keys (log2 LPT exchanges, four of them without LDS) and one lane's step to its next.
+// 16384 tokens of 256 experts, 8 of them from 4 of 8 groups by sigmoid and bias: 27 us
+// (softmax without a bias 15), and 9 for the rows' order, where reading the logits takes
+// 3.6.  What it takes is issue slots: 12 us of loads, sorting and first keys, 8 of scores
+// in fp64, 4 of groups, 0.4 for each expert chosen, at two waves a SIMD (the sixteen keys
+// and scores of a lane fill its registers; half as many experts a lane took 39 us).
 //
 // Order of rows.  Rows are sorted by expert and, within an expert, by token: a
 // counting sort without atomics on memory.  In a block of up to 64 tokens every
@@ -56,20 +61,40 @@ struct RouteArgs {
     bool sigmoid, renorm, two, bf16, vec, alone;  // two: a group's two best; alone: one block
 };
 
-__device__ __forceinline__ uint64_t sortable(double x)
+// The key of expert e: values that are no number, and infinities, become numbers past
+// all that fp32 holds, in order (NaN lowest); what is left out has the key -inf.
+__device__ __forceinline__ double key_of(double x, int e)
 {
     x += 0.0;  // -0 ranks as 0
+    x = x == __builtin_inf() ? 1e300 : x == -__builtin_inf() ? -1e300 : x != x ? -1e301 : x;
     const uint64_t u = (uint64_t)__double_as_longlong(x);
-    const uint64_t m = u >> 63 ? ~u : u | 0x8000000000000000ull;
-    return x != x ? 0ull : m;  // NaN below everything
+    return __longlong_as_double((long long)((u & ~2047ull) | (uint32_t)(u >> 63 ? e : 1024 - e)));
 }
 
-__device__ __forceinline__ uint64_t sortable(float x)
+__device__ __forceinline__ int expert_of(double key)
 {
-    x += 0.0f;
-    const uint32_t u = __float_as_uint(x);
-    const uint32_t m = u >> 31 ? ~u : u | 0x80000000u;
-    return x != x ? 0ull : (uint64_t)m << 32;
+    const uint64_t u = (uint64_t)__double_as_longlong(key);
+    const int low = (int)(u & 2047);
+    return u >> 63 ? low : 1024 - low;
+}
+
+// Descending order of N values, by Batcher's odd-even merges: static places only.
+template <int N>
+__device__ __forceinline__ void sort_down(double (&x)[N])
+{
+#pragma unroll
+    for (int p = 1; p < N; p *= 2)
+#pragma unroll
+        for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+            for (int j = q % p; j + q < N; j += 2 * q)
+#pragma unroll
+                for (int i = 0; i < q; ++i)
+                    if (i + j + q < N && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+                        const double a = x[i + j], b = x[i + j + q];
+                        x[i + j] = __builtin_fmax(a, b);
+                        x[i + j + q] = __builtin_fmin(a, b);
+                    }
 }
 
 // x of another lane, so that after the steps 1, 2, 4, ... N / 2 of a reduction its N
@@ -93,12 +118,10 @@ __device__ __forceinline__ T other(T x)
 }
 
 template <int N, int STEP = 1>
-__device__ __forceinline__ unsigned long long max_over(unsigned long long x)
+__device__ __forceinline__ double max_over(double x)
 {
-    if constexpr (STEP < N) {
-        const unsigned long long y = other<STEP>(x);
-        return max_over<N, 2 * STEP>(y > x ? y : x);
-    }
+    if constexpr (STEP < N)
+        return max_over<N, 2 * STEP>(__builtin_fmax(x, other<STEP>(x)));
     return x;
 }
 
@@ -146,53 +169,117 @@ __device__ __forceinline__ void load_logits(const void *logits, bool bf16, bool 
                         : static_cast<const float *>(logits)[at + e0 + v];
 }
 
-// The scores of a token's logits (0 past the last, and where nothing is finite
-// above -inf).
-template <int LPT, int VPL, class T>
-__device__ __forceinline__ void scores(const float (&z)[VPL], bool sigmoid, int e0, int E, T (&p)[VPL])
+// e^x for x <= 0 (and NaN) in fp64, within 2^-50: 2^n e^r with |r| <= ln 2 / 2, e^r by its
+// Taylor sum of degree 13 (the next term is below 2^-57).  Below -700 it is e^-700.
+__device__ __forceinline__ double exp_below(double x)
 {
+    x = x < -700.0 ? -700.0 : x;
+    const double n = __builtin_rint(x * 1.4426950408889634);
+    const double r = __builtin_fma(-n, 1.9082149292705877e-10, __builtin_fma(-n, 0.6931471803691238, x));
+    // the factorials' inverses in scalar registers, or each takes a move of its own
+    double c[12] = {1.0 / 6227020800.0, 1.0 / 479001600.0, 1.0 / 39916800.0, 1.0 / 3628800.0, 1.0 / 362880.0,
+                    1.0 / 40320.0,      1.0 / 5040.0,      1.0 / 720.0,      1.0 / 120.0,     1.0 / 24.0,
+                    1.0 / 6.0,          0.5};
+    double p = c[0];
+#pragma unroll
+    for (int i = 1; i < 12; ++i) {
+        asm("" : "+s"(c[i]));
+        p = __builtin_fma(p, r, c[i]);
+    }
+    p = __builtin_fma(p, r, 1.0);
+    p = __builtin_fma(p, r, 1.0);
+    return __builtin_ldexp(p, (int)n);
+}
+__device__ __forceinline__ float exp_below(float x) { return __expf(x); }
+
+// 1 / x for x in [1, 2^11]: the hardware's reciprocal and two steps of Newton's.
+__device__ __forceinline__ double inverse(double x)
+{
+    double y = __builtin_amdgcn_rcp(x);
+    y = __builtin_fma(__builtin_fma(-x, y, 1.0), y, y);
+    return __builtin_fma(__builtin_fma(-x, y, 1.0), y, y);
+}
+__device__ __forceinline__ float inverse(float x) { return 1.0f / x; }
+
+template <class T>
+__device__ __forceinline__ T sigmoid_of(float z)
+{
+    const T e = exp_below((T)-__builtin_fabsf(z)), y = inverse((T)1 + e);
+    return z < 0.0f ? e * y : y;
+}
+
+// A token's softmax: the largest logit and 1 / sum (0 for a row of -inf alone, whose
+// scores are 0).
+template <class T>
+struct Softmax {
+    float most;
+    T inv;
+    __device__ __forceinline__ T numerator(float z) const
+    {
+        const T e = exp_below((T)z - (T)most);
+        return z == -__builtin_inff() ? (T)0 : e;
+    }
+};
+
+// The scores of a token's logits (0 past the last).
+template <int LPT, int VPL, class T>
+__device__ __forceinline__ Softmax<T> scores(const float (&z)[VPL], bool sigmoid, int e0, int E, T (&p)[VPL])
+{
+    Softmax<T> m = {0.0f, (T)0};
     if (sigmoid) {
 #pragma unroll
         for (int v = 0; v < VPL; ++v) {
-            if constexpr (sizeof(T) == 8) {
-                p[v] = 1.0 / (1.0 + exp(-(double)z[v]));
-                // one at a time: sixteen side by side take more registers than there are
-                __builtin_amdgcn_sched_barrier(0);
-            } else
-                p[v] = 1.0f / (1.0f + __expf(-z[v]));
+            p[v] = sigmoid_of<T>(z[v]);
+            if constexpr (sizeof(T) == 8)  // two at a time: more side by side take more registers than there are
+                if (v & 1)
+                    __builtin_amdgcn_sched_barrier(0);
             if (e0 + v >= E)
                 p[v] = 0;
         }
-        return;
+        return m;
     }
-    float mx = z[0];
+    m.most = z[0];
 #pragma unroll
     for (int v = 1; v < VPL; ++v)
-        mx = fmaxf(mx, z[v]);
-    mx = max_over<LPT>(mx);
+        m.most = fmaxf(m.most, z[v]);
+    m.most = max_over<LPT>(m.most);
     T sum = 0;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
-        if constexpr (sizeof(T) == 8) {
-            p[v] = exp((double)z[v] - (double)mx);
-            __builtin_amdgcn_sched_barrier(0);
-        } else
-            p[v] = __expf(z[v] - mx);
-        // a row of -inf alone has no scores; NaN and inf go on as they are
-        if (mx == -__builtin_inff() && z[v] == mx)
-            p[v] = 0;
+        p[v] = m.numerator(z[v]);
+        if constexpr (sizeof(T) == 8)
+            if (v & 1)
+                __builtin_amdgcn_sched_barrier(0);
         sum += p[v];
     }
     sum = sum_over<LPT>(sum);
-    const T inv = sum > 0 || sum != sum ? (T)1 / sum : (T)0;
+    m.inv = sum == 0 ? (T)0 : inverse(sum);
 #pragma unroll
     for (int v = 0; v < VPL; ++v)
-        p[v] *= inv;
+        p[v] *= m.inv;
+    return m;
+}
+
+// The larger of two pairs' two largest.
+template <class T>
+__device__ __forceinline__ void merge2(T &x, T &y, T x2, T y2)
+{
+    const T lo = x < x2 ? x : x2, hi = y > y2 ? y : y2;
+    x = x > x2 ? x : x2;
+    y = lo > hi ? lo : hi;
+}
+
+// Whether a lane's experts are all of one group, groups being `each` experts long: the
+// groups' best are then found in registers.
+__host__ __device__ __forceinline__ bool in_registers(int each, int vpl)
+{
+    const int l = each / vpl;
+    return each % vpl == 0 && (l & (l - 1)) == 0;
 }
 
 // T: type of the scores, double where the keys are made of them.  LDS: a word an
-// expert, the chosen scores of each token, and with groups each token's keys and
-// its groups' (or, once the tokens are done, the experts' first rows).
+// expert, and where groups need it each token's keys and its groups' (or, once the tokens
+// are done, the experts' first rows).
 template <int LPT, int VPL, class T>
 __global__ __launch_bounds__(512) void route_kernel(const RouteArgs a)
 {
@@ -201,9 +288,14 @@ __global__ __launch_bounds__(512) void route_kernel(const RouteArgs a)
     uint64_t *const word = reinterpret_cast<uint64_t *>(lds);
     char *const own = lds + 8 * E;
     const int sub = threadIdx.x % LPT, slot = threadIdx.x / LPT, e0 = sub * VPL;
+    const int each = E / a.n_groups;
+    const bool groups = a.n_groups > 1, held = in_registers(each, VPL);
     T *const ks = reinterpret_cast<T *>(own) + slot * (LPT * VPL + kMaxGroups);
-    float *const taken = reinterpret_cast<float *>(
-        own + (a.n_groups > 1 ? per * (LPT * VPL + kMaxGroups) * (int)sizeof(T) : 0)) + slot * kMaxTopK;
+    const T low = -__builtin_inff();
+    float b[VPL];
+#pragma unroll
+    for (int v = 0; v < VPL; ++v)
+        b[v] = a.bias && e0 + v < E ? a.bias[e0 + v] : 0.0f;
     for (int e = threadIdx.x; e < E; e += blockDim.x)
         word[e] = 0;
     __syncthreads();
@@ -214,44 +306,78 @@ __global__ __launch_bounds__(512) void route_kernel(const RouteArgs a)
         int id = -1;
         float w = 0.0f;
         if (!(a.active && a.active[t] == 0)) {  // the same in all lanes of a token
-            float z[VPL], s[VPL];
-            unsigned long long key[VPL];
-            load_logits<VPL>(a.logits, a.bf16, a.vec, t * a.ldl, e0, E, z);
-            T p[VPL];
-            scores<LPT, VPL, T>(z, a.sigmoid, e0, E, p);
-            const bool groups = a.n_groups > 1;
+            double key[VPL];
+            Softmax<T> m;
+            T x = low, y = low;  // the lane's two best, for its group
+            {
+                float z[VPL];
+                load_logits<VPL>(a.logits, a.bf16, a.vec, t * a.ldl, e0, E, z);
+                T p[VPL];
+                m = scores<LPT, VPL, T>(z, a.sigmoid, e0, E, p);
+                if (a.bias) {
 #pragma unroll
-            for (int v = 0; v < VPL; ++v) {
-                s[v] = (float)p[v];
-                const int e = e0 + v;
-                T rank = (T)z[v];
-                if constexpr (sizeof(T) == 8) {
-                    if (a.bias)
-                        rank = p[v] + (e < E ? (double)a.bias[e] : 0.0);
-                    key[v] = a.bias ? sortable(rank) : sortable(z[v]);
-                    // value by value, or they take more registers than there are
-                    __builtin_amdgcn_sched_barrier(0);
+                    for (int v = 0; v < VPL; ++v) {
+                        p[v] += (T)b[v];
+                        key[v] = p[v];
+                    }
                 } else {
-                    key[v] = sortable(z[v]);
+#pragma unroll
+                    for (int v = 0; v < VPL; ++v)
+                        key[v] = z[v];
                 }
-                key[v] = e < E ? (key[v] & ~2047ull) | (uint32_t)(1024 - e) : 0ull;
-                if (groups)  // what ranks a group is made of
-                    ks[e] = a.two && !a.bias ? p[v] : rank;
+#pragma unroll
+                for (int v = 0; v < VPL; ++v)
+                    key[v] = e0 + v < E ? key_of(key[v], e0 + v) : -__builtin_inf();
+                // what ranks a group is made of: scores (with their bias), or logits
+                if (groups && held) {
+#pragma unroll
+                    for (int v = 0; v < VPL; ++v) {
+                        const T q = sizeof(T) == 8 ? p[v] : (T)z[v];
+                        merge2(x, y, q == q ? q : low, low);
+                    }
+                } else if (groups) {
+#pragma unroll
+                    for (int v = 0; v < VPL; ++v) {
+                        const T q = sizeof(T) == 8 ? p[v] : (T)z[v];
+                        ks[e0 + v] = q == q ? q : low;
+                    }
+                }
             }
-            if (groups) {
-                // a group's best key, or the sum of its two best
+            if (groups && held) {
+                // over the lanes of a group, then each group against the others
+                const int L = each / VPL, g = sub / L, first = (threadIdx.x & 63) / LPT * LPT;
+                if (L > 1)
+                    merge2(x, y, other<1>(x), other<1>(y));
+                if (L > 2)
+                    merge2(x, y, other<2>(x), other<2>(y));
+                if (L > 4)
+                    merge2(x, y, other<4>(x), other<4>(y));
+                if (L > 8)
+                    merge2(x, y, other<8>(x), other<8>(y));
+                if (L > 16)
+                    merge2(x, y, other<16>(x), other<16>(y));
+                x = a.two && each > 1 ? x + y : x;
+                x = x == x ? x : low;
+                int ahead = 0, o = g;
+                for (int d = 1; d < a.n_groups; ++d) {
+                    o = o + 1 == a.n_groups ? 0 : o + 1;
+                    const T q = __shfl(x, first + o * L, 64);
+                    ahead += q > x || (q == x && o < g) ? 1 : 0;
+                }
+                if (ahead >= a.top_groups) {
+#pragma unroll
+                    for (int v = 0; v < VPL; ++v)
+                        key[v] = -__builtin_inf();
+                }
+            } else if (groups) {
                 wave_order();
-                const int each = E / a.n_groups;
                 T *const best = ks + LPT * VPL;
                 for (int g = sub; g < a.n_groups; g += LPT) {
-                    T x = -__builtin_inff(), y = -__builtin_inff();
-                    for (int i = 0; i < each; ++i) {
-                        const T q = ks[g * each + i];
-                        y = q > x ? x : q > y ? q : y;
-                        x = q > x ? q : x;
-                    }
+                    x = y = low;
+                    for (int i = 0; i < each; ++i)
+                        merge2(x, y, ks[g * each + i], low);
                     x = a.two && each > 1 ? x + y : x;
-                    best[g] = x == x ? x : (T)-__builtin_inff();
+                    best[g] = x == x ? x : low;
                 }
                 wave_order();
                 uint64_t kept = 0;
@@ -276,37 +402,41 @@ __global__ __launch_bounds__(512) void route_kernel(const RouteArgs a)
 #pragma unroll
                 for (int v = 0; v < VPL; ++v) {
                     if (e0 + v < E && !(kept >> g & 1))
-                        key[v] = 0;
+                        key[v] = -__builtin_inf();
                     const bool next = ++in == each;
                     g += next ? 1 : 0;
                     in = next ? 0 : in;
                 }
                 wave_order();  // the keys' LDS is free for the next token
             }
+            sort_down(key);
             for (int j = 0; j < k; ++j) {
-                unsigned long long best = key[0];
+                const double best = max_over<LPT>(key[0]);
+                id = sub == j ? expert_of(best) : id;
+                if (key[0] == best) {
+                    // one lane of the token steps on; a branch, as selects between
+                    // neighbours of an array become a search of all of it
+                    asm volatile("");
 #pragma unroll
-                for (int v = 1; v < VPL; ++v)
-                    best = key[v] > best ? key[v] : best;
-                best = max_over<LPT>(best);
-                const int e = 1024 - (int)(best & 2047);
-                if (e >= e0 && e < e0 + VPL) {  // one lane's: keys differ
-                    float x = 0.0f;
+                    for (int v = 0; v + 1 < (VPL < 8 ? VPL : 8); ++v)
+                        key[v] = key[v + 1];
+                    if (VPL > 8 && k > 8) {
 #pragma unroll
-                    for (int v = 0; v < VPL; ++v) {
-                        x = e0 + v == e ? s[v] : x;
-                        key[v] = e0 + v == e ? 0ull : key[v];
+                        for (int v = 7; v + 1 < VPL; ++v)
+                            key[v] = key[v + 1];
                     }
-                    taken[j] = x;
+                    if (VPL <= 8 || k > 8)
+                        key[VPL - 1] = -__builtin_inf();
                 }
-                id = sub == j ? e : id;
             }
-            wave_order();
-            w = sub < k ? taken[sub] : 0.0f;
+            if (sub < k) {
+                float z[1];
+                load_logits<1>(a.logits, a.bf16, false, t * a.ldl, id, E, z);
+                w = a.sigmoid ? sigmoid_of<float>(z[0]) : (float)(m.numerator(z[0]) * m.inv);
+            }
             if (a.renorm)
                 w = w / (sum_over<LPT>(w) + 1e-20f);
             w *= a.scale;
-            wave_order();
         }
         if (sub < k) {
             a.weights[t * k + sub] = w;
@@ -619,20 +749,39 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const MoveArgs a)
     }
     for (int64_t c = (int64_t)lane * 8; here && c < a.cols; c += 8 * lanes) {
         const int n = (int)(a.cols - c < 8 ? a.cols - c : 8);
-        float dy[8];
+        float dy[8], d[8];
         load8(a.x, true, t * a.ldx + c, a.x_vec && n == 8, n, dy);
-#pragma unroll
-        for (int j = 0; j < K; ++j) {
-            if (row[j] < 0)
-                continue;
-            float e[8], d[8];
-            load8(a.e, true, row[j] * a.lde + c, a.e_vec && n == 8, n, e);
+        auto one = [&](int j, const float (&e)[8]) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 dot[j] = __builtin_fmaf(dy[i], e[i], dot[j]);
                 d[i] = w[j] * dy[i];
             }
             store8(a.out, true, row[j] * a.ldo + c, a.o_vec && n == 8, n, d);
+        };
+        if (a.e_vec && n == 8) {
+            // every row's load before the first store, which could be to a row
+            uint4 raw[K];
+#pragma unroll
+            for (int j = 0; j < K; ++j)
+                raw[j] = row[j] < 0 ? make_uint4(0, 0, 0, 0)
+                                    : *reinterpret_cast<const uint4 *>(a.e + row[j] * a.lde + c);
+#pragma unroll
+            for (int j = 0; j < K; ++j) {
+                float e[8];
+                widen8(raw[j], e);
+                if (row[j] >= 0)
+                    one(j, e);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < K; ++j) {
+                float e[8];
+                if (row[j] < 0)
+                    continue;
+                load8(a.e, true, row[j] * a.lde + c, false, n, e);
+                one(j, e);
+            }
         }
     }
     // lanes of one token: part of a wave, or the whole block
@@ -695,8 +844,9 @@ zero_status check_tokens(int64_t tokens, int32_t top_k)
     return ZERO_OK;
 }
 
-// Lanes a token and experts a lane for E experts.
-template <class F>
+// Lanes a token and experts a lane for E experts: at most MOST a lane while there are
+// lanes.
+template <int MOST = 16, class F>
 void by_experts(int E, F f)
 {
 #define ZS_CASE(L, V) f(std::integral_constant<int, L>{}, std::integral_constant<int, V>{})
@@ -707,17 +857,28 @@ void by_experts(int E, F f)
     else if (E <= 64)
         ZS_CASE(16, 4);
     else if (E <= 128)
-        ZS_CASE(16, 8);
+        ZS_CASE(128 / (MOST < 8 ? MOST : 8), (MOST < 8 ? MOST : 8));
     else if (E <= 256)
-        ZS_CASE(16, 16);
+        ZS_CASE(256 / MOST, MOST);
     else if (E <= 512)
-        ZS_CASE(32, 16);
+        ZS_CASE((MOST < 8 ? 64 : 512 / MOST), (MOST < 8 ? 8 : MOST));
     else
         ZS_CASE(64, 16);
 #undef ZS_CASE
 }
 
-int route_per_block(const zero_router *r) { return r->n_groups > 1 ? kGroupTokens : kRouteTokens; }
+// Whether a router's groups need LDS for every key.
+bool group_keys(const zero_router *r)
+{
+    bool keys = false;
+    if (r->n_groups > 1)
+        by_experts(r->n_experts, [&](auto, auto vc) {
+            keys = !in_registers(r->n_experts / r->n_groups, decltype(vc)::value);
+        });
+    return keys;
+}
+
+int route_per_block(const zero_router *r) { return group_keys(r) ? kGroupTokens : kRouteTokens; }
 int64_t route_blocks(const zero_router *r, int64_t tokens)
 {
     const int n = route_per_block(r);
@@ -827,16 +988,14 @@ zero_status zero_route_forward(const zero_router *r, int64_t tokens, const void 
     (void)hipGetLastError();
     by_experts(E, [&](auto lc, auto vc) {
         constexpr int LPT = decltype(lc)::value, VPL = decltype(vc)::value;
-        // as many threads as the block's tokens keep busy, up to 512, or with
-        // groups 256, whose keys take at most 44 KB
+        // as many threads as the block's tokens keep busy, up to 512, or with groups'
+        // keys, of at most 43 KB, 256
         const int64_t most = tokens < a.per_block ? tokens : a.per_block;
-        const int limit = r->n_groups > 1 ? 256 : 512;
+        const int limit = group_keys(r) ? 256 : 512;
         int threads = 64;
         while (threads < limit && threads / LPT < most)
             threads *= 2;
-        const int per = threads / LPT, es = deep ? 8 : 4;
-        const int keys = r->n_groups > 1 ? per * (LPT * VPL + kMaxGroups) * es : 0;
-        const int own = keys + per * kMaxTopK * 4;
+        const int own = group_keys(r) ? threads / LPT * (LPT * VPL + kMaxGroups) * (deep ? 8 : 4) : 0;
         const size_t lds = 8 * (size_t)E + (size_t)(own > 4 * E ? own : 4 * E);
         if (deep)
             hipLaunchKernelGGL((route_kernel<LPT, VPL, double>), dim3((unsigned)blocks), dim3(threads), lds, s, a);
@@ -884,7 +1043,7 @@ zero_status zero_route_backward(const zero_router *r, int64_t tokens, const void
     a.l_bf16 = logits_dtype == ZERO_BF16, a.d_bf16 = dlogits_dtype == ZERO_BF16;
     a.l_vec = vec16(logits, ldl, bytes_of(logits_dtype)), a.d_vec = vec16(dlogits, ldd, bytes_of(dlogits_dtype));
     (void)hipGetLastError();
-    by_experts(r->n_experts, [&](auto lc, auto vc) {
+    by_experts<8>(r->n_experts, [&](auto lc, auto vc) {
         constexpr int LPT = decltype(lc)::value, VPL = decltype(vc)::value, TPB = 256 / LPT;
         hipLaunchKernelGGL((route_backward_kernel<LPT, VPL>), dim3((unsigned)((tokens + TPB - 1) / TPB)), dim3(256), 0,
                            static_cast<hipStream_t>(stream), a);
