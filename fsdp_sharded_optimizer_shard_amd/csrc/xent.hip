@@ -15,14 +15,20 @@
 // the epilogue turning them into dz of the piece; dW of the piece and the piece's
 // part of dx are products from it.  dz is rounded to bf16, as any linear layer's
 // gradient is where a product reads it: half a step of 2^-8 of each dz, on terms
-// that the sums of dx and dW add with independent errors.  dx adds up over the
-// pieces in fp32 and is rounded once.  Four products of 2 rows x vocab x hidden
-// operations each, with the loss; nothing but them takes time (see the epilogues'
-// shares at zero_linear_xent_*).
+// that the sums of dx and dW add with independent errors.  The target's term, which
+// outweighs the others, would carry the rounding of dloss, the same in every row of a
+// mean; so dz is divided by the mantissa of the first counting row's dloss, which leaves
+// a common dloss a power of two, and dx and dW are multiplied by it in fp32 (100 rows
+// over 50257 words, against 64-bit dx and dW: 3.2e-3 off without, 1.7e-3 with, which is
+// what their own rounding to bf16 makes).  dx adds up over the pieces in fp32 and is
+// rounded once.  Four products of 2 rows x vocab x hidden operations each, with the loss:
+// 8192 tokens, 4096 x 128256, 26.7 ms, 1.29 PF/s, the rate of a plain product of this
+// size; 100 tokens, 768 x 50257, 116 us, most of it one read of W for each product of
+// few tiles.
 //
 // A vocabulary that is no multiple of 8 (stored with the vocabulary as rows) leaves
-// up to 7 columns that the products' 16-byte reads cannot end at: their part of dx
-// and their rows of dW are sums of their own.
+// up to 7 columns that the products' 16-byte reads cannot end at; their part of dx is a
+// sum of its own.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -56,9 +62,28 @@ struct RowLds {
 };
 constexpr int kNoTarget = -(1 << 30);
 
+// The mantissa, in [1, 2), of the first counting row's dloss: every wave for itself.
+// 1 where the first 4096 rows hold none that is a normal number.
+__device__ __forceinline__ float scale_of(const int64_t *targets, const float *dloss, int64_t rows, int64_t vocab)
+{
+    const int64_t end = rows < 4096 ? rows : 4096;
+    for (int64_t r = 0; r < end; r += 64) {
+        const int64_t row = r + (threadIdx.x & 63);
+        const int64_t t = row < end ? targets[row] : -1;
+        const uint32_t u = row < end ? __float_as_uint(dloss[row]) & 0x7fffffffu : 0u;
+        const uint64_t good = __ballot(t >= 0 && t < vocab && u >= 0x00800000u && u < 0x7f800000u);
+        if (good) {
+            const uint32_t m = (uint32_t)__builtin_amdgcn_readlane((int)u, __builtin_ctzll(good));
+            return __uint_as_float((m & 0x7fffffu) | 0x3f800000u);
+        }
+    }
+    return 1.0f;
+}
+
 template <int MODE>
 __device__ __forceinline__ void fetch_rows(const XentArgs &p, int64_t m0, int64_t M, ZS_LDS RowLds *l)
 {
+    const float scale = MODE == kGrad ? scale_of(p.targets, p.dloss, M, p.vocab) : 1.0f;
     for (int i = threadIdx.x; i < kBM; i += kGT) {
         const int64_t row = m0 + i;
         const int64_t t = row < M ? p.targets[row] : -1;
@@ -68,7 +93,7 @@ __device__ __forceinline__ void fetch_rows(const XentArgs &p, int64_t m0, int64_
         l->target[i] = !valid ? kNoTarget : c < -1 || c > 0x3fffffff ? -1 : (int)c;
         if (MODE == kGrad) {
             l->lse[i] = row < M ? p.lse[row] : 0.0f;
-            l->dloss[i] = row < M ? p.dloss[row] : 0.0f;
+            l->dloss[i] = row < M ? p.dloss[row] / scale : 0.0f;
         }
     }
 }
@@ -381,17 +406,19 @@ __global__ __launch_bounds__(kGT) void xent_dx_kernel(int64_t M, int64_t N, int6
     }
 }
 
-// dx (+)= the runs' parts, and the last n < 8 words' dz[r][c] W[c][h].  32 groups of
-// eight values a block, its eight threads a group an eighth of the runs each, added in
+// dx = acc + the runs' parts + the last n < 8 words' dz[r][c] W[c][h], times the scale of
+// dz where `targets` are given.  32 groups of eight values a block, its eight threads a group an eighth of the runs each, added in
 // order.
 __global__ __launch_bounds__(256) void xent_dx_sum_kernel(int64_t rows, int64_t hidden, int runs,
                                                           const float *__restrict__ part, int n,
                                                           const uint16_t *__restrict__ dz, int64_t ldz,
                                                           const uint16_t *__restrict__ w, int64_t ldw,
                                                           const float *acc, int64_t ldacc, void *out, int64_t ldout,
-                                                          bool bf16)
+                                                          bool bf16, const int64_t *targets, const float *dloss,
+                                                          int64_t vocab)
 {
     __shared__ float eighth[8][8][32];
+    const float scale = targets ? scale_of(targets, dloss, rows, vocab) : 1.0f;
     const int g = threadIdx.x & 31, q = threadIdx.x >> 5;
     const int64_t per = hidden / 8, all = rows * per;
     const int each = (runs + 7) / 8, end = (q + 1) * each < runs ? (q + 1) * each : runs;
@@ -430,6 +457,9 @@ __global__ __launch_bounds__(256) void xent_dx_sum_kernel(int64_t rows, int64_t 
                 for (int e = 0; e < 8; ++e)
                     s[e] = __builtin_fmaf(d, x[e], s[e]);
             }
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                s[e] *= scale;
             const uintptr_t at = reinterpret_cast<uintptr_t>(out) + (uintptr_t)(r * ldout + h) * (bf16 ? 2 : 4);
             store8(out, bf16, r * ldout + h, (at & 15) == 0, 8, s);
         }
@@ -437,16 +467,15 @@ __global__ __launch_bounds__(256) void xent_dx_sum_kernel(int64_t rows, int64_t 
     }
 }
 
-// dW of few rows: short sums, so the stores are the work.  128 x 128 tiles, two blocks a
-// CU, so that one block's loads run under the other's stores, which are whole rows of 16
-// bytes a lane.  C = A^T B over K rows; M and N are rounded up to 8, which A and B hold,
-// `m` and `n` are what is stored.
+// dW = A^T B over K rows, times the scale of dz, stored in whole rows of 16 bytes a lane.
+// M and N are rounded up to 8, which A and B hold; `m` and `n` are what is stored.
 template <bool BF16>
 struct StoreEpi {
     ZS_LDS float *lds;
     void *C;
     int64_t ldc, m, n;
     bool vec;
+    float scale;
 
     template <int I, int TM, int TN>
     __device__ __forceinline__ void step(const f32x16 (&acc)[TM][TN], int64_t row0, int64_t col0, int lane) const
@@ -458,7 +487,7 @@ struct StoreEpi {
             for (int j = 0; j < TN; ++j)
 #pragma unroll
                 for (int v = 0; v < 16; ++v)
-                    lds[(8 * (v >> 2) + 4 * fh + (v & 3)) * (CW + 4) + 32 * j + fr] = acc[I][j][v];
+                    lds[(8 * (v >> 2) + 4 * fh + (v & 3)) * (CW + 4) + 32 * j + fr] = acc[I][j][v] * scale;
             wave_lds_order();
             const int64_t col = col0 + 8 * (lane % LPR), left = n - col;
             const int k = left <= 0 ? 0 : left < 8 ? (int)left : 8;
@@ -486,51 +515,29 @@ struct StoreEpi {
     }
 };
 
-template <bool BF16>
-__global__ __launch_bounds__(kGT) void xent_dw_kernel(int64_t M, int64_t N, int64_t K, const uint16_t *__restrict__ A,
-                                                      int64_t lda, const uint16_t *__restrict__ B, int64_t ldb, void *C,
-                                                      int64_t ldc, int64_t m, int64_t n, bool vec, int tiles_m,
-                                                      int tiles_n)
-{
-    ZS_STAGES(128, 128);
-    const StoreEpi<BF16> epi{ZS_CORNER, C, ldc, m, n, vec};
-    int64_t m0, n0;
-    place<128, 128>(tiles_m, tiles_n, tiles_m * tiles_n, m0, n0);
-    gemm_tile<128, 128, true, true>(M, N, K, A, lda, B, ldb, epi, m0, n0, As, Bs);
-}
+struct DwArgs {
+    void *C;
+    int64_t ldc, m, n;
+    const int64_t *targets;
+    const float *dloss;
+    int64_t vocab;
+    bool vec;
+};
 
-// The last n < 8 words' rows of dW: dW[c][h] = sum over r of dz[r][c] x[r][h].  64
-// columns a block, its 16 waves a 16th of the rows each.
-__global__ __launch_bounds__(1024) void xent_tail_dw_kernel(int64_t rows, int64_t hidden, int n,
-                                                            const uint16_t *__restrict__ dz, int64_t ldz,
-                                                            const uint16_t *__restrict__ x, int64_t ldx, void *dw,
-                                                            int64_t lddw, bool bf16)
+// BM: 256 (and halves), or 128 for few rows: short sums, so the stores are the work, and
+// with two blocks a CU one's loads run under the other's stores.
+template <int BM, bool BF16>
+__global__ __launch_bounds__(kGT) void xent_dw_kernel(int64_t M, int64_t N, int64_t K, const uint16_t *__restrict__ A,
+                                                      int64_t lda, const uint16_t *__restrict__ B, int64_t ldb,
+                                                      DwArgs p, int tiles_m, int tiles_n, int n_big)
 {
-    __shared__ float part[16][8][64];
-    const int lane = threadIdx.x & 63, run = threadIdx.x >> 6;
-    const int64_t h = (int64_t)blockIdx.x * 64 + lane;
-    float s[8] = {};
-    if (h < hidden)
-        for (int64_t r = run; r < rows; r += 16) {
-            const float v = bf16_of(x, r * ldx + h);
-#pragma unroll
-            for (int c = 0; c < 7; ++c)
-                s[c] = __builtin_fmaf(c < n ? bf16_of(dz, r * ldz + c) : 0.0f, v, s[c]);
-        }
-#pragma unroll
-    for (int c = 0; c < 7; ++c)
-        part[run][c][lane] = s[c];
-    __syncthreads();
-    if (run >= n || h >= hidden)
-        return;
-    float t = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        t += part[i][run][lane];
-    if (bf16)
-        static_cast<uint16_t *>(dw)[run * lddw + h] = (uint16_t)pack_bf16(t, t);
-    else
-        static_cast<float *>(dw)[run * lddw + h] = t;
+    ZS_STAGES(BM, BM);
+    const StoreEpi<BF16> epi{ZS_CORNER, p.C, p.ldc, p.m, p.n, p.vec, scale_of(p.targets, p.dloss, K, p.vocab)};
+    int64_t m0, n0;
+    if (place<BM, BM>(tiles_m, tiles_n, n_big, m0, n0))
+        gemm_tile<BM, BM, true, true>(M, N, K, A, lda, B, ldb, epi, m0, n0, As, Bs);
+    else if constexpr (BM == kBM)
+        gemm_tile<BM / 2, BM, true, true>(M, N, K, A, lda, B, ldb, epi, m0, n0, As, Bs);
 }
 
 // Columns of a tile: 128 (of 128 rows, two blocks a CU) where 256 x 256 tiles would
@@ -603,44 +610,45 @@ int64_t backward_floats(int64_t rows, int64_t vocab, int64_t hidden, int64_t pie
     return rows * (ldz / 2) + rows * hidden;
 }
 
-// C = A^T B (m x n over `rows` rows), either of whose rows hold up to 7 columns more.
+// dW = A^T B (m x n over `rows` rows), A's rows holding up to 7 columns more.
 zero_status run_dw(int64_t m, int64_t n, int64_t rows, const uint16_t *A, int64_t lda, const uint16_t *B, int64_t ldb,
-                   void *C, int64_t ldc, int32_t c_dtype, hipStream_t s)
+                   void *C, int64_t ldc, int32_t c_dtype, const int64_t *targets, const float *dloss, int64_t vocab,
+                   hipStream_t s)
 {
-    // 100 rows, 50257 x 768: 33 us against 40 of the plain product's 256 x 256 tiles, 33
-    // rows, 4096 x 128256, 385 and 398; 256 rows 48 and 48, 666 and 615; 512 rows 66 and 62.
-    if (rows > 128) {
-        const int64_t m8 = m / 8 * 8;
-        const int tail = (int)(m - m8);
-        const zero_status st = gemm_run(m8, n, rows, A, lda, ZERO_K_OUTER, B, ldb, ZERO_K_OUTER, C, ldc, c_dtype, s);
-        if (st != ZERO_OK || tail == 0)
-            return st;
-        hipLaunchKernelGGL(xent_tail_dw_kernel, dim3((unsigned)((n + 63) / 64)), dim3(1024), 0, s, rows, n, tail, A + m8,
-                           lda, B, ldb, static_cast<char *>(C) + m8 * ldc * bytes_of(c_dtype), ldc,
-                           c_dtype == ZERO_BF16);
-        return launched("linear_xent tail");
-    }
     const int64_t M = (m + 7) / 8 * 8;
-    const Grid g = tiles(M, n, 128, 128, false);
+    const DwArgs p = {C, ldc, m, n, targets, dloss, vocab, vec16(C, ldc, bytes_of(c_dtype))};
     (void)hipGetLastError();
-    if (c_dtype == ZERO_BF16)
-        hipLaunchKernelGGL(xent_dw_kernel<true>, g.grid, dim3(kGT), 0, s, M, n, rows, A, lda, B, ldb, C, ldc, m, n,
-                           vec16(C, ldc, 2), g.tm, g.tn);
-    else
-        hipLaunchKernelGGL(xent_dw_kernel<false>, g.grid, dim3(kGT), 0, s, M, n, rows, A, lda, B, ldb, C, ldc, m, n,
-                           vec16(C, ldc, 4), g.tm, g.tn);
+#define ZS_DW(BM, BF)                                                                              \
+    hipLaunchKernelGGL((xent_dw_kernel<BM, BF>), g.grid, dim3(kGT), 0, s, M, n, rows, A, lda, B, ldb, p, g.tm, g.tn, \
+                       g.n_big)
+    // 100 rows, 50257 x 768: 33 us in 128 x 128 tiles and 40 in 256 x 256 ones, 33 rows, 4096
+    // x 128256, 385 and 398; 256 rows 48 and 48, 666 and 615; 512 rows 66 and 62.
+    if (rows <= 128 || small_tiles(M, n)) {
+        const Grid g = tiles(M, n, 128, 128, false);
+        if (c_dtype == ZERO_BF16)
+            ZS_DW(128, true);
+        else
+            ZS_DW(128, false);
+    } else {
+        const Grid g = tiles(M, n, kBM, kBN, true);
+        if (c_dtype == ZERO_BF16)
+            ZS_DW(kBM, true);
+        else
+            ZS_DW(kBM, false);
+    }
+#undef ZS_DW
     return launched("linear_xent dw");
 }
 
 zero_status sum_dx(int64_t rows, int64_t hidden, int runs, const float *part, int tail, const uint16_t *dz, int64_t ldz,
                    const uint16_t *w, int64_t ldw, const float *acc, int64_t ldacc, void *out, int64_t ldout,
-                   int32_t out_dtype, hipStream_t s)
+                   int32_t out_dtype, const int64_t *targets, const float *dloss, int64_t vocab, hipStream_t s)
 {
     int64_t grid = (rows * (hidden / 8) + 31) / 32;
     grid = grid > 65536 ? 65536 : grid;
     (void)hipGetLastError();
     hipLaunchKernelGGL(xent_dx_sum_kernel, dim3((unsigned)grid), dim3(256), 0, s, rows, hidden, runs, part, tail, dz, ldz,
-                       w, ldw, acc, ldacc, out, ldout, out_dtype == ZERO_BF16);
+                       w, ldw, acc, ldacc, out, ldout, out_dtype == ZERO_BF16, targets, dloss, vocab);
     return launched("linear_xent dx sum");
 }
 
@@ -799,9 +807,12 @@ zero_status xent_backward_run(int64_t rows, int64_t vocab, int64_t hidden, const
             const int64_t dw_cols = outer ? vocab : hidden;
             const bool free = lddw == dw_cols && (!outer || n == vocab) && aligned(dwp, 16);
             const int64_t runs = dx_runs(rows, hidden, n8, free ? n * hidden * es / 4 : 0);
+            // the last piece leaves dx, scaled and in its type
             void *const to = last ? dx : acc;
             const int64_t ldto = last ? lddx : ldacc;
             const int32_t tt = last ? dx_dtype : ZERO_FP32;
+            const int64_t *const scaled = last ? targets : nullptr;
+            const uint16_t *const zt = dz + n8, *const wt = wp + n8 * ldw;
             if (runs > 1) {
                 float *const part = reinterpret_cast<float *>(dwp);
                 const int64_t per = ((n8 + runs - 1) / runs + 63) / 64 * 64, real = (n8 + per - 1) / per;
@@ -815,28 +826,25 @@ zero_status xent_backward_run(int64_t rows, int64_t vocab, int64_t hidden, const
                     hipLaunchKernelGGL((xent_dx_kernel<true>), grid, dim3(kGT), 0, s, rows, hidden, n8, per, dz, ldz, wp,
                                        ldw, part, tm, tn);
                 if ((st = launched("linear_xent dx")) != ZERO_OK ||
-                    (st = sum_dx(rows, hidden, (int)real, part, tail, dz + n8, ldz, wp + n8 * ldw, ldw,
-                                 added ? acc : nullptr, ldacc, to, ldto, tt, s)) != ZERO_OK)
+                    (st = sum_dx(rows, hidden, (int)real, part, tail, zt, ldz, wt, ldw, added ? acc : nullptr, ldacc, to,
+                                 ldto, tt, scaled, dloss, vocab, s)) != ZERO_OK)
                     return st;
             } else {
-                if (tail > 0) {
-                    if ((st = sum_dx(rows, hidden, 0, nullptr, tail, dz + n8, ldz, wp + n8 * ldw, ldw,
-                                     added ? acc : nullptr, ldacc, acc, ldacc, ZERO_FP32, s)) != ZERO_OK)
-                        return st;
-                    added = true;
-                }
                 zero_epilogue ep = {};
                 ep.residual = acc;
                 ep.ldr = ldacc;
                 ep.residual_dtype = ZERO_FP32;
-                if ((st = epilogue_gemm_run(rows, hidden, n8, dz, ldz, ZERO_K_INNER, wp, ldw, w_as_b, to, ldto, tt,
-                                            added ? &ep : nullptr, s)) != ZERO_OK)
+                if ((st = epilogue_gemm_run(rows, hidden, n8, dz, ldz, ZERO_K_INNER, wp, ldw, w_as_b, acc, ldacc,
+                                            ZERO_FP32, added ? &ep : nullptr, s)) != ZERO_OK ||
+                    ((last || tail > 0) &&
+                     (st = sum_dx(rows, hidden, 0, nullptr, tail, zt, ldz, wt, ldw, acc, ldacc, to, ldto, tt, scaled,
+                                  dloss, vocab, s)) != ZERO_OK))
                     return st;
             }
             added = true;
         }
-        st = outer ? run_dw(hidden, n, rows, x, ldx, dz, ldz, dwp, lddw, dw_dtype, s)
-                   : run_dw(n, hidden, rows, dz, ldz, x, ldx, dwp, lddw, dw_dtype, s);
+        st = outer ? run_dw(hidden, n, rows, x, ldx, dz, ldz, dwp, lddw, dw_dtype, targets, dloss, vocab, s)
+                   : run_dw(n, hidden, rows, dz, ldz, x, ldx, dwp, lddw, dw_dtype, targets, dloss, vocab, s);
         if (st != ZERO_OK)
             return st;
     }

@@ -553,16 +553,17 @@ def test_head(case, xt, wt):
     assert host(loss)[(t < 0) | (t >= V)].sum() == 0
     dz = training.xent_dz(z, wlse, t, dl.astype(np.float64))
     p = np.exp(z - wlse[:, None]) * np.where((t >= 0) & (t < V), np.abs(dl), 0)[:, None]
-    # exp by its argument's error, the subtraction, the product, then bf16
-    bdz = p * np.expm1(bz + be[:, None] + (4 * np.abs(z - wlse[:, None]) + 8) * U) + 4 * U * np.abs(dz)
+    # exp by its argument's error, the subtraction, the quotient by dz's scale, the product,
+    # then bf16
+    bdz = p * np.expm1(bz + be[:, None] + (4 * np.abs(z - wlse[:, None]) + 8) * U) + 5 * U * np.abs(dz)
     bdz = stored(dz, bdz, "bf16")
     total = np.abs(dz) + bdz
-    pieces = 2 + -(-V // max(256, piece or V))
+    pieces = 3 + -(-V // max(256, piece or V))        # and the product by the scale
     bx = bdz @ np.abs(w).T + (gamma(V) + pieces * U) * (total @ np.abs(w).T)
     out, want = host(dx), dz @ w.T
     within(out[:, :H], want, stored(want, bx, xt), "dx")
     assert (out[:, H:] == 7.0).all()
-    bw = np.abs(x).T @ bdz + gamma(R) * (np.abs(x).T @ total)
+    bw = np.abs(x).T @ bdz + (gamma(R) + 2 * U) * (np.abs(x).T @ total)
     want = x.T @ dz
     out = host(dw)
     if tied:
