@@ -17,7 +17,7 @@
 // gradient is where a product reads it: half a step of 2^-8 of each dz, on terms
 // that the sums of dx and dW add with independent errors.  The target's term, which
 // outweighs the others, would carry the rounding of dloss, the same in every row of a
-// mean; so dz is divided by the mantissa of the first counting row's dloss, which leaves
+// mean; so dz is divided by the mantissa of a counting row's dloss, which leaves
 // a common dloss a power of two, and dx and dW are multiplied by it in fp32 (100 rows
 // over 50257 words, against 64-bit dx and dW: 3.2e-3 off without, 1.7e-3 with, which is
 // what their own rounding to bf16 makes).  dx adds up over the pieces in fp32 and is
@@ -62,28 +62,48 @@ struct RowLds {
 };
 constexpr int kNoTarget = -(1 << 30);
 
-// The mantissa, in [1, 2), of the first counting row's dloss: every wave for itself.
-// 1 where the first 4096 rows hold none that is a normal number.
-__device__ __forceinline__ float scale_of(const int64_t *targets, const float *dloss, int64_t rows, int64_t vocab)
-{
-    const int64_t end = rows < 4096 ? rows : 4096;
-    for (int64_t r = 0; r < end; r += 64) {
-        const int64_t row = r + (threadIdx.x & 63);
-        const int64_t t = row < end ? targets[row] : -1;
-        const uint32_t u = row < end ? __float_as_uint(dloss[row]) & 0x7fffffffu : 0u;
-        const uint64_t good = __ballot(t >= 0 && t < vocab && u >= 0x00800000u && u < 0x7f800000u);
-        if (good) {
-            const uint32_t m = (uint32_t)__builtin_amdgcn_readlane((int)u, __builtin_ctzll(good));
-            return __uint_as_float((m & 0x7fffffu) | 0x3f800000u);
+// The scale of dz: the mantissa, in [1, 2), of a counting row's dloss, the same row for
+// every wave that asks: the first of 256 that lie evenly over the rows.  1 where none of
+// them counts and has a normal number.  begin() reads, end() waits and decides.
+struct ScaleOf {
+    int64_t t[4], vocab;
+    uint32_t u[4];
+
+    __device__ __forceinline__ void begin(const int64_t *targets, const float *dloss, int64_t rows, int64_t words)
+    {
+        const int64_t step = rows < 512 ? 1 : rows / 256;
+        vocab = words;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int64_t row = (64 * k + (threadIdx.x & 63)) * step;
+            t[k] = row < rows ? targets[row] : -1;
+            u[k] = row < rows ? __float_as_uint(dloss[row]) & 0x7fffffffu : 0u;
         }
     }
-    return 1.0f;
-}
+
+    __device__ __forceinline__ float end() const
+    {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint64_t good = __ballot(t[k] >= 0 && t[k] < vocab && u[k] >= 0x00800000u && u[k] < 0x7f800000u);
+            if (good) {
+                const uint32_t m = (uint32_t)__builtin_amdgcn_readlane((int)u[k], __builtin_ctzll(good));
+                return __uint_as_float((m & 0x7fffffu) | 0x3f800000u);
+            }
+        }
+        return 1.0f;
+    }
+};
 
 template <int MODE>
 __device__ __forceinline__ void fetch_rows(const XentArgs &p, int64_t m0, int64_t M, ZS_LDS RowLds *l)
 {
-    const float scale = MODE == kGrad ? scale_of(p.targets, p.dloss, M, p.vocab) : 1.0f;
+    float scale = 1.0f;
+    if constexpr (MODE == kGrad) {
+        ScaleOf of;
+        of.begin(p.targets, p.dloss, M, p.vocab);
+        scale = of.end();
+    }
     for (int i = threadIdx.x; i < kBM; i += kGT) {
         const int64_t row = m0 + i;
         const int64_t t = row < M ? p.targets[row] : -1;
@@ -407,18 +427,60 @@ __global__ __launch_bounds__(kGT) void xent_dx_kernel(int64_t M, int64_t N, int6
 }
 
 // dx = acc + the runs' parts + the last n < 8 words' dz[r][c] W[c][h], times the scale of
-// dz where `targets` are given.  32 groups of eight values a block, its eight threads a group an eighth of the runs each, added in
-// order.
+// dz where `targets` are given.
+struct DxOut {
+    const uint16_t *dz, *w;
+    int64_t ldz, ldw;
+    const float *acc;
+    int64_t ldacc;
+    void *out;
+    int64_t ldout;
+    const int64_t *targets;
+    const float *dloss;
+    int64_t vocab;
+    int n;
+    bool bf16;
+
+    __device__ __forceinline__ float scale(int64_t rows) const
+    {
+        if (!targets)
+            return 1.0f;
+        ScaleOf of;
+        of.begin(targets, dloss, rows, vocab);
+        return of.end();
+    }
+
+    __device__ __forceinline__ void store(int64_t r, int64_t h, float (&s)[8], float scale) const
+    {
+        float x[8];
+        if (acc) {
+            load8(acc, false, r * ldacc + h, (reinterpret_cast<uintptr_t>(acc + r * ldacc + h) & 15) == 0, 8, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                s[e] += x[e];
+        }
+        for (int c = 0; c < n; ++c) {
+            const float d = bf16_of(dz, r * ldz + c);
+            load8(w, true, c * ldw + h, true, 8, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                s[e] = __builtin_fmaf(d, x[e], s[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            s[e] *= scale;
+        const uintptr_t at = reinterpret_cast<uintptr_t>(out) + (uintptr_t)(r * ldout + h) * (bf16 ? 2 : 4);
+        store8(out, bf16, r * ldout + h, (at & 15) == 0, 8, s);
+    }
+};
+
+// 32 groups of eight values a block, its eight threads a group an eighth of the runs
+// each, added in order.
 __global__ __launch_bounds__(256) void xent_dx_sum_kernel(int64_t rows, int64_t hidden, int runs,
-                                                          const float *__restrict__ part, int n,
-                                                          const uint16_t *__restrict__ dz, int64_t ldz,
-                                                          const uint16_t *__restrict__ w, int64_t ldw,
-                                                          const float *acc, int64_t ldacc, void *out, int64_t ldout,
-                                                          bool bf16, const int64_t *targets, const float *dloss,
-                                                          int64_t vocab)
+                                                          const float *__restrict__ part, DxOut p)
 {
     __shared__ float eighth[8][8][32];
-    const float scale = targets ? scale_of(targets, dloss, rows, vocab) : 1.0f;
+    const float scale = p.scale(rows);
     const int g = threadIdx.x & 31, q = threadIdx.x >> 5;
     const int64_t per = hidden / 8, all = rows * per;
     const int each = (runs + 7) / 8, end = (q + 1) * each < runs ? (q + 1) * each : runs;
@@ -444,26 +506,20 @@ __global__ __launch_bounds__(256) void xent_dx_sum_kernel(int64_t rows, int64_t 
 #pragma unroll
                 for (int k = 1; k < 8; ++k)
                     s[e] += eighth[k][e][g];
-            if (acc) {
-                load8(acc, false, r * ldacc + h, (reinterpret_cast<uintptr_t>(acc + r * ldacc + h) & 15) == 0, 8, x);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    s[e] += x[e];
-            }
-            for (int c = 0; c < n; ++c) {
-                const float d = bf16_of(dz, r * ldz + c);
-                load8(w, true, c * ldw + h, true, 8, x);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    s[e] = __builtin_fmaf(d, x[e], s[e]);
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                s[e] *= scale;
-            const uintptr_t at = reinterpret_cast<uintptr_t>(out) + (uintptr_t)(r * ldout + h) * (bf16 ? 2 : 4);
-            store8(out, bf16, r * ldout + h, (at & 15) == 0, 8, s);
+            p.store(r, h, s, scale);
         }
         __syncthreads();
+    }
+}
+
+// The same of one product, which is in acc: eight values a thread.
+__global__ __launch_bounds__(256) void xent_dx_out_kernel(int64_t rows, int64_t hidden, DxOut p)
+{
+    const float scale = p.scale(rows);
+    const int64_t per = hidden / 8, all = rows * per;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+        float s[8] = {};
+        p.store(i / per, i % per * 8, s, scale);
     }
 }
 
@@ -475,10 +531,11 @@ struct StoreEpi {
     void *C;
     int64_t ldc, m, n;
     bool vec;
-    float scale;
+    ScaleOf of;
 
     template <int I, int TM, int TN>
-    __device__ __forceinline__ void step(const f32x16 (&acc)[TM][TN], int64_t row0, int64_t col0, int lane) const
+    __device__ __forceinline__ void step(const f32x16 (&acc)[TM][TN], int64_t row0, int64_t col0, int lane,
+                                         float scale) const
     {
         if constexpr (I < TM) {
             constexpr int CW = 32 * TN, LPR = CW / 8, RPI = 64 / LPR;
@@ -502,7 +559,7 @@ struct StoreEpi {
                 store8(C, BF16, (row0 + 32 * I + r) * ldc + col, vec && k == 8, k, x);
             }
             wave_lds_order();
-            step<I + 1>(acc, row0, col0, lane);
+            step<I + 1>(acc, row0, col0, lane, scale);
         }
     }
 
@@ -511,7 +568,7 @@ struct StoreEpi {
                                            int lane) const
     {
         __syncthreads();
-        step<0>(acc, row0, col0, lane);
+        step<0>(acc, row0, col0, lane, of.end());
     }
 };
 
@@ -532,7 +589,8 @@ __global__ __launch_bounds__(kGT) void xent_dw_kernel(int64_t M, int64_t N, int6
                                                       DwArgs p, int tiles_m, int tiles_n, int n_big)
 {
     ZS_STAGES(BM, BM);
-    const StoreEpi<BF16> epi{ZS_CORNER, p.C, p.ldc, p.m, p.n, p.vec, scale_of(p.targets, p.dloss, K, p.vocab)};
+    StoreEpi<BF16> epi{ZS_CORNER, p.C, p.ldc, p.m, p.n, p.vec, {}};
+    epi.of.begin(p.targets, p.dloss, K, p.vocab);
     int64_t m0, n0;
     if (place<BM, BM>(tiles_m, tiles_n, n_big, m0, n0))
         gemm_tile<BM, BM, true, true>(M, N, K, A, lda, B, ldb, epi, m0, n0, As, Bs);
@@ -644,11 +702,17 @@ zero_status sum_dx(int64_t rows, int64_t hidden, int runs, const float *part, in
                    const uint16_t *w, int64_t ldw, const float *acc, int64_t ldacc, void *out, int64_t ldout,
                    int32_t out_dtype, const int64_t *targets, const float *dloss, int64_t vocab, hipStream_t s)
 {
-    int64_t grid = (rows * (hidden / 8) + 31) / 32;
-    grid = grid > 65536 ? 65536 : grid;
+    const DxOut p = {dz, w, ldz, ldw, acc, ldacc, out, ldout, targets, dloss, vocab, tail, out_dtype == ZERO_BF16};
+    const int64_t eights = rows * (hidden / 8), each = runs > 0 ? 32 : 256;
+    int64_t grid = (eights + each - 1) / each;
+    // a block's scale, 1 us, before several rounds of it where there is no sum to wait for
+    const int64_t most = runs > 0 ? 65536 : 2048;
+    grid = grid > most ? most : grid;
     (void)hipGetLastError();
-    hipLaunchKernelGGL(xent_dx_sum_kernel, dim3((unsigned)grid), dim3(256), 0, s, rows, hidden, runs, part, tail, dz, ldz,
-                       w, ldw, acc, ldacc, out, ldout, out_dtype == ZERO_BF16, targets, dloss, vocab);
+    if (runs > 0)
+        hipLaunchKernelGGL(xent_dx_sum_kernel, dim3((unsigned)grid), dim3(256), 0, s, rows, hidden, runs, part, p);
+    else
+        hipLaunchKernelGGL(xent_dx_out_kernel, dim3((unsigned)grid), dim3(256), 0, s, rows, hidden, p);
     return launched("linear_xent dx sum");
 }
 

@@ -928,7 +928,7 @@ zero_status zero_experts_combine_backward(int64_t tokens, int32_t top_k, int64_t
    hidden (ZERO_K_INNER, as an embedding does) bf16.  The logits never reach memory.
      lse[r]  = log(sum over c of exp z[r][c]),  loss[r] = lse[r] - z[r][targets[r]];
      dz      = (exp(z - lse) - [c = target]) dloss[r], rounded to bf16 once divided by the
-               mantissa of the first counted dloss, which dx and dw are multiplied by
+               mantissa of a counted row's dloss, which dx and dw are multiplied by
                (a piece of the vocabulary at a time, in the workspace);
      dx      = dz W^T (rows x hidden), dw = x^T dz (as W lies), fp32 sums, bf16 or fp32.
    A target outside [0, vocab) is none: loss 0, no gradient.  hidden and the leading
