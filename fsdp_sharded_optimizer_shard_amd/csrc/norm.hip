@@ -27,17 +27,17 @@ struct Raw8 {
 };
 
 template <bool W>
-__device__ __forceinline__ Raw8<W> raw8(const void *p, bool bf16, int64_t i, bool vec, int n)
+__device__ __forceinline__ Raw8<W> raw8(const void *p, bool bf16, int64_t i, int n)
 {
     Raw8<W> r = {};
     if (n <= 0)
         return r;
-    if (vec && n == 8) {
+    if (n == 8) {
         if (!W || bf16) {
-            r.w[0] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
+            r.w[0] = load16(static_cast<const uint16_t *>(p) + i);
         } else {
-            r.w[0] = *reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + i);
-            r.w[W ? 1 : 0] = *reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + i + 4);
+            r.w[0] = load16(static_cast<const float *>(p) + i);
+            r.w[W ? 1 : 0] = load16(static_cast<const float *>(p) + i + 4);
         }
         return r;
     }
@@ -117,7 +117,6 @@ struct NormArgs {
     float *mean, *rstd;
     float eps, inv_n;
     bool x_bf16, p_bf16, y_bf16;
-    bool x_vec, p_vec, y_vec;
 };
 
 // TPR threads a row, each NC chunks of eight columns, TPR chunks apart.  A block of
@@ -136,7 +135,7 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(const NormArgs p)
     auto fetch = [&](int64_t row) {
 #pragma unroll
         for (int j = 0; j < NC; ++j)
-            raw[j] = raw8<W>(p.x, p.x_bf16, row * p.ldx + (int64_t)(t + j * TPR) * 8, p.x_vec, row < p.rows ? n[j] : 0);
+            raw[j] = raw8<W>(p.x, p.x_bf16, row * p.ldx + (int64_t)(t + j * TPR) * 8, row < p.rows ? n[j] : 0);
     };
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
@@ -147,8 +146,8 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(const NormArgs p)
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
         const int64_t col = (int64_t)(t + j * TPR) * 8;
-        rg[j] = raw8<W>(p.gain, p.p_bf16, col, p.p_vec, p.gain ? n[j] : 0);
-        rb[j] = raw8<W>(p.bias, p.p_bf16, col, p.p_vec, p.bias ? n[j] : 0);
+        rg[j] = raw8<W>(p.gain, p.p_bf16, col, p.gain ? n[j] : 0);
+        rb[j] = raw8<W>(p.bias, p.p_bf16, col, p.bias ? n[j] : 0);
     }
     int turn = 0;
     for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < p.rows; row0 += step, turn ^= 1) {
@@ -190,7 +189,7 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(const NormArgs p)
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 x[j][k] = __builtin_fmaf(x[j][k] * r, p.gain ? gain[k] : 1.0f, bias[k]);
-            store8(p.y, p.y_bf16, row * p.ldy + (int64_t)(t + j * TPR) * 8, p.y_vec && n[j] == 8, n[j], x[j]);
+            store8(p.y, p.y_bf16, row * p.ldy + (int64_t)(t + j * TPR) * 8, n[j] == 8, n[j], x[j]);
         }
     }
 }
@@ -205,7 +204,7 @@ __global__ __launch_bounds__(1024) void norm_forward_long_kernel(const NormArgs 
     auto each = [&](auto f) {
         for (int64_t col = (int64_t)threadIdx.x * 8; col < p.cols; col += 8192) {
             const int n = (int)(p.cols - col < 8 ? p.cols - col : 8);
-            unraw8(raw8<true>(p.x, p.x_bf16, at + col, p.x_vec, n), p.x_bf16, x);
+            unraw8(raw8<true>(p.x, p.x_bf16, at + col, n), p.x_bf16, x);
             f(col, n);
         }
     };
@@ -231,12 +230,12 @@ __global__ __launch_bounds__(1024) void norm_forward_long_kernel(const NormArgs 
     }
     each([&](int64_t col, int n) {
         float gain[8], bias[8];
-        unraw8(raw8<true>(p.gain, p.p_bf16, col, p.p_vec, p.gain ? n : 0), p.p_bf16, gain);
-        unraw8(raw8<true>(p.bias, p.p_bf16, col, p.p_vec, p.bias ? n : 0), p.p_bf16, bias);
+        unraw8(raw8<true>(p.gain, p.p_bf16, col, p.gain ? n : 0), p.p_bf16, gain);
+        unraw8(raw8<true>(p.bias, p.p_bf16, col, p.bias ? n : 0), p.p_bf16, bias);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             x[k] = __builtin_fmaf((x[k] - mu) * r, p.gain ? gain[k] : 1.0f, bias[k]);
-        store8(p.y, p.y_bf16, row * p.ldy + col, p.y_vec && n == 8, n, x);
+        store8(p.y, p.y_bf16, row * p.ldy + col, n == 8, n, x);
     });
 }
 
@@ -249,7 +248,6 @@ struct NormBackArgs {
     float *dgain, *dbias;  // one row of sums a block: gridDim.x x cols each; NULL: left out
     float inv_n;
     bool y_bf16, x_bf16, p_bf16, d_bf16;
-    bool y_vec, x_vec, p_vec, r_vec, d_vec;
 };
 
 // A block of 1024 threads takes rows blockIdx.x, + gridDim.x, ... of groups of
@@ -286,9 +284,9 @@ __global__ __launch_bounds__(kNormThreads) void norm_backward_kernel(const NormB
         for (int j = 0; j < NC; ++j) {
             const int64_t col = (int64_t)(t + j * TPR) * 8;
             const int m = here ? n[j] : 0;
-            ry[j] = raw8<W>(p.dy, p.y_bf16, row * p.ldy + col, p.y_vec, m);
-            rx[j] = raw8<W>(p.x, p.x_bf16, row * p.ldx + col, p.x_vec, m);
-            rr[j] = raw8<W>(p.res, p.d_bf16, row * p.ldr + col, p.r_vec, p.res ? m : 0);
+            ry[j] = raw8<W>(p.dy, p.y_bf16, row * p.ldy + col, m);
+            rx[j] = raw8<W>(p.x, p.x_bf16, row * p.ldx + col, m);
+            rr[j] = raw8<W>(p.res, p.d_bf16, row * p.ldr + col, p.res ? m : 0);
         }
         mu = here ? p.mean[row] : 0.0f;
         r = here ? p.rstd[row] : 0.0f;
@@ -306,7 +304,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_backward_kernel(const NormB
             unraw8(ry[j], p.y_bf16, dy);
             unraw8(rx[j], p.x_bf16, xh[j]);
             unraw8(rr[j], p.d_bf16, res[j]);
-            unraw8(raw8<true>(p.gain, p.p_bf16, (int64_t)(t + j * TPR) * 8, p.p_vec, p.gain ? n[j] : 0), p.p_bf16,
+            unraw8(raw8<true>(p.gain, p.p_bf16, (int64_t)(t + j * TPR) * 8, p.gain ? n[j] : 0), p.p_bf16,
                    gain);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -330,7 +328,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_backward_kernel(const NormB
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 h[j][k] = __builtin_fmaf(rs, __builtin_fmaf(-xh[j][k], s2, h[j][k] - s1), res[j][k]);
-            store8(p.dx, p.d_bf16, row * p.ldd + (int64_t)(t + j * TPR) * 8, p.d_vec && n[j] == 8, n[j], h[j]);
+            store8(p.dx, p.d_bf16, row * p.ldd + (int64_t)(t + j * TPR) * 8, n[j] == 8, n[j], h[j]);
         }
         if constexpr (NC > 1)
             fetch(row + step);
@@ -375,9 +373,9 @@ __global__ __launch_bounds__(1024) void norm_backward_long_kernel(const NormBack
         for (int64_t col = (int64_t)threadIdx.x * 8; col < p.cols; col += 8192) {
             const int n = (int)(p.cols - col < 8 ? p.cols - col : 8);
             float gain[8];
-            unraw8(raw8<true>(p.dy, p.y_bf16, row * p.ldy + col, p.y_vec, n), p.y_bf16, h);
-            unraw8(raw8<true>(p.x, p.x_bf16, row * p.ldx + col, p.x_vec, n), p.x_bf16, xh);
-            unraw8(raw8<true>(p.gain, p.p_bf16, col, p.p_vec, p.gain ? n : 0), p.p_bf16, gain);
+            unraw8(raw8<true>(p.dy, p.y_bf16, row * p.ldy + col, n), p.y_bf16, h);
+            unraw8(raw8<true>(p.x, p.x_bf16, row * p.ldx + col, n), p.x_bf16, xh);
+            unraw8(raw8<true>(p.gain, p.p_bf16, col, p.gain ? n : 0), p.p_bf16, gain);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 xh[k] = k < n ? (xh[k] - mu) * r : 0.0f;
@@ -398,11 +396,11 @@ __global__ __launch_bounds__(1024) void norm_backward_long_kernel(const NormBack
     s2 *= p.inv_n;
     each([&](int64_t col, int n) {
         float res[8];
-        unraw8(raw8<true>(p.res, p.d_bf16, row * p.ldr + col, p.r_vec, p.res ? n : 0), p.d_bf16, res);
+        unraw8(raw8<true>(p.res, p.d_bf16, row * p.ldr + col, p.res ? n : 0), p.d_bf16, res);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             h[k] = __builtin_fmaf(r, __builtin_fmaf(-xh[k], s2, h[k] - s1), res[k]);
-        store8(p.dx, p.d_bf16, row * p.ldd + col, p.d_vec && n == 8, n, h);
+        store8(p.dx, p.d_bf16, row * p.ldd + col, n == 8, n, h);
     });
 }
 
@@ -419,8 +417,8 @@ __global__ __launch_bounds__(64) void norm_columns_kernel(const NormBackArgs p)
     for (int64_t row = blockIdx.y; row < p.rows; row += gridDim.y) {
         const float mu = p.mean[row], r = p.rstd[row];
         float dy[8], x[8];
-        unraw8(raw8<true>(p.dy, p.y_bf16, row * p.ldy + col, p.y_vec, n), p.y_bf16, dy);
-        unraw8(raw8<true>(p.x, p.x_bf16, row * p.ldx + col, p.x_vec, n), p.x_bf16, x);
+        unraw8(raw8<true>(p.dy, p.y_bf16, row * p.ldy + col, n), p.y_bf16, dy);
+        unraw8(raw8<true>(p.x, p.x_bf16, row * p.ldx + col, n), p.x_bf16, x);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             sb[k] += dy[k];
@@ -429,9 +427,9 @@ __global__ __launch_bounds__(64) void norm_columns_kernel(const NormBackArgs p)
     }
     const int64_t at = (int64_t)blockIdx.y * p.cols + col;
     if (p.dgain)
-        store8(p.dgain, false, at, false, n, sg);
+        store8(p.dgain, false, at, n == 8, n, sg);
     if (p.dbias)
-        store8(p.dbias, false, at, false, n, sb);
+        store8(p.dbias, false, at, n == 8, n, sb);
 }
 
 // out[c] = sum of n rows of partial sums, for one or two outputs (blockIdx.y):
@@ -505,7 +503,6 @@ zero_status norm_common(int64_t rows, int64_t cols, const void *x, int64_t ldx, 
     return check_matrix("x", x, ldx, cols, x_dtype);
 }
 
-bool vec_or_null(const void *p) { return aligned(p, 16); }
 
 }  // namespace
 }  // namespace zs
@@ -543,8 +540,6 @@ zero_status zero_layer_norm_forward(int64_t rows, int64_t cols, const void *x, i
     p.x = x, p.ldx = ldx, p.gain = gain, p.bias = bias, p.y = y, p.ldy = ldy;
     p.mean = mean, p.rstd = rstd, p.eps = eps, p.inv_n = (float)(1.0 / (double)cols);
     p.x_bf16 = x_dtype == ZERO_BF16, p.p_bf16 = param_dtype == ZERO_BF16, p.y_bf16 = y_dtype == ZERO_BF16;
-    p.x_vec = vec16(x, ldx, bytes_of(x_dtype)), p.y_vec = vec16(y, ldy, bytes_of(y_dtype));
-    p.p_vec = vec_or_null(gain) && vec_or_null(bias);
     const hipStream_t s = static_cast<hipStream_t>(stream);
     (void)hipGetLastError();
 #define ZS_NORM(THREADS, TPR, NC)                                                                  \
@@ -650,9 +645,6 @@ zero_status zero_layer_norm_backward(int64_t rows, int64_t cols, const void *dy,
     p.mean = mean, p.rstd = rstd, p.dx = dx, p.inv_n = (float)(1.0 / (double)cols);
     p.y_bf16 = dy_dtype == ZERO_BF16, p.x_bf16 = x_dtype == ZERO_BF16;
     p.p_bf16 = param_dtype == ZERO_BF16, p.d_bf16 = dx_dtype == ZERO_BF16;
-    p.y_vec = vec16(dy, lddy, bytes_of(dy_dtype)), p.x_vec = vec16(x, ldx, bytes_of(x_dtype));
-    p.p_vec = vec_or_null(gain), p.r_vec = vec16(residual, ldr, bytes_of(dx_dtype));
-    p.d_vec = vec16(dx, lddx, bytes_of(dx_dtype));
     const int64_t blocks = norm_blocks(rows, cols);
     const bool direct = blocks <= 1;
     float *const pg = !dgain ? nullptr : direct ? dgain : workspace;

@@ -58,7 +58,7 @@ struct RouteArgs {
     int32_t *totals;  // experts
     float scale;
     int32_t n_experts, top_k, n_groups, top_groups, per_block;
-    bool sigmoid, renorm, two, bf16, vec, alone;  // two: a group's two best; alone: one block
+    bool sigmoid, renorm, two, bf16, alone;  // two: a group's two best; alone: one block
 };
 
 // The key of expert e: values that are no number, and infinities, become numbers past
@@ -143,14 +143,14 @@ __device__ __forceinline__ T sum_over(T x)
 
 // VPL neighbouring logits from expert e0 on; -inf past the last.
 template <int VPL>
-__device__ __forceinline__ void load_logits(const void *logits, bool bf16, bool vec, int64_t at, int e0, int E,
+__device__ __forceinline__ void load_logits(const void *logits, bool bf16, int64_t at, int e0, int E,
                                             float (&z)[VPL])
 {
 #pragma unroll
     for (int v = 0; v < VPL; ++v)
         z[v] = -__builtin_inff();
     if constexpr (VPL >= 8) {
-        if (vec && e0 + VPL <= E) {
+        if (e0 + VPL <= E) {
 #pragma unroll
             for (int v = 0; v < VPL; v += 8) {
                 float w[8];
@@ -311,7 +311,7 @@ __global__ __launch_bounds__(512) void route_kernel(const RouteArgs a)
             T x = low, y = low;  // the lane's two best, for its group
             {
                 float z[VPL];
-                load_logits<VPL>(a.logits, a.bf16, a.vec, t * a.ldl, e0, E, z);
+                load_logits<VPL>(a.logits, a.bf16, t * a.ldl, e0, E, z);
                 T p[VPL];
                 m = scores<LPT, VPL, T>(z, a.sigmoid, e0, E, p);
                 if (a.bias) {
@@ -431,7 +431,7 @@ __global__ __launch_bounds__(512) void route_kernel(const RouteArgs a)
             }
             if (sub < k) {
                 float z[1];
-                load_logits<1>(a.logits, a.bf16, false, t * a.ldl, id, E, z);
+                load_logits<1>(a.logits, a.bf16, t * a.ldl, id, E, z);
                 w = a.sigmoid ? sigmoid_of<float>(z[0]) : (float)(m.numerator(z[0]) * m.inv);
             }
             if (a.renorm)
@@ -571,7 +571,7 @@ struct RouteBackArgs {
     void *dlogits;
     float scale;
     int32_t n_experts, top_k;
-    bool sigmoid, renorm, l_bf16, d_bf16, l_vec, d_vec;
+    bool sigmoid, renorm, l_bf16, d_bf16;
 };
 
 // With w_j = scale s_j (/ S, S = sum of the chosen s + 1e-20) and D = dw scale:
@@ -591,7 +591,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteBackArgs
         return;
     float *const ds = scatter[slot];
     float z[VPL], p[VPL];
-    load_logits<VPL>(a.logits, a.l_bf16, a.l_vec, t * a.ldl, e0, E, z);
+    load_logits<VPL>(a.logits, a.l_bf16, t * a.ldl, e0, E, z);
     const int id = sub < k ? a.experts[t * k + sub] : -1;
     const bool chosen = id >= 0 && id < E;
     float d = chosen ? a.dweights[t * k + sub] * a.scale : 0.0f;
@@ -633,7 +633,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteBackArgs
                 w[i] = dz[v + i];
             const int n = E - e0 - v < 8 ? E - e0 - v : 8;
             if (n > 0)
-                store8(a.dlogits, a.d_bf16, at + e0 + v, a.d_vec && n == 8, n, w);
+                store8(a.dlogits, a.d_bf16, at + e0 + v, n == 8, n, w);
         }
     } else {
 #pragma unroll
@@ -662,7 +662,7 @@ struct MoveArgs {
     float *dweights;
     int64_t ldx, lde, ldo, ldy, ldr;
     int32_t top_k, shift;  // 1 << shift lanes a token
-    bool x_vec, e_vec, o_vec, y_vec, r_vec, y_bf16;
+    bool y_bf16;
 };
 
 // Row of choice j of token t, -1 where it is none of the `rows`.
@@ -682,7 +682,7 @@ __global__ __launch_bounds__(256) void dispatch_kernel(const MoveArgs a)
     for (int64_t c = (threadIdx.x & (lanes - 1)) * 8; c < a.cols; c += 8 * lanes) {
         const int n = (int)(a.cols - c < 8 ? a.cols - c : 8);
         float x[8], y[8];
-        load8(a.x, true, t * a.ldx + c, a.x_vec && n == 8, n, x);
+        load8(a.x, true, t * a.ldx + c, n == 8, n, x);
         for (int j = 0; j < a.top_k; ++j) {
             const int64_t r = row_at(a, t, j);
             if (r < 0)
@@ -691,7 +691,7 @@ __global__ __launch_bounds__(256) void dispatch_kernel(const MoveArgs a)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 y[i] = a.weights ? x[i] * w : x[i];
-            store8(a.out, true, r * a.ldo + c, a.o_vec && n == 8, n, y);
+            store8(a.out, true, r * a.ldo + c, n == 8, n, y);
         }
     }
 }
@@ -713,19 +713,19 @@ __global__ __launch_bounds__(256) void combine_kernel(const MoveArgs a)
                 continue;
             const float w = a.weights ? a.weights[t * a.top_k + j] : 1.0f;
             float x[8];
-            load8(a.e, true, r * a.lde + c, a.e_vec && n == 8, n, x);
+            load8(a.e, true, r * a.lde + c, n == 8, n, x);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 s[i] = __builtin_fmaf(w, x[i], s[i]);
         }
         if (a.residual) {
             float x[8];
-            load8(a.residual, true, t * a.ldr + c, a.r_vec && n == 8, n, x);
+            load8(a.residual, true, t * a.ldr + c, n == 8, n, x);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 s[i] += x[i];
         }
-        store8(a.y, a.y_bf16, t * a.ldy + c, a.y_vec && n == 8, n, s);
+        store8(a.y, a.y_bf16, t * a.ldy + c, n == 8, n, s);
     }
 }
 
@@ -750,22 +750,22 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const MoveArgs a)
     for (int64_t c = (int64_t)lane * 8; here && c < a.cols; c += 8 * lanes) {
         const int n = (int)(a.cols - c < 8 ? a.cols - c : 8);
         float dy[8], d[8];
-        load8(a.x, true, t * a.ldx + c, a.x_vec && n == 8, n, dy);
+        load8(a.x, true, t * a.ldx + c, n == 8, n, dy);
         auto one = [&](int j, const float (&e)[8]) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 dot[j] = __builtin_fmaf(dy[i], e[i], dot[j]);
                 d[i] = w[j] * dy[i];
             }
-            store8(a.out, true, row[j] * a.ldo + c, a.o_vec && n == 8, n, d);
+            store8(a.out, true, row[j] * a.ldo + c, n == 8, n, d);
         };
-        if (a.e_vec && n == 8) {
+        if (n == 8) {
             // every row's load before the first store, which could be to a row
             uint4 raw[K];
 #pragma unroll
             for (int j = 0; j < K; ++j)
                 raw[j] = row[j] < 0 ? make_uint4(0, 0, 0, 0)
-                                    : *reinterpret_cast<const uint4 *>(a.e + row[j] * a.lde + c);
+                                    : load16(a.e + row[j] * a.lde + c);
 #pragma unroll
             for (int j = 0; j < K; ++j) {
                 float e[8];
@@ -975,7 +975,6 @@ zero_status zero_route_forward(const zero_router *r, int64_t tokens, const void 
     a.n_experts = r->n_experts, a.top_k = r->top_k, a.n_groups = r->n_groups, a.top_groups = r->top_groups;
     a.scale = r->scale, a.sigmoid = r->score == ZERO_SCORE_SIGMOID, a.renorm = r->renormalize != 0;
     a.two = r->group_best == 2, a.bf16 = logits_dtype == ZERO_BF16;
-    a.vec = vec16(logits, ldl, bytes_of(logits_dtype));
     const int64_t blocks = tokens > 0 ? route_blocks(r, tokens) : 1;
     a.per_block = route_per_block(r);
     a.alone = blocks == 1;
@@ -1041,7 +1040,6 @@ zero_status zero_route_backward(const zero_router *r, int64_t tokens, const void
     a.dlogits = dlogits, a.scale = r->scale, a.n_experts = r->n_experts, a.top_k = r->top_k;
     a.sigmoid = r->score == ZERO_SCORE_SIGMOID, a.renorm = r->renormalize != 0;
     a.l_bf16 = logits_dtype == ZERO_BF16, a.d_bf16 = dlogits_dtype == ZERO_BF16;
-    a.l_vec = vec16(logits, ldl, bytes_of(logits_dtype)), a.d_vec = vec16(dlogits, ldd, bytes_of(dlogits_dtype));
     (void)hipGetLastError();
     by_experts<8>(r->n_experts, [&](auto lc, auto vc) {
         constexpr int LPT = decltype(lc)::value, VPL = decltype(vc)::value, TPB = 256 / LPT;
@@ -1071,7 +1069,6 @@ zero_status zero_experts_dispatch(int64_t tokens, int32_t top_k, int64_t cols, c
     MoveArgs a = {};
     a.tokens = tokens, a.cols = cols, a.rows = rows, a.x = x, a.ldx = ldx, a.out = out, a.ldo = ldo;
     a.rows_of = rows_of, a.weights = weights, a.top_k = top_k, a.shift = lanes_shift(cols);
-    a.x_vec = vec16(x, ldx, 2), a.o_vec = vec16(out, ldo, 2);
     (void)hipGetLastError();
     hipLaunchKernelGGL(dispatch_kernel, dim3(move_grid(tokens, a.shift)), dim3(256), 0,
                        static_cast<hipStream_t>(stream), a);
@@ -1103,7 +1100,6 @@ zero_status zero_experts_combine(int64_t tokens, int32_t top_k, int64_t cols, co
     a.tokens = tokens, a.cols = cols, a.rows = rows, a.e = in, a.lde = ldi, a.y = y, a.ldy = ldy;
     a.rows_of = rows_of, a.weights = weights, a.top_k = top_k, a.shift = lanes_shift(cols);
     a.residual = residual, a.ldr = ldr, a.y_bf16 = y_dtype == ZERO_BF16;
-    a.e_vec = vec16(in, ldi, 2), a.y_vec = vec16(y, ldy, bytes_of(y_dtype)), a.r_vec = vec16(residual, ldr, 2);
     (void)hipGetLastError();
     hipLaunchKernelGGL(combine_kernel, dim3(move_grid(tokens, a.shift)), dim3(256), 0,
                        static_cast<hipStream_t>(stream), a);
@@ -1141,7 +1137,6 @@ zero_status zero_experts_combine_backward(int64_t tokens, int32_t top_k, int64_t
     a.tokens = tokens, a.cols = cols, a.rows = rows, a.x = dy, a.ldx = lddy, a.e = in, a.lde = ldi, a.out = din;
     a.ldo = lddi, a.rows_of = rows_of, a.weights = weights, a.dweights = dweights, a.top_k = top_k;
     a.shift = lanes_shift(cols);
-    a.x_vec = vec16(dy, lddy, 2), a.e_vec = vec16(in, ldi, 2), a.o_vec = vec16(din, lddi, 2);
     const dim3 grid(move_grid(tokens, a.shift));
     const hipStream_t s = static_cast<hipStream_t>(stream);
     (void)hipGetLastError();

@@ -49,7 +49,7 @@ struct Tensor {
     void *m, *v;
     uint8_t *ms, *vs;
     int64_t n, number, tile0;  // elements, the first one's number in the list, first tile
-    int32_t decay, vec;        // vec: 16-byte aligned values and 8-byte aligned codes
+    int32_t decay;
 };
 
 struct TensorArgs {
@@ -224,7 +224,7 @@ __global__ __launch_bounds__(256) void tensors_kernel(const TensorArgs a)
     const int64_t i = ((int64_t)blockIdx.x - t.tile0) * kTensorTile + threadIdx.x * 8;
     const int64_t left = t.n - i;
     const int n = left <= 0 ? 0 : left < 8 ? (int)left : 8;
-    const bool vec = t.vec && n == 8;
+    const bool vec = n == 8;
     float g[8], p[8], m[8], v[8];
     load8(t.grad, a.g_bf16, i, vec, n, g);
     load8(t.master, false, i, vec, n, p);
@@ -305,7 +305,7 @@ __global__ __launch_bounds__(256) void tensors_sum_kernel(const TensorArgs a)
             break;
         const int n = left < 8 ? (int)left : 8;
         float g[8];
-        load8(t.grad, a.g_bf16, i, t.vec && n == 8, n, g);
+        load8(t.grad, a.g_bf16, i, n == 8, n, g);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             s += (double)g[k] * (double)g[k];
@@ -323,7 +323,7 @@ __global__ __launch_bounds__(256) void tensors_sum_kernel(const TensorArgs a)
 // What 8-bit states stand for; `second`: the square, which is v.  Exact in bf16
 // (a root has four bits, its square eight) down to fp32's smallest numbers.
 __global__ __launch_bounds__(256) void state_read_kernel(int64_t n_all, const uint8_t *codes, const uint8_t *scales,
-                                                         bool second, void *out, bool bf16, bool vec)
+                                                         bool second, void *out, bool bf16)
 {
     const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8, left = n_all - i;
     if (left <= 0)
@@ -331,12 +331,12 @@ __global__ __launch_bounds__(256) void state_read_kernel(int64_t n_all, const ui
     const int n = left < 8 ? (int)left : 8;
     const uint32_t b = scales[i >> 5] * 0x01010101u;
     float x[8];
-    decode8(load_bytes8(codes + i, vec && n == 8, n), make_uint2(b, b), x);
+    decode8(load_bytes8(codes + i, n == 8, n), make_uint2(b, b), x);
     if (second)
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             x[k] *= x[k];
-    store8(out, bf16, i, vec && n == 8, n, x);
+    store8(out, bf16, i, n == 8, n, x);
 }
 
 int64_t tensor_tiles(int64_t n, int tile) { return (n + tile - 1) / tile; }
@@ -376,7 +376,7 @@ zero_status check_tensors(int32_t n_tensors, const zero_tensor *ts, int32_t form
 // Launches `go(args, blocks)` for kTensors tensors at a time, the empty ones left
 // out.
 template <class F>
-zero_status each_launch(int32_t n_tensors, const zero_tensor *ts, bool small, int32_t grad_dtype, int tile,
+zero_status each_launch(int32_t n_tensors, const zero_tensor *ts, int32_t grad_dtype, int tile,
                         TensorArgs &a, const char *what, F go)
 {
     constexpr int64_t kMost = int64_t(0xffffffffu) / 256;
@@ -404,9 +404,6 @@ zero_status each_launch(int32_t n_tensors, const zero_tensor *ts, bool small, in
             d.master = t.master, d.grad = t.grad, d.param = t.param, d.m = t.m, d.v = t.v;
             d.ms = t.m_scales, d.vs = t.v_scales, d.n = t.n, d.number = number, d.tile0 = tiles;
             d.decay = t.decay;
-            const int sa = small ? 8 : 16;
-            d.vec = aligned(t.master, 16) && aligned(t.grad, 16) && aligned(t.param, 16) && aligned(t.m, sa) &&
-                    aligned(t.v, sa);
             tiles += tensor_tiles(t.n, tile);
         }
         number += (t.n + 31) / 32 * 32;
@@ -427,7 +424,7 @@ zero_status run_tensors(int32_t n_tensors, const zero_tensor *ts, int32_t format
                         hipStream_t s)
 {
     const bool small = format == ZERO_STATE_E4M3;
-    return each_launch(n_tensors, ts, small, grad_dtype, kTensorTile, a, "adam_tensors",
+    return each_launch(n_tensors, ts, grad_dtype, kTensorTile, a, "adam_tensors",
                        [&](const TensorArgs &args, unsigned blocks) {
                            if (small)
                                hipLaunchKernelGGL(tensors_kernel<true>, dim3(blocks), dim3(256), 0, s, args);
@@ -530,7 +527,7 @@ zero_status zero_tensors_sumsq(int32_t n_tensors, const zero_tensor *tensors, in
     std::memset(&a, 0, offsetof(TensorArgs, t));
     a.sums = partials;
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    return each_launch(n_tensors, tensors, true, grad_dtype, kSumTile, a, "tensors_sumsq",
+    return each_launch(n_tensors, tensors, grad_dtype, kSumTile, a, "tensors_sumsq",
                        [&](const TensorArgs &args, unsigned blocks) {
                            hipLaunchKernelGGL(tensors_sum_kernel, dim3(blocks), dim3(256), 0, s, args);
                        });
@@ -557,8 +554,7 @@ zero_status zero_adam_state_read(int64_t n, const uint8_t *codes, const uint8_t 
         return fail(ZERO_ERR_UNSUPPORTED, "too long for one launch");
     (void)hipGetLastError();
     hipLaunchKernelGGL(state_read_kernel, dim3((unsigned)blocks), dim3(256), 0, static_cast<hipStream_t>(stream), n,
-                       codes, scales, second != 0, out, out_dtype == ZERO_BF16,
-                       aligned(codes, 8) && aligned(out, 16));
+                       codes, scales, second != 0, out, out_dtype == ZERO_BF16);
     return launched("adam_state_read");
 }
 

@@ -1,5 +1,7 @@
 // Eight neighbouring values at a time, in bf16, fp32 or codes: one or two
-// 16-byte (codes: 8-byte) accesses where the address allows, else one by one.
+// 16-byte (codes: 8-byte) accesses where the caller says that all are there, else one
+// by one.  Device memory takes such an access at any element's address (a misaligned one
+// touches one more line), LDS does not.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -8,6 +10,20 @@
 
 namespace zs {
 namespace {
+
+typedef uint32_t Words4 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t Words2 __attribute__((ext_vector_type(2), aligned(1)));
+
+__device__ __forceinline__ uint4 load16(const void *q)
+{
+    const Words4 w = *static_cast<const Words4 *>(q);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ void store16(void *q, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    *static_cast<Words4 *>(q) = Words4{a, b, c, d};
+}
 
 // Two values to bf16, nearest even, the first in the low half: one
 // v_cvt_pk_bf16_f32.  NaN stays NaN.
@@ -29,14 +45,14 @@ __device__ __forceinline__ void widen8(uint4 w, float (&x)[8])
     }
 }
 
-// x[0 .. n) of 8 neighbouring values of dtype DT at element i; `vec`: the
-// address is 16-byte aligned (and n is 8).
+// x[0 .. n) of 8 neighbouring values of dtype DT at element i; `vec`: n is 8, and the
+// values are read at once.
 __device__ __forceinline__ void load8(const void *p, bool bf16, int64_t i, bool vec, int n, float (&x)[8])
 {
     if (bf16) {
         const uint16_t *q = static_cast<const uint16_t *>(p) + i;
         if (vec) {
-            widen8(*reinterpret_cast<const uint4 *>(q), x);
+            widen8(load16(q), x);
         } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -45,10 +61,11 @@ __device__ __forceinline__ void load8(const void *p, bool bf16, int64_t i, bool 
     } else {
         const float *q = static_cast<const float *>(p) + i;
         if (vec) {
-            const float4 a = *reinterpret_cast<const float4 *>(q);
-            const float4 b = *reinterpret_cast<const float4 *>(q + 4);
-            x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-            x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+            const uint4 a = load16(q), b = load16(q + 4);
+            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                x[k] = __uint_as_float(w[k]);
         } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -64,7 +81,7 @@ __device__ __forceinline__ void store8(void *p, bool bf16, int64_t i, bool vec, 
         const uint32_t h[4] = {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
                                pack_bf16(x[6], x[7])};
         if (vec) {
-            *reinterpret_cast<uint4 *>(q) = make_uint4(h[0], h[1], h[2], h[3]);
+            store16(q, h[0], h[1], h[2], h[3]);
         } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -74,8 +91,8 @@ __device__ __forceinline__ void store8(void *p, bool bf16, int64_t i, bool vec, 
     } else {
         float *q = static_cast<float *>(p) + i;
         if (vec) {
-            *reinterpret_cast<float4 *>(q) = make_float4(x[0], x[1], x[2], x[3]);
-            *reinterpret_cast<float4 *>(q + 4) = make_float4(x[4], x[5], x[6], x[7]);
+            store16(q, __float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+            store16(q + 4, __float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
         } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -87,8 +104,10 @@ __device__ __forceinline__ void store8(void *p, bool bf16, int64_t i, bool vec, 
 
 __device__ __forceinline__ uint2 load_bytes8(const uint8_t *q, bool vec, int n)
 {
-    if (vec)
-        return *reinterpret_cast<const uint2 *>(q);
+    if (vec) {
+        const Words2 w = *reinterpret_cast<const Words2 *>(q);
+        return make_uint2(w[0], w[1]);
+    }
     uint32_t w[2] = {0, 0};
 #pragma unroll
     for (int k = 0; k < 8; ++k)
@@ -100,7 +119,7 @@ __device__ __forceinline__ uint2 load_bytes8(const uint8_t *q, bool vec, int n)
 __device__ __forceinline__ void store_bytes8(uint8_t *q, bool vec, int n, uint2 w)
 {
     if (vec) {
-        *reinterpret_cast<uint2 *>(q) = w;
+        *reinterpret_cast<Words2 *>(q) = Words2{w.x, w.y};
         return;
     }
     const uint32_t ww[2] = {w.x, w.y};

@@ -454,7 +454,7 @@ struct DxOut {
     {
         float x[8];
         if (acc) {
-            load8(acc, false, r * ldacc + h, (reinterpret_cast<uintptr_t>(acc + r * ldacc + h) & 15) == 0, 8, x);
+            load8(acc, false, r * ldacc + h, true, 8, x);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 s[e] += x[e];
@@ -469,8 +469,7 @@ struct DxOut {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             s[e] *= scale;
-        const uintptr_t at = reinterpret_cast<uintptr_t>(out) + (uintptr_t)(r * ldout + h) * (bf16 ? 2 : 4);
-        store8(out, bf16, r * ldout + h, (at & 15) == 0, 8, s);
+        store8(out, bf16, r * ldout + h, true, 8, s);
     }
 };
 
@@ -530,7 +529,6 @@ struct StoreEpi {
     ZS_LDS float *lds;
     void *C;
     int64_t ldc, m, n;
-    bool vec;
     ScaleOf of;
 
     template <int I, int TM, int TN>
@@ -556,7 +554,7 @@ struct StoreEpi {
                 const ZS_LDS f32x4 *q = reinterpret_cast<const ZS_LDS f32x4 *>(lds + r * (CW + 4) + 8 * (lane % LPR));
                 const f32x4 lo = q[0], hi = q[1];
                 const float x[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-                store8(C, BF16, (row0 + 32 * I + r) * ldc + col, vec && k == 8, k, x);
+                store8(C, BF16, (row0 + 32 * I + r) * ldc + col, k == 8, k, x);
             }
             wave_lds_order();
             step<I + 1>(acc, row0, col0, lane, scale);
@@ -578,7 +576,6 @@ struct DwArgs {
     const int64_t *targets;
     const float *dloss;
     int64_t vocab;
-    bool vec;
 };
 
 // BM: 256 (and halves), or 128 for few rows: short sums, so the stores are the work, and
@@ -589,7 +586,7 @@ __global__ __launch_bounds__(kGT) void xent_dw_kernel(int64_t M, int64_t N, int6
                                                       DwArgs p, int tiles_m, int tiles_n, int n_big)
 {
     ZS_STAGES(BM, BM);
-    StoreEpi<BF16> epi{ZS_CORNER, p.C, p.ldc, p.m, p.n, p.vec, {}};
+    StoreEpi<BF16> epi{ZS_CORNER, p.C, p.ldc, p.m, p.n, {}};
     epi.of.begin(p.targets, p.dloss, K, p.vocab);
     int64_t m0, n0;
     if (place<BM, BM>(tiles_m, tiles_n, n_big, m0, n0))
@@ -674,7 +671,7 @@ zero_status run_dw(int64_t m, int64_t n, int64_t rows, const uint16_t *A, int64_
                    hipStream_t s)
 {
     const int64_t M = (m + 7) / 8 * 8;
-    const DwArgs p = {C, ldc, m, n, targets, dloss, vocab, vec16(C, ldc, bytes_of(c_dtype))};
+    const DwArgs p = {C, ldc, m, n, targets, dloss, vocab};
     (void)hipGetLastError();
 #define ZS_DW(BM, BF)                                                                              \
     hipLaunchKernelGGL((xent_dw_kernel<BM, BF>), g.grid, dim3(kGT), 0, s, M, n, rows, A, lda, B, ldb, p, g.tm, g.tn, \
