@@ -744,8 +744,16 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const MoveArgs a)
 #pragma unroll
     for (int j = 0; j < K; ++j) {
         dot[j] = 0.0f;
-        row[j] = here && a.cols > 0 && j < a.top_k ? row_at(a, t, j) : -1;
-        w[j] = row[j] >= 0 ? a.weights[t * a.top_k + j] : 0.0f;
+        row[j] = -1;
+        w[j] = 0.0f;
+    }
+    if (here && a.cols > 0) {
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+            if (j < a.top_k) {
+                row[j] = row_at(a, t, j);
+                w[j] = a.weights[t * a.top_k + j];
+            }
     }
     for (int64_t c = (int64_t)lane * 8; here && c < a.cols; c += 8 * lanes) {
         const int n = (int)(a.cols - c < 8 ? a.cols - c : 8);
@@ -760,12 +768,12 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const MoveArgs a)
             store8(a.out, true, row[j] * a.ldo + c, n == 8, n, d);
         };
         if (n == 8) {
-            // every row's load before the first store, which could be to a row
+            // every row's load before the first store, which could be to a row; none's
+            // is one of dy, which is there, so that no branch parts the loads
             uint4 raw[K];
 #pragma unroll
             for (int j = 0; j < K; ++j)
-                raw[j] = row[j] < 0 ? make_uint4(0, 0, 0, 0)
-                                    : load16(a.e + row[j] * a.lde + c);
+                raw[j] = load16(row[j] < 0 ? a.x + t * a.ldx + c : a.e + row[j] * a.lde + c);
 #pragma unroll
             for (int j = 0; j < K; ++j) {
                 float e[8];
