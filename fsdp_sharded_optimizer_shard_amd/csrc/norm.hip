@@ -254,7 +254,8 @@ struct NormBackArgs {
 // RPB rows, TPR threads a row; a thread keeps its columns' sums in registers
 // over all of them, so that a block leaves one row of sums.  The next row's loads
 // go out before the present one's sums meet, where a thread has one chunk (with
-// two the registers do not hold both rows).
+// two the registers do not hold both rows).  4096 rows of 8192 with a residual, 268 MB:
+// 52 us, and 5 for the blocks' sums (a copy of as much: 53).
 constexpr int kNormThreads = 1024;
 constexpr int kNormBlocks = 256;  // one a CU; a fixed number, so that the sums have the same bits everywhere
 

@@ -22,8 +22,8 @@
 // over 50257 words, against 64-bit dx and dW: 3.2e-3 off without, 1.7e-3 with, which is
 // what their own rounding to bf16 makes).  dx adds up over the pieces in fp32 and is
 // rounded once.  Four products of 2 rows x vocab x hidden operations each, with the loss:
-// 8192 tokens, 4096 x 128256, 26.7 ms, 1.29 PF/s, the rate of a plain product of this
-// size; 100 tokens, 768 x 50257, 116 us, most of it one read of W for each product of
+// 4096 tokens, 8192 x 128256, 26.2 ms, 1.31 PF/s, the rate of a plain product of this
+// size; 100 tokens, 768 x 50257, 115 us, most of it one read of W for each product of
 // few tiles.
 //
 // A vocabulary that is no multiple of 8 (stored with the vocabulary as rows) leaves
@@ -511,7 +511,8 @@ __global__ __launch_bounds__(256) void xent_dx_sum_kernel(int64_t rows, int64_t 
     }
 }
 
-// The same of one product, which is in acc: eight values a thread.
+// The same of one product, which is in acc: eight values a thread, 4096 x 8192 in 39 us,
+// 5.2 TB/s (the kernel above, which has one thread in eight for this, 193).
 __global__ __launch_bounds__(256) void xent_dx_out_kernel(int64_t rows, int64_t hidden, DxOut p)
 {
     const float scale = p.scale(rows);

@@ -893,14 +893,16 @@ int64_t zero_route_workspace(const zero_router *router, int64_t tokens);
 /* The gradient of the weights with respect to the logits, the choice held fixed:
    dlogits (tokens x n_experts, bf16 or fp32; it may be logits) from dweights
    (tokens x top_k).  `experts` as zero_route_forward left them; numbers outside
-   [0, n_experts) count as none, and a token without experts has a gradient of 0. */
+   [0, n_experts) count as none, and a token without experts has a gradient of 0.  No
+   expert is named twice for a token. */
 zero_status zero_route_backward(const zero_router *router, int64_t tokens, const void *logits,
                                 int64_t ldl, int32_t logits_dtype, const int32_t *experts,
                                 const float *dweights, void *dlogits, int64_t ldd,
                                 int32_t dlogits_dtype, void *stream);
 
 /* Tokens' rows to their experts and back.  rows_of is tokens x top_k (top_k at most
-   16); numbers outside [0, rows) are none.
+   16); numbers outside [0, rows) are none, and no row is named twice (what dispatch and
+   combine_backward leave in such a row is unspecified).
      dispatch          out[rows_of[t][j]] = w[t][j] x[t]   (bf16; weights NULL: copies).
                        Rows that no token has are left as they were.
      combine           y[t] = sum over j of w[t][j] in[rows_of[t][j]] + residual[t], in
@@ -931,7 +933,8 @@ zero_status zero_experts_combine_backward(int64_t tokens, int32_t top_k, int64_t
                mantissa of a counted row's dloss, which dx and dw are multiplied by
                (a piece of the vocabulary at a time, in the workspace);
      dx      = dz W^T (rows x hidden), dw = x^T dz (as W lies), fp32 sums, bf16 or fp32.
-   A target outside [0, vocab) is none: loss 0, no gradient.  hidden and the leading
+   A target outside [0, vocab) is none: loss 0, dx 0, and a dz of 0 in dw, which makes
+   a row of x that is not finite NaN there all the same.  hidden and the leading
    dimensions of x and W are multiples of 8, a vocabulary stored as columns too; x and
    W 16-byte aligned; limits of zero_gemm_bf16.  loss, lse and dloss are fp32, one a
    row; lse is what the loss left.  piece: words at a time, 0 or a multiple of 256; 0
