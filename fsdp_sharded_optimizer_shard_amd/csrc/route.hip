@@ -22,7 +22,8 @@
 // expert has one 64-bit word in LDS, token i's choices set bit i of their experts'
 // words (an `or`, so their order does not matter), and a choice's place within the
 // block is the number of bits below its own.  The blocks' counts are then summed over
-// the blocks, expert by expert, and over the experts.
+// the blocks, expert by expert, and over the experts: by each block for itself, or in a
+// launch of its own where that is many counts.
 //
 // Memory bounds the moves: a wave or more of lanes per token, 16 bytes a lane, a
 // token read once for all its copies.  8192 tokens of 4096 values to 2 of 8 experts take
@@ -522,6 +523,63 @@ __global__ __launch_bounds__(1024) void route_scan_kernel(int32_t *counts, int32
     }
 }
 
+// The same two steps in one launch, each block summing the counts for itself: 2^shift
+// threads, at least E, read a row of counts, and the block's 1024 >> shift such runs of
+// threads a part of the rows each.
+__global__ __launch_bounds__(1024) void route_order_kernel(const int32_t *counts, const int32_t *experts,
+                                                           int32_t *rows_of, int64_t *offsets, int64_t n,
+                                                           int per_block, int n_blocks, int E, int shift)
+{
+    __shared__ int32_t all[1024], before[1024], first[kMaxExperts], wave_total[16];
+    const int tid = threadIdx.x, e = tid & ((1 << shift) - 1), run = tid >> shift, runs = 1024 >> shift;
+    const int per = (n_blocks + runs - 1) / runs;
+    const int b0 = run * per, b1 = b0 + per < n_blocks ? b0 + per : n_blocks, mine = blockIdx.x;
+    int s = 0, p = 0;
+    if (e < E) {
+#pragma unroll 16
+        for (int b = b0; b < b1; ++b) {
+            const int c = counts[(int64_t)b * E + e];
+            s += c;
+            p += b < mine ? c : 0;
+        }
+    }
+    all[tid] = s;
+    before[tid] = p;
+    __syncthreads();
+    s = p = 0;
+    if (run == 0)
+        for (int i = 0; i < runs; ++i) {
+            s += all[(i << shift) + e];
+            p += before[(i << shift) + e];
+        }
+    int sum = s;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int o = __shfl_up(sum, d, 64);
+        sum += (tid & 63) >= d ? o : 0;
+    }
+    if ((tid & 63) == 63)
+        wave_total[tid >> 6] = sum;
+    __syncthreads();
+    for (int i = 0; i < tid >> 6; ++i)
+        sum += wave_total[i];
+    if (run == 0 && e < E) {
+        first[e] = sum - s + p;
+        if (mine == 0) {
+            offsets[e] = sum - s;
+            if (e == E - 1)
+                offsets[E] = sum;
+        }
+    }
+    __syncthreads();
+    const int64_t i0 = (int64_t)mine * per_block, i1 = i0 + per_block < n ? i0 + per_block : n;
+    for (int64_t i = i0 + tid; i < i1; i += 1024) {
+        const int id = experts[i];
+        if (id >= 0)
+            rows_of[i] += first[id];
+    }
+}
+
 // Adds to every choice's place in its block where its expert's rows of that block
 // begin; the first block leaves the offsets.
 __global__ __launch_bounds__(256) void route_place_kernel(const int32_t *counts, const int32_t *totals,
@@ -1014,6 +1072,17 @@ zero_status zero_route_forward(const zero_router *r, int64_t tokens, const void 
     });
     if ((st = launched("route")) != ZERO_OK || a.alone)
         return st;
+    int shift = 6;
+    while ((1 << shift) < E)
+        ++shift;
+    // One launch or two, us in all: 200 tokens of 64 10.4 and 12.8, 16384 of 64 12.4 and
+    // 15.3, 8192 of 256 19.8 and 21.0; 16384 of 256 23.2 and 23.5, 8192 of 512 35.2 and
+    // 34.9, 32768 of 64 18.4 and 17.5.  So one up to 32 counts a thread.
+    if (blocks << shift <= 32768) {
+        hipLaunchKernelGGL(route_order_kernel, dim3((unsigned)blocks), dim3(1024), 0, s, a.counts, experts, rows_of,
+                           offsets, tokens * r->top_k, a.per_block * r->top_k, (int)blocks, E, shift);
+        return launched("route order");
+    }
     hipLaunchKernelGGL(route_scan_kernel, dim3((unsigned)((E + 15) / 16)), dim3(1024), 0, s, a.counts, a.totals,
                        (int)blocks, E);
     hipLaunchKernelGGL(route_place_kernel, dim3((unsigned)blocks), dim3(256), 0, s, a.counts, a.totals, experts, rows_of,

@@ -311,6 +311,24 @@ def test_route_forward(case, idle):
     within(host(w), ww, 2 * rel.max(1, keepdims=True) * np.abs(ww) + 8 * U * np.abs(ww) + 2.0 ** -120, "weights")
 
 
+@pytest.mark.parametrize("T,E,k,G", [(8192, 256, 8, 1), (8193, 256, 8, 1), (32768, 64, 3, 1), (40000, 8, 2, 1),
+                                     (2048, 1000, 4, 1), (2049, 1000, 4, 1), (8000, 40, 5, 5), (9000, 40, 5, 5)])
+def test_rows_of_many_blocks(T, E, k, G):
+    """The rows' order of the experts chosen, on both sides of the rule for its launches."""
+    z = torch.randn(T, E, device=DEV)
+    z[::2, 0] += 2.0                    # an expert with many rows
+    active = (torch.rand(T, device=DEV) > 0.1).to(torch.uint8)
+    router = zs.Router(E, k, groups=G, top_groups=min(G, 3))
+    ids, w, off, rows, work = new_route(router, T, k)
+    zs.route_forward(router, T, z, E, ids, w, off, rows, work, active=active)
+    torch.cuda.synchronize()
+    ids = ids.cpu().numpy()
+    assert (ids[active.cpu().numpy() == 0] == -1).all() and ids.max() < E
+    woff, wrows = training.rows_by_expert(ids, E)
+    assert np.array_equal(off.cpu().numpy(), woff)
+    assert np.array_equal(rows.cpu().numpy(), wrows)
+
+
 def test_route_ties_masks_and_what_is_not_a_number():
     """Equal logits go to the lowest number, NaN comes last, a row of -inf alone has
     weights of 0, and every token's experts are different ones."""
