@@ -793,6 +793,23 @@ def test_adam_of_more_tensors_than_a_launch_holds(state):
     same_state(out, ref, adam_oracle(ref, sizes, state, CFG, 5, 3, decay, None), state)
 
 
+def test_adam_decay_and_sums_over_launches():
+    """Which tensors decay, and the sum of squares, where the list takes three launches,
+    the last tensor of each and the first of the next unlike."""
+    rng = np.random.default_rng(19)
+    sizes = [int(n) for n in rng.integers(1, 9000, 123)]
+    out, ref = adam_lists(rng, sizes, "fp32", "fp32")
+    decay = [i % 3 != 1 for i in range(len(sizes))]
+    ts = tensor_list(out, "fp32", decay)
+    partials = torch.full((ts.partials_count(),), float("nan"), dtype=torch.float64, device=DEV)
+    zs.tensors_sumsq(ts, partials)
+    zs.adam_tensors(ts, zs.adam_cfg(step=2, **CFG), seed=3)
+    torch.cuda.synchronize()
+    want = sum(float((g.astype(np.float64) ** 2).sum()) for g in ref["grad"])
+    assert abs(float(partials.sum()) / want - 1) < 2.0 ** -40
+    same_state(out, ref, adam_oracle(ref, sizes, "fp32", CFG, 2, 3, decay, None), "fp32")
+
+
 def test_adam_step_has_the_shard_steps_bits():
     """fp32 states: what zero_adam_step gives for the same values."""
     rng = np.random.default_rng(1)
