@@ -102,7 +102,7 @@ struct TensorArgs {
 static_assert(sizeof(TensorArgs) <= 4096, "kernel arguments");
 
 // The tensor that a tile belongs to: a lane looks at one tensor each (a search in steps
-// waits for each of its reads: 12 small tensors 8.3 us, so 7.3).
+// waits for each of its reads: 12 small tensors 8.3 us, so 7.7).
 __device__ __forceinline__ int tensor_of(const TensorArgs &a, int tile)
 {
     const int lane = threadIdx.x & 63;
