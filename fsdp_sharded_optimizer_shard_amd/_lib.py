@@ -1503,15 +1503,18 @@ class TensorList:
             self.set_grads(grads)
 
     def set_grads(self, grads) -> None:
-        """Other gradient tensors for the next steps."""
+        """Other gradient tensors for the next steps.  A list that is refused changes
+        nothing."""
         _need_len("grads", grads, self.n)
         call = _Call()
         call.device = self.device
-        kind = None
+        kind, pointers = None, []
         for i, x in enumerate(grads):
             if kind is None:
                 kind = _dtype_of(x, BF16)
-            self.s[i].grad = call(x, f"gradient of tensor {i}", self.sizes[i], _kind(kind))
+            pointers.append(call(x, f"gradient of tensor {i}", self.sizes[i], _kind(kind)))
+        for d, p in zip(self.s, pointers):
+            d.grad = p
         self.grad_dtype = BF16 if kind is None else kind
         self._keep[1:] = [grads]
 

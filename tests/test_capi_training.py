@@ -487,3 +487,57 @@ def test_tensor_lists_are_checked_once():
         zs.TensorList([host], None, None, [host, host], [host])
     with pytest.raises(ValueError, match="expected 1 entries"):
         zs.TensorList([host], None, None, [host], [host], decay=[True, False])
+
+
+class Stand:
+    """A stand-in for a GPU tensor: what the binding asks of one, and no memory."""
+    is_cuda = True
+
+    def __init__(self, address, n, dtype):
+        self.address, self.n, self.dtype = address, n, dtype
+
+    def numel(self):
+        return self.n
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return 0
+
+    def data_ptr(self):
+        return self.address
+
+
+def stands(first, sizes, dtype=torch.float32):
+    return [Stand(at(first) + (i << 24), n, dtype) for i, n in enumerate(sizes)]
+
+
+def stand_list(sizes, grads):
+    return zs.TensorList(stands(0, sizes), grads, None, stands(2, sizes), stands(3, sizes))
+
+
+def grads_of(tensors):
+    return [tensors.s[i].grad for i in range(tensors.n)], tensors.grad_dtype
+
+
+@pytest.mark.parametrize("wrong", ["short", "type", "host"])
+def test_gradients_that_are_refused_change_nothing(wrong):
+    """The last tensor's gradient is refused: every pointer, and the type, are the old ones."""
+    sizes = [40, 50, 60]
+    old = stands(1, sizes)
+    tensors = stand_list(sizes, old)
+    want = [g.data_ptr() for g in old], zs.FP32
+    assert grads_of(tensors) == want
+    new = stands(4, sizes, torch.bfloat16)
+    new[2] = {"short": Stand(at(5), 59, torch.bfloat16), "type": Stand(at(5), 60, torch.float32),
+              "host": torch.zeros(60, dtype=torch.bfloat16)}[wrong]
+    with pytest.raises(ValueError):
+        tensors.set_grads(new)
+    assert grads_of(tensors) == want
+    with pytest.raises(ValueError, match="expected 3 entries"):
+        tensors.set_grads(new[:2])
+    assert grads_of(tensors) == want
+    new[2] = Stand(at(5), 60, torch.bfloat16)
+    tensors.set_grads(new)
+    assert grads_of(tensors) == ([g.data_ptr() for g in new], zs.BF16)
