@@ -1476,6 +1476,8 @@ class TensorList:
                  "v_scales": none if v_scales is None else v_scales}
         for name, x in lists.items():
             _need_len(name, x, self.n)
+        # the tensors, not the caller's lists, which may change
+        lists = {name: tuple(x) for name, x in lists.items()}
         decay = [True] * self.n if decay is None else decay
         _need_len("decay", decay, self.n)
         self.s = (_Tensor * max(1, self.n))()
@@ -1483,7 +1485,7 @@ class TensorList:
         kinds = {"master": "fp32", "param": "bf16", "m": "fp32", "v": "fp32"}
         if self.state == STATE_E4M3:
             kinds.update({"m": "codes", "v": "codes", "m_scales": "codes", "v_scales": "codes"})
-        self.sizes = [x.numel() for x in masters]
+        self.sizes = [x.numel() for x in lists["master"]]
         for i, size in enumerate(self.sizes):
             d = self.s[i]
             d.n, d.decay = size, int(bool(decay[i]))
@@ -1506,6 +1508,7 @@ class TensorList:
         """Other gradient tensors for the next steps.  A list that is refused changes
         nothing."""
         _need_len("grads", grads, self.n)
+        grads = tuple(grads)
         call = _Call()
         call.device = self.device
         kind, pointers = None, []

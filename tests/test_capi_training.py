@@ -1,8 +1,10 @@
 """Host-side checks of the training operators (no GPU): what each call refuses, with
 which status, before anything is launched.  Addresses are fake, so a check that
 misses would show as a HIP error."""
+import gc
 import os
 import re
+import weakref
 
 import pytest
 import torch
@@ -541,3 +543,26 @@ def test_gradients_that_are_refused_change_nothing(wrong):
     new[2] = Stand(at(5), 60, torch.bfloat16)
     tensors.set_grads(new)
     assert grads_of(tensors) == ([g.data_ptr() for g in new], zs.BF16)
+
+
+def test_tensor_lists_keep_their_tensors():
+    """The caller's own lists may be emptied or filled with others after the call."""
+    sizes = [40, 50]
+    lists = [stands(i, sizes) for i in range(3)] + [stands(i, sizes, torch.uint8) for i in range(3, 7)]
+    lists[1], lists[2] = stands(1, sizes), stands(2, sizes, torch.bfloat16)
+    refs = [weakref.ref(t) for x in lists for t in x]
+    tensors = zs.TensorList(*lists)
+    for x in lists:
+        x.clear()
+    del x
+    gc.collect()
+    assert all(r() is not None for r in refs)
+    more = stands(8, sizes)
+    refs, old = refs + [weakref.ref(t) for t in more], refs[2:4]
+    tensors.set_grads(more)
+    more[:] = [None, None]
+    gc.collect()
+    assert all((r() is None) == (r in old) for r in refs)
+    del tensors
+    gc.collect()
+    assert not any(r() for r in refs)
