@@ -1461,10 +1461,10 @@ def fsdp_head_backward(layout: Layout, unit: int, w_shards, w_order: int, batch:
 
 class TensorList:
     """The tensors of one optimizer step, described once: a list each of masters (fp32),
-    gradients (all bf16 or all fp32; None until set_grads), parameters (bf16, or None), m
-    and v (fp32, or 8-bit codes with m_scales and v_scales), and whether weight decay
-    applies (default: to all).  Tensors are contiguous, of any shape; no two may share
-    memory.  Keeps its buffers alive."""
+    gradients (all bf16 or all fp32; None until set_grads, and for a tensor without
+    elements), parameters (bf16, or None), m and v (fp32, or 8-bit codes with m_scales and
+    v_scales), and whether weight decay applies (default: to all).  Tensors are contiguous,
+    of any shape; no two may share memory.  Keeps its buffers alive."""
     __slots__ = ("s", "n", "state", "grad_dtype", "device", "sizes", "_keep")
 
     def __init__(self, masters, grads, params, m, v, m_scales=None, v_scales=None, decay=None):
@@ -1513,9 +1513,9 @@ class TensorList:
         call.device = self.device
         kind, pointers = None, []
         for i, x in enumerate(grads):
-            if kind is None:
+            if kind is None and x is not None:
                 kind = _dtype_of(x, BF16)
-            pointers.append(call(x, f"gradient of tensor {i}", self.sizes[i], _kind(kind)))
+            pointers.append(call(x, f"gradient of tensor {i}", self.sizes[i], _kind(kind or BF16)))
         for d, p in zip(self.s, pointers):
             d.grad = p
         self.grad_dtype = BF16 if kind is None else kind

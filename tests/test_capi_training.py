@@ -566,3 +566,16 @@ def test_tensor_lists_keep_their_tensors():
     del tensors
     gc.collect()
     assert not any(r() for r in refs)
+
+
+def test_an_empty_tensor_needs_no_gradient():
+    """A rank that holds none of a parameter has no gradient of it; the others' type is the
+    list's."""
+    for first in (True, False):
+        sizes = [0, 40, 0, 50] if first else [40, 0, 50, 0]
+        grads = [Stand(at(4 + i), n, torch.float32) if n else None for i, n in enumerate(sizes)]
+        tensors = stand_list(sizes, grads)
+        assert grads_of(tensors) == ([g and g.data_ptr() for g in grads], zs.FP32)
+    tensors.set_grads([None] * 4)                       # none to keep; a step is refused
+    with pytest.raises(zs.ZeroShardError, match="tensor 0: master, grad"):
+        zs.adam_tensors(tensors, zs.adam_cfg(), stream=0)
