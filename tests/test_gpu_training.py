@@ -933,3 +933,102 @@ def test_captured_adam_steps_follow_their_counter():
     g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(before, out["master"]))
+
+
+# dW without gaps: dx of few rows is then cut into runs of the vocabulary, whose parts lie in
+# dW's memory until dW is written
+PACKED_HEADS = [
+    # rows, vocab, hidden, tied, piece
+    (1, 1024, 8, True, 0), (1, 1032, 8, False, 0), (33, 3079, 264, True, 0),
+    (300, 33288, 40, True, 0), (300, 33288, 40, False, 0), (70, 35003, 72, True, 0),
+    (128, 5128, 136, False, 0),
+    # several pieces, each cut, the last with a tail of 5, 7 and 0 words
+    (520, 23045, 40, True, 8192), (9, 6007, 264, True, 2048), (40, 4096, 200, True, 2048),
+]
+
+
+def dx_runs(R, H, words, room):
+    """How many runs a piece's dx is cut into."""
+    tiles = -(-R // 128) * -(-H // 128)
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    runs = min(2 * cus // tiles, words // 512, room // (R * H))
+    return 1 if 2 * tiles > cus or runs < 2 else runs
+
+
+@pytest.mark.parametrize("case", PACKED_HEADS, ids=lambda c: "-".join(map(str, c)))
+@pytest.mark.parametrize("xt,wt", [("bf16", "fp32"), ("fp32", "bf16"), ("fp32", "fp32"), ("bf16", "bf16")])
+def test_head_with_packed_dw(case, xt, wt):
+    R, V, H, tied, piece = case
+    n = -(-V // piece) if piece else 1
+    words = V if n == 1 else min(piece, -(-(-(-V // n)) // 256) * 256)
+    last, es = V - words * (n - 1), 2 if wt == "bf16" else 4
+    assert dx_runs(R, H, last // 8 * 8, last * H * es // 4) > 1
+    xd, x, wd, w, t, td = head_case(R, V, H, tied, 0)
+    order, ldw = (zs.K_INNER, H) if tied else (zs.K_OUTER, V)
+    work = torch.full((max(zs.linear_xent_workspace(R, V, H), zs.linear_xent_workspace(R, V, H, True, piece)),),
+                      float("nan"), device=DEV)
+    loss, lse = torch.empty(R, device=DEV), torch.empty(R, device=DEV)
+    zs.linear_xent_forward(R, V, H, xd, H, wd, ldw, order, td, loss, lse, work)
+    dl = np.float32(np.random.default_rng(6).standard_normal(R))
+    dx = torch.full((R + 1, H), 7.0, dtype=DT[xt], device=DEV)
+    room = torch.full((V * H + 128,), 7.0, dtype=DT[wt], device=DEV)
+    dw = room[64:64 + V * H]
+    out = []
+    for _ in range(2):
+        zs.linear_xent_backward(R, V, H, xd, H, wd, ldw, order, td, lse, torch.from_numpy(dl).to(DEV), dx, H, dw, ldw,
+                                piece, work)
+        torch.cuda.synchronize()
+        assert (room[:64] == 7.0).all() and (room[64 + V * H:] == 7.0).all() and (dx[R:] == 7.0).all()
+        out.append((dx.clone(), dw.clone()))
+        work.fill_(float("nan"))
+        dw.fill_(float("nan"))
+    assert all(torch.equal(a, b) for a, b in zip(*out))
+    _, wlse, z = training.xent(x, w, t)
+    bz, be, _ = xent_bounds(x, w, z, wlse, t)
+    dz = training.xent_dz(z, wlse, t, dl.astype(np.float64))
+    # dz in bf16 as in test_head; the sums in any order, so also by runs
+    p = np.exp(z - wlse[:, None]) * np.where((t >= 0) & (t < V), np.abs(dl), 0)[:, None]
+    bdz = p * np.expm1(bz + be[:, None] + (4 * np.abs(z - wlse[:, None]) + 8) * U) + 5 * U * np.abs(dz)
+    bdz = stored(dz, bdz, "bf16")
+    total = np.abs(dz) + bdz
+    bx = bdz @ np.abs(w).T + (gamma(V) + (3 + n) * U) * (total @ np.abs(w).T)
+    want = dz @ w.T
+    within(host(out[0][0][:R]), want, stored(want, bx, xt), "dx")
+    bw, want = np.abs(x).T @ bdz + (gamma(R) + 2 * U) * (np.abs(x).T @ total), x.T @ dz
+    want, bw = (want.T, bw.T) if tied else (want, bw)
+    within(host(out[0][1]).reshape(want.shape), want, stored(want, bw, wt), "dw")
+
+
+@pytest.mark.parametrize("tied", [False, True])
+def test_head_as_a_sharded_unit_with_its_dx_by_runs(tied):
+    """A unit long enough for dx to be cut: the bits of the plain call on a packed dW, the
+    padding rows zero."""
+    n, V, H, R = 5, 4104, 72, 50
+    rows, cols = (V, H) if tied else (H, V)
+    assert dx_runs(R, H, V, V * H) > 1
+    L = zs.shard_init_rows("fsdp2", n, 0, [(rows, cols)])
+    Lu, per = L.query(0)["padded_len"], L.shard_len
+    g = torch.Generator(device=DEV).manual_seed(7)
+    w = torch.randn(rows, cols, generator=g, device=DEV).to(torch.bfloat16)
+    flat = torch.zeros(Lu, dtype=torch.bfloat16, device=DEV)
+    flat[:rows * cols] = w.view(-1)
+    shards = [flat[q * per:(q + 1) * per].clone() for q in range(n)]
+    x = torch.randn(R, H, generator=g, device=DEV).to(torch.bfloat16)
+    t = torch.randint(0, V, (R,), generator=g, device=DEV)
+    dl = torch.randn(R, generator=g, device=DEV)
+    order = zs.K_INNER if tied else zs.K_OUTER
+    work = torch.empty(max(zs.linear_xent_workspace(R, V, H), zs.linear_xent_workspace(R, V, H, True)), device=DEV)
+    loss, lse = torch.empty(R, device=DEV), torch.empty(R, device=DEV)
+    zs.linear_xent_forward(R, V, H, x, H, w, cols, order, t, loss, lse, work)
+    full = torch.zeros(Lu, dtype=torch.bfloat16, device=DEV)
+    out = []
+    for unit in (False, True):
+        dx, dw = torch.empty(R, H, dtype=torch.bfloat16, device=DEV), torch.full((Lu,), 9.0, device=DEV)
+        if unit:
+            zs.fsdp_head_backward(L, 0, shards, order, R, x, full, t, lse, dl, dx, dw, 0, work)
+        else:
+            zs.linear_xent_backward(R, V, H, x, H, w, cols, order, t, lse, dl, dx, H, dw, cols, 0, work)
+        torch.cuda.synchronize()
+        out.append((dx, dw))
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(full, flat)
+    assert torch.equal(out[0][1][:rows * cols], out[1][1][:rows * cols]) and not out[1][1][rows * cols:].any()
