@@ -116,7 +116,7 @@ def route_backward(z, kind, ids, dw, renormalize, scale):
     ds = np.zeros_like(p)
     for j in range(ids.shape[1]):
         np.add.at(ds, (np.arange(z.shape[0])[ok[:, j]], at[ok[:, j], j]), d[ok[:, j], j])
-    dz = p * (ds - (d * s).sum(1, keepdims=True)) if kind == "softmax" else ds * p * (1 - p)
+    dz = p * (ds - (d * s).sum(1, keepdims=True)) if kind == "softmax" else ds * p * scores(-z, kind)
     return np.where(ok.any(1, keepdims=True), dz, 0.0)
 
 

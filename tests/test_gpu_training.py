@@ -409,6 +409,40 @@ def test_route_backward(case, dt):
         assert not out[3, :E].any()
 
 
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("E,k", [(12, 3), (64, 6), (200, 4)])
+def test_route_gradient_of_sigmoids_near_their_ends(E, k, renorm):
+    """The slope p (1 - p) has its own relative error at logits of up to +-40, where 1 - p is
+    far below p's rounding: p and 1 - p with a score's error each."""
+    rng = np.random.default_rng(E + k)
+    T = 60
+    zd, z = place(rng.uniform(-40, 40, (T, E)), "fp32")
+    ids = np.stack([rng.permutation(E)[:k] for _ in range(T)])
+    dw = np.float32(rng.standard_normal((T, k)))
+    dz = torch.empty(T, E, device=DEV)
+    zs.route_backward(zs.Router(E, k, "sigmoid", renormalize=renorm, scale=2.0), T, zd, E,
+                      torch.from_numpy(ids.astype(np.int32)).to(DEV), torch.from_numpy(dw).to(DEV), dz, E)
+    torch.cuda.synchronize()
+    want = training.route_backward(z, "sigmoid", ids, dw.astype(np.float64), renorm, 2.0)
+    p, q = training.scores(z, "sigmoid"), training.scores(-z, "sigmoid")
+    s, d = np.take_along_axis(p, ids, 1), np.abs(dw) * 2.0
+    if renorm:
+        S = s.sum(1, keepdims=True) + 1e-20
+        d = (d + (d * s).sum(1, keepdims=True) / S) / S
+    size = np.zeros_like(p)
+    np.put_along_axis(size, ids, d, 1)
+    size *= p * q
+    bound = size * (6 * score_bound(z, "sigmoid").max(1, keepdims=True) + (4 * k + 20) * U) + 2.0 ** -110
+    within(host(dz), want, stored(want, bound, "fp32"), "dlogits")
+    # and at 17, where fp32 rounds p to 1
+    far = torch.full((1, E), 17.0, device=DEV)
+    zs.route_backward(zs.Router(E, 1, "sigmoid", renormalize=False), 1, far, E,
+                      torch.tensor([[2]], dtype=torch.int32, device=DEV), torch.ones(1, device=DEV), dz, E)
+    torch.cuda.synchronize()
+    slope = np.exp(-17.0) / (1 + np.exp(-17.0)) ** 2
+    assert abs(float(dz[0, 2]) / slope - 1) < 2 * (6 * 17 + 24) * U and not dz[0, 3:].any()
+
+
 def test_route_gradient_against_differences():
     rng = np.random.default_rng(2)
     z = rng.standard_normal((3, 9))
