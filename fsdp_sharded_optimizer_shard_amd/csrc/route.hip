@@ -662,14 +662,14 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteBackArgs
         ds[e0 + v] = p[v];
     wave_order();
     const float s = chosen ? ds[id] : 0.0f;
+    const int n_chosen = sum_over<LPT>(chosen ? 1 : 0);
     if (a.renorm) {
         const float total = sum_over<LPT>(s) + 1e-20f;
         const float mean = sum_over<LPT>(d * s) / total;
         // of one expert alone d - mean is d 1e-20 / total, which the difference loses
-        d = !chosen ? 0.0f : k == 1 ? d * (1e-20f / total) / total : (d - mean) / total;
+        d = !chosen ? 0.0f : n_chosen == 1 ? d * (1e-20f / total) / total : (d - mean) / total;
     }
     const float dot = sum_over<LPT>(d * s);
-    const bool any = sum_over<LPT>(chosen ? 1 : 0) > 0;  // a token without experts has no gradient
     wave_order();
 #pragma unroll
     for (int v = 0; v < VPL; ++v)
@@ -678,12 +678,12 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteBackArgs
     if (chosen)
         atomicAdd(&ds[id], d);  // of one token's experts no two are the same
     wave_order();
-    float dz[VPL];
+    float dz[VPL];  // 0 for a token without experts
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
         const float x = ds[e0 + v];
         // 1 - s as the sigmoid of -z: the difference would lose all of it past z = 17
-        dz[v] = !any ? 0.0f : a.sigmoid ? x * (p[v] * sigmoid_of<float>(-z[v])) : p[v] * (x - dot);
+        dz[v] = n_chosen == 0 ? 0.0f : a.sigmoid ? x * (p[v] * sigmoid_of<float>(-z[v])) : p[v] * (x - dot);
     }
     const int64_t at = t * a.ldd;
     if constexpr (VPL >= 8) {

@@ -443,6 +443,31 @@ def test_route_gradient_of_sigmoids_near_their_ends(E, k, renorm):
     assert abs(float(dz[0, 2]) / slope - 1) < 2 * (6 * 17 + 24) * U and not dz[0, 3:].any()
 
 
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [8, 200])
+def test_route_gradient_of_one_choice_left(E, kind):
+    """Choices struck out (experts over their capacity) until one is left, renormalised: that
+    weight is s / (s + 1e-20), whose slope nearly vanishes, and no rounding stands in for
+    it.  Bound: the closed form's, as where one expert is chosen."""
+    rng = np.random.default_rng(E)
+    T, k = 50, 4
+    zd, z = place(rng.standard_normal((T, E)), "fp32")
+    ids = np.stack([rng.permutation(E)[:k] for _ in range(T)])
+    left = rng.integers(0, k, T)
+    ids[np.arange(k) != left[:, None]] = -1
+    ids[::3, 0] = np.where(left[::3] == 0, ids[::3, 0], E)      # a number past the experts is none too
+    dw = np.float32(rng.standard_normal((T, k)))
+    dz = torch.empty(T, E, device=DEV)
+    zs.route_backward(zs.Router(E, k, kind, scale=2.0), T, zd, E, torch.from_numpy(ids.astype(np.int32)).to(DEV),
+                      torch.from_numpy(dw).to(DEV), dz, E)
+    torch.cuda.synchronize()
+    want = training.route_backward(z, kind, ids, dw.astype(np.float64), True, 2.0)
+    ok = (ids >= 0) & (ids < E)
+    s = np.where(ok, np.take_along_axis(training.scores(z, kind), np.where(ok, ids, 0), 1), 0.0).sum(1, keepdims=True)
+    size = np.where(ok, np.abs(dw), 0.0).sum(1, keepdims=True) * 2.0 * 1e-20 / s ** 2
+    within(host(dz), want, size * (6 * score_bound(z, kind).max(1, keepdims=True) + 40 * U) + 2.0 ** -110, "dlogits")
+
+
 def test_route_gradient_against_differences():
     rng = np.random.default_rng(2)
     z = rng.standard_normal((3, 9))
