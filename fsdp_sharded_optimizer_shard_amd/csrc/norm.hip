@@ -467,7 +467,9 @@ __global__ __launch_bounds__(256) void fill_zero_kernel(float *p, int64_t n)
 }
 
 constexpr int64_t kHeld = 16384;  // the longest row that is held in registers
-constexpr int64_t kMaxGrid = int64_t(0xffffffffu) / 1024;
+// Rows: held ones are strided over; of the longer ones each takes a block of 1024, and
+// the dispatch counts threads in 32 bits.
+constexpr int64_t kMaxRows = 0x7fffffff, kMaxLongRows = int64_t(0xffffffffu) / 1024;
 
 // Threads a row of the backward kernel: eight columns each up to 8192.
 int back_tpr(int64_t cols)
@@ -495,8 +497,9 @@ zero_status norm_common(int64_t rows, int64_t cols, const void *x, int64_t ldx, 
         return st;
     if (!known_dtype(x_dtype) || !known_dtype(param_dtype))
         return fail(ZERO_ERR_INVALID_ARG, "unknown dtype (x %d, parameters %d)", x_dtype, param_dtype);
-    if (rows > kMaxGrid)
-        return fail(ZERO_ERR_UNSUPPORTED, "too many rows for one launch");
+    if (rows > (cols > kHeld ? kMaxLongRows : kMaxRows))
+        return fail(ZERO_ERR_UNSUPPORTED, "%lld rows of %lld columns are too many for one launch", (long long)rows,
+                    (long long)cols);
     if (!aligned(gain, bytes_of(param_dtype)) || !aligned(bias, bytes_of(param_dtype)))
         return fail(ZERO_ERR_ALIGNMENT, "gain and bias must be aligned to their type");
     if (rows == 0 || cols == 0)

@@ -823,7 +823,8 @@ zero_status zero_fsdp_experts_backward(const zero_layout *layout, int32_t unit,
        y = (x - mu) r gain + bias.
    x and y bf16 or fp32; gain and bias cols values of param_dtype, each may be NULL
    (1, 0); mean and rstd receive mu and r (fp32, rows each; may be NULL).  y may be
-   x (same type and leading dimension).  eps >= 0. */
+   x (same type and leading dimension).  eps >= 0.  Fewer than 2^31 rows, or 2^22 of
+   more than 16384 columns, here and in the gradient. */
 zero_status zero_layer_norm_forward(int64_t rows, int64_t cols, const void *x, int64_t ldx,
                                     int32_t x_dtype, const void *gain, const void *bias,
                                     int32_t param_dtype, float eps, void *y, int64_t ldy,

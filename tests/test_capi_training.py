@@ -122,6 +122,22 @@ def test_norm_backward_refusals():
     norm_backward(rows=0, dy=None, x=None, mean=None, rstd=None, dx=None, dgain=None, dbias=None, work=None)
 
 
+def test_norm_rows_that_one_launch_has():
+    """Rows that a block strides over are counted in 31 bits; longer ones take a block each, and
+    a launch has 32 bits of threads.  (What comes behind the count is refused, or an
+    accepted call would run on these addresses.)"""
+    forward, backward = refuses(norm_forward, {}), refuses(norm_backward, {})
+    for rows in ((1 << 22) - 1, 1 << 22, (1 << 31) - 1):
+        forward(INV, "y is required", rows=rows, y=None)
+        forward(INV, "y is required", rows=rows, y=None, cols=16384, ldx=16384, ldy=16384)
+        backward(INV, "dy is required", rows=rows, dy=None)
+    long = dict(cols=16385, ldx=16385, ldy=16385)
+    forward(INV, "y is required", rows=(1 << 22) - 1, y=None, **long)
+    forward(UNSUP, "rows", rows=1 << 22, y=None, **long)
+    forward(UNSUP, "rows", rows=1 << 31, y=None)
+    backward(UNSUP, "rows", rows=1 << 31, dy=None)
+
+
 def test_norm_workspace():
     assert zs.layer_norm_workspace(0, 64) == zs.layer_norm_workspace(64, 0) == 0
     assert zs.layer_norm_workspace(1, 8192) == 0        # one block writes the sums itself

@@ -231,6 +231,42 @@ def test_norm_backward_in_place(cols):
         assert all(torch.equal(a, b) for a, b in zip(got, want)), k
 
 
+def test_norm_of_more_rows_than_a_launch_has_blocks():
+    """One row a token and head: past 2^22 rows, forward and backward, against 64 bits.  A
+    thread's sums of dgain and dbias have rows / (256 blocks * 16 rows) terms, then 16
+    rows' and 256 blocks' are added."""
+    rows, cols, eps = (1 << 22) + 70003, 40, 1e-5
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x, dy = (torch.randn(rows, cols, generator=g, device=DEV).to(torch.bfloat16) for _ in range(2))
+    gain, bias = (torch.randn(cols, generator=g, device=DEV) for _ in range(2))
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    mean, rstd = torch.empty(rows, device=DEV), torch.empty(rows, device=DEV)
+    dg, db = torch.empty(cols, device=DEV), torch.empty(cols, device=DEV)
+    work = torch.empty(zs.layer_norm_workspace(rows, cols), device=DEV)
+    zs.layer_norm_forward(rows, cols, x, cols, gain, bias, eps, y, cols, mean, rstd)
+    zs.layer_norm_backward(rows, cols, dy, cols, x, cols, gain, mean, rstd, dx, cols, dg, db, work)
+    torch.cuda.synchronize()
+    ends = torch.cat([torch.arange(0, 500), torch.arange((1 << 22) - 500, (1 << 22) + 500),
+                      torch.arange(rows - 500, rows)]).to(DEV)
+    xe, dye = host(x[ends]), host(dy[ends])
+    gn, bn = host(gain), host(bias)
+    want, wm, wr = training.norm_forward(xe, gn, bn, float(np.float32(eps)))
+    dm, dr = norm_stats(xe, wm, wr, eps)
+    within(host(mean[ends]), wm, dm + U * np.abs(wm), "mean")
+    within(host(rstd[ends]), wr, dr, "rstd")
+    xh = (xe - wm[:, None]) * wr[:, None]
+    bound = (dm[:, None] * wr[:, None] + np.abs(xh) * (dr / wr + 4 * U)[:, None]) * np.abs(gn) + \
+        3 * U * (np.abs(want) + np.abs(bn))
+    within(host(y[ends]), want, stored(want, bound, "bf16"), "y")
+    m, r = host(mean[ends]), host(rstd[ends])
+    want, _, _ = training.norm_backward(dye, xe, gn, m, r, None)
+    within(host(dx[ends]), want, stored(want, norm_back_bound(dye, xe, gn, m, r, None, want), "bf16"), "dx")
+    terms = -(-rows // (256 * 16)) + 16 + 256
+    xh, dyd = (x.double() - mean.double()[:, None]) * rstd.double()[:, None], dy.double()
+    within(host(dg), host((dyd * xh).sum(0)), gamma(terms + 4) * host((dyd * xh).abs().sum(0)), "dgain")
+    within(host(db), host(dyd.sum(0)), gamma(terms + 1) * host(dyd.abs().sum(0)), "dbias")
+
+
 def test_norm_of_nothing():
     dg, db = torch.ones(70, device=DEV), torch.ones(70, device=DEV)
     e = torch.empty(0, 70, dtype=torch.bfloat16, device=DEV)
