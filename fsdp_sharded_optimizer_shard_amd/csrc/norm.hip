@@ -470,6 +470,8 @@ constexpr int64_t kHeld = 16384;  // the longest row that is held in registers
 // Rows: held ones are strided over; of the longer ones each takes a block of 1024, and
 // the dispatch counts threads in 32 bits.
 constexpr int64_t kMaxRows = 0x7fffffff, kMaxLongRows = int64_t(0xffffffffu) / 1024;
+// Columns that norm_sum_kernel's blocks of 1024 threads have, 32 each.
+constexpr int64_t kMaxSumCols = int64_t(0xffffffffu) / 1024 * 32;
 
 // Threads a row of the backward kernel: eight columns each up to 8192.
 int back_tpr(int64_t cols)
@@ -632,6 +634,8 @@ zero_status zero_layer_norm_backward(int64_t rows, int64_t cols, const void *dy,
         (dx == residual && lddx != ldr))
         return fail(ZERO_ERR_INVALID_ARG, "dx in place of another matrix needs its type and leading dimension");
     const int64_t need = dgain || dbias ? zero_layer_norm_workspace(rows, cols) : 0;
+    if (need > 0 && cols > kMaxSumCols)
+        return fail(ZERO_ERR_UNSUPPORTED, "dgain and dbias: %lld columns are too many for one launch", (long long)cols);
     if (need > 0 && (!workspace || n_workspace < need))
         return fail(ZERO_ERR_INVALID_ARG, "dgain and dbias of %lld x %lld need a workspace of %lld floats",
                     (long long)rows, (long long)cols, (long long)need);

@@ -838,7 +838,8 @@ zero_status zero_layer_norm_forward(int64_t rows, int64_t cols, const void *x, i
    and leading dimension).  dgain and dbias may be NULL; either needs `workspace` of
    zero_layer_norm_workspace(rows, cols) floats (at most 512 cols), used until the
    call's work has run: calls that overlap in time, and captured graphs that do, need
-   one each.  The sums run in a fixed order.  rows = 0 writes zeros to both. */
+   one each.  The sums run in a fixed order; over several rows they take fewer than
+   2^27 columns.  rows = 0 writes zeros to both. */
 zero_status zero_layer_norm_backward(int64_t rows, int64_t cols, const void *dy, int64_t lddy,
                                      int32_t dy_dtype, const void *x, int64_t ldx,
                                      int32_t x_dtype, const void *gain, int32_t param_dtype,

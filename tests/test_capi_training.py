@@ -138,6 +138,19 @@ def test_norm_rows_that_one_launch_has():
     backward(UNSUP, "rows", rows=1 << 31, dy=None)
 
 
+def test_norm_columns_that_the_sums_have():
+    """The last launch of dgain and dbias takes 32 threads a column: too many columns are refused
+    before the first."""
+    bad = refuses(norm_backward, {})
+    n = 1 << 27
+    wide = dict(rows=2, cols=n, lddy=n, ldx=n, lddx=n, ldr=n)
+    bad(UNSUP, "columns", **wide)
+    bad(UNSUP, "columns", dgain=None, **wide)
+    bad(INV, "dy is required", dy=None, **wide)
+    n -= 32
+    bad(INV, "workspace", work=None, **dict(rows=2, cols=n, lddy=n, ldx=n, lddx=n, ldr=n))
+
+
 def test_norm_workspace():
     assert zs.layer_norm_workspace(0, 64) == zs.layer_norm_workspace(64, 0) == 0
     assert zs.layer_norm_workspace(1, 8192) == 0        # one block writes the sums itself
