@@ -991,10 +991,35 @@ zero_status check_side(const char *what, const void *p, int64_t ld, int64_t rows
     return check_matrix(what, p, ld, cols, dtype);
 }
 
-unsigned move_grid(int64_t tokens, int shift)
+// Blocks of 256 threads that a launch has: the dispatch counts threads in 32 bits.
+constexpr int64_t kMaxBlocks = int64_t(0xffffffffu) / 256;
+
+// go(args, blocks) for all tokens, as many at a time as a launch has blocks for.
+template <class F>
+zero_status each_launch(MoveArgs a, const char *what, F go)
 {
-    const int per = 256 >> shift;
-    return (unsigned)((tokens + per - 1) / per);
+    const int64_t per = 256 >> a.shift, most = kMaxBlocks * per;
+    const int64_t es = a.y_bf16 ? 2 : 4;
+    (void)hipGetLastError();
+    for (int64_t left = a.tokens; left > 0; left -= most) {
+        a.tokens = left < most ? left : most;
+        go(a, dim3((unsigned)((a.tokens + per - 1) / per)));
+        const zero_status st = launched(what);
+        if (st != ZERO_OK || left <= most)
+            return st;
+        a.rows_of += most * a.top_k;
+        if (a.x)
+            a.x += most * a.ldx;
+        if (a.y)
+            a.y = static_cast<char *>(a.y) + most * a.ldy * es;
+        if (a.residual)
+            a.residual += most * a.ldr;
+        if (a.weights)
+            a.weights += most * a.top_k;
+        if (a.dweights)
+            a.dweights += most * a.top_k;
+    }
+    return ZERO_OK;
 }
 
 }  // namespace
@@ -1150,10 +1175,10 @@ zero_status zero_experts_dispatch(int64_t tokens, int32_t top_k, int64_t cols, c
     MoveArgs a = {};
     a.tokens = tokens, a.cols = cols, a.rows = rows, a.x = x, a.ldx = ldx, a.out = out, a.ldo = ldo;
     a.rows_of = rows_of, a.weights = weights, a.top_k = top_k, a.shift = lanes_shift(cols);
-    (void)hipGetLastError();
-    hipLaunchKernelGGL(dispatch_kernel, dim3(move_grid(tokens, a.shift)), dim3(256), 0,
-                       static_cast<hipStream_t>(stream), a);
-    return launched("experts_dispatch");
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    return each_launch(a, "experts_dispatch", [&](const MoveArgs &m, dim3 grid) {
+        hipLaunchKernelGGL(dispatch_kernel, grid, dim3(256), 0, s, m);
+    });
 }
 
 zero_status zero_experts_combine(int64_t tokens, int32_t top_k, int64_t cols, const uint16_t *in, int64_t ldi,
@@ -1181,10 +1206,10 @@ zero_status zero_experts_combine(int64_t tokens, int32_t top_k, int64_t cols, co
     a.tokens = tokens, a.cols = cols, a.rows = rows, a.e = in, a.lde = ldi, a.y = y, a.ldy = ldy;
     a.rows_of = rows_of, a.weights = weights, a.top_k = top_k, a.shift = lanes_shift(cols);
     a.residual = residual, a.ldr = ldr, a.y_bf16 = y_dtype == ZERO_BF16;
-    (void)hipGetLastError();
-    hipLaunchKernelGGL(combine_kernel, dim3(move_grid(tokens, a.shift)), dim3(256), 0,
-                       static_cast<hipStream_t>(stream), a);
-    return launched("experts_combine");
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    return each_launch(a, "experts_combine", [&](const MoveArgs &m, dim3 grid) {
+        hipLaunchKernelGGL(combine_kernel, grid, dim3(256), 0, s, m);
+    });
 }
 
 zero_status zero_experts_combine_backward(int64_t tokens, int32_t top_k, int64_t cols, const uint16_t *dy,
@@ -1218,20 +1243,19 @@ zero_status zero_experts_combine_backward(int64_t tokens, int32_t top_k, int64_t
     a.tokens = tokens, a.cols = cols, a.rows = rows, a.x = dy, a.ldx = lddy, a.e = in, a.lde = ldi, a.out = din;
     a.ldo = lddi, a.rows_of = rows_of, a.weights = weights, a.dweights = dweights, a.top_k = top_k;
     a.shift = lanes_shift(cols);
-    const dim3 grid(move_grid(tokens, a.shift));
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    (void)hipGetLastError();
-    if (top_k <= 1)
-        hipLaunchKernelGGL(combine_backward_kernel<1>, grid, dim3(256), 0, s, a);
-    else if (top_k <= 2)
-        hipLaunchKernelGGL(combine_backward_kernel<2>, grid, dim3(256), 0, s, a);
-    else if (top_k <= 4)
-        hipLaunchKernelGGL(combine_backward_kernel<4>, grid, dim3(256), 0, s, a);
-    else if (top_k <= 8)
-        hipLaunchKernelGGL(combine_backward_kernel<8>, grid, dim3(256), 0, s, a);
-    else
-        hipLaunchKernelGGL(combine_backward_kernel<16>, grid, dim3(256), 0, s, a);
-    return launched("experts_combine_backward");
+    return each_launch(a, "experts_combine_backward", [&](const MoveArgs &m, dim3 grid) {
+        if (top_k <= 1)
+            hipLaunchKernelGGL(combine_backward_kernel<1>, grid, dim3(256), 0, s, m);
+        else if (top_k <= 2)
+            hipLaunchKernelGGL(combine_backward_kernel<2>, grid, dim3(256), 0, s, m);
+        else if (top_k <= 4)
+            hipLaunchKernelGGL(combine_backward_kernel<4>, grid, dim3(256), 0, s, m);
+        else if (top_k <= 8)
+            hipLaunchKernelGGL(combine_backward_kernel<8>, grid, dim3(256), 0, s, m);
+        else
+            hipLaunchKernelGGL(combine_backward_kernel<16>, grid, dim3(256), 0, s, m);
+    });
 }
 
 }  // extern "C"

@@ -608,6 +608,46 @@ def test_gradient_of_the_way_back(T, k, cols, pad):
     assert torch.equal(dw, dw2) and torch.equal(de[used, :cols], ed[used, :cols])
 
 
+def test_moves_of_more_tokens_than_a_launch_has_blocks():
+    """Over 1024 columns a token takes a block of 256 threads, and a launch has 32 bits of them:
+    tokens on both sides of the 2^24th, all others without a row.  35 GB."""
+    T, k, cols, R = (1 << 24) + 1000, 2, 1032, 16
+    t = torch.tensor([0, 5, (1 << 24) - 3, (1 << 24) - 2, (1 << 24) - 1, 1 << 24, (1 << 24) + 1, T - 1], device=DEV)
+    rng = np.random.default_rng(0)
+    to = torch.full((T, k), -1, dtype=torch.int32, device=DEV)
+    rows = rng.permutation(R).reshape(t.numel(), k)
+    to[t] = torch.from_numpy(rows.astype(np.int32)).to(DEV)
+    w = torch.full((T, k), float("nan"), device=DEV)
+    wd, wv = vector(rng.standard_normal(R), "fp32")
+    w[t], wv = wd.view(-1, k), wv.reshape(-1, k)
+    xd, x = place(rng.standard_normal((t.numel(), cols)), "bf16")
+    ed, e = place(rng.standard_normal((R, cols)), "bf16")
+    big = torch.zeros(T, cols, dtype=torch.bfloat16, device=DEV)
+    big[t] = xd
+    out = torch.full((R, cols), 7.0, dtype=torch.bfloat16, device=DEV)
+    zs.experts_dispatch(T, k, cols, big, cols, to, R, out, cols, weights=w)
+    want = np.empty((R, cols))
+    want[rows] = wv[:, :, None] * x[:, None]
+    within(host(out), want, stored(want, U * np.abs(want), "bf16"), "rows")
+    de, dw = torch.full((R, cols), 7.0, dtype=torch.bfloat16, device=DEV), torch.full((T, k), 9.0, device=DEV)
+    zs.experts_combine_backward(T, k, cols, big, cols, R, to, w, ed, cols, de, cols, dw)
+    assert torch.equal(de, out)
+    terms = x[:, None] * e[rows]
+    within(host(dw[t]), terms.sum(2), gamma(cols) * np.abs(terms).sum(2) + TINY, "dw")
+    dw[t] = 0.0
+    assert not dw.any()
+    # in place of the residual: every other token's row stays
+    zs.experts_combine(T, k, cols, ed, cols, R, to, big, cols, weights=w, residual=big, ldr=cols)
+    terms = wv[:, :, None] * e[rows]
+    want = terms.sum(1) + x
+    within(host(big[t]), want, stored(want, gamma(k + 2) * (np.abs(terms).sum(1) + np.abs(x)), "bf16"), "y")
+    big[t] = 0.0
+    torch.cuda.synchronize()
+    assert not any(part.any() for part in big.split(1 << 20))
+    del big
+    torch.cuda.empty_cache()
+
+
 # ------------------------------------------------------------------- head --
 
 HEADS = [
