@@ -949,6 +949,8 @@ bool group_keys(const zero_router *r)
 }
 
 int route_per_block(const zero_router *r) { return group_keys(r) ? kGroupTokens : kRouteTokens; }
+// Threads of a full block: with groups' keys, of at most 43 KB, 256.
+int route_threads(const zero_router *r) { return group_keys(r) ? 256 : 512; }
 int64_t route_blocks(const zero_router *r, int64_t tokens)
 {
     const int n = route_per_block(r);
@@ -991,14 +993,14 @@ zero_status check_side(const char *what, const void *p, int64_t ld, int64_t rows
     return check_matrix(what, p, ld, cols, dtype);
 }
 
-// Blocks of 256 threads that a launch has: the dispatch counts threads in 32 bits.
-constexpr int64_t kMaxBlocks = int64_t(0xffffffffu) / 256;
+// The dispatch counts a launch's threads in 32 bits.
+constexpr int64_t kMaxThreads = 0xffffffffu;
 
 // go(args, blocks) for all tokens, as many at a time as a launch has blocks for.
 template <class F>
 zero_status each_launch(MoveArgs a, const char *what, F go)
 {
-    const int64_t per = 256 >> a.shift, most = kMaxBlocks * per;
+    const int64_t per = 256 >> a.shift, most = kMaxThreads / 256 * per;
     const int64_t es = a.y_bf16 ? 2 : 4;
     (void)hipGetLastError();
     for (int64_t left = a.tokens; left > 0; left -= most) {
@@ -1054,6 +1056,8 @@ zero_status zero_route_forward(const zero_router *r, int64_t tokens, const void 
     if (!aligned(offsets, 8) || !aligned(experts, 4) || !aligned(weights, 4) || !aligned(rows_of, 4) ||
         !aligned(bias, 4) || !aligned(workspace, 4))
         return fail(ZERO_ERR_ALIGNMENT, "a routing buffer is misaligned");
+    if (route_blocks(r, tokens) > kMaxThreads / route_threads(r))
+        return fail(ZERO_ERR_UNSUPPORTED, "%lld tokens are too many for one launch", (long long)tokens);
     const int64_t need = zero_route_workspace(r, tokens);
     if (need > 0 && (!workspace || n_workspace < need))
         return fail(ZERO_ERR_INVALID_ARG, "routing %lld tokens needs a workspace of %lld int32", (long long)tokens,
@@ -1082,10 +1086,9 @@ zero_status zero_route_forward(const zero_router *r, int64_t tokens, const void 
     (void)hipGetLastError();
     by_experts(E, [&](auto lc, auto vc) {
         constexpr int LPT = decltype(lc)::value, VPL = decltype(vc)::value;
-        // as many threads as the block's tokens keep busy, up to 512, or with groups'
-        // keys, of at most 43 KB, 256
+        // as many threads as the block's tokens keep busy
         const int64_t most = tokens < a.per_block ? tokens : a.per_block;
-        const int limit = group_keys(r) ? 256 : 512;
+        const int limit = route_threads(r);
         int threads = 64;
         while (threads < limit && threads / LPT < most)
             threads *= 2;
@@ -1149,10 +1152,20 @@ zero_status zero_route_backward(const zero_router *r, int64_t tokens, const void
     (void)hipGetLastError();
     by_experts<8>(r->n_experts, [&](auto lc, auto vc) {
         constexpr int LPT = decltype(lc)::value, VPL = decltype(vc)::value, TPB = 256 / LPT;
-        hipLaunchKernelGGL((route_backward_kernel<LPT, VPL>), dim3((unsigned)((tokens + TPB - 1) / TPB)), dim3(256), 0,
-                           static_cast<hipStream_t>(stream), a);
+        // as many tokens at a time as a launch has blocks for
+        constexpr int64_t most = kMaxThreads / 256 * TPB;
+        for (int64_t t0 = 0; t0 < tokens && st == ZERO_OK; t0 += most) {
+            a.tokens = tokens - t0 < most ? tokens - t0 : most;
+            a.logits = static_cast<const char *>(logits) + t0 * ldl * bytes_of(logits_dtype);
+            a.dlogits = static_cast<char *>(dlogits) + t0 * ldd * bytes_of(dlogits_dtype);
+            a.experts = experts + t0 * a.top_k;
+            a.dweights = dweights + t0 * a.top_k;
+            hipLaunchKernelGGL((route_backward_kernel<LPT, VPL>), dim3((unsigned)((a.tokens + TPB - 1) / TPB)),
+                               dim3(256), 0, static_cast<hipStream_t>(stream), a);
+            st = launched("route_backward");
+        }
     });
-    return launched("route_backward");
+    return st;
 }
 
 zero_status zero_experts_dispatch(int64_t tokens, int32_t top_k, int64_t cols, const uint16_t *x, int64_t ldx,

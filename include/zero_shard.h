@@ -883,7 +883,8 @@ typedef struct zero_router {
      rows_of  tokens x top_k int32: each choice's row when the rows are sorted by expert
               and, within an expert, by token; -1 there.
    workspace: zero_route_workspace int32 (0 for one block's tokens, when it may be
-   NULL), used until the call's work has run.  tokens x top_k is below 2^31.
+   NULL), used until the call's work has run.  tokens x top_k is below 2^31, and tokens
+   at most 2^29 - 64, with groups 2^28 - 16.
    tokens = 0 writes zero offsets. */
 zero_status zero_route_forward(const zero_router *router, int64_t tokens, const void *logits,
                                int64_t ldl, int32_t logits_dtype, const float *bias,

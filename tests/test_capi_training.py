@@ -213,6 +213,19 @@ def test_route_forward_refusals():
     assert zs.route_workspace(zs.Router(16, 2), -1) == 0
 
 
+def test_route_tokens_that_one_launch_has():
+    """Eight or sixteen threads a token, 32 bits of them a launch; too many are refused before
+    any runs (what is accepted here, for want of a workspace)."""
+    bad = refuses(route_forward, dict(work=None, top_k=1))
+    last = (1 << 29) - 64                               # blocks of 512 threads for 64 tokens
+    bad(INV, "workspace", tokens=last)
+    bad(UNSUP, "tokens", tokens=last + 1)
+    odd = dict(n_experts=33, groups=3, ldl=33)          # groups' keys in LDS: 256 for 16
+    last = (1 << 28) - 16
+    bad(INV, "workspace", tokens=last, **odd)
+    bad(UNSUP, "tokens", tokens=last + 1, **odd)
+
+
 def route_backward(tokens=100, logits=at(0), ldl=64, experts=at(1), dweights=at(2), dlogits=at(3), ldd=64, lt=zs.BF16,
                    dt=zs.BF16, **kw):
     zs.route_backward(zs.Router(**{**ROUTER, **kw}), tokens, logits, ldl, experts, dweights, dlogits, ldd,

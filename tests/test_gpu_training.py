@@ -520,6 +520,30 @@ def test_route_gradient_against_differences():
                 assert abs((f[0] - f[1]) / 2e-6 - got[i]) < 1e-8
 
 
+def test_route_gradient_of_more_tokens_than_a_launch_has_blocks():
+    """Two experts take 16 lanes a token, so a launch ends at 2^28 - 16 tokens; in place.  3 GB."""
+    T, E = (1 << 28) + 1000, 2
+    t = torch.tensor([0, 7, (1 << 28) - 17, (1 << 28) - 16, (1 << 28) - 15, 1 << 28, T - 1], device=DEV)
+    rng = np.random.default_rng(3)
+    zd, z = place(rng.standard_normal((t.numel(), E)), "bf16")
+    big = torch.zeros(T, E, dtype=torch.bfloat16, device=DEV)
+    big[t] = zd
+    ids = torch.full((T, 1), -1, dtype=torch.int32, device=DEV)
+    dw = torch.full((T, 1), float("nan"), device=DEV)
+    i, d = rng.integers(0, E, (t.numel(), 1)), np.float32(rng.standard_normal((t.numel(), 1)))
+    ids[t], dw[t] = torch.from_numpy(i.astype(np.int32)).to(DEV), torch.from_numpy(d).to(DEV)
+    zs.route_backward(zs.Router(E, 1, renormalize=False), T, big, E, ids, dw, big, E)
+    torch.cuda.synchronize()
+    want = training.route_backward(z, "softmax", i, d.astype(np.float64), False, 1.0)
+    size = training.scores(z, "softmax") * 2 * np.abs(d)
+    bound = size * (6 * score_bound(z, "softmax").max(1, keepdims=True) + 24 * U)
+    within(host(big[t]), want, stored(want, bound, "bf16"), "dlogits")
+    big[t] = 0.0
+    assert not any(part.any() for part in big.split(1 << 26))
+    del big, ids, dw
+    torch.cuda.empty_cache()
+
+
 # -------------------------------------------------------------- the moves --
 
 MOVES = [(1, 1, 1, 1), (1, 2, 8, 0), (7, 3, 40, 8), (33, 8, 129, 1), (20, 16, 520, 8), (100, 2, 1000, 0),
