@@ -721,13 +721,17 @@ zero_status check_piece(int64_t piece)
     return ZERO_OK;
 }
 
+// xent_join_kernel takes 1024 threads for 16 rows, and the dispatch counts a launch's
+// threads in 32 bits.
+constexpr int64_t kMaxRows = int64_t(0xffffffffu) / 1024 * 16;
+
 // Sizes for which the workspace's own can be computed.
 zero_status check_sizes(int64_t rows, int64_t vocab, int64_t hidden)
 {
     if (rows < 0 || vocab < 1 || hidden < 1)
         return fail(ZERO_ERR_INVALID_ARG, "rows >= 0, vocab >= 1 and hidden >= 1 are required");
-    if (rows > (int64_t(1) << 30) || vocab > (int64_t(1) << 30) || hidden > (int64_t(1) << 30))
-        return fail(ZERO_ERR_UNSUPPORTED, "rows, vocab and hidden are at most 2^30");
+    if (rows > kMaxRows || vocab > (int64_t(1) << 30) || hidden > (int64_t(1) << 30))
+        return fail(ZERO_ERR_UNSUPPORTED, "at most %lld rows, a vocab and hidden of 2^30", (long long)kMaxRows);
     return ZERO_OK;
 }
 

@@ -939,12 +939,12 @@ zero_status zero_experts_combine_backward(int64_t tokens, int32_t top_k, int64_t
    A target outside [0, vocab) is none: loss 0, dx 0, and a dz of 0 in dw, which makes
    a row of x that is not finite NaN there all the same.  hidden and the leading
    dimensions of x and W are multiples of 8, a vocabulary stored as columns too; x and
-   W 16-byte aligned; limits of zero_gemm_bf16.  loss, lse and dloss are fp32, one a
-   row; lse is what the loss left.  piece: words at a time, 0 or a multiple of 256; 0
-   takes the widest pieces of at most ZERO_XENT_PIECE_ELEMS dz (and at least 4096
-   words).  workspace: zero_linear_xent_workspace floats of the pass (`backward`;
-   16-byte aligned), used until the call's work has run.  rows = 0 writes zeros to
-   dw. */
+   W 16-byte aligned; limits of zero_gemm_bf16, and at most 2^26 - 16 rows.  loss, lse
+   and dloss are fp32, one a row; lse is what the loss left.  piece: words at a time, 0
+   or a multiple of 256; 0 takes the widest pieces of at most ZERO_XENT_PIECE_ELEMS dz
+   (and at least 4096 words).  workspace: zero_linear_xent_workspace floats of the pass
+   (`backward`; 16-byte aligned), used until the call's work has run.  rows = 0 writes
+   zeros to dw. */
 #define ZERO_XENT_PIECE_ELEMS 67108864
 zero_status zero_linear_xent_forward(int64_t rows, int64_t vocab, int64_t hidden,
                                      const uint16_t *x, int64_t ldx, const uint16_t *w,

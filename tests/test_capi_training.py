@@ -373,6 +373,18 @@ def test_head_backward_refusals():
     shares(bad, base, *[(a, b) for a in ("dx", "dw", "work") for b in names if a != b])
 
 
+@pytest.mark.parametrize("call", [xent_forward, xent_backward])
+def test_head_rows_that_one_launch_has(call):
+    """64 threads a row join its tiles, and a launch has 32 bits of them: too many rows are
+    refused before the first launch (what is accepted here, for want of a workspace)."""
+    bad = refuses(call, dict(work=None))
+    last = (1 << 26) - 16
+    bad(INV, "workspace", rows=last)
+    bad(UNSUP, "rows", rows=last + 1)
+    assert zs.linear_xent_workspace(last, 512, 64, call is xent_backward) > 0
+    assert zs.linear_xent_workspace(last + 1, 512, 64, call is xent_backward) == 0
+
+
 def test_head_workspace():
     for R, V, H in ((1, 1, 8), (100, 50257, 768), (4096, 128256, 8192), (257, 1000, 64)):
         f, b = zs.linear_xent_workspace(R, V, H), zs.linear_xent_workspace(R, V, H, True)
