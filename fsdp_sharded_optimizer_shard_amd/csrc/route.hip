@@ -682,8 +682,9 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteBackArgs
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
         const float x = ds[e0 + v];
-        // 1 - s as the sigmoid of -z: the difference would lose all of it past z = 17
-        dz[v] = n_chosen == 0 ? 0.0f : a.sigmoid ? x * (p[v] * sigmoid_of<float>(-z[v])) : p[v] * (x - dot);
+        // 1 - s is e^-z s where s is the larger: the difference would lose all of it past z = 17
+        const float rest = z[v] > 0.0f ? exp_below(-z[v]) * p[v] : 1.0f - p[v];
+        dz[v] = n_chosen == 0 ? 0.0f : a.sigmoid ? x * (p[v] * rest) : p[v] * (x - dot);
     }
     const int64_t at = t * a.ldd;
     if constexpr (VPL >= 8) {
