@@ -253,9 +253,13 @@ struct NormBackArgs {
 // A block of 1024 threads takes rows blockIdx.x, + gridDim.x, ... of groups of
 // RPB rows, TPR threads a row; a thread keeps its columns' sums in registers
 // over all of them, so that a block leaves one row of sums.  The next row's loads
-// go out before the present one's sums meet, where a thread has one chunk (with
-// two the registers do not hold both rows).  4096 rows of 8192 with a residual, 268 MB:
-// 52 us, and 5 for the blocks' sums (a copy of as much: 53).
+// go out before the present one's sums meet, where a thread has one chunk.  With 1024
+// threads a thread has 128 registers, of which bf16 rows of one chunk take 98 to 108.
+// Two chunks do not fit, even without a second row: 24 to 26 values go to scratch.
+// Operands in fp32 leave 6 or 7 there up to 4096 columns.  4096 rows of 8192 with a
+// residual, 268 MB: 52 us, and 5 for the blocks' sums (a copy of as much: 46); all in
+// fp32, 537 MB, 110 in all; 8192 rows of 4096 55 in bf16 and 112 in fp32.  A few long rows
+// are bound by their blocks' rows of sums, written and read again: 181 of 14363, 37 us.
 constexpr int kNormThreads = 1024;
 constexpr int kNormBlocks = 256;  // one a CU; a fixed number, so that the sums have the same bits everywhere
 

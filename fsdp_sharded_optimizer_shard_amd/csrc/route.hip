@@ -13,9 +13,11 @@
 // keys (log2 LPT exchanges, four of them without LDS) and one lane's step to its next.
 // 16384 tokens of 256 experts, 8 of them from 4 of 8 groups by sigmoid and bias: 27 us
 // (softmax without a bias 15), and 9 for the rows' order, where reading the logits takes
-// 3.6.  What it takes is issue slots: 12 us of loads, sorting and first keys, 8 of scores
-// in fp64, 4 of groups, 0.4 for each expert chosen, at two waves a SIMD (the sixteen keys
-// and scores of a lane fill its registers; half as many experts a lane took 39 us).
+// 3.6.  Latency at two waves a SIMD bounds it: the sixteen keys and scores of a lane take
+// 241 registers, the waves issue in 29 % of their cycles and wait in 51 %.  12 us go to
+// loads, sorting and first keys, 8 to scores in fp64, 4 to groups, 0.4 to each expert
+// chosen; half as many experts a lane took 39 us.  The order's two launches wait in
+// four fifths of their cycles.
 //
 // Order of rows.  Rows are sorted by expert and, within an expert, by token: a
 // counting sort without atomics on memory.  In a block of up to 64 tokens every
@@ -174,7 +176,9 @@ __device__ __forceinline__ void load_logits(const void *logits, bool bf16, int64
 }
 
 // e^x for x <= 0 (and NaN) in fp64, within 2^-50: 2^n e^r with |r| <= ln 2 / 2, e^r by its
-// Taylor sum of degree 13 (the next term is below 2^-57).  Below -700 it is e^-700.
+// Taylor sum of degree 13 (the next term is below 2^-57).  r = x - n ln 2 takes ln 2 in two
+// parts (Cody and Waite's reduction): its first 33 bits, of which n times is exact, and
+// what is left, rounded.  Below -700 it is e^-700.
 __device__ __forceinline__ double exp_below(double x)
 {
     x = x < -700.0 ? -700.0 : x;
@@ -433,6 +437,9 @@ __global__ __launch_bounds__(512) void route_kernel(const RouteArgs a)
                         key[VPL - 1] = -__builtin_inf();
                 }
             }
+            // The weight, from the logit again, as the score lies in some other lane; a sigmoid,
+            // the sum and the quotient in fp32, which the result is: 6e-8 off 64 bits, of which
+            // its own rounding makes 3e-8.
             if (sub < k) {
                 float z[1];
                 load_logits<1>(a.logits, a.bf16, t * a.ldl, id, E, z);

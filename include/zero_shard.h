@@ -904,8 +904,8 @@ zero_status zero_route_backward(const zero_router *router, int64_t tokens, const
                                 int32_t dlogits_dtype, void *stream);
 
 /* Tokens' rows to their experts and back.  rows_of is tokens x top_k (top_k at most
-   16); numbers outside [0, rows) are none, and no row is named twice (what dispatch and
-   combine_backward leave in such a row is unspecified).
+   16, tokens x top_k below 2^31); numbers outside [0, rows) are none, and no row is named
+   twice (what dispatch and combine_backward leave in such a row is unspecified).
      dispatch          out[rows_of[t][j]] = w[t][j] x[t]   (bf16; weights NULL: copies).
                        Rows that no token has are left as they were.
      combine           y[t] = sum over j of w[t][j] in[rows_of[t][j]] + residual[t], in
@@ -934,7 +934,9 @@ zero_status zero_experts_combine_backward(int64_t tokens, int32_t top_k, int64_t
      lse[r]  = log(sum over c of exp z[r][c]),  loss[r] = lse[r] - z[r][targets[r]];
      dz      = (exp(z - lse) - [c = target]) dloss[r], rounded to bf16 once divided by the
                mantissa of a counted row's dloss, which dx and dw are multiplied by
-               (a piece of the vocabulary at a time, in the workspace);
+               (a piece of the vocabulary at a time, in the workspace): in fp32 dx and
+               dw are then 1e-4 off or less, in the 2-norm, where all counted rows have
+               one dloss, 2e-3 where each has its own;
      dx      = dz W^T (rows x hidden), dw = x^T dz (as W lies), fp32 sums, bf16 or fp32.
    A target outside [0, vocab) is none: loss 0, dx 0, and a dz of 0 in dw, which makes
    a row of x that is not finite NaN there all the same.  hidden and the leading
@@ -1034,7 +1036,8 @@ zero_status zero_tensors_sumsq(int32_t n_tensors, const zero_tensor *tensors, in
 int64_t zero_tensors_partials_count(int32_t n_tensors, const zero_tensor *tensors);
 
 /* What n 8-bit state codes and their scales stand for: m, or with `second` v (the
-   square of what is kept), bf16 or fp32, both exact. */
+   square of what is kept), bf16 or fp32, both exact but for a v below 2^-126, the
+   least normal number, or past the largest. */
 zero_status zero_adam_state_read(int64_t n, const uint8_t *codes, const uint8_t *scales,
                                  int32_t second, void *out, int32_t out_dtype, void *stream);
 

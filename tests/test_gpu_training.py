@@ -941,6 +941,30 @@ def test_adam_of_many_tensors(state, grad, shift, decoupled):
 
 
 @pytest.mark.parametrize("state", ["fp32", "e4m3"])
+def test_adam_of_new_gradients_each_step(state):
+    """One list, other gradient tensors for every step, in bf16 and fp32 by turns; the caller
+    keeps none of them."""
+    rng = np.random.default_rng(23)
+    out, ref = adam_lists(rng, SIZES, state, "bf16")
+    ts = tensor_list(dict(out, grad=None), state, None)
+    for step, grad in ((1, "bf16"), (2, "fp32"), (3, "bf16")):
+        g, ref["grad"] = [], []
+        for n in SIZES:
+            t, x = vector(rng.standard_normal(n) * 1e-3, grad)
+            g.append(t)
+            ref["grad"].append(np.float32(x))
+        ts.set_grads(g)
+        del g, t
+        parts = torch.empty(ts.partials_count(), dtype=torch.float64, device=DEV)
+        zs.tensors_sumsq(ts, parts)
+        zs.adam_tensors(ts, zs.adam_cfg(step=step, **CFG), seed=4)
+        torch.cuda.synchronize()
+        want = sum(float((x.astype(np.float64) ** 2).sum()) for x in ref["grad"])
+        assert abs(float(parts.sum()) / want - 1) < 2.0 ** -40
+        same_state(out, ref, adam_oracle(ref, SIZES, state, CFG, step, 4, [True] * len(SIZES), None), state)
+
+
+@pytest.mark.parametrize("state", ["fp32", "e4m3"])
 def test_adam_of_more_tensors_than_a_launch_holds(state):
     rng = np.random.default_rng(9)
     sizes = [int(n) for n in rng.integers(1, 400, 101)]
